@@ -449,6 +449,85 @@ int moe_route_bwd(const float* d_topk_w, const float* topk_w, const int32_t* top
                   float* d_logits, float* dx_router, float* dw_router, void* ws, size_t ws_bytes,
                   void* stream);
 
+/* moe_route_bwd with a gradient of the logits from elsewhere added (the
+ * auxiliary losses': moe_balance_loss_bwd), so every expert takes part:
+ *   d_logits[t,e] = d_logits_add[t,e] + the gate gradient (kept experts)
+ *   dx_router[t]  = sum_e d_logits[t,e] * w_router[:,e]     [T,H] fp32 or NULL
+ *   dw_router     = x^T . d_logits                          [H,E] fp32 or NULL
+ * d_logits may be d_logits_add.  The input gradient of the layer is then
+ * moe_combine(dx_perm, NULL, dest_row, dx_router).  Other arguments, workspace
+ * (MOE_OP_ROUTE_BWD), limits and errors as moe_route_bwd; dx_router is the
+ * dense product with two bf16 halves for bf16 with E % 64 == 0, else summed in
+ * fp32 over all experts in expert order. */
+int moe_route_bwd_add(const float* d_topk_w, const float* topk_w, const int32_t* topk_idx,
+                      const float* d_logits_add, const void* x, const void* w_router, int T, int H,
+                      int E, int k, int dtype, float* d_logits, float* dx_router, float* dw_router,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* Auxiliary losses of the router over the logits [T,E] of moe_route: the
+ * load-balance loss with its per-expert counts, and the z loss.  The T rows
+ * are packed sequences s = 0..S-1, rows [seq_offsets[s], seq_offsets[s+1]);
+ * seq_offsets NULL: one sequence of all rows (S = 1).  Rows with
+ * token_mask[t] == 0 (padding) and rows outside the sequences are not live:
+ * nothing of them is used, whatever they hold.  With p[t,:] = softmax(z[t,:]),
+ * lse[t] = log sum_e exp z[t,e], n_s live rows in s and N in all:
+ *   counts[s,e]   = live slots of s with topk_idx == e (entries outside [0,E) are skipped)
+ *   prob_sum[s,e] = sum over live t in s of p[t,e]
+ *   loss[0] = E / (k N) sum_s (1/n_s) sum_e counts[s,e] prob_sum[s,e]   (balance:
+ *             E sum_e f_e P_e of each sequence, weighted by its rows; 1 when even)
+ *   loss[1] = (1/N) sum_t lse[t]^2                                      (z)
+ *   loss[2] = balance_coef * loss[0] + z_coef * loss[1]
+ * A sequence without live rows adds nothing; N = 0 gives 0.  Logits of -inf
+ * have probability 0; a row of -inf alone has probabilities and lse 0.  Sums
+ * are fp32 within a chunk of rows and in a fixed order, the last ones fp64.
+ *   seq_offsets [S+1] int32 ascending (device), token_mask [T] uint8 or NULL
+ *   counts, prob_sum [S,E], tokens [S+1] int32 (n_s, then N), lse [T] fp32 (0
+ *   for rows not live), loss [3] fp32
+ *   ws       moe_balance_ws_bytes(T, E, S) bytes
+ * T = 0 writes zeros to counts, prob_sum, tokens and loss. */
+int64_t moe_balance_ws_bytes(int T, int E, int S);
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
+                     const uint8_t* token_mask, int T, int E, int k, int S, float balance_coef,
+                     float z_coef, int32_t* counts, float* prob_sum, int32_t* tokens, float* lse,
+                     float* loss, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of loss[2] wrt the logits, with the counts held fixed (they are
+ * whole numbers), for the upstream gradient *d_loss (device scalar; NULL: 1):
+ *   d_logits[t,e] = d_loss p[t,e] (balance_coef E / (k N n_s) (counts[s,e] - sum_j p[t,j] counts[s,j])
+ *                                  + z_coef 2 lse[t] / N)
+ * Rows that are not live get 0.  accumulate != 0 adds to d_logits.  logits,
+ * lse, counts, tokens, seq_offsets and token_mask as given to and written by
+ * moe_balance_loss. */
+int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* counts,
+                         const int32_t* tokens, const int32_t* seq_offsets,
+                         const uint8_t* token_mask, const float* d_loss, int T, int E, int k, int S,
+                         float balance_coef, float z_coef, int accumulate, float* d_logits,
+                         void* stream);
+
+/* moe_combine with dropout of the combined rows and the residual added:
+ *   y[t,h] = residual[t,h] + keep[t,h] / (1 - p) * sum_j topk_w[t,j] * y_perm[dest_row[t*k+j],h]
+ * in fp32, rounded once.  keep[t,h] comes from a counter-based generator and
+ * is never stored: word i % 4, i = t*H + h, of Philox4x32-10 (Salmon, Moraes,
+ * Dror, Shaw 2011) at the 128-bit counter (i / 4, offset) (low words first)
+ * under the key seed is kept when it is >= floor(p * 2^32).  rng is a DEVICE
+ * array {seed, offset}, so a captured graph takes new numbers each replay when
+ * the caller advances offset.  0 <= p < 1; a dropped element is residual
+ * whatever y_perm holds.
+ *   residual [T,H] dtype or NULL (0); y may be residual
+ *   rng      [2] uint64;  other arguments as moe_combine */
+int moe_combine_dropout(const void* y_perm, const float* topk_w, const int32_t* dest_row,
+                        const void* residual, double p, const uint64_t* rng, int T, int H, int k,
+                        int dtype, void* y, void* stream);
+
+/* Backward of moe_combine_dropout under the same rng and p: with
+ * g[t,h] = keep[t,h] / (1 - p) * dy[t,h] (fp32, not rounded),
+ *   dy_perm[dest_row[t*k+j]] = topk_w[t,j] * g[t]            (stored as dtype)
+ *   d_topk_w[t,j] = <g[t], y_perm[dest_row[t*k+j]]> over kept elements (fp32; 0 for non-local slots)
+ * The residual's gradient is dy. */
+int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* topk_w,
+                            const int32_t* dest_row, double p, const uint64_t* rng, int T, int H,
+                            int k, int dtype, void* dy_perm, float* d_topk_w, void* stream);
+
 /* Kernel timing hook (benchmarks and profilers).  After this call the library
  * records start_events[i] and stop_events[i] (each a hipEvent_t created by
  * the caller) on the launch stream immediately before and after the i-th
@@ -476,7 +555,11 @@ typedef enum {
   MOE_KERNEL_ROUTE_BWD_DX = 15,   /* router input gradient as an MFMA product (moe_route_bwd) */
   MOE_KERNEL_COMBINE_ADD = 16,    /* moe_combine with an addend (an input gradient's unpermute-reduce) */
   MOE_KERNEL_FFN_WGRAD_REDUCE = 17, /* split experts' weight-gradient partials added (moe_grouped_ffn_bwd) */
-  MOE_KERNEL_COUNT = 18
+  MOE_KERNEL_BALANCE = 18,           /* auxiliary losses, forward (both launches) */
+  MOE_KERNEL_BALANCE_BWD = 19,
+  MOE_KERNEL_COMBINE_DROPOUT = 20,
+  MOE_KERNEL_COMBINE_DROPOUT_BWD = 21,
+  MOE_KERNEL_COUNT = 22
 } moe_kernel;
 
 int moe_profile_kernel(int kernel_id, void** start_events, void** stop_events, int n);

@@ -13,7 +13,9 @@ forward: moe_quantize_fp8, moe_grouped_ffn_fwd_fp8; data gradients:
 moe_quantize_fp8_t, moe_grouped_ffn_dgrad_fp8; both weight layouts at once:
 moe_quantize_fp8_w; weight gradients:
 moe_quantize_fp8_group_t, moe_grouped_ffn_wgrad_fp8, and its two halves
-moe_grouped_ffn_wgrad_fp8_begin / _end) and return
+moe_grouped_ffn_wgrad_fp8_begin / _end; around the layer: the router's
+auxiliary losses moe_balance_loss / _bwd with moe_route_bwd_add, and the combine
+with dropout moe_combine_dropout / _bwd) and return
 freshly allocated torch tensors; each also accepts preallocated outputs via
 ``out=`` dictionaries so that steady-state loops allocate nothing.
 """
@@ -45,6 +47,7 @@ def _load():
             f"{LIB_PATH} is not built; run __graft_entry__.build() (hipcc --offload-arch=gfx950)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    F32, F64 = ctypes.c_float, ctypes.c_double
     sig = {
         "moe_abi_version": ([], I32),
         "moe_last_error": ([], ctypes.c_char_p),
@@ -79,6 +82,12 @@ def _load():
                                       I32),
         "moe_grouped_ffn_wgrad_fp8_begin": ([P, P, P, P, P, I32, I32, I32, I32, P, I32, P, SZ, P], I32),
         "moe_grouped_ffn_wgrad_fp8_end": ([P, P, I32, I32, I32, I32, P, P, P, I32, P, SZ, P], I32),
+        "moe_route_bwd_add": ([P, P, P, P, P, P, I32, I32, I32, I32, I32, P, P, P, P, SZ, P], I32),
+        "moe_balance_ws_bytes": ([I32] * 3, I64),
+        "moe_balance_loss": ([P, P, P, P, I32, I32, I32, I32, F32, F32, P, P, P, P, P, P, SZ, P], I32),
+        "moe_balance_loss_bwd": ([P, P, P, P, P, P, P, I32, I32, I32, I32, F32, F32, I32, P, P], I32),
+        "moe_combine_dropout": ([P, P, P, P, F64, P, I32, I32, I32, I32, P, P], I32),
+        "moe_combine_dropout_bwd": ([P, P, P, P, F64, P, I32, I32, I32, I32, P, P, P], I32),
         "moe_profile_kernel": ([I32, ctypes.POINTER(P), ctypes.POINTER(P), I32], I32),
         "moe_profile_recorded": ([], I32),
     }
@@ -379,6 +388,199 @@ def moe_route_bwd(d_topk_w: torch.Tensor, topk_w: torch.Tensor, topk_idx: torch.
                              _ptr(w_router), T, H, E, k, dt, _ptr(o["d_logits"]),
                              _ptr(o["dx_router"]), _ptr(o["dw_router"]), _ptr(ws), _nbytes(ws),
                              _stream()), "moe_route_bwd")
+    return o
+
+
+# ---------------------------------------------------------------------------
+# Auxiliary losses, dropout.  Their arguments are checked here for device, type
+# and shape (the library sees plain pointers).
+# ---------------------------------------------------------------------------
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, dev, optional: bool = False):
+    """Pointer of a dense tensor of this type and shape on the device in use."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} must be given")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device(t: torch.Tensor) -> torch.device:
+    """The device of the call: t's, which has to be the current GPU (whose current
+    stream the call is enqueued on)."""
+    if not t.is_cuda:
+        raise ValueError(f"expected tensors on a GPU, got {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device} while cuda:{torch.cuda.current_device()} is the "
+                         f"current device")
+    return t.device
+
+
+def _into(o: Dict[str, torch.Tensor], name: str, shape, dtype, dev) -> int:
+    """Pointer of output `name`: the caller's tensor from o (checked), else a new one."""
+    if o.get(name) is None:
+        o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        return o[name].data_ptr()
+    return _arg(o[name], name, dtype, shape, dev)
+
+
+def _row_type(t: torch.Tensor, name: str) -> torch.dtype:
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
+    return t.dtype
+
+
+def _shape2(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def moe_route_bwd_add(d_topk_w: torch.Tensor, topk_w: torch.Tensor, topk_idx: torch.Tensor,
+                      d_logits_add: torch.Tensor, x: torch.Tensor, w_router: torch.Tensor,
+                      want_dx: bool = True, want_dw: bool = True, ws: Optional[torch.Tensor] = None,
+                      out: Optional[Dict[str, torch.Tensor]] = None):
+    """moe_route_bwd with d_logits_add [T,E] (e.g. moe_balance_loss_bwd's) added to the logit
+    gradient.  Returns dict d_logits [T,E], dx_router [T,H] fp32 (or None), dw_router [H,E] fp32
+    (or None); out["d_logits"] may be d_logits_add."""
+    dev = _device(x)
+    T, H = _shape2(x, "x")
+    E = _shape2(w_router, "w_router")[1]
+    k = _shape2(topk_idx, "topk_idx")[1]
+    dt, f32 = _row_type(x, "x"), torch.float32
+    o = dict(out or {})
+    a = [_arg(d_topk_w, "d_topk_w", f32, (T, k), dev), _arg(topk_w, "topk_w", f32, (T, k), dev),
+         _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+         _arg(d_logits_add, "d_logits_add", f32, (T, E), dev), _arg(x, "x", dt, (T, H), dev),
+         _arg(w_router, "w_router", dt, (H, E), dev)]
+    d_logits = _into(o, "d_logits", (T, E), f32, dev)
+    dx = _into(o, "dx_router", (T, H), f32, dev) if want_dx else None
+    dw = _into(o, "dw_router", (H, E), f32, dev) if want_dw else None
+    if not want_dx:
+        o["dx_router"] = None
+    if not want_dw:
+        o["dw_router"] = None
+    code = _dtype_code(x)
+    ws = _ws(workspace_bytes(MOE_OP_ROUTE_BWD, T, H, 1, E, k, 0, E, code), dev, ws)
+    _check(lib.moe_route_bwd_add(*a, T, H, E, k, code, d_logits, dx, dw, _ptr(ws), _nbytes(ws),
+                                 _stream()), "moe_route_bwd_add")
+    return o
+
+
+def _sequences(seq_offsets: Optional[torch.Tensor], dev):
+    """(S, pointer): the packed sequences, or all rows as one."""
+    if seq_offsets is None:
+        return 1, None
+    S = seq_offsets.numel() - 1
+    return S, _arg(seq_offsets, "seq_offsets", torch.int32, (S + 1,), dev)
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef: float,
+                     z_coef: float = 0.0, seq_offsets: Optional[torch.Tensor] = None,
+                     token_mask: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                     out: Optional[Dict[str, torch.Tensor]] = None):
+    """Load-balance and z loss of the router's logits [T,E] fp32, with the per-expert counts.
+    seq_offsets [S+1] int32: packed sequences (None: one); token_mask [T] uint8, 0 = padding.
+    Returns dict loss [3] (balance, z, balance_coef * balance + z_coef * z), counts [S,E] int32,
+    prob_sum [S,E], tokens [S+1] int32 (live rows of each sequence, then of all), lse [T], and the
+    workspace ws used (pass it and the dict back in to allocate nothing)."""
+    dev = _device(logits)
+    T, E = _shape2(logits, "logits")
+    k = _shape2(topk_idx, "topk_idx")[1]
+    S, off = _sequences(seq_offsets, dev)
+    f32, i32 = torch.float32, torch.int32
+    o = dict(out or {})
+    a = [_arg(logits, "logits", f32, (T, E), dev), _arg(topk_idx, "topk_idx", i32, (T, k), dev), off,
+         _arg(token_mask, "token_mask", torch.uint8, (T,), dev, optional=True)]
+    nb = lib.moe_balance_ws_bytes(T, E, S)
+    if nb < 0:
+        _check(int(nb), "moe_balance_ws_bytes")
+    o["ws"] = _ws(int(nb), dev, ws)
+    _check(lib.moe_balance_loss(*a, T, E, k, S, balance_coef, z_coef,
+                                _into(o, "counts", (S, E), i32, dev),
+                                _into(o, "prob_sum", (S, E), f32, dev),
+                                _into(o, "tokens", (S + 1,), i32, dev), _into(o, "lse", (T,), f32, dev),
+                                _into(o, "loss", (3,), f32, dev), _ptr(o["ws"]), _nbytes(o["ws"]),
+                                _stream()), "moe_balance_loss")
+    return o
+
+
+def moe_balance_loss_bwd(logits: torch.Tensor, fwd: Dict[str, torch.Tensor], k: int,
+                         balance_coef: float, z_coef: float = 0.0,
+                         d_loss: Optional[torch.Tensor] = None,
+                         seq_offsets: Optional[torch.Tensor] = None,
+                         token_mask: Optional[torch.Tensor] = None, accumulate: bool = False,
+                         out: Optional[torch.Tensor] = None):
+    """Gradient of loss[2] wrt the logits; fwd: moe_balance_loss's dict (lse, counts, tokens) for
+    the same logits, k, seq_offsets and token_mask; d_loss [1] fp32: the upstream gradient (None:
+    1).  Returns d_logits [T,E] (out, added to with accumulate=True)."""
+    dev = _device(logits)
+    T, E = _shape2(logits, "logits")
+    S, off = _sequences(seq_offsets, dev)
+    f32, i32 = torch.float32, torch.int32
+    if accumulate and out is None:
+        raise ValueError("accumulate=True needs out")
+    o = {"d_logits": out}
+    a = [_arg(logits, "logits", f32, (T, E), dev), _arg(fwd["lse"], "lse", f32, (T,), dev),
+         _arg(fwd["counts"], "counts", i32, (S, E), dev),
+         _arg(fwd["tokens"], "tokens", i32, (S + 1,), dev), off,
+         _arg(token_mask, "token_mask", torch.uint8, (T,), dev, optional=True),
+         _arg(d_loss, "d_loss", f32, (1,), dev, optional=True)]
+    _check(lib.moe_balance_loss_bwd(*a, T, E, k, S, balance_coef, z_coef, 1 if accumulate else 0,
+                                    _into(o, "d_logits", (T, E), f32, dev), _stream()),
+           "moe_balance_loss_bwd")
+    return o["d_logits"]
+
+
+def moe_combine_dropout(y_perm: torch.Tensor, topk_w: Optional[torch.Tensor], dest_row: torch.Tensor,
+                        T: int, p: float, rng: torch.Tensor,
+                        residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """moe_combine with dropout (probability p) and the residual [T,H] added.  rng [2] int64 on the
+    GPU: seed and offset of the counter-based generator; the same rng goes to
+    moe_combine_dropout_bwd.  Returns y [T,H] (out may be residual)."""
+    dev = _device(y_perm)
+    R_cap, H = _shape2(y_perm, "y_perm")
+    dt = _row_type(y_perm, "y_perm")
+    if T < 0 or dest_row.numel() % max(T, 1):
+        raise ValueError(f"dest_row has {dest_row.numel()} entries, not a multiple of T = {T}")
+    k = dest_row.numel() // T if T > 0 else 1
+    o = {"y": out}
+    a = [_arg(y_perm, "y_perm", dt, (R_cap, H), dev),
+         _arg(topk_w, "topk_w", torch.float32, (T, k), dev, optional=True),
+         _arg(dest_row, "dest_row", torch.int32, (T * k,), dev),
+         _arg(residual, "residual", dt, (T, H), dev, optional=True)]
+    _check(lib.moe_combine_dropout(*a, p, _arg(rng, "rng", torch.int64, (2,), dev), T, H, k,
+                                   _dtype_code(y_perm), _into(o, "y", (T, H), dt, dev), _stream()),
+           "moe_combine_dropout")
+    return o["y"]
+
+
+def moe_combine_dropout_bwd(dy: torch.Tensor, y_perm: torch.Tensor, topk_w: torch.Tensor,
+                            dest_row: torch.Tensor, p: float, rng: torch.Tensor,
+                            out: Optional[Dict[str, torch.Tensor]] = None):
+    """Backward of moe_combine_dropout under its p and rng (the residual's gradient is dy).
+    Returns dict dy_perm [R_cap,H], d_topk_w [T,k]."""
+    dev = _device(dy)
+    T, H = _shape2(dy, "dy")
+    k = _shape2(topk_w, "topk_w")[1]
+    R_cap = _shape2(y_perm, "y_perm")[0]
+    dt, f32 = _row_type(dy, "dy"), torch.float32
+    o = dict(out or {})
+    a = [_arg(dy, "dy", dt, (T, H), dev), _arg(y_perm, "y_perm", dt, (R_cap, H), dev),
+         _arg(topk_w, "topk_w", f32, (T, k), dev),
+         _arg(dest_row, "dest_row", torch.int32, (T * k,), dev)]
+    _check(lib.moe_combine_dropout_bwd(*a, p, _arg(rng, "rng", torch.int64, (2,), dev), T, H, k,
+                                       _dtype_code(dy), _into(o, "dy_perm", (R_cap, H), dt, dev),
+                                       _into(o, "d_topk_w", (T, k), f32, dev), _stream()),
+           "moe_combine_dropout_bwd")
     return o
 
 

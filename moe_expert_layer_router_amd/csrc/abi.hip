@@ -825,11 +825,12 @@ int moe_grouped_ffn_bwd_split(const void* dy_perm, const void* x_perm, const voi
                  accumulate, ws, ws_bytes, stream, wgrad_stream);
 }
 
-int moe_route_bwd(const float* d_topk_w, const float* topk_w, const int32_t* topk_idx,
-                  const void* x, const void* w_router, int T, int H, int E, int k, int dtype,
-                  float* d_logits, float* dx_router, float* dw_router, void* ws, size_t ws_bytes,
-                  void* stream) {
-  const char* fn = "moe_route_bwd";
+namespace {
+// d_add null: the gate gradient alone
+int route_bwd(const char* fn, const float* d_topk_w, const float* topk_w, const int32_t* topk_idx,
+              const float* d_add, const void* x, const void* w_router, int T, int H, int E, int k,
+              int dtype, float* d_logits, float* dx_router, float* dw_router, void* ws,
+              size_t ws_bytes, void* stream) {
   if (int rc = check_dtype(dtype, fn)) return rc;
   if (int rc = check_routing_shape(T, E, k, fn)) return rc;
   if (int rc = check_row_width(H, dtype, fn)) return rc;
@@ -871,10 +872,14 @@ int moe_route_bwd(const float* d_topk_w, const float* topk_w, const int32_t* top
   const bool dx_mfma = bf16 && dx_router != nullptr && router_dx_mfma_ok(H, E);
   if (T > 0 && dx_router != nullptr && !dx_mfma)
     e = launch_transpose(w_router, wt, H, E, elem_bytes(dtype), s);
+  float* dx_gather = dx_mfma ? nullptr : dx_router;
+  bf16_t* halves = (bf16 && (dw_router != nullptr || dx_mfma)) ? dz_hilo : nullptr;
   if (e == hipSuccess && T > 0)
-    e = launch_route_bwd_dz(d_topk_w, topk_w, topk_idx, wt, T, H, E, k, bf16, d_logits,
-                            dx_mfma ? nullptr : dx_router,
-                            (bf16 && (dw_router != nullptr || dx_mfma)) ? dz_hilo : nullptr, s);
+    e = d_add != nullptr
+            ? launch_route_bwd_dense(d_topk_w, topk_w, topk_idx, d_add, wt, T, H, E, k, bf16,
+                                     d_logits, dx_gather, halves, s)
+            : launch_route_bwd_dz(d_topk_w, topk_w, topk_idx, wt, T, H, E, k, bf16, d_logits,
+                                  dx_gather, halves, s);
   if (e == hipSuccess && T > 0 && dx_mfma)
     e = launch_router_dx(dz_hilo, (const bf16_t*)w_router, T, H, E, dx_router, s);
   if (e == hipSuccess && dw_router != nullptr) {
@@ -891,6 +896,134 @@ int moe_route_bwd(const float* d_topk_w, const float* topk_w, const int32_t* top
     }
   }
   return hip_status(e, fn);
+}
+}  // namespace
+
+int moe_route_bwd(const float* d_topk_w, const float* topk_w, const int32_t* topk_idx,
+                  const void* x, const void* w_router, int T, int H, int E, int k, int dtype,
+                  float* d_logits, float* dx_router, float* dw_router, void* ws, size_t ws_bytes,
+                  void* stream) {
+  return route_bwd("moe_route_bwd", d_topk_w, topk_w, topk_idx, nullptr, x, w_router, T, H, E, k,
+                   dtype, d_logits, dx_router, dw_router, ws, ws_bytes, stream);
+}
+
+int moe_route_bwd_add(const float* d_topk_w, const float* topk_w, const int32_t* topk_idx,
+                      const float* d_logits_add, const void* x, const void* w_router, int T, int H,
+                      int E, int k, int dtype, float* d_logits, float* dx_router, float* dw_router,
+                      void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_route_bwd_add";
+  if (T > 0)
+    if (int rc = check_ptr(d_logits_add, "d_logits_add", fn)) return rc;
+  return route_bwd(fn, d_topk_w, topk_w, topk_idx, d_logits_add, x, w_router, T, H, E, k, dtype,
+                   d_logits, dx_router, dw_router, ws, ws_bytes, stream);
+}
+
+namespace {
+int check_balance(int T, int E, int k, int S, const int32_t* seq_offsets, const char* fn) {
+  if (int rc = check_routing_shape(T, E, k, fn)) return rc;
+  if (S < 1 || S > (1 << 20)) return fail(MOE_EINVAL, "%s: S=%d outside [1, 2^20]", fn, S);
+  if (seq_offsets == nullptr && S != 1)
+    return fail(MOE_EINVAL, "%s: S=%d sequences need seq_offsets", fn, S);
+  return MOE_OK;
+}
+}  // namespace
+
+int64_t moe_balance_ws_bytes(int T, int E, int S) {
+  const char* fn = "moe_balance_ws_bytes";
+  if (T < 0 || E < 1 || E > kMaxE || S < 1 || S > (1 << 20))
+    return fail(MOE_EINVAL, "%s: need T >= 0, E in [1, %d] and S in [1, 2^20] (T=%d, E=%d, S=%d)",
+                fn, kMaxE, T, E, S);
+  return (int64_t)balance_ws_bytes(T, E, S);
+}
+
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
+                     const uint8_t* token_mask, int T, int E, int k, int S, float balance_coef,
+                     float z_coef, int32_t* counts, float* prob_sum, int32_t* tokens, float* lse,
+                     float* loss, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_balance_loss";
+  if (int rc = check_balance(T, E, k, S, seq_offsets, fn)) return rc;
+  if (T > 0) {
+    if (int rc = check_ptr(logits, "logits", fn)) return rc;
+    if (int rc = check_ptr(topk_idx, "topk_idx", fn)) return rc;
+    if (int rc = check_ptr(lse, "lse", fn)) return rc;
+  }
+  if (int rc = check_ptr(counts, "counts", fn)) return rc;
+  if (int rc = check_ptr(prob_sum, "prob_sum", fn)) return rc;
+  if (int rc = check_ptr(tokens, "tokens", fn)) return rc;
+  if (int rc = check_ptr(loss, "loss", fn)) return rc;
+  if (int rc = check_ws(ws, ws_bytes, balance_ws_bytes(T, E, S), fn)) return rc;
+  return hip_status(launch_balance_loss(logits, topk_idx, seq_offsets, token_mask, T, E, k, S,
+                                        balance_coef, z_coef, counts, prob_sum, tokens, lse, loss,
+                                        ws, begin_launch(stream)),
+                    fn);
+}
+
+int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* counts,
+                         const int32_t* tokens, const int32_t* seq_offsets,
+                         const uint8_t* token_mask, const float* d_loss, int T, int E, int k, int S,
+                         float balance_coef, float z_coef, int accumulate, float* d_logits,
+                         void* stream) {
+  const char* fn = "moe_balance_loss_bwd";
+  if (int rc = check_balance(T, E, k, S, seq_offsets, fn)) return rc;
+  if (accumulate != 0 && accumulate != 1) return fail(MOE_EINVAL, "%s: accumulate must be 0 or 1", fn);
+  if (T == 0) return MOE_OK;
+  if (int rc = check_ptr(logits, "logits", fn)) return rc;
+  if (int rc = check_ptr(lse, "lse", fn)) return rc;
+  if (int rc = check_ptr(counts, "counts", fn)) return rc;
+  if (int rc = check_ptr(tokens, "tokens", fn)) return rc;
+  if (int rc = check_ptr(d_logits, "d_logits", fn)) return rc;
+  return hip_status(launch_balance_loss_bwd(logits, lse, counts, tokens, seq_offsets, token_mask,
+                                            d_loss, T, E, k, S, balance_coef, z_coef,
+                                            accumulate != 0, d_logits, begin_launch(stream)),
+                    fn);
+}
+
+namespace {
+int check_dropout(double p, const uint64_t* rng, int T, int H, int k, int dtype, const char* fn) {
+  if (int rc = check_dtype(dtype, fn)) return rc;
+  if (T < 0) return fail(MOE_EINVAL, "%s: T must be >= 0", fn);
+  if (k < 1 || k > kMaxK) return fail(MOE_EINVAL, "%s: k=%d outside [1, %d]", fn, k, kMaxK);
+  if (int rc = check_row_width(H, dtype, fn)) return rc;
+  if (!(p >= 0.0 && p < 1.0)) return fail(MOE_EINVAL, "%s: p=%g outside [0, 1)", fn, p);
+  if (T == 0) return MOE_OK;
+  if (int rc = check_ptr(rng, "rng", fn)) return rc;
+  if (((uintptr_t)rng & 7u) != 0) return fail(MOE_EINVAL, "%s: rng must be 8-byte aligned", fn);
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_combine_dropout(const void* y_perm, const float* topk_w, const int32_t* dest_row,
+                        const void* residual, double p, const uint64_t* rng, int T, int H, int k,
+                        int dtype, void* y, void* stream) {
+  const char* fn = "moe_combine_dropout";
+  if (int rc = check_dropout(p, rng, T, H, k, dtype, fn)) return rc;
+  if (T == 0) return MOE_OK;
+  if (int rc = check_ptr(y_perm, "y_perm", fn, true)) return rc;
+  if (int rc = check_ptr(dest_row, "dest_row", fn)) return rc;
+  if (int rc = check_ptr(y, "y", fn, true)) return rc;
+  if (residual != nullptr && !aligned16(residual))
+    return fail(MOE_EINVAL, "%s: residual must be 16-byte aligned", fn);
+  return hip_status(launch_combine_dropout(y_perm, topk_w, dest_row, residual, p, rng, T, H, k,
+                                           dtype == MOE_BF16, y, begin_launch(stream)),
+                    fn);
+}
+
+int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* topk_w,
+                            const int32_t* dest_row, double p, const uint64_t* rng, int T, int H,
+                            int k, int dtype, void* dy_perm, float* d_topk_w, void* stream) {
+  const char* fn = "moe_combine_dropout_bwd";
+  if (int rc = check_dropout(p, rng, T, H, k, dtype, fn)) return rc;
+  if (T == 0) return MOE_OK;
+  if (int rc = check_ptr(dy, "dy", fn, true)) return rc;
+  if (int rc = check_ptr(y_perm, "y_perm", fn, true)) return rc;
+  if (int rc = check_ptr(topk_w, "topk_w", fn)) return rc;
+  if (int rc = check_ptr(dest_row, "dest_row", fn)) return rc;
+  if (int rc = check_ptr(dy_perm, "dy_perm", fn, true)) return rc;
+  if (int rc = check_ptr(d_topk_w, "d_topk_w", fn)) return rc;
+  return hip_status(launch_combine_dropout_bwd(dy, y_perm, topk_w, dest_row, p, rng, T, H, k,
+                                               dtype == MOE_BF16, dy_perm, d_topk_w,
+                                               begin_launch(stream)),
+                    fn);
 }
 
 }  // extern "C"

@@ -6,108 +6,9 @@
 // the 16-byte loads of up to four grouped rows x four chunks per lane at once
 // and sums them in fp32 in slot order j = 0..k-1.  No atomics, so the result is
 // deterministic and independent of the launch shape.
-#include "common.h"
+#include "rows.h"
 
 namespace moe {
-
-// 16 bytes of a row: 8 bf16 or 4 fp32 elements, held as a native vector.
-template <bool BF16>
-struct Row {
-  static constexpr int N = BF16 ? 8 : 4;
-  static constexpr int EB = BF16 ? 2 : 4;
-  __device__ static u32x4_t ld(const void* base, size_t elem) {
-    return *reinterpret_cast<const u32x4_t*>((const char*)base + elem * EB);
-  }
-  __device__ static void st(void* base, size_t elem, u32x4_t v) {
-    *reinterpret_cast<u32x4_t*>((char*)base + elem * EB) = v;
-  }
-  // Streaming (non-temporal) forms for rows touched once per call: grouped
-  // rows, token rows and the outputs.  They keep the caches for what is
-  // re-read (the router weight rows); on the full 128-expert layer they raise
-  // the combine from 0.64 to 0.76 of HBM.
-  __device__ static u32x4_t ld_s(const void* base, size_t elem) {
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>((const char*)base + elem * EB));
-  }
-  __device__ static void st_s(void* base, size_t elem, u32x4_t v) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>((char*)base + elem * EB));
-  }
-  __device__ static void to_f32(u32x4_t v, float* f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (BF16) {
-        f[2 * i] = __uint_as_float(v[i] << 16);
-        f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-      } else {
-        f[i] = __uint_as_float(v[i]);
-      }
-    }
-  }
-  __device__ static u32x4_t from_f32(const float* f) {
-    u32x4_t v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = BF16 ? pack_bf2(f[2 * i], f[2 * i + 1]) : __float_as_uint(f[i]);
-    return v;
-  }
-};
-
-// Chunks of 16 bytes per lane per pass and slots whose rows are loaded
-// together: all CU x SG row loads of a pass are in flight at once.  Eight
-// slots (a top-8 token in one round trip) double the load registers and halve
-// the waves per SIMD, which costs more on an EP share (about one local slot
-// per token) than it gains on the full layer.
-constexpr int kCU = 4;
-constexpr int kSG = 4;
-
-// Moves the lanes holding a local slot (d >= 0; lanes >= k hold d = -1) to
-// lanes 0..n-1, keeping slot order; returns n.  Lane i then holds that slot's
-// row d, weight w and slot index j.  Lanes without a slot all send to lane
-// 63, which is never read (n <= k <= 32).
-__device__ __forceinline__ int pack_slots(int d, float w, int& dc, float& wc, int& jc) {
-  const int lane = lane_id();
-  const uint64_t m = __ballot(d >= 0);
-  const int rank = __popcll(m & ((1ull << lane) - 1ull));
-  const int to = (d >= 0 ? rank : 63) << 2;
-  dc = __builtin_amdgcn_ds_permute(to, d);
-  wc = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(w)));
-  jc = __builtin_amdgcn_ds_permute(to, lane);
-  return __popcll(m);
-}
-
-// out[c] = sum over packed slots j < n (ascending) of wc_j * rows[dc_j][c] for
-// this lane's chunks c0 + u * 64 + lane; fp32 accumulation.  STREAM: the rows
-// are read once (streaming loads).
-template <bool BF16, bool STREAM>
-__device__ __forceinline__ void gather_rows(const void* __restrict__ rows, int H, int nch, int c0,
-                                            int n, int dc, float wc,
-                                            float (&acc)[kCU][Row<BF16>::N]) {
-  using R = Row<BF16>;
-  const int lane = lane_id();
-  for (int j0 = 0; j0 < n; j0 += kSG) {
-    u32x4_t raw[kSG][kCU];
-    float wj[kSG];
-#pragma unroll
-    for (int s = 0; s < kSG; ++s) {
-      const int j = j0 + s;  // < 36: a valid lane index
-      const int dj = __shfl(dc, j, kWave);
-      wj[s] = (j < n) ? __shfl(wc, j, kWave) : 0.f;
-#pragma unroll
-      for (int u = 0; u < kCU; ++u) {
-        const int c = c0 + u * kWave + lane;
-        const size_t e = (size_t)dj * H + (size_t)c * R::N;
-        raw[s][u] = (j < n && c < nch) ? (STREAM ? R::ld_s(rows, e) : R::ld(rows, e)) : u32x4_t{};
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < kSG; ++s)
-#pragma unroll
-      for (int u = 0; u < kCU; ++u) {
-        float v[R::N];
-        R::to_f32(raw[s][u], v);
-#pragma unroll
-        for (int i = 0; i < R::N; ++i) acc[u][i] = fmaf(wj[s], v[i], acc[u][i]);
-      }
-  }
-}
 
 // y[t] = sum over local slots j (ascending) of w_j * y_perm[dest_j] (+ addend[t]).
 template <bool BF16>
@@ -344,6 +245,76 @@ __global__ __launch_bounds__(256) void route_bwd_dz_kernel(
   }
 }
 
+// Router backward with a dense addition to the logit gradient (the auxiliary
+// losses'): d_logits[t,e] = d_add[t,e] + the gate gradient of the kept experts.
+// Every expert then enters the input gradient:
+//   dx_router[t] = sum_e d_logits[t,e] * W_r[:,e]
+// which this kernel gathers in expert order when DX (shapes without the
+// matrix-core product; all E rows of the transposed weight per token).
+template <bool BF16, bool DX>
+__global__ __launch_bounds__(256) void route_bwd_dense_kernel(
+    const float* __restrict__ d_topk_w, const float* __restrict__ topk_w,
+    const int32_t* __restrict__ topk_idx, const float* d_add, const void* __restrict__ w_router_t,
+    int T, int H, int E, int k, float* d_logits, float* __restrict__ dx_router,
+    bf16_t* __restrict__ dz_hilo) {
+  using R = Row<BF16>;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  const int lane = lane_id();
+  float w = 0.f, dw = 0.f;
+  int id = -1;
+  if (lane < k) {
+    w = topk_w[(size_t)t * k + lane];
+    dw = d_topk_w[(size_t)t * k + lane];
+    id = topk_idx[(size_t)t * k + lane];
+  }
+  const float inner = wave_sum(w * dw);
+  const float dz = w * (dw - inner);
+  float v[kMaxE / kWave];
+#pragma unroll
+  for (int q = 0; q < kMaxE / kWave; ++q) {
+    const int e = q * kWave + lane;
+    v[q] = 0.f;
+    if (q * kWave >= E) continue;  // the same for the whole wave
+    for (int j = 0; j < k; ++j) {
+      const int ij = __builtin_amdgcn_readlane(id, j);
+      const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dz), j));
+      v[q] += (ij == e) ? dj : 0.f;
+    }
+    if (e >= E) continue;
+    v[q] += d_add[(size_t)t * E + e];
+    d_logits[(size_t)t * E + e] = v[q];
+    if (dz_hilo != nullptr) {
+      const bf16_t hi = f2bf(v[q]);
+      dz_hilo[(size_t)t * 2 * E + e] = hi;
+      dz_hilo[(size_t)t * 2 * E + E + e] = f2bf(v[q] - bf2f(hi));
+    }
+  }
+  if constexpr (!DX) return;
+  const int nch = H / R::N;
+  for (int c0 = 0; c0 < nch; c0 += kWave * kCU) {
+    float acc[kCU][R::N];
+#pragma unroll
+    for (int u = 0; u < kCU; ++u)
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) acc[u][i] = 0.f;
+#pragma unroll
+    for (int q = 0; q < kMaxE / kWave; ++q)
+      if (q * kWave < E)
+        gather_rows<BF16, false>(w_router_t, H, nch, c0, min(kWave, E - q * kWave),
+                                 q * kWave + lane, v[q], acc);
+#pragma unroll
+    for (int u = 0; u < kCU; ++u) {
+      const int c = c0 + u * kWave + lane;
+      if (c >= nch) continue;
+#pragma unroll
+      for (int q = 0; q < R::N / 4; ++q)
+        *reinterpret_cast<f32x4_t*>(dx_router + (size_t)t * H + (size_t)c * R::N + 4 * q) =
+            f32x4_t{acc[u][4 * q], acc[u][4 * q + 1], acc[u][4 * q + 2], acc[u][4 * q + 3]};
+    }
+  }
+}
+
 // fp32 path: dw_router[h, e] = sum_t x[t, h] * d_logits[t, e], t ascending.
 __global__ __launch_bounds__(256) void dw_router_f32_kernel(const float* __restrict__ x,
                                                             const float* __restrict__ dz, int T,
@@ -456,6 +427,26 @@ hipError_t launch_route_bwd_dz(const float* d_topk_w, const float* topk_w,
 #define MOE_DZ(B, D)                                                                             \
   route_bwd_dz_kernel<B, D><<<blocks, 256, 0, s>>>(d_topk_w, topk_w, topk_idx, w_router_t, T, H, E, \
                                                    k, d_logits, dx_router, dz_hilo)
+  if (bf16) {
+    if (dx_router != nullptr) MOE_DZ(true, true); else MOE_DZ(true, false);
+  } else {
+    if (dx_router != nullptr) MOE_DZ(false, true); else MOE_DZ(false, false);
+  }
+#undef MOE_DZ
+  return hipGetLastError();
+}
+
+hipError_t launch_route_bwd_dense(const float* d_topk_w, const float* topk_w,
+                                  const int32_t* topk_idx, const float* d_add,
+                                  const void* w_router_t, int T, int H, int E, int k, bool bf16,
+                                  float* d_logits, float* dx_router, bf16_t* dz_hilo,
+                                  hipStream_t s) {
+  const int blocks = (T + 3) / 4;
+  ProfScope ps(MOE_KERNEL_ROUTE_BWD_DZ, s);
+#define MOE_DZ(B, D)                                                                          \
+  route_bwd_dense_kernel<B, D><<<blocks, 256, 0, s>>>(d_topk_w, topk_w, topk_idx, d_add,      \
+                                                      w_router_t, T, H, E, k, d_logits,       \
+                                                      dx_router, dz_hilo)
   if (bf16) {
     if (dx_router != nullptr) MOE_DZ(true, true); else MOE_DZ(true, false);
   } else {

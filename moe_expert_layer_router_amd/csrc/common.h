@@ -179,10 +179,36 @@ hipError_t launch_route_bwd_dz(const float* d_topk_w, const float* topk_w,
                                const int32_t* topk_idx, const void* w_router_t, int T, int H, int E,
                                int k, bool bf16, float* d_logits, float* dx_router,
                                bf16_t* dz_hilo, hipStream_t s);
+hipError_t launch_route_bwd_dense(const float* d_topk_w, const float* topk_w,
+                                  const int32_t* topk_idx, const float* d_add,
+                                  const void* w_router_t, int T, int H, int E, int k, bool bf16,
+                                  float* d_logits, float* dx_router, bf16_t* dz_hilo,
+                                  hipStream_t s);
 hipError_t launch_dw_router_f32(const float* x, const float* d_logits, int T, int H, int E,
                                 float* dw_router, hipStream_t s);
 hipError_t launch_dw_router_reduce(const float* partials, int nsplit, int H, int E, bool folded,
                                    float* dw_router, hipStream_t s);
+
+// dropout.hip
+hipError_t launch_combine_dropout(const void* y_perm, const float* topk_w, const int32_t* dest_row,
+                                  const void* residual, double p, const uint64_t* rng, int T, int H,
+                                  int k, bool bf16, void* y, hipStream_t s);
+hipError_t launch_combine_dropout_bwd(const void* dy, const void* y_perm, const float* topk_w,
+                                      const int32_t* dest_row, double p, const uint64_t* rng, int T,
+                                      int H, int k, bool bf16, void* dy_perm, float* d_topk_w,
+                                      hipStream_t s);
+
+// balance.hip
+size_t balance_ws_bytes(int T, int E, int S);
+hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
+                               const int32_t* seq_offsets, const uint8_t* mask, int T, int E, int k,
+                               int S, float cb, float cz, int32_t* counts, float* prob_sum,
+                               int32_t* tokens, float* lse, float* loss, void* ws, hipStream_t s);
+hipError_t launch_balance_loss_bwd(const float* logits, const float* lse, const int32_t* counts,
+                                   const int32_t* tokens, const int32_t* seq_offsets,
+                                   const uint8_t* mask, const float* d_loss, int T, int E, int k,
+                                   int S, float cb, float cz, bool accumulate, float* d_logits,
+                                   hipStream_t s);
 
 // gemm.hip (bf16 MFMA grouped GEMMs)
 int gemm_tiles(int M, int N);  // output tiles of one M x N product
