@@ -528,6 +528,57 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
                             const int32_t* dest_row, double p, const uint64_t* rng, int T, int H,
                             int k, int dtype, void* dy_perm, float* d_topk_w, void* stream);
 
+/* Low-rank adapters of many requests beside a shared projection (an expert's
+ * weight, or any other): row r with adapter a = row_id[r] gets
+ *   v[r,:] = scale[a] * A[a] . x_r                (rank values, fp32)
+ *   y[r,:] = y[r,:] + B[a] . v[r,:]               (added in fp32, rounded once)
+ * with x_r = x[src_row[r]] if src_row is not NULL, else x[r].  Rows whose
+ * row_id is outside [0, n_ids) (-1: none), or whose src_row is outside
+ * [0, x_rows), have no adapter: y is not touched and v is 0.  Rows may be in
+ * any order; rows of one adapter next to each other share the reads of its
+ * weights.  In bf16, v enters the second product as two bf16 halves (16 bits).
+ * One request's weights and rows never reach another's result, whatever they
+ * hold.
+ *   x [x_rows,K] dtype at row pitch ldx, y [R,N] dtype at row pitch ldy (in
+ *   elements; columns past N untouched), A [n_ids,rank,K], B [n_ids,N,rank]
+ *   dtype, scale [n_ids] fp32 or NULL (1), row_id [R], src_row [R] int32,
+ *   v [R,rank] fp32 or NULL (kept for moe_adapter_bwd)
+ * K, N, ldx, ldy multiples of 8 (bf16) or 4 (fp32), at most 2^20; rank a
+ * multiple of 8, at most 128 (else MOE_EUNSUPPORTED); 1 <= n_ids <= 2^20; row
+ * data 16-byte aligned.  R = 0 enqueues nothing. */
+int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id, const void* A,
+                    const void* B, const float* scale, int R, int x_rows, int K, int N, int ldx,
+                    int ldy, int n_ids, int rank, int dtype, void* y, float* v, void* stream);
+
+/* Backward of moe_adapter_fwd for dy [R,N] (pitch ldy), with the forward's v:
+ *   w[r,:]  = scale[a] * B[a]^T . dy[r,:]
+ *   dx[r,:] = dx[r,:] + A[a]^T . w[r,:]    [R,K] dtype at row pitch lddx, or NULL: not
+ *             wanted; row r of dx belongs to row r (of dx_perm), not to x[src_row[r]]
+ *   dA[a]   = sum_r w[r,:] x_r^T  [n_ids,rank,K],  dB[a] = sum_r dy[r,:] v[r,:]^T
+ *             [n_ids,N,rank], fp32 (both or neither), overwritten or, with
+ *             accumulate != 0, added to; 0 for an adapter without rows.  The rows
+ *             of an adapter are summed in row order, in chunks whose sums are
+ *             added in order: the same bits every run.  The fp32 factors enter
+ *             the bf16 products whole (three bf16 parts).
+ *   ws      moe_adapter_ws_bytes(R, K, N, n_ids, rank, dtype) bytes (transposed
+ *           weights, w, the rows in adapter order, partial sums)
+ * Limits as moe_adapter_fwd, with n_ids <= 256 (else MOE_EUNSUPPORTED). */
+int64_t moe_adapter_ws_bytes(int R, int K, int N, int n_ids, int rank, int dtype);
+int moe_adapter_bwd(const void* dy, const void* x, const int32_t* src_row, const int32_t* row_id,
+                    const void* A, const void* B, const float* v, const float* scale, int R,
+                    int x_rows, int K, int N, int ldx, int ldy, int lddx, int n_ids, int rank,
+                    int dtype, void* dx, float* dA, float* dB, int accumulate, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* Adapter ids of grouped rows for adapters held per expert, A [n_adapters,E_l,
+ * rank,K] and B [n_adapters,E_l,N,rank]: row r < offsets[E_l] of local expert e
+ * gets token_adapter[src_row[r]] * E_l + e, or -1 when its token has no adapter
+ * (token_adapter outside [0, n_adapters)); rows r >= offsets[E_l] get -1.
+ *   offsets [E_l+1], src_row [R_cap] of moe_permute, token_adapter [T] int32,
+ *   row_id [R_cap] int32 (all written) */
+int moe_adapter_rows(const int32_t* offsets, const int32_t* src_row, const int32_t* token_adapter,
+                     int E_l, int T, int n_adapters, int R_cap, int32_t* row_id, void* stream);
+
 /* Kernel timing hook (benchmarks and profilers).  After this call the library
  * records start_events[i] and stop_events[i] (each a hipEvent_t created by
  * the caller) on the launch stream immediately before and after the i-th
@@ -559,7 +610,10 @@ typedef enum {
   MOE_KERNEL_BALANCE_BWD = 19,
   MOE_KERNEL_COMBINE_DROPOUT = 20,
   MOE_KERNEL_COMBINE_DROPOUT_BWD = 21,
-  MOE_KERNEL_COUNT = 22
+  MOE_KERNEL_ADAPTER = 22,           /* moe_adapter_fwd */
+  MOE_KERNEL_ADAPTER_DGRAD = 23,     /* moe_adapter_bwd: w and dx */
+  MOE_KERNEL_ADAPTER_WGRAD = 24,     /* moe_adapter_bwd: dA and dB, without the partials' sum */
+  MOE_KERNEL_COUNT = 25
 } moe_kernel;
 
 int moe_profile_kernel(int kernel_id, void** start_events, void** stop_events, int n);

@@ -15,7 +15,8 @@ moe_quantize_fp8_w; weight gradients:
 moe_quantize_fp8_group_t, moe_grouped_ffn_wgrad_fp8, and its two halves
 moe_grouped_ffn_wgrad_fp8_begin / _end; around the layer: the router's
 auxiliary losses moe_balance_loss / _bwd with moe_route_bwd_add, and the combine
-with dropout moe_combine_dropout / _bwd) and return
+with dropout moe_combine_dropout / _bwd, and low-rank adapters moe_adapter_fwd /
+_bwd with moe_adapter_rows) and return
 freshly allocated torch tensors; each also accepts preallocated outputs via
 ``out=`` dictionaries so that steady-state loops allocate nothing.
 """
@@ -88,6 +89,10 @@ def _load():
         "moe_balance_loss_bwd": ([P, P, P, P, P, P, P, I32, I32, I32, I32, F32, F32, I32, P, P], I32),
         "moe_combine_dropout": ([P, P, P, P, F64, P, I32, I32, I32, I32, P, P], I32),
         "moe_combine_dropout_bwd": ([P, P, P, P, F64, P, I32, I32, I32, I32, P, P, P], I32),
+        "moe_adapter_fwd": ([P] * 6 + [I32] * 9 + [P, P, P], I32),
+        "moe_adapter_ws_bytes": ([I32] * 6, I64),
+        "moe_adapter_bwd": ([P] * 8 + [I32] * 10 + [P, P, P, I32, P, SZ, P], I32),
+        "moe_adapter_rows": ([P, P, P, I32, I32, I32, I32, P, P], I32),
         "moe_profile_kernel": ([I32, ctypes.POINTER(P), ctypes.POINTER(P), I32], I32),
         "moe_profile_recorded": ([], I32),
     }
@@ -582,6 +587,101 @@ def moe_combine_dropout_bwd(dy: torch.Tensor, y_perm: torch.Tensor, topk_w: torc
                                        _into(o, "d_topk_w", (T, k), f32, dev), _stream()),
            "moe_combine_dropout_bwd")
     return o
+
+
+def _rows_arg(t: torch.Tensor, name: str, dtype, rows: int, cols: int, dev):
+    """(pointer, row pitch) of a matrix whose rows are dense, at any pitch."""
+    if t.dtype != dtype or t.shape != (rows, cols) or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} [{rows}, {cols}] on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} must have dense rows that do not overlap, got strides {t.stride()}")
+    return t.data_ptr(), ld
+
+
+def _adapter_args(x, row_id, A, B, scale, src_row):
+    dev = _device(row_id)
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [n_ids, rank, K] and B [n_ids, N, rank]")
+    n_ids, rank, K = A.shape
+    N, R = B.shape[1], row_id.numel()
+    dt = _row_type(A, "A")
+    x_rows = _shape2(x, "x")[0]
+    if src_row is None and x_rows != R:
+        raise ValueError(f"x has {x_rows} rows, row_id {R} (src_row maps one to the other)")
+    i32 = torch.int32
+    ptrs = (_arg(src_row, "src_row", i32, (R,), dev, optional=True), _arg(row_id, "row_id", i32, (R,), dev),
+            _arg(A, "A", dt, (n_ids, rank, K), dev), _arg(B, "B", dt, (n_ids, N, rank), dev))
+    sc = _arg(scale, "scale", torch.float32, (n_ids,), dev, optional=True)
+    xp, ldx = _rows_arg(x, "x", dt, x_rows, K, dev)
+    return dev, dt, n_ids, rank, K, N, R, x_rows, xp, ldx, ptrs, sc
+
+
+def moe_adapter_fwd(x: torch.Tensor, row_id: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                    y: torch.Tensor, scale: Optional[torch.Tensor] = None,
+                    src_row: Optional[torch.Tensor] = None, want_v: bool = False,
+                    out: Optional[torch.Tensor] = None):
+    """Low-rank adapters added to y [R,N] in place: row r gets
+    scale[a] * B[a] (A[a] x[src_row[r]]), a = row_id[r] (-1: none).  A [n_ids,rank,K],
+    B [n_ids,N,rank]; rows of x and y may lie at any pitch.  Returns v [R,rank] fp32 for
+    moe_adapter_bwd with want_v=True (written to out if given), else None."""
+    dev, dt, n_ids, rank, K, N, R, x_rows, xp, ldx, (src, ids, a, b), sc = \
+        _adapter_args(x, row_id, A, B, scale, src_row)
+    yp, ldy = _rows_arg(y, "y", dt, R, N, dev)
+    o = {"v": out}
+    v = _into(o, "v", (R, rank), torch.float32, dev) if want_v else None
+    _check(lib.moe_adapter_fwd(xp, src, ids, a, b, sc, R, x_rows, K, N, ldx, ldy, n_ids, rank,
+                               _dtype_code(A), yp, v, _stream()), "moe_adapter_fwd")
+    return o["v"] if want_v else None
+
+
+def moe_adapter_bwd(dy: torch.Tensor, x: torch.Tensor, row_id: torch.Tensor, A: torch.Tensor,
+                    B: torch.Tensor, v: Optional[torch.Tensor], dx: Optional[torch.Tensor],
+                    scale: Optional[torch.Tensor] = None, src_row: Optional[torch.Tensor] = None,
+                    want_dw: bool = True, accumulate: bool = False,
+                    ws: Optional[torch.Tensor] = None,
+                    out: Optional[Dict[str, torch.Tensor]] = None):
+    """Backward of moe_adapter_fwd for dy [R,N] and the forward's v: dx [R,K] (None: not wanted)
+    is added to in place.  Returns dict dA [n_ids,rank,K], dB [n_ids,N,rank] fp32 (None with
+    want_dw=False; added to with accumulate=True) and the workspace ws used."""
+    dev, dt, n_ids, rank, K, N, R, x_rows, xp, ldx, (src, ids, a, b), sc = \
+        _adapter_args(x, row_id, A, B, scale, src_row)
+    dyp, ldy = _rows_arg(dy, "dy", dt, R, N, dev)
+    dxp, lddx = _rows_arg(dx, "dx", dt, R, K, dev) if dx is not None else (None, K)
+    f32 = torch.float32
+    o = dict(out or {})
+    if accumulate and want_dw and (o.get("dA") is None or o.get("dB") is None):
+        raise ValueError("accumulate=True needs out with dA and dB")
+    dA = _into(o, "dA", (n_ids, rank, K), f32, dev) if want_dw else None
+    dB = _into(o, "dB", (n_ids, N, rank), f32, dev) if want_dw else None
+    if not want_dw:
+        o["dA"] = o["dB"] = None
+    vp = _arg(v, "v", f32, (R, rank), dev, optional=not want_dw)
+    nb = lib.moe_adapter_ws_bytes(R, K, N, n_ids, rank, _dtype_code(A))
+    if nb < 0:
+        _check(int(nb), "moe_adapter_ws_bytes")
+    o["ws"] = _ws(int(nb), dev, ws)
+    _check(lib.moe_adapter_bwd(dyp, xp, src, ids, a, b, vp, sc, R, x_rows, K, N, ldx, ldy, lddx,
+                               n_ids, rank, _dtype_code(A), dxp, dA, dB, 1 if accumulate else 0,
+                               _ptr(o["ws"]), _nbytes(o["ws"]), _stream()), "moe_adapter_bwd")
+    return o
+
+
+def moe_adapter_rows(offsets: torch.Tensor, src_row: torch.Tensor, token_adapter: torch.Tensor,
+                     n_adapters: int, out: Optional[torch.Tensor] = None):
+    """Adapter ids of moe_permute's grouped rows for adapters held per expert: row_id [R_cap] =
+    token_adapter[src_row[r]] * E_l + expert of r, or -1."""
+    dev = _device(offsets)
+    E_l, R_cap, T = offsets.numel() - 1, src_row.numel(), token_adapter.numel()
+    i32 = torch.int32
+    o = {"row_id": out}
+    _check(lib.moe_adapter_rows(_arg(offsets, "offsets", i32, (E_l + 1,), dev),
+                                _arg(src_row, "src_row", i32, (R_cap,), dev),
+                                _arg(token_adapter, "token_adapter", i32, (T,), dev), E_l, T,
+                                n_adapters, R_cap, _into(o, "row_id", (R_cap,), i32, dev), _stream()),
+           "moe_adapter_rows")
+    return o["row_id"]
 
 
 from .layer import MoELayer  # noqa: E402,F401

@@ -1026,4 +1026,113 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
                     fn);
 }
 
+namespace {
+constexpr int kAdapterMaxWidth = 1 << 20;
+
+int check_adapter(int R, int K, int N, int n_ids, int rank, int dtype, int most_ids, const char* fn) {
+  if (int rc = check_dtype(dtype, fn)) return rc;
+  if (R < 0) return fail(MOE_EINVAL, "%s: R must be >= 0 (got %d)", fn, R);
+  const int q = dtype == MOE_BF16 ? 8 : 4;
+  if (K <= 0 || N <= 0 || K % q != 0 || N % q != 0)
+    return fail(MOE_EINVAL, "%s: K=%d and N=%d must be positive multiples of %d for this dtype", fn, K, N, q);
+  if (n_ids < 1) return fail(MOE_EINVAL, "%s: n_ids must be positive (got %d)", fn, n_ids);
+  if (rank < 1) return fail(MOE_EINVAL, "%s: rank must be positive (got %d)", fn, rank);
+  if (rank % 8 != 0 || rank > 128)
+    return fail(MOE_EUNSUPPORTED, "%s: rank=%d must be a multiple of 8, at most 128", fn, rank);
+  if (K > kAdapterMaxWidth || N > kAdapterMaxWidth || n_ids > most_ids)
+    return fail(MOE_EUNSUPPORTED, "%s: needs K, N <= %d and n_ids <= %d (K=%d, N=%d, n_ids=%d)", fn,
+                kAdapterMaxWidth, most_ids, K, N, n_ids);
+  return MOE_OK;
+}
+
+int check_pitch(int ld, int width, int dtype, const char* name, const char* fn) {
+  const int q = dtype == MOE_BF16 ? 8 : 4;
+  if (ld < width || ld % q != 0)
+    return fail(MOE_EINVAL, "%s: %s=%d must be a multiple of %d and at least %d", fn, name, ld, q, width);
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id, const void* A,
+                    const void* B, const float* scale, int R, int x_rows, int K, int N, int ldx,
+                    int ldy, int n_ids, int rank, int dtype, void* y, float* v, void* stream) {
+  const char* fn = "moe_adapter_fwd";
+  if (int rc = check_adapter(R, K, N, n_ids, rank, dtype, 1 << 20, fn)) return rc;
+  if (x_rows < 0) return fail(MOE_EINVAL, "%s: x_rows must be >= 0 (got %d)", fn, x_rows);
+  if (int rc = check_pitch(ldx, K, dtype, "ldx", fn)) return rc;
+  if (int rc = check_pitch(ldy, N, dtype, "ldy", fn)) return rc;
+  if (R == 0) return MOE_OK;
+  if (int rc = check_ptr(x, "x", fn, true)) return rc;
+  if (int rc = check_ptr(row_id, "row_id", fn)) return rc;
+  if (int rc = check_ptr(A, "A", fn, true)) return rc;
+  if (int rc = check_ptr(B, "B", fn, true)) return rc;
+  if (int rc = check_ptr(y, "y", fn, true)) return rc;
+  if (v != nullptr && !aligned16(v)) return fail(MOE_EINVAL, "%s: v must be 16-byte aligned", fn);
+  const AdapterShape d = {dtype == MOE_BF16, R, x_rows, K, N, n_ids, rank, ldx, ldy};
+  return hip_status(launch_adapter_fwd(d, x, src_row, row_id, A, B, scale, y, v, begin_launch(stream)), fn);
+}
+
+int64_t moe_adapter_ws_bytes(int R, int K, int N, int n_ids, int rank, int dtype) {
+  const char* fn = "moe_adapter_ws_bytes";
+  if (int rc = check_adapter(R, K, N, n_ids, rank, dtype, kMaxE, fn)) return rc;
+  return (int64_t)adapter_bwd_ws_bytes(R, K, N, n_ids, rank, elem_bytes(dtype));
+}
+
+int moe_adapter_bwd(const void* dy, const void* x, const int32_t* src_row, const int32_t* row_id,
+                    const void* A, const void* B, const float* v, const float* scale, int R,
+                    int x_rows, int K, int N, int ldx, int ldy, int lddx, int n_ids, int rank,
+                    int dtype, void* dx, float* dA, float* dB, int accumulate, void* ws,
+                    size_t ws_bytes, void* stream) {
+  const char* fn = "moe_adapter_bwd";
+  if (int rc = check_adapter(R, K, N, n_ids, rank, dtype, kMaxE, fn)) return rc;
+  if (x_rows < 0) return fail(MOE_EINVAL, "%s: x_rows must be >= 0 (got %d)", fn, x_rows);
+  if (accumulate != 0 && accumulate != 1) return fail(MOE_EINVAL, "%s: accumulate must be 0 or 1", fn);
+  if (int rc = check_pitch(ldx, K, dtype, "ldx", fn)) return rc;
+  if (int rc = check_pitch(ldy, N, dtype, "ldy", fn)) return rc;
+  if (dx != nullptr) {
+    if (int rc = check_pitch(lddx, K, dtype, "lddx", fn)) return rc;
+    if (int rc = check_ptr(dx, "dx", fn, true)) return rc;
+  }
+  if ((dA == nullptr) != (dB == nullptr))
+    return fail(MOE_EINVAL, "%s: dA and dB must be given together", fn);
+  if (dA != nullptr) {
+    if (int rc = check_ptr(dA, "dA", fn, true)) return rc;
+    if (int rc = check_ptr(dB, "dB", fn, true)) return rc;
+  }
+  if (R > 0) {
+    if (int rc = check_ptr(dy, "dy", fn, true)) return rc;
+    if (int rc = check_ptr(row_id, "row_id", fn)) return rc;
+    if (int rc = check_ptr(A, "A", fn, true)) return rc;
+    if (int rc = check_ptr(B, "B", fn, true)) return rc;
+    if (dA != nullptr) {
+      if (int rc = check_ptr(x, "x", fn, true)) return rc;
+      if (int rc = check_ptr(v, "v", fn, true)) return rc;
+    }
+  }
+  if (int rc = check_ws(ws, ws_bytes, adapter_bwd_ws_bytes(R, K, N, n_ids, rank, elem_bytes(dtype)), fn))
+    return rc;
+  const AdapterShape d = {dtype == MOE_BF16, R, x_rows, K, N, n_ids, rank, ldx, ldy};
+  return hip_status(launch_adapter_bwd(d, dy, x, src_row, row_id, A, B, v, scale, dx, lddx, dA, dB,
+                                       accumulate != 0, ws, begin_launch(stream)),
+                    fn);
+}
+
+int moe_adapter_rows(const int32_t* offsets, const int32_t* src_row, const int32_t* token_adapter,
+                     int E_l, int T, int n_adapters, int R_cap, int32_t* row_id, void* stream) {
+  const char* fn = "moe_adapter_rows";
+  if (E_l < 1 || E_l > kMaxE) return fail(MOE_EINVAL, "%s: E_l=%d outside [1, %d]", fn, E_l, kMaxE);
+  if (T < 0 || R_cap < 0) return fail(MOE_EINVAL, "%s: T and R_cap must be >= 0", fn);
+  if (n_adapters < 0 || (long long)n_adapters * E_l > 0x7fffffffLL)
+    return fail(MOE_EINVAL, "%s: n_adapters=%d is negative, or n_adapters * E_l overflows int32", fn,
+                n_adapters);
+  if (R_cap == 0) return MOE_OK;
+  if (int rc = check_ptr(offsets, "offsets", fn)) return rc;
+  if (int rc = check_ptr(src_row, "src_row", fn)) return rc;
+  if (int rc = check_ptr(token_adapter, "token_adapter", fn)) return rc;
+  if (int rc = check_ptr(row_id, "row_id", fn)) return rc;
+  return hip_status(launch_adapter_rows(offsets, src_row, token_adapter, E_l, T, n_adapters, R_cap,
+                                        row_id, begin_launch(stream)),
+                    fn);
+}
+
 }  // extern "C"

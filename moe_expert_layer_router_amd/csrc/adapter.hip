@@ -1,0 +1,738 @@
+// Low-rank adapters of many requests beside a shared projection, for gfx950.
+//
+// Row r with adapter a = row_id[r] (rows without one are left alone):
+//   forward   v_r = s_a A_a x_r,  y_r += B_a v_r
+//   backward  w_r = s_a B_a^T dy_r,  dx_r += A_a^T w_r,
+//             dA_a = sum_r w_r x_r^T,  dB_a = sum_r dy_r v_r^T
+// The backward's data part is the forward on transposed weights (B_a^T in the
+// place of A_a, A_a^T in the place of B_a), so one kernel does both.
+//
+// A fragment of the matrix instruction is 16 bytes per lane in both types: row
+// (or column) lane % 16, 16-byte chunk lane / 16 of the summed axis.  bf16
+// takes 8 values and one 16x16x32 instruction, fp32 4 values and four 16x16x4
+// instructions (instruction i sums element i of every chunk).  Any order of
+// the summed axis is right as long as both operands share it.
+#include "common.h"
+
+namespace moe {
+
+namespace {
+
+inline size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+template <bool BF16>
+struct Elem {
+  static constexpr int EB = BF16 ? 2 : 4;
+  static constexpr int CE = BF16 ? 8 : 4;  // values of one 16-byte chunk
+  static constexpr int KE = 4 * CE;        // summed values of one fragment step
+};
+
+__device__ __forceinline__ u32x4_t load16(const char* p) {
+  return *reinterpret_cast<const u32x4_t*>(p);
+}
+
+// d += a b^T over one fragment step.
+template <bool BF16>
+__device__ __forceinline__ f32x4_t step(u32x4_t a, u32x4_t b, f32x4_t d) {
+  if constexpr (BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      d = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), d, 0,
+                                               0, 0);
+    return d;
+  }
+}
+
+struct AdapterArgs {
+  const char* x;            // [x_rows][ldx]
+  const int32_t* src_row;   // token row of row r, or null: r
+  int gather;               // x holds token rows: row r is x[src_row[r]]
+  const int32_t* row_id;    // [R]
+  const char* a;            // [n_ids][rank][K]
+  const char* b;            // [n_ids][N][rank]
+  const float* scale;       // [n_ids] or null: 1
+  char* y;                  // [R][ldy], added to (null: v alone)
+  float* v;                 // [R][rank] or null
+  long ldx, ldy;
+  int x_rows, R, K, N, n_ids, rank;
+  int rows, splits;         // rows of a workgroup, column ranges per row tile
+};
+
+constexpr int kAdWaves = 4;
+
+// A workgroup takes `rows` <= 16 MT rows and one of `splits` column ranges of
+// y.  First A_a x for its rows, the summed axis cut over the waves and added
+// through LDS in wave order; then the waves go over the columns 64 at a time.
+// Every distinct adapter among the rows is a pass over the rows that have it:
+// lanes of other rows compute on a row of this adapter and are not used, so
+// nothing of one request's adapter or activations reaches another's row.
+template <bool BF16, int RT, int MT>
+__global__ __launch_bounds__(kAdWaves* kWave) void adapter_kernel(AdapterArgs p) {
+  using E = Elem<BF16>;
+  constexpr int RL = 16 * RT + 4;  // LDS row pitch of the rank values
+  extern __shared__ __align__(16) float red[];  // [waves][16 MT rows][RL]
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane & 15, g = lane >> 4;
+  const int bid = xcd_remap(blockIdx.x, gridDim.x);
+  const int tile = bid / p.splits, split = bid % p.splits;
+  const int row0 = tile * p.rows;
+
+  // lane i: adapter and x row of the workgroup's row i
+  int id = -1, xr = 0;
+  if (lane < p.rows && row0 + lane < p.R) {
+    id = p.row_id[row0 + lane];
+    xr = p.src_row != nullptr ? p.src_row[row0 + lane] : row0 + lane;
+    if (id < 0 || id >= p.n_ids || xr < 0 || xr >= p.x_rows) id = -1;
+    if (!p.gather) xr = row0 + lane;
+  }
+  const uint64_t live = __ballot(id >= 0);
+  if (live == 0 && (p.v == nullptr || split != 0)) return;
+  int idm[MT], xrm[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    idm[m] = __shfl(id, 16 * m + l, kWave);
+    xrm[m] = __shfl(xr, 16 * m + l, kWave);
+  }
+
+  f32x4_t tot[MT][RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) tot[m][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // the wave's part of the summed axis, whole fragment steps; the last wave
+  // that has any also takes the rest behind the last whole step
+  const int steps = p.K / E::KE;
+  const int k0 = wave * steps / kAdWaves * E::KE, k1 = (wave + 1) * steps / kAdWaves * E::KE;
+  const bool tail = wave == kAdWaves - 1 && steps * E::KE < p.K;
+  for (uint64_t todo = live; todo != 0;) {
+    const int first = __builtin_ctzll(todo);
+    const int cur = __builtin_amdgcn_readlane(id, first);
+    const int xfirst = __builtin_amdgcn_readlane(xr, first);
+    const uint64_t same = __ballot(id == cur);
+    todo &= ~same;
+    const char* xp[MT];
+    const char* ap[RT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = idm[m] == cur ? xrm[m] : xfirst;
+      xp[m] = p.x + ((size_t)row * p.ldx + g * E::CE) * E::EB;
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int j = min(16 * r + l, p.rank - 1);  // rank values past the last are not used
+      ap[r] = p.a + (((size_t)cur * p.rank + j) * p.K + g * E::CE) * E::EB;
+    }
+    f32x4_t acc[MT][RT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[m][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = k0; k < k1; k += E::KE) {
+      u32x4_t xf[MT], af[RT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xf[m] = load16(xp[m] + (size_t)k * E::EB);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) af[r] = load16(ap[r] + (size_t)k * E::EB);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[m][r] = step<BF16>(af[r], xf[m], acc[m][r]);
+    }
+    if (tail) {
+      const int k = steps * E::KE;
+      const bool in = k + g * E::CE < p.K;  // chunks behind the end: zeros on both sides
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const u32x4_t xf = in ? load16(xp[m] + (size_t)k * E::EB) : u32x4_t{};
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          acc[m][r] = step<BF16>(in ? load16(ap[r] + (size_t)k * E::EB) : u32x4_t{}, xf, acc[m][r]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tot[m][r][i] = idm[m] == cur ? acc[m][r][i] : tot[m][r][i];
+  }
+  // tot[m][r][i] = this wave's part of value 16 r + 4 g + i of row 16 m + l
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      *reinterpret_cast<f32x4_t*>(red + (wave * 16 * MT + 16 * m + l) * RL + 16 * r + 4 * g) =
+          tot[m][r];
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.rows * 4 * RT; i += kAdWaves * kWave) {
+    const int row = i / (4 * RT), j = 4 * (i % (4 * RT));
+    f32x4_t s = *reinterpret_cast<f32x4_t*>(red + row * RL + j);
+#pragma unroll
+    for (int w = 1; w < kAdWaves; ++w)
+      s += *reinterpret_cast<f32x4_t*>(red + (w * 16 * MT + row) * RL + j);
+    if (row0 + row < p.R) {
+      const int a = p.row_id[row0 + row];
+      const bool on = (live >> row & 1) != 0;
+      s *= on ? (p.scale != nullptr ? p.scale[a] : 1.f) : 0.f;
+      if (!on) s = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (p.v != nullptr && split == 0 && j < p.rank)
+        *reinterpret_cast<f32x4_t*>(p.v + (size_t)(row0 + row) * p.rank + j) = s;
+    }
+    *reinterpret_cast<f32x4_t*>(red + row * RL + j) = s;
+  }
+  if (p.y == nullptr) return;
+  __syncthreads();
+
+  // The rank values as fragments: chunk c = 4 s + g.  bf16 holds each fp32
+  // value as two bf16 halves (16 significant bits: the values' rounding stays
+  // 2^-9 below that of y), chunks 0 .. rank/8 - 1 the upper halves and the
+  // next rank/8 the lower ones, both against the same weights; RT steps hold
+  // the 2 rank/8 chunks.
+  const int rc = p.rank / E::CE;
+  u32x4_t vf[MT][RT];
+  int bc[RT];  // the weights' chunk, or -1: no chunk
+#pragma unroll
+  for (int s = 0; s < RT; ++s) {
+    const int c = 4 * s + g;
+    const bool low = BF16 && c >= rc;
+    const int at = low ? c - rc : c;
+    bc[s] = at < rc ? at : -1;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float* vr = red + (16 * m + l) * RL + max(bc[s], 0) * E::CE;
+      u32x4_t f{};
+      if constexpr (BF16) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = vr[i];
+          if (low) {
+            const float lo = e[i] - bf2f(f2bf(e[i]));
+            e[i] = __builtin_isfinite(lo) ? lo : 0.f;  // an infinity is in the upper half alone
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = pack_bf2(e[2 * i], e[2 * i + 1]);
+      } else {
+        f = *reinterpret_cast<const u32x4_t*>(vr);
+      }
+      vf[m][s] = bc[s] >= 0 && idm[m] >= 0 ? f : u32x4_t{};
+    }
+  }
+  const int per = ((p.N + 63) / 64 + p.splits - 1) / p.splits * 64;
+  const int n1 = min(p.N, (split + 1) * per);
+  // tile q of a 64-column block: weight row l is column 16 (l / 4) + 4 q + l % 4,
+  // so a lane's four tiles are 16 columns in a row of y, 16 g .. 16 g + 15
+  for (int nb = split * per + 64 * wave; nb < n1; nb += 64 * kAdWaves) {
+    for (uint64_t todo = live; todo != 0;) {
+      const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+      todo &= ~__ballot(id == cur);
+      f32x4_t acc[4][MT];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = min(nb + 16 * (l >> 2) + 4 * q + (l & 3), p.N - 1);
+        const char* bp = p.b + ((size_t)cur * p.N + n) * p.rank * E::EB;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[q][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < RT; ++s) {
+          const u32x4_t w = bc[s] >= 0 ? load16(bp + bc[s] * 16) : u32x4_t{};
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[q][m] = step<BF16>(w, vf[m][s], acc[q][m]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (idm[m] != cur) continue;
+        char* yp = p.y + ((size_t)(row0 + 16 * m + l) * p.ldy + nb + 16 * g) * E::EB;
+#pragma unroll
+        for (int c = 0; c < 16 / E::CE; ++c) {
+          if (nb + 16 * g + c * E::CE >= n1) continue;
+          u32x4_t v = load16(yp + 16 * c);
+          if constexpr (BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const f32x4_t& d = acc[2 * c + i / 2][m];
+              const int o = 2 * (i % 2);
+              v[i] = pack_bf2(__uint_as_float(v[i] << 16) + d[o],
+                              __uint_as_float(v[i] & 0xffff0000u) + d[o + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + acc[c][m][i]);
+          }
+          *reinterpret_cast<u32x4_t*>(yp + 16 * c) = v;
+        }
+      }
+    }
+  }
+}
+
+template <bool BF16, int RT, int MT>
+hipError_t launch_one(const AdapterArgs& p, hipStream_t s) {
+  const size_t lds = (size_t)kAdWaves * 16 * MT * (16 * RT + 4) * 4;
+  const int tiles = (p.R + p.rows - 1) / p.rows;
+  adapter_kernel<BF16, RT, MT><<<tiles * p.splits, kAdWaves * kWave, lds, s>>>(p);
+  return hipGetLastError();
+}
+
+// Rows of a workgroup and column ranges: 64 rows (32 above rank 64, whose
+// partial sums fill the LDS) share one read of the weights when that still
+// gives two workgroups per CU; fewer rows when it does not, down to one row
+// (a decode batch, each row with its own adapter), and then the columns are
+// cut as well, each range repeating the small first product.
+template <bool BF16>
+hipError_t launch_adapter(AdapterArgs p, hipStream_t s) {
+  const int most = p.rank > 64 ? 32 : 64;
+  int rows = 1;
+  while (rows < most && (p.R + 2 * rows - 1) / (2 * rows) >= 2 * kCUs) rows *= 2;
+  p.rows = rows;
+  const int tiles = (p.R + rows - 1) / rows;
+  p.splits = p.y == nullptr ? 1 : max(1, min((p.N + 255) / 256, 4 * kCUs / tiles));
+  const int rt = (p.rank + 15) / 16;
+#define MOE_AD(RT)                                             \
+  do {                                                         \
+    if (rows <= 16) return launch_one<BF16, RT, 1>(p, s);      \
+    if (rows <= 32) return launch_one<BF16, RT, 2>(p, s);      \
+    if constexpr (RT <= 4) return launch_one<BF16, RT, 4>(p, s); \
+  } while (0)
+  if (rt <= 1) MOE_AD(1);
+  else if (rt <= 2) MOE_AD(2);
+  else if (rt <= 4) MOE_AD(4);
+  else MOE_AD(8);
+#undef MOE_AD
+  return hipErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------------------
+// weight gradients
+// ---------------------------------------------------------------------------
+
+// Row chunks of the weight gradients: the rows of one adapter (in row order)
+// are cut into chunks of `chunk`; an adapter of one chunk (or no row) writes
+// its gradient whole, one of more writes fp32 partials that a second pass adds
+// in chunk order.  plan[0] = number of chunks; then {id, begin, end, slot}.
+struct ChunkPlan {
+  int32_t* count;   // chunks in all
+  int32_t* chunks;  // [upper][4]
+  int32_t* first;   // [n_ids] first slot of an id of several chunks
+};
+
+__global__ __launch_bounds__(kMaxE) void adapter_plan_kernel(const int32_t* __restrict__ offsets,
+                                                             int n_ids, int chunk, ChunkPlan plan) {
+  __shared__ int s_n[kMaxE], s_m[kMaxE];
+  const int i = threadIdx.x;
+  const int a = i < n_ids ? offsets[i] : 0, b = i < n_ids ? offsets[i + 1] : 0;
+  const int n = i < n_ids ? max(1, (b - a + chunk - 1) / chunk) : 0;
+  const int m = n > 1 ? n : 0;
+  s_n[i] = n;
+  s_m[i] = m;
+  __syncthreads();
+  for (int o = 1; o < kMaxE; o <<= 1) {
+    const int x = i >= o ? s_n[i - o] : 0, y = i >= o ? s_m[i - o] : 0;
+    __syncthreads();
+    s_n[i] += x;
+    s_m[i] += y;
+    __syncthreads();
+  }
+  if (i == kMaxE - 1) *plan.count = s_n[i];
+  if (i >= n_ids) return;
+  const int at = s_n[i] - n, slot = s_m[i] - m;
+  plan.first[i] = slot;
+  for (int c = 0; c < n; ++c) {
+    int32_t* e = plan.chunks + 4 * (size_t)(at + c);
+    e[0] = i;
+    e[1] = a + c * chunk;
+    e[2] = min(b, a + (c + 1) * chunk);
+    e[3] = n > 1 ? slot + c : -1;
+  }
+}
+
+struct WgradArgs {
+  const float* p[2];         // [R][rank]: w (for dA), v (for dB)
+  const char* q[2];          // x rows (through src_row), dy rows
+  const int32_t* src_row;    // of q[0]
+  const int32_t* order;      // rows in adapter order
+  float* out[2];             // dA [n_ids][rank][K], dB [n_ids][N][rank]
+  float* part;               // [slots][rank (K + N)]
+  ChunkPlan plan;
+  long ldq[2];
+  int C[2];                  // K, N
+  int nb0;                   // 256-column blocks of the first product
+  int x_rows, rank, accumulate;
+};
+
+constexpr int kWgMaxChunk = 1024;
+
+// One fp32 value as three bf16 parts whose sum is the value (24 bits).
+__device__ __forceinline__ void split3(const float* v, u32x4_t* f) {
+  float h[8], m[8], o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = bf2f(f2bf(v[i]));
+    const float r = v[i] - h[i];
+    m[i] = bf2f(f2bf(r));
+    o[i] = r - m[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[0][i] = pack_bf2(h[2 * i], h[2 * i + 1]);
+    f[1][i] = pack_bf2(m[2 * i], m[2 * i + 1]);
+    f[2][i] = pack_bf2(o[2 * i], o[2 * i + 1]);
+  }
+}
+
+// G = sum over a chunk's rows of p_r q_r^T: the rows are the summed axis.  A
+// wave holds 64 columns, lane l the columns 4 l .. 4 l + 3 of the rows of its
+// 16-lane group g; loaded row by row (128 contiguous bytes of a bf16 row per
+// group), the eight rows of a lane are put together per column by 16-bit
+// permutes, without LDS.  bf16 takes the fp32 factor as three bf16 parts, so
+// the products are exact and the sums fp32 like those of the fp32 path.
+template <bool BF16, int RT>
+__global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
+  constexpr int SR = BF16 ? 32 : 16;  // rows of one step
+  constexpr int LR = SR / 4;          // rows of a lane
+  __shared__ int s_row[kWgMaxChunk], s_q[kWgMaxChunk];
+  if ((int)blockIdx.x >= *a.plan.count) return;
+  const int32_t* e = a.plan.chunks + 4 * (size_t)blockIdx.x;
+  const int id = e[0], begin = e[1], end = e[2], slot = e[3];
+  const int z = (int)blockIdx.y >= a.nb0 ? 1 : 0;
+  const int C = a.C[z];
+  const int lane = lane_id(), wave = threadIdx.x >> 6, l = lane & 15, g = lane >> 4;
+  const int c0 = 256 * ((int)blockIdx.y - z * a.nb0) + 64 * wave + 4 * l;
+  const int n = end - begin;
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int r = a.order[begin + i];
+    int q = a.src_row != nullptr ? a.src_row[r] : r;
+    if (q < 0 || q >= a.x_rows) q = -1;  // a row that the forward left alone too
+    else if (z == 1) q = r;
+    s_row[i] = r;
+    s_q[i] = q;
+  }
+  __syncthreads();
+  const float* P = a.p[z];
+  const char* Q = a.q[z];
+  const long ldq = a.ldq[z];
+  const bool in = c0 < C;
+  f32x4_t acc[RT][4];  // tile q: columns 4 l' + q
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[r][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < n; i0 += SR) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    u32x2_t raw[LR];
+    u32x4_t rawf[LR];
+    float pv[RT][LR];
+#pragma unroll
+    for (int i = 0; i < LR; ++i) {
+      const int at = i0 + LR * g + i;
+      const int row = at < n ? s_row[at] : -1, qr = at < n ? s_q[at] : -1;
+      if constexpr (BF16)
+        raw[i] = in && qr >= 0 ? *reinterpret_cast<const u32x2_t*>(Q + ((size_t)qr * ldq + c0) * 2) : u32x2_t{};
+      else
+        rawf[i] = in && qr >= 0 ? load16(Q + ((size_t)qr * ldq + c0) * 4) : u32x4_t{};
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int j = 16 * r + l;
+        pv[r][i] = qr >= 0 && j < a.rank ? P[(size_t)row * a.rank + j] : 0.f;
+      }
+    }
+    if constexpr (BF16) {
+      u32x4_t col[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = raw[2 * i][h], y = raw[2 * i + 1][h];
+          col[2 * h][i] = (x & 0xffffu) | (y << 16);
+          col[2 * h + 1][i] = (x >> 16) | (y & 0xffff0000u);
+        }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        u32x4_t f[3];
+        split3(pv[r], f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int s = 0; s < 3; ++s) acc[r][q] = step<true>(f[s], col[q], acc[r][q]);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < LR; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            acc[r][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(pv[r][i], __uint_as_float(rawf[i][q]),
+                                                             acc[r][q], 0, 0, 0);
+    }
+  }
+  if (!in) return;
+  // acc[r][q][i]: rank value 16 r + 4 g + i, column c0 + q
+  float* out;
+  const bool add = slot < 0 && a.accumulate;
+  if (slot >= 0)
+    out = a.part + (size_t)slot * a.rank * (a.C[0] + a.C[1]) + (z ? (size_t)a.rank * a.C[0] : 0);
+  else
+    out = a.out[z] + (size_t)id * a.rank * C;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int j = 16 * r + 4 * g;
+    if (j >= a.rank) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f32x4_t v;
+      float* o;
+      if (z == 0) {  // [rank][K]: four columns of one rank value
+        v = f32x4_t{acc[r][0][i], acc[r][1][i], acc[r][2][i], acc[r][3][i]};
+        o = out + (size_t)(j + i) * C + c0;
+      } else {  // [N][rank]: four rank values of one column
+        v = acc[r][i];
+        o = out + (size_t)(c0 + i) * a.rank + j;
+      }
+      if (add) v += *reinterpret_cast<const f32x4_t*>(o);
+      *reinterpret_cast<f32x4_t*>(o) = v;
+    }
+  }
+}
+
+// Gradients of the adapters of several chunks: their partials in chunk order.
+__global__ __launch_bounds__(256) void adapter_wgrad_sum_kernel(
+    const int32_t* __restrict__ offsets, int chunk, ChunkPlan plan, const f32x4_t* __restrict__ part,
+    int rank, int K, int N, int accumulate, f32x4_t* __restrict__ dA, f32x4_t* __restrict__ dB) {
+  const int id = blockIdx.y;
+  const int n = (offsets[id + 1] - offsets[id] + chunk - 1) / chunk;
+  if (n <= 1) return;
+  const int ka = rank * K / 4, all = rank * (K + N) / 4;  // 16-byte groups
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= all) return;
+  f32x4_t* o = i < ka ? dA + (size_t)id * ka + i : dB + (size_t)id * (all - ka) + (i - ka);
+  f32x4_t v = accumulate ? *o : f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const f32x4_t* q = part + (size_t)plan.first[id] * all + i;
+  for (int c = 0; c < n; ++c) v += q[(size_t)c * all];
+  *o = v;
+}
+
+// Both transposed weights: A [ids][rank][K] -> [ids][K][rank] and
+// B [ids][N][rank] -> [ids][rank][N], 32x32 tiles through LDS.
+template <typename U>
+__global__ __launch_bounds__(256) void adapter_transpose_kernel(const U* __restrict__ A,
+                                                                const U* __restrict__ B, int rank,
+                                                                int K, int N, U* __restrict__ At,
+                                                                U* __restrict__ Bt) {
+  __shared__ U tile[32][33];
+  const int ktiles = (K + 31) / 32;
+  const bool second = (int)blockIdx.x >= ktiles;
+  const int rows = second ? N : rank, cols = second ? rank : K;
+  const int c0 = 32 * (second ? (int)blockIdx.y : (int)blockIdx.x);
+  const int r0 = 32 * (second ? (int)blockIdx.x - ktiles : (int)blockIdx.y);
+  const size_t base = (size_t)blockIdx.z * rows * cols;
+  const U* src = (second ? B : A) + base;
+  U* dst = (second ? Bt : At) + base;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  for (int i = ty; i < 32; i += 8)
+    if (r0 + i < rows && c0 + tx < cols) tile[i][tx] = src[(size_t)(r0 + i) * cols + c0 + tx];
+  __syncthreads();
+  for (int i = ty; i < 32; i += 8)
+    if (c0 + i < cols && r0 + tx < rows) dst[(size_t)(c0 + i) * rows + r0 + tx] = tile[tx][i];
+}
+
+// Adapter of grouped row r: that of its token, of its expert.
+__global__ __launch_bounds__(256) void adapter_rows_kernel(const int32_t* __restrict__ offsets,
+                                                           const int32_t* __restrict__ src_row,
+                                                           const int32_t* __restrict__ token_adapter,
+                                                           int E_l, int T, int n_adapters, int R_cap,
+                                                           int32_t* __restrict__ row_id) {
+  const int r = blockIdx.x * 256 + threadIdx.x;
+  if (r >= R_cap) return;
+  int id = -1;
+  if (r < offsets[E_l]) {
+    const int t = src_row[r];
+    const int a = t >= 0 && t < T ? token_adapter[t] : -1;
+    if (a >= 0 && a < n_adapters) {
+      int lo = 0, hi = E_l - 1;  // the last expert whose rows begin at or before r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (offsets[mid] <= r) lo = mid; else hi = mid - 1;
+      }
+      id = a * E_l + lo;
+    }
+  }
+  row_id[r] = id;
+}
+
+// Rows of a chunk: about 2048 workgroups of the weight gradients, in powers of
+// two between 128 rows (a workgroup's fixed cost) and what its LDS lists.
+int wgrad_chunk(int R, int K, int N) {
+  const int blocks = (K + 255) / 256 + (N + 255) / 256;
+  int c = 128;
+  while (c < kWgMaxChunk && (long)R * blocks > 2048L * c) c *= 2;
+  return c;
+}
+
+struct BwdLayout {
+  size_t at, bt, w, sort, counts, offsets, dest, order, count, chunks, first, part, total;
+  int chunk, upper;
+};
+
+BwdLayout bwd_layout(int R, int K, int N, int n_ids, int rank, int eb) {
+  BwdLayout l;
+  size_t at = 0;
+  auto take = [&](size_t bytes) { const size_t was = at; at += up256(bytes); return was; };
+  l.chunk = wgrad_chunk(R, K, N);
+  l.upper = R / l.chunk + n_ids;
+  l.at = take((size_t)n_ids * rank * K * eb);
+  l.bt = take((size_t)n_ids * rank * N * eb);
+  l.w = take((size_t)R * rank * 4);
+  l.sort = take(permute_ws_bytes(R, 1, n_ids));
+  l.counts = take((size_t)n_ids * 4);
+  l.offsets = take((size_t)(n_ids + 1) * 4);
+  l.dest = take((size_t)R * 4);
+  l.order = take((size_t)R * 4);
+  l.count = take(4);
+  l.chunks = take((size_t)l.upper * 16);
+  l.first = take((size_t)n_ids * 4);
+  l.part = take((size_t)(2 * (R / l.chunk)) * rank * (K + N) * 4);
+  l.total = at;
+  return l;
+}
+
+}  // namespace
+
+size_t adapter_bwd_ws_bytes(int R, int K, int N, int n_ids, int rank, int elem_bytes) {
+  return bwd_layout(R, K, N, n_ids, rank, elem_bytes).total;
+}
+
+hipError_t launch_adapter_rows(const int32_t* offsets, const int32_t* src_row,
+                               const int32_t* token_adapter, int E_l, int T, int n_adapters,
+                               int R_cap, int32_t* row_id, hipStream_t s) {
+  adapter_rows_kernel<<<(R_cap + 255) / 256, 256, 0, s>>>(offsets, src_row, token_adapter, E_l, T,
+                                                          n_adapters, R_cap, row_id);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_fwd(const AdapterShape& d, const void* x, const int32_t* src_row,
+                              const int32_t* row_id, const void* A, const void* B,
+                              const float* scale, void* y, float* v, hipStream_t s) {
+  AdapterArgs p{};
+  p.x = (const char*)x;
+  p.src_row = src_row;
+  p.gather = src_row != nullptr;
+  p.row_id = row_id;
+  p.a = (const char*)A;
+  p.b = (const char*)B;
+  p.scale = scale;
+  p.y = (char*)y;
+  p.v = v;
+  p.ldx = d.ldx;
+  p.ldy = d.ldy;
+  p.x_rows = d.x_rows;
+  p.R = d.R;
+  p.K = d.K;
+  p.N = d.N;
+  p.n_ids = d.n_ids;
+  p.rank = d.rank;
+  ProfScope ps(MOE_KERNEL_ADAPTER, s);
+  return d.bf16 ? launch_adapter<true>(p, s) : launch_adapter<false>(p, s);
+}
+
+hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void* x,
+                              const int32_t* src_row, const int32_t* row_id, const void* A,
+                              const void* B, const float* v, const float* scale, void* dx,
+                              long lddx, float* dA, float* dB, bool accumulate, void* ws,
+                              hipStream_t s) {
+  const int eb = d.bf16 ? 2 : 4;
+  const BwdLayout l = bwd_layout(d.R, d.K, d.N, d.n_ids, d.rank, eb);
+  char* w = (char*)ws;
+  hipError_t e = hipSuccess;
+  if (d.R > 0) {
+    const dim3 grid((d.K + 31) / 32 + (d.N + 31) / 32, (d.rank + 31) / 32, d.n_ids);
+    if (d.bf16)
+      adapter_transpose_kernel<uint16_t><<<grid, 256, 0, s>>>(
+          (const uint16_t*)A, (const uint16_t*)B, d.rank, d.K, d.N, (uint16_t*)(w + l.at),
+          (uint16_t*)(w + l.bt));
+    else
+      adapter_transpose_kernel<uint32_t><<<grid, 256, 0, s>>>(
+          (const uint32_t*)A, (const uint32_t*)B, d.rank, d.K, d.N, (uint32_t*)(w + l.at),
+          (uint32_t*)(w + l.bt));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    // the data part: the forward from dy's rows to dx's on the transposed weights
+    AdapterArgs p{};
+    p.x = (const char*)dy;
+    p.src_row = src_row;  // not followed: names the rows that have none
+    p.row_id = row_id;
+    p.a = w + l.bt;
+    p.b = w + l.at;
+    p.scale = scale;
+    p.y = (char*)dx;
+    p.v = (float*)(w + l.w);
+    p.ldx = d.ldy;
+    p.ldy = lddx;
+    p.x_rows = d.x_rows;
+    p.R = d.R;
+    p.K = d.N;
+    p.N = d.K;
+    p.n_ids = d.n_ids;
+    p.rank = d.rank;
+    ProfScope ps(MOE_KERNEL_ADAPTER_DGRAD, s);
+    e = d.bf16 ? launch_adapter<true>(p, s) : launch_adapter<false>(p, s);
+    if (e != hipSuccess) return e;
+  }
+  if (dA == nullptr) return e;
+  // rows in adapter order (a stable sort by adapter: the permutation of
+  // routed rows with one slot per row), then the chunks of each adapter
+  int32_t* offsets = (int32_t*)(w + l.offsets);
+  e = launch_permute(nullptr, row_id, d.R, d.K, 1, 0, d.n_ids, eb, (int32_t*)(w + l.counts), offsets,
+                     (int32_t*)(w + l.dest), (int32_t*)(w + l.order), nullptr, w + l.sort, s);
+  if (e != hipSuccess) return e;
+  const ChunkPlan plan = {(int32_t*)(w + l.count), (int32_t*)(w + l.chunks), (int32_t*)(w + l.first)};
+  adapter_plan_kernel<<<1, kMaxE, 0, s>>>(offsets, d.n_ids, l.chunk, plan);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  WgradArgs a{};
+  a.p[0] = (const float*)(w + l.w);
+  a.p[1] = v;
+  a.q[0] = (const char*)x;
+  a.q[1] = (const char*)dy;
+  a.src_row = src_row;
+  a.order = (const int32_t*)(w + l.order);
+  a.out[0] = dA;
+  a.out[1] = dB;
+  a.part = (float*)(w + l.part);
+  a.plan = plan;
+  a.ldq[0] = d.ldx;
+  a.ldq[1] = d.ldy;
+  a.C[0] = d.K;
+  a.C[1] = d.N;
+  a.nb0 = (d.K + 255) / 256;
+  a.x_rows = d.x_rows;
+  a.rank = d.rank;
+  a.accumulate = accumulate ? 1 : 0;
+  const dim3 grid(l.upper, a.nb0 + (d.N + 255) / 256);
+  const int rt = (d.rank + 15) / 16;
+  {
+    ProfScope ps(MOE_KERNEL_ADAPTER_WGRAD, s);
+#define MOE_WG(RT)                                                       \
+  do {                                                                   \
+    if (d.bf16) adapter_wgrad_kernel<true, RT><<<grid, 256, 0, s>>>(a);  \
+    else adapter_wgrad_kernel<false, RT><<<grid, 256, 0, s>>>(a);        \
+  } while (0)
+    if (rt <= 1) MOE_WG(1);
+    else if (rt <= 2) MOE_WG(2);
+    else if (rt <= 4) MOE_WG(4);
+    else MOE_WG(8);
+#undef MOE_WG
+  }
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (d.R <= l.chunk) return e;  // no adapter has more than one chunk
+  adapter_wgrad_sum_kernel<<<dim3((d.rank * (d.K + d.N) / 4 + 255) / 256, d.n_ids), 256, 0, s>>>(
+      offsets, l.chunk, plan, (const f32x4_t*)(w + l.part), d.rank, d.K, d.N, accumulate ? 1 : 0,
+      (f32x4_t*)dA, (f32x4_t*)dB);
+  return hipGetLastError();
+}
+
+}  // namespace moe

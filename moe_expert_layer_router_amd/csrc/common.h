@@ -210,6 +210,25 @@ hipError_t launch_balance_loss_bwd(const float* logits, const float* lse, const 
                                    int S, float cb, float cz, bool accumulate, float* d_logits,
                                    hipStream_t s);
 
+// adapter.hip (low-rank adapters)
+struct AdapterShape {
+  bool bf16;
+  int R, x_rows, K, N, n_ids, rank;  // rows, rows of x, widths of x and y
+  long ldx, ldy;                     // row pitches of x and of y (dy), in elements
+};
+hipError_t launch_adapter_rows(const int32_t* offsets, const int32_t* src_row,
+                               const int32_t* token_adapter, int E_l, int T, int n_adapters,
+                               int R_cap, int32_t* row_id, hipStream_t s);
+hipError_t launch_adapter_fwd(const AdapterShape& d, const void* x, const int32_t* src_row,
+                              const int32_t* row_id, const void* A, const void* B,
+                              const float* scale, void* y, float* v, hipStream_t s);
+size_t adapter_bwd_ws_bytes(int R, int K, int N, int n_ids, int rank, int elem_bytes);
+hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void* x,
+                              const int32_t* src_row, const int32_t* row_id, const void* A,
+                              const void* B, const float* v, const float* scale, void* dx,
+                              long lddx, float* dA, float* dB, bool accumulate, void* ws,
+                              hipStream_t s);
+
 // gemm.hip (bf16 MFMA grouped GEMMs)
 int gemm_tiles(int M, int N);  // output tiles of one M x N product
 // Whether the router weight gradient's split products add their hi and lo
