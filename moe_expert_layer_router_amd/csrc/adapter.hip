@@ -61,18 +61,24 @@ struct AdapterArgs {
   int rows, splits;         // rows of a workgroup, column ranges per row tile
 };
 
-constexpr int kAdWaves = 4;
-
-// A workgroup takes `rows` <= 16 MT rows and one of `splits` column ranges of
-// y.  First A_a x for its rows, the summed axis cut over the waves and added
-// through LDS in wave order; then the waves go over the columns 64 at a time.
-// Every distinct adapter among the rows is a pass over the rows that have it:
-// lanes of other rows compute on a row of this adapter and are not used, so
-// nothing of one request's adapter or activations reaches another's row.
-template <bool BF16, int RT, int MT>
-__global__ __launch_bounds__(kAdWaves* kWave) void adapter_kernel(AdapterArgs p) {
+// A workgroup of NW waves takes `rows` <= 16 MT rows and one of `splits`
+// column ranges of y.  First A_a x for its rows, the summed axis cut over the
+// waves and added through LDS in wave order; then the waves go over the
+// columns 64 at a time.  Every distinct adapter among the rows is a pass over
+// the rows that have it: lanes of other rows compute on a row of this adapter
+// and are not used, so nothing of one request's adapter or activations reaches
+// another's row.
+//
+// Bound by the reads of x, the read and write of y and, for few rows per
+// adapter, the weights.  The operands of a wave's first columns (y and the
+// first adapter's B) are loaded before the first product and those of its next
+// columns before the current ones are computed, so that a decode batch waits
+// for memory about once and not once per stage.
+template <bool BF16, int RT, int MT, int NW>
+__global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
   using E = Elem<BF16>;
   constexpr int RL = 16 * RT + 4;  // LDS row pitch of the rank values
+  constexpr int NY = 16 / E::CE;   // 16-byte chunks of a lane's 16 columns
   extern __shared__ __align__(16) float red[];  // [waves][16 MT rows][RL]
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 15, g = lane >> 4;
@@ -89,7 +95,12 @@ __global__ __launch_bounds__(kAdWaves* kWave) void adapter_kernel(AdapterArgs p)
     if (!p.gather) xr = row0 + lane;
   }
   const uint64_t live = __ballot(id >= 0);
-  if (live == 0 && (p.v == nullptr || split != 0)) return;
+  if (live == 0) {
+    if (p.v != nullptr && split == 0)
+      for (int i = threadIdx.x; i < min(p.rows, p.R - row0) * p.rank; i += NW * kWave)
+        p.v[(size_t)row0 * p.rank + i] = 0.f;
+    return;
+  }
   int idm[MT], xrm[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -97,22 +108,71 @@ __global__ __launch_bounds__(kAdWaves* kWave) void adapter_kernel(AdapterArgs p)
     xrm[m] = __shfl(xr, 16 * m + l, kWave);
   }
 
+  // ---- operands of the second product: 64 columns of y and of an adapter's B.
+  // A lane's chunk c of y is columns 4 CE c + CE g (a row's four lanes together
+  // 64 bytes); tile q, rows 4 g .. 4 g + 3 of the product, are 4 of them.
+  constexpr int KF = BF16 ? (RT + 1) / 2 : RT;  // fragment steps of a row of B
+  const int rc = p.rank / E::CE;                // its chunks: 4 s + g in step s
+  struct Ops {
+    u32x4_t y[MT][NY];
+    u32x4_t w[4][KF];
+  };
+  const int per = ((p.N + 63) / 64 + p.splits - 1) / p.splits * 64;
+  const int n1 = p.y != nullptr ? min(p.N, (split + 1) * per) : 0;
+  // Loads take no branch (lanes without a row, column or chunk read one that
+  // exists and its value is not used), so that they all go out together.
+  const char* yrow[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = idm[m] >= 0 ? 16 * m + l : __builtin_ctzll(live);
+    yrow[m] = p.y + (size_t)(row0 + row) * p.ldy * E::EB;
+  }
+  auto load_y = [&](Ops& o, int nb) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < NY; ++c)
+        o.y[m][c] = load16(yrow[m] + (size_t)min(nb + 4 * E::CE * c + E::CE * g, n1 - E::CE) * E::EB);
+  };
+  auto load_w = [&](Ops& o, int nb, int cur) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = BF16 ? nb + 32 * (q >> 1) + 8 * (l >> 2) + 4 * (q & 1) + (l & 3) : nb + 16 * q + l;
+      const char* bp = p.b + ((size_t)cur * p.N + min(n, p.N - 1)) * p.rank * E::EB;
+#pragma unroll
+      for (int s = 0; s < KF; ++s) o.w[q][s] = load16(bp + min(4 * s + g, rc - 1) * 16);
+    }
+  };
+  constexpr bool kEarly = (MT == 1 || RT >= 4) && MT * NY + 4 * KF <= 16;  // 64 registers a set
+  const int cur0 = __builtin_amdgcn_readlane(id, __builtin_ctzll(live));
+  int nb = split * per + 64 * wave;
+  Ops o;
+  if (kEarly && nb < n1) {
+    load_y(o, nb);
+    load_w(o, nb, cur0);
+  }
+
+  // ---- first product
   f32x4_t tot[MT][RT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int r = 0; r < RT; ++r) tot[m][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // the wave's part of the summed axis, whole fragment steps; the last wave
-  // that has any also takes the rest behind the last whole step
-  const int steps = p.K / E::KE;
-  const int k0 = wave * steps / kAdWaves * E::KE, k1 = (wave + 1) * steps / kAdWaves * E::KE;
-  const bool tail = wave == kAdWaves - 1 && steps * E::KE < p.K;
+  // The wave's part of the summed axis, in groups of G fragment steps: the
+  // next group's loads go out before the current one is multiplied.  The last
+  // wave also takes what is behind the last whole group.
+  constexpr int G = MT + RT <= 3 ? 4 : MT + RT <= 6 ? 2 : 1;
+  constexpr int GE = G * E::KE;
+  const int groups = p.K / GE;
+  const int k0 = wave * groups / NW * GE, k1 = (wave + 1) * groups / NW * GE;
+  struct Frags {
+    u32x4_t x[G][MT], a[G][RT];
+  };
   for (uint64_t todo = live; todo != 0;) {
     const int first = __builtin_ctzll(todo);
     const int cur = __builtin_amdgcn_readlane(id, first);
     const int xfirst = __builtin_amdgcn_readlane(xr, first);
-    const uint64_t same = __ballot(id == cur);
-    todo &= ~same;
+    todo &= ~__ballot(id == cur);
     const char* xp[MT];
     const char* ap[RT];
 #pragma unroll
@@ -130,29 +190,59 @@ __global__ __launch_bounds__(kAdWaves* kWave) void adapter_kernel(AdapterArgs p)
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[m][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = k0; k < k1; k += E::KE) {
-      u32x4_t xf[MT], af[RT];
+    auto load_f = [&](Frags& f, int k) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xf[m] = load16(xp[m] + (size_t)k * E::EB);
+      for (int u = 0; u < G; ++u) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) af[r] = load16(ap[r] + (size_t)k * E::EB);
+        for (int m = 0; m < MT; ++m) f.x[u][m] = load16(xp[m] + (size_t)(k + u * E::KE) * E::EB);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int r = 0; r < RT; ++r) f.a[u][r] = load16(ap[r] + (size_t)(k + u * E::KE) * E::EB);
+      }
+    };
+    auto multiply = [&](const Frags& f) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[m][r] = step<BF16>(af[r], xf[m], acc[m][r]);
-    }
-    if (tail) {
-      const int k = steps * E::KE;
-      const bool in = k + g * E::CE < p.K;  // chunks behind the end: zeros on both sides
+      for (int u = 0; u < G; ++u)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const u32x4_t xf = in ? load16(xp[m] + (size_t)k * E::EB) : u32x4_t{};
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-          acc[m][r] = step<BF16>(in ? load16(ap[r] + (size_t)k * E::EB) : u32x4_t{}, xf, acc[m][r]);
+          for (int r = 0; r < RT; ++r) acc[m][r] = step<BF16>(f.a[u][r], f.x[u][m], acc[m][r]);
+    };
+    if (k0 < k1) {
+      // two sets in turn (a copy from one to the other would wait for its loads)
+      Frags f0, f1;
+      load_f(f0, k0);
+      for (int k = k0 + GE;; k += 2 * GE) {
+        if (k >= k1) {
+          multiply(f0);
+          break;
+        }
+        load_f(f1, k);
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay in front of the products
+        multiply(f0);
+        if (k + GE >= k1) {
+          multiply(f1);
+          break;
+        }
+        load_f(f0, k + GE);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(f1);
       }
     }
+    if (wave == NW - 1)
+      for (int k = groups * GE; k < p.K; k += E::KE) {
+        const bool in = k + g * E::CE < p.K;  // chunks behind the end: zeros on both sides
+        const long at = (long)(in ? k : p.K - E::CE - g * E::CE) * E::EB;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          u32x4_t xf = load16(xp[m] + at);
+          xf = in ? xf : u32x4_t{};
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            u32x4_t af = load16(ap[r] + at);
+            acc[m][r] = step<BF16>(in ? af : u32x4_t{}, xf, acc[m][r]);
+          }
+        }
+      }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -163,142 +253,179 @@ __global__ __launch_bounds__(kAdWaves* kWave) void adapter_kernel(AdapterArgs p)
   // tot[m][r][i] = this wave's part of value 16 r + 4 g + i of row 16 m + l
 #pragma unroll
   for (int m = 0; m < MT; ++m)
+    if (16 * m + l < p.rows)
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-      *reinterpret_cast<f32x4_t*>(red + (wave * 16 * MT + 16 * m + l) * RL + 16 * r + 4 * g) =
-          tot[m][r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.rows * 4 * RT; i += kAdWaves * kWave) {
-    const int row = i / (4 * RT), j = 4 * (i % (4 * RT));
+      for (int r = 0; r < RT; ++r)
+        *reinterpret_cast<f32x4_t*>(red + (wave * 16 * MT + 16 * m + l) * RL + 16 * r + 4 * g) =
+            tot[m][r];
+  lds_barrier();
+  for (int i0 = wave * kWave; i0 < p.rows * 4 * RT; i0 += NW * kWave) {
+    const int i = i0 + lane;
+    const int row = min(i / (4 * RT), p.rows - 1), j = 4 * (i % (4 * RT));
+    const int a = __shfl(id, row, kWave);
+    if (i >= p.rows * 4 * RT) continue;
     f32x4_t s = *reinterpret_cast<f32x4_t*>(red + row * RL + j);
 #pragma unroll
-    for (int w = 1; w < kAdWaves; ++w)
+    for (int w = 1; w < NW; ++w)
       s += *reinterpret_cast<f32x4_t*>(red + (w * 16 * MT + row) * RL + j);
-    if (row0 + row < p.R) {
-      const int a = p.row_id[row0 + row];
-      const bool on = (live >> row & 1) != 0;
-      s *= on ? (p.scale != nullptr ? p.scale[a] : 1.f) : 0.f;
-      if (!on) s = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      if (p.v != nullptr && split == 0 && j < p.rank)
-        *reinterpret_cast<f32x4_t*>(p.v + (size_t)(row0 + row) * p.rank + j) = s;
-    }
+    s = a < 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : s * (p.scale != nullptr ? p.scale[a] : 1.f);
+    if (p.v != nullptr && split == 0 && row0 + row < p.R && j < p.rank)
+      *reinterpret_cast<f32x4_t*>(p.v + (size_t)(row0 + row) * p.rank + j) = s;
     *reinterpret_cast<f32x4_t*>(red + row * RL + j) = s;
   }
   if (p.y == nullptr) return;
-  __syncthreads();
+  lds_barrier();
 
-  // The rank values as fragments: chunk c = 4 s + g.  bf16 holds each fp32
-  // value as two bf16 halves (16 significant bits: the values' rounding stays
-  // 2^-9 below that of y), chunks 0 .. rank/8 - 1 the upper halves and the
-  // next rank/8 the lower ones, both against the same weights; RT steps hold
-  // the 2 rank/8 chunks.
-  const int rc = p.rank / E::CE;
-  u32x4_t vf[MT][RT];
-  int bc[RT];  // the weights' chunk, or -1: no chunk
+  // The rank values as fragments.  bf16 holds each fp32 value as two bf16
+  // halves (16 significant bits: their rounding stays 2^-9 below that of y),
+  // two instructions on the same weights.
+  constexpr int NH = BF16 ? 2 : 1;
+  u32x4_t vf[NH][MT][KF];
 #pragma unroll
-  for (int s = 0; s < RT; ++s) {
-    const int c = 4 * s + g;
-    const bool low = BF16 && c >= rc;
-    const int at = low ? c - rc : c;
-    bc[s] = at < rc ? at : -1;
+  for (int s = 0; s < KF; ++s)
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const float* vr = red + (16 * m + l) * RL + max(bc[s], 0) * E::CE;
-      u32x4_t f{};
-      if constexpr (BF16) {
-        float e[8];
+      const bool on = 4 * s + g < rc && idm[m] >= 0;
+      const float* vr = red + min(16 * m + l, p.rows - 1) * RL + min(4 * s + g, rc - 1) * E::CE;
+      float v[E::CE];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          e[i] = vr[i];
-          if (low) {
-            const float lo = e[i] - bf2f(f2bf(e[i]));
-            e[i] = __builtin_isfinite(lo) ? lo : 0.f;  // an infinity is in the upper half alone
-          }
+      for (int i = 0; i < E::CE; i += 4) *reinterpret_cast<f32x4_t*>(v + i) = *reinterpret_cast<const f32x4_t*>(vr + i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+          const float h0 = bf2f(f2bf(v[2 * i])), h1 = bf2f(f2bf(v[2 * i + 1]));
+          float l0 = v[2 * i] - h0, l1 = v[2 * i + 1] - h1;
+          l0 = __builtin_isfinite(l0) ? l0 : 0.f;  // an infinity is in the upper half alone
+          l1 = __builtin_isfinite(l1) ? l1 : 0.f;
+          vf[0][m][s][i] = on ? pack_bf2(h0, h1) : 0u;
+          vf[NH - 1][m][s][i] = on ? pack_bf2(l0, l1) : 0u;
+        } else {
+          vf[0][m][s][i] = on ? __float_as_uint(v[i]) : 0u;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = pack_bf2(e[2 * i], e[2 * i + 1]);
-      } else {
-        f = *reinterpret_cast<const u32x4_t*>(vr);
       }
-      vf[m][s] = bc[s] >= 0 && idm[m] >= 0 ? f : u32x4_t{};
     }
-  }
-  const int per = ((p.N + 63) / 64 + p.splits - 1) / p.splits * 64;
-  const int n1 = min(p.N, (split + 1) * per);
-  // tile q of a 64-column block: weight row l is column 16 (l / 4) + 4 q + l % 4,
-  // so a lane's four tiles are 16 columns in a row of y, 16 g .. 16 g + 15
-  for (int nb = split * per + 64 * wave; nb < n1; nb += 64 * kAdWaves) {
+
+  // ---- second product
+  auto columns = [&](Ops& o, int nb) {
+    f32x4_t d[4][MT];
+    bool loaded = kEarly;
     for (uint64_t todo = live; todo != 0;) {
       const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
       todo &= ~__ballot(id == cur);
-      f32x4_t acc[4][MT];
+      if (!loaded) load_w(o, nb, cur);
+      loaded = false;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int n = min(nb + 16 * (l >> 2) + 4 * q + (l & 3), p.N - 1);
-        const char* bp = p.b + ((size_t)cur * p.N + n) * p.rank * E::EB;
+        u32x4_t w[KF];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[q][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < KF; ++s) w[s] = 4 * s + g < rc ? o.w[q][s] : u32x4_t{};
 #pragma unroll
-        for (int s = 0; s < RT; ++s) {
-          const u32x4_t w = bc[s] >= 0 ? load16(bp + bc[s] * 16) : u32x4_t{};
+        for (int m = 0; m < MT; ++m) {
+          f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int m = 0; m < MT; ++m) acc[q][m] = step<BF16>(w, vf[m][s], acc[q][m]);
+          for (int s = 0; s < KF; ++s)
+#pragma unroll
+            for (int h = 0; h < NH; ++h) acc = step<BF16>(w[s], vf[h][m][s], acc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[q][m][i] = idm[m] == cur ? acc[i] : d[q][m][i];
         }
       }
+    }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if (idm[m] != cur) continue;
-        char* yp = p.y + ((size_t)(row0 + 16 * m + l) * p.ldy + nb + 16 * g) * E::EB;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int c = 0; c < 16 / E::CE; ++c) {
-          if (nb + 16 * g + c * E::CE >= n1) continue;
-          u32x4_t v = load16(yp + 16 * c);
-          if constexpr (BF16) {
+      for (int c = 0; c < NY; ++c) {
+        const int n = nb + 4 * E::CE * c + E::CE * g;
+        if (idm[m] < 0 || n >= n1) continue;
+        u32x4_t v = o.y[m][c];
+        if constexpr (BF16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const f32x4_t& d = acc[2 * c + i / 2][m];
-              const int o = 2 * (i % 2);
-              v[i] = pack_bf2(__uint_as_float(v[i] << 16) + d[o],
-                              __uint_as_float(v[i] & 0xffff0000u) + d[o + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + acc[c][m][i]);
+          for (int i = 0; i < 4; ++i) {
+            const f32x4_t& t = d[2 * c + i / 2][m];
+            const int k = 2 * (i % 2);
+            v[i] = pack_bf2(__uint_as_float(v[i] << 16) + t[k],
+                            __uint_as_float(v[i] & 0xffff0000u) + t[k + 1]);
           }
-          *reinterpret_cast<u32x4_t*>(yp + 16 * c) = v;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + d[c][m][i]);
         }
+        *reinterpret_cast<u32x4_t*>(p.y + ((size_t)(row0 + 16 * m + l) * p.ldy + n) * E::EB) = v;
       }
+  };
+  if constexpr (kEarly) {
+    constexpr int ST = 64 * NW;
+    Ops o1;
+    for (; nb < n1; nb += 2 * ST) {
+      if (nb + ST < n1) {
+        load_y(o1, nb + ST);
+        load_w(o1, nb + ST, cur0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      columns(o, nb);
+      if (nb + ST >= n1) break;
+      if (nb + 2 * ST < n1) {
+        load_y(o, nb + 2 * ST);
+        load_w(o, nb + 2 * ST, cur0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      columns(o1, nb + ST);
+    }
+  } else {
+    for (; nb < n1; nb += 64 * NW) {
+      load_y(o, nb);
+      columns(o, nb);
     }
   }
 }
 
-template <bool BF16, int RT, int MT>
+template <bool BF16, int RT, int MT, int NW>
 hipError_t launch_one(const AdapterArgs& p, hipStream_t s) {
-  const size_t lds = (size_t)kAdWaves * 16 * MT * (16 * RT + 4) * 4;
+  const size_t lds = (size_t)NW * 16 * MT * (16 * RT + 4) * 4;
   const int tiles = (p.R + p.rows - 1) / p.rows;
-  adapter_kernel<BF16, RT, MT><<<tiles * p.splits, kAdWaves * kWave, lds, s>>>(p);
+  adapter_kernel<BF16, RT, MT, NW><<<tiles * p.splits, NW * kWave, lds, s>>>(p);
   return hipGetLastError();
 }
 
-// Rows of a workgroup and column ranges: 64 rows (32 above rank 64, whose
-// partial sums fill the LDS) share one read of the weights when that still
-// gives two workgroups per CU; fewer rows when it does not, down to one row
-// (a decode batch, each row with its own adapter), and then the columns are
-// cut as well, each range repeating the small first product.
+// Rows of a workgroup and column ranges.  More rows share one read of an
+// adapter's weights, more column ranges repeat the first product, and fewer
+// than one workgroup per CU leaves CUs idle: the choice is the one whose
+// busiest CU moves the fewest elements, with the adapters among `rows` rows
+// taken as twice those of rows sorted by adapter (1 .. rows).
 template <bool BF16>
 hipError_t launch_adapter(AdapterArgs p, hipStream_t s) {
   const int most = p.rank > 64 ? 32 : 64;
-  int rows = 1;
-  while (rows < most && (p.R + 2 * rows - 1) / (2 * rows) >= 2 * kCUs) rows *= 2;
-  p.rows = rows;
-  const int tiles = (p.R + rows - 1) / rows;
-  p.splits = p.y == nullptr ? 1 : max(1, min((p.N + 255) / 256, 4 * kCUs / tiles));
+  double best = 0.0;
+  for (int rows = 1; rows <= most; rows *= 2)
+    for (int splits = 1; splits <= (p.y == nullptr ? 1 : 8); splits *= 2) {
+      if (splits > 1 && 256 * splits > p.N) break;
+      const long tiles = ((long)p.R + rows - 1) / rows;
+      const double ids = min((double)rows, max(1.0, 2.0 * rows * p.n_ids / p.R)) * p.rank;
+      const double each = (rows + ids) * p.K + (ids + 2.0 * rows) * p.N / splits;
+      const double cost = (double)((tiles * splits + kCUs - 1) / kCUs) * each;
+      if (best > 0.0 && cost >= best) continue;
+      best = cost;
+      p.rows = rows;
+      p.splits = splits;
+    }
   const int rt = (p.rank + 15) / 16;
-#define MOE_AD(RT)                                             \
-  do {                                                         \
-    if (rows <= 16) return launch_one<BF16, RT, 1>(p, s);      \
-    if (rows <= 32) return launch_one<BF16, RT, 2>(p, s);      \
-    if constexpr (RT <= 4) return launch_one<BF16, RT, 4>(p, s); \
+  // eight waves where their partial sums fit 64 KB of LDS
+  const int mt = (p.rows + 15) / 16;
+  int nw = 8 * 16 * mt * (16 * (rt > 4 ? 8 : rt > 2 ? 4 : rt) + 4) * 4 <= 65536 ? 8 : 4;
+#define MOE_AD(RT)                                                             \
+  do {                                                                         \
+    if (p.rows <= 16) {                                                        \
+      if (nw == 8) return launch_one<BF16, RT, 1, 8>(p, s);                     \
+      return launch_one<BF16, RT, 1, 4>(p, s);                                  \
+    }                                                                          \
+    if (p.rows <= 32) {                                                        \
+      if (nw == 8) return launch_one<BF16, RT, 2, 8>(p, s);                     \
+      return launch_one<BF16, RT, 2, 4>(p, s);                                  \
+    }                                                                          \
+    if constexpr (RT <= 4) {                                                   \
+      if (nw == 8) return launch_one<BF16, RT, 4, 8>(p, s);                     \
+      return launch_one<BF16, RT, 4, 4>(p, s);                                  \
+    }                                                                          \
   } while (0)
   if (rt <= 1) MOE_AD(1);
   else if (rt <= 2) MOE_AD(2);
