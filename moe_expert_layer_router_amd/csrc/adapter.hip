@@ -61,6 +61,34 @@ struct AdapterArgs {
   int rows, splits;         // rows of a workgroup, column ranges per row tile
 };
 
+// 64 lanes x 16 bytes from per-lane global addresses to LDS at lds + 16 * lane.
+// Inline asm, as in the grouped GEMMs: the compiler keeps no count of these
+// loads; the explicit vmcnt waits below order every access.
+__device__ __forceinline__ void dma16g(const char* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// LDS of one wave of adapter_kernel, in bytes: two stages of the first
+// product's operands, whose place the partial sums, the second product's
+// results and a set of B's columns take afterwards.  For small ranks another
+// set of B's columns behind them, loaded before the first product and then in
+// turn with the other (TWO).
+template <bool BF16, int RT, int MT>
+struct AdapterLds {
+  static constexpr int ST = 2048 * (MT + RT);               // a stage: 128 bytes of every row
+  static constexpr int RL = 16 * RT + 4;                    // pitch of the rank values (floats)
+  static constexpr int RED = 16 * MT * RL * 4;              // partial sums
+  static constexpr int DL = 68;                             // pitch of the results (floats)
+  static constexpr int DELTA = 16 * DL * 4;                 // 16 rows x 64 columns
+  static constexpr int JB = (BF16 ? 2 : 4) * RT;            // KB of 64 columns of B at most
+  static constexpr bool TWO = JB <= 4;
+  static constexpr int B1 = RED + DELTA;
+  static constexpr int FIRST = 2 * ST > B1 + 1024 * JB ? 2 * ST : B1 + 1024 * JB;
+  static constexpr int B0 = TWO ? FIRST : B1;
+  static constexpr int WAVE = FIRST + (TWO ? 1024 * JB : 0);
+};
+
 // A workgroup of NW waves takes `rows` <= 16 MT rows and one of `splits`
 // column ranges of y.  First A_a x for its rows, the summed axis cut over the
 // waves and added through LDS in wave order; then the waves go over the
@@ -70,16 +98,20 @@ struct AdapterArgs {
 // another's row.
 //
 // Bound by the reads of x, the read and write of y and, for few rows per
-// adapter, the weights.  The operands of a wave's first columns (y and the
-// first adapter's B) are loaded before the first product and those of its next
-// columns before the current ones are computed, so that a decode batch waits
-// for memory about once and not once per stage.
+// adapter, the weights.  A fragment wants 16 rows in neighbouring lanes, and
+// loaded like that every lane quad touches four cache lines, which the L1's
+// tag lookups serve at a quarter of their rate (8191 rows, rank 64: 40 us).  So
+// everything is loaded with a row's 128 bytes in eight neighbouring lanes: x,
+// A and B straight into the wave's own LDS (16-byte chunk c of row r at place
+// c ^ (r % 8): fragment reads hit all banks), y into registers, where the
+// second product's results meet it through LDS.  No barrier: only the wave
+// that loaded reads.
 template <bool BF16, int RT, int MT, int NW>
 __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
   using E = Elem<BF16>;
-  constexpr int RL = 16 * RT + 4;  // LDS row pitch of the rank values
-  constexpr int NY = 16 / E::CE;   // 16-byte chunks of a lane's 16 columns
-  extern __shared__ __align__(16) float red[];  // [waves][16 MT rows][RL]
+  using S = AdapterLds<BF16, RT, MT>;
+  constexpr int RL = S::RL;
+  extern __shared__ __align__(16) char lds[];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 15, g = lane >> 4;
   const int bid = xcd_remap(blockIdx.x, gridDim.x);
@@ -101,55 +133,60 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
         p.v[(size_t)row0 * p.rank + i] = 0.f;
     return;
   }
-  int idm[MT], xrm[MT];
+  int idm[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    idm[m] = __shfl(id, 16 * m + l, kWave);
-    xrm[m] = __shfl(xr, 16 * m + l, kWave);
-  }
+  for (int m = 0; m < MT; ++m) idm[m] = __shfl(id, 16 * m + l, kWave);
+  char* my = lds + wave * S::WAVE;
+  const uint32_t my_lds = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t*)my);
 
-  // ---- operands of the second product: 64 columns of y and of an adapter's B.
-  // A lane's chunk c of y is columns 4 CE c + CE g (a row's four lanes together
-  // 64 bytes); tile q, rows 4 g .. 4 g + 3 of the product, are 4 of them.
-  constexpr int KF = BF16 ? (RT + 1) / 2 : RT;  // fragment steps of a row of B
-  const int rc = p.rank / E::CE;                // its chunks: 4 s + g in step s
-  struct Ops {
-    u32x4_t y[MT][NY];
-    u32x4_t w[4][KF];
-  };
+  // ---- operands of the second product: 64 columns of y and of an adapter's B
+  constexpr int YR = 64 / (64 / E::CE);  // rows of y in one load: 64 columns are 64 / CE lanes
+  constexpr int YL = 64 / E::CE;
+  constexpr int NYI = 16 * MT / YR;      // loads of y
   const int per = ((p.N + 63) / 64 + p.splits - 1) / p.splits * 64;
   const int n1 = p.y != nullptr ? min(p.N, (split + 1) * per) : 0;
-  // Loads take no branch (lanes without a row, column or chunk read one that
-  // exists and its value is not used), so that they all go out together.
-  const char* yrow[MT];
+  char* yrow[NYI];
+  bool yon[NYI];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = idm[m] >= 0 ? 16 * m + l : __builtin_ctzll(live);
-    yrow[m] = p.y + (size_t)(row0 + row) * p.ldy * E::EB;
+  for (int j = 0; j < NYI; ++j) {
+    const int r = YR * j + lane / YL;
+    yon[j] = __shfl(id, r, kWave) >= 0;
+    // a row without an adapter reads one that has, and is not written
+    yrow[j] = p.y + (size_t)(row0 + (yon[j] ? r : __builtin_ctzll(live))) * p.ldy * E::EB;
   }
-  auto load_y = [&](Ops& o, int nb) {
+  const int yc = lane % YL * E::CE;  // this lane's first column of the 64
+  auto load_y = [&](u32x4_t (&y)[NYI], int nb) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int c = 0; c < NY; ++c)
-        o.y[m][c] = load16(yrow[m] + (size_t)min(nb + 4 * E::CE * c + E::CE * g, n1 - E::CE) * E::EB);
+    for (int j = 0; j < NYI; ++j)
+      y[j] = load16(yrow[j] + (size_t)min(nb + yc, n1 - E::CE) * E::EB);
   };
-  auto load_w = [&](Ops& o, int nb, int cur) {
+  // B's 64 rows of rank values lie one after another: chunk p of the block is
+  // chunk p % rc of row p / rc, at LDS place p with the chunk swizzled by the
+  // row so that 16 rows' chunks spread over the banks
+  const int rc = p.rank / E::CE;
+  const int jb = p.rank / (BF16 ? 8 : 4);  // KB of the block
+  const int sw = min(rc & -rc, 8);
+  const int sh = __builtin_ctz(8 / sw);
+  auto swz = [&](int n, int c) { return c ^ ((n >> sh) & (sw - 1)); };
+  int boff[S::JB];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = BF16 ? nb + 32 * (q >> 1) + 8 * (l >> 2) + 4 * (q & 1) + (l & 3) : nb + 16 * q + l;
-      const char* bp = p.b + ((size_t)cur * p.N + min(n, p.N - 1)) * p.rank * E::EB;
+  for (int j = 0; j < S::JB; ++j) {
+    const int q = 64 * j + lane, n = q / rc;
+    boff[j] = (n * rc + swz(n, q - n * rc)) * 16;
+  }
+  auto load_b = [&](int at, int nb, int cur) {
+    const char* base = p.b + (size_t)cur * p.N * p.rank * E::EB;
+    const long first = (long)nb * p.rank * E::EB, last = (long)p.N * p.rank * E::EB - 16;
 #pragma unroll
-      for (int s = 0; s < KF; ++s) o.w[q][s] = load16(bp + min(4 * s + g, rc - 1) * 16);
-    }
+    for (int j = 0; j < S::JB; ++j)
+      if (j < jb) dma16g(base + min(first + boff[j], last), my_lds + at + 1024 * j);
   };
-  constexpr bool kEarly = (MT == 1 || RT >= 4) && MT * NY + 4 * KF <= 16;  // 64 registers a set
   const int cur0 = __builtin_amdgcn_readlane(id, __builtin_ctzll(live));
   int nb = split * per + 64 * wave;
-  Ops o;
-  if (kEarly && nb < n1) {
-    load_y(o, nb);
-    load_w(o, nb, cur0);
+  u32x4_t y[NYI];
+  if (nb < n1) {
+    if (S::TWO) load_b(S::B0, nb, cur0);
+    load_y(y, nb);
   }
 
   // ---- first product
@@ -158,91 +195,98 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int r = 0; r < RT; ++r) tot[m][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // The wave's part of the summed axis, in groups of G fragment steps: the
-  // next group's loads go out before the current one is multiplied.  The last
-  // wave also takes what is behind the last whole group.
-  constexpr int G = MT + RT <= 3 ? 4 : MT + RT <= 6 ? 2 : 1;
-  constexpr int GE = G * E::KE;
-  const int groups = p.K / GE;
-  const int k0 = wave * groups / NW * GE, k1 = (wave + 1) * groups / NW * GE;
-  struct Frags {
-    u32x4_t x[G][MT], a[G][RT];
-  };
+  // The wave's part of the summed axis in stages of 128 bytes a row (two
+  // fragment steps), the next two in flight; the last wave also takes what is
+  // behind the last whole stage.
+  constexpr int GE = 2 * E::KE;
+  constexpr int NI = 2 * (MT + RT);  // loads of a stage, 8 rows each
+  const int stages = p.K / GE;
+  const int s0 = wave * stages / NW, s1 = (wave + 1) * stages / NW;
+  const bool tail = wave == NW - 1 && stages * GE < p.K;
   for (uint64_t todo = live; todo != 0;) {
     const int first = __builtin_ctzll(todo);
     const int cur = __builtin_amdgcn_readlane(id, first);
     const int xfirst = __builtin_amdgcn_readlane(xr, first);
     todo &= ~__ballot(id == cur);
-    const char* xp[MT];
-    const char* ap[RT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int row = idm[m] == cur ? xrm[m] : xfirst;
-      xp[m] = p.x + ((size_t)row * p.ldx + g * E::CE) * E::EB;
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int j = min(16 * r + l, p.rank - 1);  // rank values past the last are not used
-      ap[r] = p.a + (((size_t)cur * p.rank + j) * p.K + g * E::CE) * E::EB;
-    }
+    const int xs = id == cur ? xr : xfirst;
+    const char* ab = p.a + (size_t)cur * p.rank * p.K * E::EB;
     f32x4_t acc[MT][RT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[m][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    auto load_f = [&](Frags& f, int k) {
+    u32x4_t tx[2][MT], ta[2][RT];
+    if (tail) {  // loaded before the stages, multiplied after them
 #pragma unroll
-      for (int u = 0; u < G; ++u) {
+      for (int u = 0; u < 2; ++u) {
+        const int k = min(stages * GE + u * E::KE + g * E::CE, p.K - E::CE);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) f.x[u][m] = load16(xp[m] + (size_t)(k + u * E::KE) * E::EB);
+        for (int m = 0; m < MT; ++m)
+          tx[u][m] = load16(p.x + ((size_t)__shfl(xs, 16 * m + l, kWave) * p.ldx + k) * E::EB);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) f.a[u][r] = load16(ap[r] + (size_t)(k + u * E::KE) * E::EB);
+        for (int r = 0; r < RT; ++r)
+          ta[u][r] = load16(ab + ((size_t)min(16 * r + l, p.rank - 1) * p.K + k) * E::EB);
       }
-    };
-    auto multiply = [&](const Frags& f) {
+    }
+    if (s0 < s1) {
+      const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+      const char* src[NI];
 #pragma unroll
-      for (int u = 0; u < G; ++u)
+      for (int j = 0; j < 2 * MT; ++j)
+        src[j] = p.x + (size_t)__shfl(xs, 8 * j + (lane >> 3), kWave) * p.ldx * E::EB + chunk;
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j)  // rank values past the last are not used
+        src[2 * MT + j] = ab + (size_t)(8 * min(j, p.rank / 8 - 1) + (lane >> 3)) * p.K * E::EB + chunk;
+      auto issue = [&](int s) {
+        const uint32_t dst = my_lds + (s & 1) * S::ST;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) dma16g(src[j] + 128 * (size_t)s, dst + 1024 * j);
+      };
+      auto read = [&](int s, u32x4_t (&x)[2][MT], u32x4_t (&a)[2][RT]) {
+        const char* st = my + (s & 1) * S::ST;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int at = l * 128 + ((4 * u + g) ^ (l & 7)) * 16;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) x[u][m] = load16(st + 2048 * m + at);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) a[u][r] = load16(st + 2048 * (MT + r) + at);
+        }
+      };
+      auto multiply = [&](const u32x4_t (&x)[2][MT], const u32x4_t (&a)[2][RT]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[m][r] = step<BF16>(a[u][r], x[u][m], acc[m][r]);
+      };
+      u32x4_t xf[2][MT], af[2][RT];
+      wait_lds_reads();  // an earlier adapter's stages have been read
+      issue(s0);
+      if (s0 + 1 < s1) issue(s0 + 1);
+      for (int s = s0; s + 1 < s1; ++s) {
+        wait_vm<NI>();  // stage s has landed, s + 1 is in flight
+        read(s, xf, af);
+        wait_lds_reads();
+        if (s + 2 < s1) issue(s + 2);
+        multiply(xf, af);
+      }
+      wait_vm<0>();
+      read(s1 - 1, xf, af);
+      multiply(xf, af);
+    }
+    if (tail) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool in = stages * GE + u * E::KE + g * E::CE < p.K;  // behind the end: zeros on both sides
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int r = 0; r < RT; ++r) acc[m][r] = step<BF16>(f.a[u][r], f.x[u][m], acc[m][r]);
-    };
-    if (k0 < k1) {
-      // two sets in turn (a copy from one to the other would wait for its loads)
-      Frags f0, f1;
-      load_f(f0, k0);
-      for (int k = k0 + GE;; k += 2 * GE) {
-        if (k >= k1) {
-          multiply(f0);
-          break;
-        }
-        load_f(f1, k);
-        __builtin_amdgcn_sched_barrier(0);  // the loads stay in front of the products
-        multiply(f0);
-        if (k + GE >= k1) {
-          multiply(f1);
-          break;
-        }
-        load_f(f0, k + GE);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(f1);
+          for (int r = 0; r < RT; ++r)
+            acc[m][r] = step<BF16>(in ? ta[u][r] : u32x4_t{}, in ? tx[u][m] : u32x4_t{}, acc[m][r]);
       }
     }
-    if (wave == NW - 1)
-      for (int k = groups * GE; k < p.K; k += E::KE) {
-        const bool in = k + g * E::CE < p.K;  // chunks behind the end: zeros on both sides
-        const long at = (long)(in ? k : p.K - E::CE - g * E::CE) * E::EB;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          u32x4_t xf = load16(xp[m] + at);
-          xf = in ? xf : u32x4_t{};
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            u32x4_t af = load16(ap[r] + at);
-            acc[m][r] = step<BF16>(in ? af : u32x4_t{}, xf, acc[m][r]);
-          }
-        }
-      }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -251,34 +295,35 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
         for (int i = 0; i < 4; ++i) tot[m][r][i] = idm[m] == cur ? acc[m][r][i] : tot[m][r][i];
   }
   // tot[m][r][i] = this wave's part of value 16 r + 4 g + i of row 16 m + l
+  float* red = reinterpret_cast<float*>(my);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     if (16 * m + l < p.rows)
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-        *reinterpret_cast<f32x4_t*>(red + (wave * 16 * MT + 16 * m + l) * RL + 16 * r + 4 * g) =
-            tot[m][r];
+        *reinterpret_cast<f32x4_t*>(red + (16 * m + l) * RL + 16 * r + 4 * g) = tot[m][r];
   lds_barrier();
   for (int i0 = wave * kWave; i0 < p.rows * 4 * RT; i0 += NW * kWave) {
     const int i = i0 + lane;
     const int row = min(i / (4 * RT), p.rows - 1), j = 4 * (i % (4 * RT));
     const int a = __shfl(id, row, kWave);
     if (i >= p.rows * 4 * RT) continue;
-    f32x4_t s = *reinterpret_cast<f32x4_t*>(red + row * RL + j);
+    float* r0 = reinterpret_cast<float*>(lds) + row * RL + j;
+    f32x4_t s = *reinterpret_cast<f32x4_t*>(r0);
 #pragma unroll
-    for (int w = 1; w < NW; ++w)
-      s += *reinterpret_cast<f32x4_t*>(red + (w * 16 * MT + row) * RL + j);
+    for (int w = 1; w < NW; ++w) s += *reinterpret_cast<f32x4_t*>(r0 + w * S::WAVE / 4);
     s = a < 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : s * (p.scale != nullptr ? p.scale[a] : 1.f);
     if (p.v != nullptr && split == 0 && row0 + row < p.R && j < p.rank)
       *reinterpret_cast<f32x4_t*>(p.v + (size_t)(row0 + row) * p.rank + j) = s;
-    *reinterpret_cast<f32x4_t*>(red + row * RL + j) = s;
+    *reinterpret_cast<f32x4_t*>(r0) = s;
   }
   if (p.y == nullptr) return;
   lds_barrier();
 
-  // The rank values as fragments.  bf16 holds each fp32 value as two bf16
-  // halves (16 significant bits: their rounding stays 2^-9 below that of y),
-  // two instructions on the same weights.
+  // The rank values (in the first wave's place) as fragments.  bf16 holds each
+  // fp32 value as two bf16 halves (16 significant bits: their rounding stays
+  // 2^-9 below that of y), two instructions on the same weights.
+  constexpr int KF = BF16 ? (RT + 1) / 2 : RT;  // fragment steps of the rank values
   constexpr int NH = BF16 ? 2 : 1;
   u32x4_t vf[NH][MT][KF];
 #pragma unroll
@@ -286,10 +331,12 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const bool on = 4 * s + g < rc && idm[m] >= 0;
-      const float* vr = red + min(16 * m + l, p.rows - 1) * RL + min(4 * s + g, rc - 1) * E::CE;
+      const float* vr = reinterpret_cast<const float*>(lds) + min(16 * m + l, p.rows - 1) * RL +
+                        min(4 * s + g, rc - 1) * E::CE;
       float v[E::CE];
 #pragma unroll
-      for (int i = 0; i < E::CE; i += 4) *reinterpret_cast<f32x4_t*>(v + i) = *reinterpret_cast<const f32x4_t*>(vr + i);
+      for (int i = 0; i < E::CE; i += 4)
+        *reinterpret_cast<f32x4_t*>(v + i) = *reinterpret_cast<const f32x4_t*>(vr + i);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (BF16) {
@@ -306,19 +353,45 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
     }
 
   // ---- second product
-  auto columns = [&](Ops& o, int nb) {
+  int bfr[4][KF];  // this lane's chunk of row 16 q + l of B in step s
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int s = 0; s < KF; ++s) {
+      const int n = 16 * q + l;
+      bfr[q][s] = (n * rc + swz(n, min(4 * s + g, rc - 1))) * 16;
+    }
+  float* delta = reinterpret_cast<float*>(my + S::RED);
+  int at = S::B0;
+  for (; nb < n1; nb += 64 * NW) {
+    if (!S::TWO) load_b(at, nb, cur0);
+    wait_vm<0>();  // the block's B and y
+    u32x4_t yn[NYI];
+    const bool more = nb + 64 * NW < n1;
+    const int atn = S::TWO && at == S::B0 ? S::B1 : S::B0;
+    if (more) {  // the next block's, before this one's products
+      if (S::TWO) load_b(atn, nb + 64 * NW, cur0);
+      load_y(yn, nb + 64 * NW);
+    }
     f32x4_t d[4][MT];
-    bool loaded = kEarly;
+    bool loaded = true;
     for (uint64_t todo = live; todo != 0;) {
       const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
       todo &= ~__ballot(id == cur);
-      if (!loaded) load_w(o, nb, cur);
+      if (!loaded) {
+        wait_lds_reads();
+        load_b(at, nb, cur);
+        wait_vm<0>();
+      }
       loaded = false;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         u32x4_t w[KF];
 #pragma unroll
-        for (int s = 0; s < KF; ++s) w[s] = 4 * s + g < rc ? o.w[q][s] : u32x4_t{};
+        for (int s = 0; s < KF; ++s) {
+          w[s] = load16(my + at + bfr[q][s]);
+          w[s] = 4 * s + g < rc ? w[s] : u32x4_t{};
+        }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
@@ -331,57 +404,49 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
         }
       }
     }
+    // d[q][m][i]: column 16 q + 4 g + i of row 16 m + l, to y's lanes
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int c = 0; c < NY; ++c) {
-        const int n = nb + 4 * E::CE * c + E::CE * g;
-        if (idm[m] < 0 || n >= n1) continue;
-        u32x4_t v = o.y[m][c];
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_t*>(delta + l * S::DL + 16 * q + 4 * g) = d[q][m];
+      asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
+#pragma unroll
+      for (int j = m * (16 / YR); j < (m + 1) * (16 / YR); ++j) {
+        const float* dr = delta + (YR * j + lane / YL - 16 * m) * S::DL + yc;
+        u32x4_t v = y[j];
         if constexpr (BF16) {
+          const f32x4_t d0 = *reinterpret_cast<const f32x4_t*>(dr);
+          const f32x4_t d1 = *reinterpret_cast<const f32x4_t*>(dr + 4);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const f32x4_t& t = d[2 * c + i / 2][m];
+            const f32x4_t& t = i < 2 ? d0 : d1;
             const int k = 2 * (i % 2);
             v[i] = pack_bf2(__uint_as_float(v[i] << 16) + t[k],
                             __uint_as_float(v[i] & 0xffff0000u) + t[k + 1]);
           }
         } else {
+          const f32x4_t d0 = *reinterpret_cast<const f32x4_t*>(dr);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + d[c][m][i]);
+          for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + d0[i]);
         }
-        *reinterpret_cast<u32x4_t*>(p.y + ((size_t)(row0 + 16 * m + l) * p.ldy + n) * E::EB) = v;
+        if (yon[j] && nb + yc < n1)
+          *reinterpret_cast<u32x4_t*>(yrow[j] + (size_t)(nb + yc) * E::EB) = v;
       }
-  };
-  if constexpr (kEarly) {
-    constexpr int ST = 64 * NW;
-    Ops o1;
-    for (; nb < n1; nb += 2 * ST) {
-      if (nb + ST < n1) {
-        load_y(o1, nb + ST);
-        load_w(o1, nb + ST, cur0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      columns(o, nb);
-      if (nb + ST >= n1) break;
-      if (nb + 2 * ST < n1) {
-        load_y(o, nb + 2 * ST);
-        load_w(o, nb + 2 * ST, cur0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      columns(o1, nb + ST);
+      asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
     }
-  } else {
-    for (; nb < n1; nb += 64 * NW) {
-      load_y(o, nb);
-      columns(o, nb);
-    }
+    wait_lds_reads();  // this block's B has been read before it is loaded over
+    if (more)
+#pragma unroll
+      for (int j = 0; j < NYI; ++j) y[j] = yn[j];
+    at = atn;
   }
 }
 
 template <bool BF16, int RT, int MT, int NW>
 hipError_t launch_one(const AdapterArgs& p, hipStream_t s) {
-  const size_t lds = (size_t)NW * 16 * MT * (16 * RT + 4) * 4;
+  constexpr int lds = NW * AdapterLds<BF16, RT, MT>::WAVE;
+  static_assert(lds <= 160 * 1024, "the LDS of one CU");
   const int tiles = (p.R + p.rows - 1) / p.rows;
   adapter_kernel<BF16, RT, MT, NW><<<tiles * p.splits, NW * kWave, lds, s>>>(p);
   return hipGetLastError();
@@ -391,10 +456,18 @@ hipError_t launch_one(const AdapterArgs& p, hipStream_t s) {
 // adapter's weights, more column ranges repeat the first product, and fewer
 // than one workgroup per CU leaves CUs idle: the choice is the one whose
 // busiest CU moves the fewest elements, with the adapters among `rows` rows
-// taken as twice those of rows sorted by adapter (1 .. rows).
+// taken as twice those of rows sorted by adapter (1 .. rows).  Up to 16 rows
+// (one tile): 32 rows gain 2 % at 131072 sorted rows (217 us for 222) and lose
+// on 8191 rows in mixed order (165 us for 73) and on 8285 sorted ones (24 for
+// 21).  Above rank 64, where the weights are most of the traffic, 32 (8191 rows
+// of rank 128: 44 us for 65).
+// Eight waves where there are few workgroups (2048 rows: 10.6 us for 13.3 with
+// four), four where a CU takes several in turn (131072 rows: 222 us for 243) or
+// where two workgroups of eight do not fit its LDS (8191 rows of rank 64: 29 us
+// for 34).
 template <bool BF16>
 hipError_t launch_adapter(AdapterArgs p, hipStream_t s) {
-  const int most = p.rank > 64 ? 32 : 64;
+  const int most = p.rank > 64 ? 32 : 16;
   double best = 0.0;
   for (int rows = 1; rows <= most; rows *= 2)
     for (int splits = 1; splits <= (p.y == nullptr ? 1 : 8); splits *= 2) {
@@ -403,36 +476,27 @@ hipError_t launch_adapter(AdapterArgs p, hipStream_t s) {
       const double ids = min((double)rows, max(1.0, 2.0 * rows * p.n_ids / p.R)) * p.rank;
       const double each = (rows + ids) * p.K + (ids + 2.0 * rows) * p.N / splits;
       const double cost = (double)((tiles * splits + kCUs - 1) / kCUs) * each;
-      if (best > 0.0 && cost >= best) continue;
+      if (best > 0.0 && cost > best) continue;
       best = cost;
       p.rows = rows;
       p.splits = splits;
     }
   const int rt = (p.rank + 15) / 16;
-  // eight waves where their partial sums fit 64 KB of LDS
-  const int mt = (p.rows + 15) / 16;
-  int nw = 8 * 16 * mt * (16 * (rt > 4 ? 8 : rt > 2 ? 4 : rt) + 4) * 4 <= 65536 ? 8 : 4;
-#define MOE_AD(RT)                                                             \
-  do {                                                                         \
-    if (p.rows <= 16) {                                                        \
-      if (nw == 8) return launch_one<BF16, RT, 1, 8>(p, s);                     \
-      return launch_one<BF16, RT, 1, 4>(p, s);                                  \
-    }                                                                          \
-    if (p.rows <= 32) {                                                        \
-      if (nw == 8) return launch_one<BF16, RT, 2, 8>(p, s);                     \
-      return launch_one<BF16, RT, 2, 4>(p, s);                                  \
-    }                                                                          \
-    if constexpr (RT <= 4) {                                                   \
-      if (nw == 8) return launch_one<BF16, RT, 4, 8>(p, s);                     \
-      return launch_one<BF16, RT, 4, 4>(p, s);                                  \
-    }                                                                          \
+  const long wgs = (long)((p.R + p.rows - 1) / p.rows) * p.splits;
+#define MOE_AD(RT)                                                                              \
+  do {                                                                                          \
+    constexpr int mt = RT <= 4 ? 1 : 2;                                                         \
+    constexpr int wave = AdapterLds<BF16, RT, mt>::WAVE;                                        \
+    if constexpr (8 * wave <= 160 * 1024)                                                       \
+      if (wgs <= (8 * wave <= 80 * 1024 ? 4 : 1) * kCUs)                                        \
+        return launch_one<BF16, RT, mt, 8>(p, s);                                               \
+    return launch_one<BF16, RT, mt, 4 * wave <= 160 * 1024 ? 4 : 2>(p, s);                      \
   } while (0)
   if (rt <= 1) MOE_AD(1);
   else if (rt <= 2) MOE_AD(2);
   else if (rt <= 4) MOE_AD(4);
   else MOE_AD(8);
 #undef MOE_AD
-  return hipErrorInvalidValue;
 }
 
 // ---------------------------------------------------------------------------
