@@ -407,15 +407,21 @@ def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, dev, optional: bool
         if optional:
             return None
         raise ValueError(f"{name} must be given")
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _raw_stream(dev: torch.device) -> int:
+    """The current stream of a device as a pointer (without building a Stream object, which
+    costs as much as a small kernel)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _device(t: torch.Tensor) -> torch.device:
@@ -476,7 +482,7 @@ def moe_route_bwd_add(d_topk_w: torch.Tensor, topk_w: torch.Tensor, topk_idx: to
     code = _dtype_code(x)
     ws = _ws(workspace_bytes(MOE_OP_ROUTE_BWD, T, H, 1, E, k, 0, E, code), dev, ws)
     _check(lib.moe_route_bwd_add(*a, T, H, E, k, code, d_logits, dx, dw, _ptr(ws), _nbytes(ws),
-                                 _stream()), "moe_route_bwd_add")
+                                 _raw_stream(dev)), "moe_route_bwd_add")
     return o
 
 
@@ -514,7 +520,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
                                 _into(o, "prob_sum", (S, E), f32, dev),
                                 _into(o, "tokens", (S + 1,), i32, dev), _into(o, "lse", (T,), f32, dev),
                                 _into(o, "loss", (3,), f32, dev), _ptr(o["ws"]), _nbytes(o["ws"]),
-                                _stream()), "moe_balance_loss")
+                                _raw_stream(dev)), "moe_balance_loss")
     return o
 
 
@@ -540,7 +546,7 @@ def moe_balance_loss_bwd(logits: torch.Tensor, fwd: Dict[str, torch.Tensor], k: 
          _arg(token_mask, "token_mask", torch.uint8, (T,), dev, optional=True),
          _arg(d_loss, "d_loss", f32, (1,), dev, optional=True)]
     _check(lib.moe_balance_loss_bwd(*a, T, E, k, S, balance_coef, z_coef, 1 if accumulate else 0,
-                                    _into(o, "d_logits", (T, E), f32, dev), _stream()),
+                                    _into(o, "d_logits", (T, E), f32, dev), _raw_stream(dev)),
            "moe_balance_loss_bwd")
     return o["d_logits"]
 
@@ -563,7 +569,7 @@ def moe_combine_dropout(y_perm: torch.Tensor, topk_w: Optional[torch.Tensor], de
          _arg(dest_row, "dest_row", torch.int32, (T * k,), dev),
          _arg(residual, "residual", dt, (T, H), dev, optional=True)]
     _check(lib.moe_combine_dropout(*a, p, _arg(rng, "rng", torch.int64, (2,), dev), T, H, k,
-                                   _dtype_code(y_perm), _into(o, "y", (T, H), dt, dev), _stream()),
+                                   _dtype_code(y_perm), _into(o, "y", (T, H), dt, dev), _raw_stream(dev)),
            "moe_combine_dropout")
     return o["y"]
 
@@ -584,7 +590,7 @@ def moe_combine_dropout_bwd(dy: torch.Tensor, y_perm: torch.Tensor, topk_w: torc
          _arg(dest_row, "dest_row", torch.int32, (T * k,), dev)]
     _check(lib.moe_combine_dropout_bwd(*a, p, _arg(rng, "rng", torch.int64, (2,), dev), T, H, k,
                                        _dtype_code(dy), _into(o, "dy_perm", (R_cap, H), dt, dev),
-                                       _into(o, "d_topk_w", (T, k), f32, dev), _stream()),
+                                       _into(o, "d_topk_w", (T, k), f32, dev), _raw_stream(dev)),
            "moe_combine_dropout_bwd")
     return o
 
@@ -632,7 +638,7 @@ def moe_adapter_fwd(x: torch.Tensor, row_id: torch.Tensor, A: torch.Tensor, B: t
     o = {"v": out}
     v = _into(o, "v", (R, rank), torch.float32, dev) if want_v else None
     _check(lib.moe_adapter_fwd(xp, src, ids, a, b, sc, R, x_rows, K, N, ldx, ldy, n_ids, rank,
-                               _dtype_code(A), yp, v, _stream()), "moe_adapter_fwd")
+                               _dtype_code(A), yp, v, _raw_stream(dev)), "moe_adapter_fwd")
     return o["v"] if want_v else None
 
 
@@ -664,7 +670,7 @@ def moe_adapter_bwd(dy: torch.Tensor, x: torch.Tensor, row_id: torch.Tensor, A: 
     o["ws"] = _ws(int(nb), dev, ws)
     _check(lib.moe_adapter_bwd(dyp, xp, src, ids, a, b, vp, sc, R, x_rows, K, N, ldx, ldy, lddx,
                                n_ids, rank, _dtype_code(A), dxp, dA, dB, 1 if accumulate else 0,
-                               _ptr(o["ws"]), _nbytes(o["ws"]), _stream()), "moe_adapter_bwd")
+                               _ptr(o["ws"]), _nbytes(o["ws"]), _raw_stream(dev)), "moe_adapter_bwd")
     return o
 
 
@@ -679,7 +685,7 @@ def moe_adapter_rows(offsets: torch.Tensor, src_row: torch.Tensor, token_adapter
     _check(lib.moe_adapter_rows(_arg(offsets, "offsets", i32, (E_l + 1,), dev),
                                 _arg(src_row, "src_row", i32, (R_cap,), dev),
                                 _arg(token_adapter, "token_adapter", i32, (T,), dev), E_l, T,
-                                n_adapters, R_cap, _into(o, "row_id", (R_cap,), i32, dev), _stream()),
+                                n_adapters, R_cap, _into(o, "row_id", (R_cap,), i32, dev), _raw_stream(dev)),
            "moe_adapter_rows")
     return o["row_id"]
 

@@ -23,11 +23,16 @@ namespace {
 constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / kWave;
 
-// Tokens per chunk: at most 512 chunks, so that the second launch has few
-// partial rows to add, and at least 32 tokens, one per 16-lane group and more.
-int balance_chunk(int T) {
-  const int c = (T + 511) / 512;
-  return c <= 32 ? 32 : (c + 31) / 32 * 32;
+// Tokens a workgroup takes at once: U for every group of LPT lanes.
+constexpr int kBalU = 4;
+constexpr int bal_batch(int LPT) { return kBalWaves * (kWave / LPT) * kBalU; }
+int lanes_per_token(int E) { return E <= 32 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64; }
+
+// Tokens per chunk: whole batches, at most 512 chunks, so that the second
+// launch has few partial rows to add.
+int balance_chunk(int T, int E) {
+  const int b = bal_batch(lanes_per_token(E));
+  return ((T + 511) / 512 + b - 1) / b * b + (T == 0 ? b : 0);
 }
 
 // Offset i of the sequences, inside [0, T] whatever the array holds; without
@@ -37,28 +42,58 @@ __device__ __forceinline__ int seq_off(const int32_t* off, int i, int T) {
   return min(max(off[i], 0), T);
 }
 
-// The first sequence whose end lies behind token t, or S (then t is in none).
+// The first sequence whose end lies behind token t (the same in the whole
+// wave), or S: t is in none.  64 places are probed at once.
 __device__ __forceinline__ int seq_find(const int32_t* off, int S, int t, int T) {
-  int lo = 0, hi = S;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (seq_off(off, mid + 1, T) > t) hi = mid; else lo = mid + 1;
+  if (off == nullptr) return 0;
+  int lo = 0, n = S;
+  for (;;) {
+    const int stride = (n + kWave - 1) / kWave;
+    const int i = lo + min((lane_id() + 1) * stride, n) - 1;
+    const uint64_t m = __ballot(seq_off(off, i + 1, T) > t);
+    if (m == 0) return S;
+    const int f = __builtin_ctzll(m);
+    if (stride == 1) return lo + f;
+    lo += f * stride;
+    n = min(stride, n - f * stride);
   }
-  return lo;
 }
 
-// Reductions over the LPT lanes that hold one token.
+// Reductions over the LPT lanes that hold one token: within 16 lanes by data
+// moves of the vector unit (neighbour, pair, half-row and row mirrored), the
+// last one or two steps by shuffles.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int LPT, typename F>
+__device__ __forceinline__ float group_reduce(float v, F f) {
+  v = f(v, moved<0xB1>(v));   // quad: lanes 1 0 3 2
+  v = f(v, moved<0x4E>(v));   // quad: lanes 2 3 0 1
+  v = f(v, moved<0x141>(v));  // mirror of 8
+  if (LPT > 8) v = f(v, moved<0x140>(v));  // mirror of 16
+  if (LPT > 16) v = f(v, __shfl_xor(v, 16, kWave));
+  if (LPT > 32) v = f(v, __shfl_xor(v, 32, kWave));
+  return v;
+}
 template <int LPT>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
+  return group_reduce<LPT>(v, [](float a, float b) { return a + b; });
 }
 template <int LPT>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
+  return group_reduce<LPT>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// exp(d) for d <= 0 (NaN stays NaN; below the normal range 0): 2^(d log2 e)
+// with the product's rounding error, and that of log2 e, put back to first
+// order, so that the error stays near 1 ulp for every d.
+__device__ __forceinline__ float exp_neg(float d) {
+  d = d < -150.f ? -150.f : d;
+  const float hi = d * 1.44269502f;                       // log2 e rounded to fp32
+  const float lo = fmaf(d, 1.44269502f, -hi) + d * 1.92596299e-8f;
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return fmaf(e, lo * 0.693147181f, e);
 }
 
 // The four values of columns 4 h .. 4 h + 3 of a row of E; VEC: one 16-byte load.
@@ -86,6 +121,10 @@ struct BalWs {
   double* zterms;  // [S] sums of lse^2
 };
 
+// A workgroup goes through its chunk in batches, the next batch's logits on
+// their way while it computes, with the running sums of the current sequence in
+// registers; where a sequence ends inside the chunk, and at the chunk's end,
+// the sums go out.
 template <int LPT, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
@@ -93,7 +132,8 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
     int S, int C, float* __restrict__ lse_out, BalWs ws) {
   constexpr int G = kWave / LPT;          // tokens a wave holds at once
   constexpr int NG = kBalWaves * G;       // tokens a workgroup holds at once
-  constexpr int U = 4;                    // tokens of one group in flight
+  constexpr int U = kBalU;                // of them for each group
+  constexpr int BT = NG * U;
   __shared__ int s_cnt[kMaxE];
   __shared__ f32x4_t s_p[NG][LPT];
   __shared__ float s_z[NG];
@@ -102,59 +142,44 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
   const int h = lane % LPT, g = (tid >> 6) * G + lane / LPT;
   const int t0 = blockIdx.x * C, t1 = min(T, t0 + C);
   if (blockIdx.x == 0 && tid == 0) *ws.ticket = 0;
-  int at = t0;  // rows of the chunk that no sequence takes get lse 0
-  for (int s = seq_find(seq_offsets, S, t0, T); s < S; ++s) {
-    const int a = max(t0, seq_off(seq_offsets, s, T)), b = min(t1, seq_off(seq_offsets, s + 1, T));
-    if (a >= t1) break;
-    for (int t = at + tid; t < a; t += kBalThreads) lse_out[t] = 0.f;
-    at = max(at, b);
-    if (a >= b) continue;
-    for (int e = tid; e < E; e += kBalThreads) s_cnt[e] = 0;
-    __syncthreads();
-    for (int i = a * k + tid; i < b * k; i += kBalThreads) {
-      const int e = topk_idx[i];
-      const bool live = mask == nullptr || mask[i / k] != 0;
-      if (live && e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+  if (t0 >= t1) return;
+  const f32x4_t none4 = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  constexpr int IQ = 4;  // choices of a thread loaded ahead (a batch has BT k)
+  f32x4_t z[U];
+  uint8_t mk[U];
+  int pick[IQ];
+  auto choice = [&](int i, int te) {  // -1: not live
+    if (i >= te * k) return -1;
+    const int e = topk_idx[i];
+    return mask == nullptr || mask[i / k] != 0 ? e : -1;
+  };
+  auto fetch = [&](int tb) {
+#pragma unroll
+    for (int q = 0; q < IQ; ++q) pick[q] = choice(tb * k + q * kBalThreads + tid, min(t1, tb + BT));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * NG + g;
+      mk[u] = t < t1 ? (mask != nullptr ? mask[t] : (uint8_t)1) : (uint8_t)0;
+      z[u] = t < t1 ? load4<VEC>(logits + (size_t)t * E, 4 * h, E, -INFINITY) : none4;
     }
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    float z2 = 0.f;
-    int n = 0;
-    for (int tb = a + g; tb < b; tb += U * NG) {
-      f32x4_t z[U];
-      bool live[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u * NG;
-        live[u] = t < b && (mask == nullptr || mask[t] != 0);
-        z[u] = live[u] ? load4<VEC>(logits + (size_t)t * E, 4 * h, E, -INFINITY)
-                       : f32x4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float top = group_max<LPT>(fmaxf(fmaxf(z[u][0], z[u][1]), fmaxf(z[u][2], z[u][3])));
-        // a row of -inf alone: probabilities 0 and lse 0
-        const bool none = top == -INFINITY;
-        f32x4_t ex;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ex[i] = none ? 0.f : expf(z[u][i] - top);
-        const float sum = group_sum<LPT>((ex[0] + ex[1]) + (ex[2] + ex[3]));
-        const float inv = none ? 0.f : 1.f / sum;
-        const float lse = none ? 0.f : top + logf(sum);
-        const int t = tb + u * NG;
-        if (live[u]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = fmaf(ex[i], inv, acc[i]);
-          z2 = fmaf(lse, lse, z2);
-          ++n;
-        }
-        if (t < b && h == 0) lse_out[t] = lse;
-      }
-    }
+  };
+  fetch(t0);
+  for (int e = tid; e < E; e += kBalThreads) s_cnt[e] = 0;
+  int s = seq_find(seq_offsets, S, t0, T);
+  int a = s < S ? seq_off(seq_offsets, s, T) : T, b = s < S ? seq_off(seq_offsets, s + 1, T) : T;
+  __syncthreads();
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  float z2 = 0.f;
+  int n = 0;
+  auto flush = [&]() {
     s_p[g][h] = acc;
     if (h == 0) {
       s_z[g] = z2;
       s_n[g] = n;
     }
+    acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    z2 = 0.f;
+    n = 0;
     __syncthreads();
     const size_t slot = (size_t)blockIdx.x + s;
     for (int e = tid; e < E; e += kBalThreads) {
@@ -163,6 +188,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
       for (int i = 0; i < NG; ++i) q += s_p[i][e / 4][e % 4];
       ws.psum[slot * E + e] = q;
       ws.counts[slot * E + e] = s_cnt[e];
+      s_cnt[e] = 0;
     }
     if (tid == 0) {
       float zs = 0.f;
@@ -175,38 +201,113 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
       ws.tokens[slot] = ns;
     }
     __syncthreads();
+  };
+  for (int tb = t0; tb < t1; tb += BT) {
+    f32x4_t p[U];
+    float lse[U];
+    bool live[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // a row that does not count, whatever it holds, as a row of -inf
+      live[u] = mk[u] != 0;
+      const f32x4_t v = live[u] ? z[u] : none4;
+      const float top = group_max<LPT>(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+      // a row of -inf alone: probabilities 0 and lse 0.  (A NaN leaves top
+      // unless all are NaN; it comes back with the exponentials' sum.)
+      const bool none = top == -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[u][i] = none ? (v[i] == v[i] ? 0.f : v[i]) : exp_neg(v[i] - top);
+      const float sum = group_sum<LPT>((p[u][0] + p[u][1]) + (p[u][2] + p[u][3]));
+      const float inv = none ? (sum == sum ? 0.f : sum) : 1.f / sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[u][i] *= inv;
+      lse[u] = none ? inv : top + logf(sum);
+    }
+    const int te = min(t1, tb + BT);
+    int now[IQ];
+#pragma unroll
+    for (int q = 0; q < IQ; ++q) now[q] = pick[q];
+    if (tb + BT < t1) fetch(tb + BT);
+    uint32_t counted = 0;  // tokens of this batch that a sequence has taken
+    while (s < S && a < te) {
+      const int pa = max(a, tb), pb = min(b, te);
+#pragma unroll
+      for (int q = 0; q < IQ; ++q) {
+        const int i = tb * k + q * kBalThreads + tid;
+        if (i >= pa * k && i < pb * k && now[q] >= 0 && now[q] < E) atomicAdd(&s_cnt[now[q]], 1);
+      }
+      for (int i = max(pa * k, tb * k + IQ * kBalThreads) + tid; i < pb * k; i += kBalThreads) {
+        const int e = choice(i, te);
+        if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * NG + g;
+        const bool in = t >= pa && t < pb;
+        if (in) counted |= 1u << u;
+        if (in && live[u]) {
+          acc += p[u];
+          z2 = fmaf(lse[u], lse[u], z2);
+          ++n;
+        }
+      }
+      if (b > te) break;  // it goes on
+      if (max(a, t0) < b) flush();
+      ++s;
+      a = b;
+      b = s < S ? seq_off(seq_offsets, s + 1, T) : T;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * NG + g;
+      if (t < t1 && h == 0) lse_out[t] = (counted >> u & 1) && live[u] ? lse[u] : 0.f;
+    }
   }
-  for (int t = at + tid; t < t1; t += kBalThreads) lse_out[t] = 0.f;
+  if (s < S && a < t1) flush();  // the sequence that goes on in the next chunk
 }
 
-// One workgroup per (sequence, 32 experts): 8 threads of a column each add
-// every eighth partial row, then the eight in order.  The workgroup that
-// finishes last adds the losses over sequences in order.
-__global__ __launch_bounds__(kBalThreads) void balance_sum_kernel(
+// One workgroup per (sequence, 32 experts): 32 threads of a column each add
+// every 32nd partial row, then the 32 in order.  The workgroup that finishes
+// last adds the losses over sequences in order.
+constexpr int kSumThreads = 1024;
+constexpr int kSumParts = kSumThreads / 32;
+
+__global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
     const int32_t* __restrict__ seq_offsets, int T, int E, int k, int S, int C, float cb, float cz,
     BalWs ws, int32_t* __restrict__ counts, float* __restrict__ prob_sum, int32_t* tokens,
     float* __restrict__ loss) {
-  __shared__ float s_q[8][32], s_z[8];
-  __shared__ int s_c[8][32], s_n[8];
-  __shared__ double s_bal[kBalWaves], s_zt[kBalWaves];
-  __shared__ int s_tok[kBalWaves];
-  __shared__ int s_last;
+  __shared__ float s_q[kSumParts][32], s_z[kSumParts];
+  __shared__ int s_c[kSumParts][32], s_n[kSumParts];
   const int nb = (E + 31) / 32;
   const int s = blockIdx.x / nb, eb = blockIdx.x % nb;
   const int tid = threadIdx.x, col = tid & 31, part = tid >> 5;
   const int e = 32 * eb + col;
   const int a = seq_off(seq_offsets, s, T), b = seq_off(seq_offsets, s + 1, T);
   const int b0 = a / C, b1 = b > a ? (b - 1) / C + 1 : b0;
+  constexpr int U = 4;  // partial rows of a thread in flight
   float q = 0.f, zs = 0.f;
   int c = 0, n = 0;
-  for (int i = b0 + part; i < b1; i += 8) {
-    const size_t slot = (size_t)i + s;
-    if (e < E) {
-      q += ws.psum[slot * E + e];
-      c += ws.counts[slot * E + e];
+  for (int i0 = b0 + part; i0 < b1; i0 += U * kSumParts) {
+    float qv[U], zv[U];
+    int cv[U], nv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kSumParts;
+      const size_t slot = (size_t)min(i, b1 - 1) + s;
+      const int ec = min(e, E - 1);
+      qv[u] = ws.psum[slot * E + ec];
+      cv[u] = ws.counts[slot * E + ec];
+      zv[u] = ws.zsum[slot];
+      nv[u] = ws.tokens[slot];
     }
-    n += ws.tokens[slot];
-    zs += ws.zsum[slot];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * kSumParts >= b1) continue;
+      q += qv[u];
+      c += cv[u];
+      zs += zv[u];
+      n += nv[u];
+    }
   }
   s_q[part][col] = q;
   s_c[part][col] = c;
@@ -215,13 +316,13 @@ __global__ __launch_bounds__(kBalThreads) void balance_sum_kernel(
     s_z[part] = zs;
   }
   __syncthreads();
+  int last = 0;
   if (tid < 32) {
-    q = s_q[0][col];
-    c = s_c[0][col];
-    n = s_n[0];
-    double z2 = s_z[0];
+    q = 0.f;
+    c = n = 0;
+    double z2 = 0.0;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
+    for (int i = 0; i < kSumParts; ++i) {
       q += s_q[i][col];
       c += s_c[i][col];
       n += s_n[i];
@@ -242,17 +343,17 @@ __global__ __launch_bounds__(kBalThreads) void balance_sum_kernel(
       }
       // this workgroup's terms before its ticket, the others' behind the last ticket
       __threadfence();
-      s_last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
+      last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
       __threadfence();
     }
   }
-  __syncthreads();
-  if (!s_last) return;
+  if (tid >= kWave) return;  // one wave holds tid 0 and adds the losses
+  if (!__builtin_amdgcn_readfirstlane(last)) return;
   double bal = 0.0, z = 0.0;
   int N = 0;
-  for (int i = tid; i < (int)gridDim.x; i += kBalThreads)
+  for (int i = tid; i < (int)gridDim.x; i += kWave)
     bal += __hip_atomic_load(&ws.terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int i = tid; i < S; i += kBalThreads) {
+  for (int i = tid; i < S; i += kWave) {
     z += __hip_atomic_load(&ws.zterms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     N += __hip_atomic_load(&tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
@@ -262,18 +363,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_sum_kernel(
     z += __shfl_xor(z, o, kWave);
     N += __shfl_xor(N, o, kWave);
   }
-  if (lane_id() == 0) {
-    s_bal[tid >> 6] = bal;
-    s_zt[tid >> 6] = z;
-    s_tok[tid >> 6] = N;
-  }
-  __syncthreads();
   if (tid == 0) {
-    for (int i = 1; i < kBalWaves; ++i) {
-      bal += s_bal[i];
-      z += s_zt[i];
-      N += s_tok[i];
-    }
     bal = N > 0 ? bal * E / ((double)k * N) : 0.0;
     z = N > 0 ? z / N : 0.0;
     tokens[S] = N;
@@ -283,46 +373,77 @@ __global__ __launch_bounds__(kBalThreads) void balance_sum_kernel(
   }
 }
 
+// U tokens of every group at once, their logits loaded before their sequence
+// (the wave's first by search, then by walking) is known.
 template <int LPT, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
     const float* __restrict__ logits, const float* __restrict__ lse,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
     const int32_t* __restrict__ seq_offsets, const uint8_t* __restrict__ mask,
     const float* __restrict__ d_loss, int T, int E, int k, int S, float cb, float cz, int accumulate,
-    float* __restrict__ d_logits) {
-  constexpr int G = kWave / LPT;
+    float* d_logits) {
+  constexpr int G = kWave / LPT, U = kBalU;
   const int lane = lane_id(), h = lane % LPT;
-  const int t = (blockIdx.x * kBalWaves + (threadIdx.x >> 6)) * G + lane / LPT;
-  if (t >= T) return;
-  const int s = seq_find(seq_offsets, S, t, T);
-  const bool live = s < S && seq_off(seq_offsets, s, T) <= t && (mask == nullptr || mask[t] != 0);
-  f32x4_t d = {0.f, 0.f, 0.f, 0.f};
-  if (live) {  // the same for the LPT lanes of a token
-    const float g = d_loss != nullptr ? *d_loss : 1.f;
-    const float n = (float)tokens[s], N = (float)tokens[S];
-    const float l = lse[t];
-    const f32x4_t z = load4<VEC>(logits + (size_t)t * E, 4 * h, E, -INFINITY);
-    const int32_t* cs = counts + (size_t)s * E;
-    float c[4], dot = 0.f, p[4];
+  const int tw = (blockIdx.x * kBalWaves + (threadIdx.x >> 6)) * G * U;  // the wave's first token
+  if (tw >= T) return;
+  f32x4_t z[U];
+  float l[U];
+  bool live[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = 4 * h + i < E ? (float)cs[4 * h + i] : 0.f;
-      p[i] = expf(z[i] - l);
-      dot = fmaf(p[i], c[i], dot);
-    }
-    dot = group_sum<LPT>(dot);
-    const float kb = cb * (float)E / ((float)k * N) / n, kz = cz * 2.f * l / N;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = g * p[i] * fmaf(kb, c[i] - dot, kz);
+  for (int u = 0; u < U; ++u) {
+    const int t = min(tw + u * G + lane / LPT, T - 1);
+    z[u] = load4<VEC>(logits + (size_t)t * E, 4 * h, E, -INFINITY);
+    l[u] = lse[t];
+    live[u] = mask == nullptr || mask[t] != 0;
   }
-  float* out = d_logits + (size_t)t * E;
-  if (accumulate) d += load4<VEC>(out, 4 * h, E, 0.f);
-  if constexpr (VEC) {
-    if (4 * h < E) *reinterpret_cast<f32x4_t*>(out + 4 * h) = d;
-  } else {
+  const float gl = d_loss != nullptr ? *d_loss : 1.f;
+  const float N = (float)tokens[S];
+  // the current sequence of the lane's group: its rows [a, b), counts, factor
+  int s = seq_find(seq_offsets, S, tw, T), a = T, b = T;
+  float c[4] = {0.f, 0.f, 0.f, 0.f}, kb = 0.f;
+  auto enter = [&]() {
+    if (s >= S) {
+      a = b = T;
+      return;
+    }
+    a = seq_off(seq_offsets, s, T);
+    b = seq_off(seq_offsets, s + 1, T);
+    const int32_t* cs = counts + (size_t)s * E;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * h + i < E) out[4 * h + i] = d[i];
+    for (int i = 0; i < 4; ++i) c[i] = (float)cs[min(4 * h + i, E - 1)];
+    kb = cb * (float)E / ((float)k * N) / (float)tokens[s];
+  };
+  enter();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int t = tw + u * G + lane / LPT;
+    if (t >= T) continue;
+    while (t >= b && s < S) {
+      ++s;
+      enter();
+    }
+    f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+    if (live[u] && t >= a && t < b) {  // the same in a token's lanes
+      float p[4], dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = exp_neg(z[u][i] - l[u]);
+        dot = fmaf(p[i], c[i], dot);
+      }
+      dot = group_sum<LPT>(dot);
+      const float kz = cz * 2.f * l[u] / N;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = gl * p[i] * fmaf(kb, c[i] - dot, kz);
+    }
+    float* out = d_logits + (size_t)t * E;
+    if (accumulate) d += load4<VEC>(out, 4 * h, E, 0.f);
+    if constexpr (VEC) {
+      if (4 * h < E) *reinterpret_cast<f32x4_t*>(out + 4 * h) = d;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * h + i < E) out[4 * h + i] = d[i];
+    }
   }
 }
 
@@ -333,7 +454,7 @@ struct BalLayout {
 };
 
 BalLayout balance_layout(int T, int E, int S) {
-  const int C = balance_chunk(T);
+  const int C = balance_chunk(T, E);
   const size_t slots = (size_t)(T + C - 1) / C + S;
   BalLayout l;
   size_t at = 0;
@@ -363,7 +484,7 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
   const BalWs ws = {(int32_t*)(w + l.counts), (float*)(w + l.psum), (int32_t*)(w + l.tokens),
                     (float*)(w + l.zsum), (uint32_t*)(w + l.ticket), (double*)(w + l.terms),
                     (double*)(w + l.zterms)};
-  const int C = balance_chunk(T);
+  const int C = balance_chunk(T, E);
   // one workgroup at least: it also clears the second launch's ticket
   const int grid = T > 0 ? (T + C - 1) / C : 1;
   const bool vec = E % 4 == 0 && ((uintptr_t)logits & 15) == 0;
@@ -371,15 +492,17 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
 #define MOE_BAL(L, V) \
   balance_part_kernel<L, V><<<grid, kBalThreads, 0, s>>>(logits, topk_idx, seq_offsets, mask, T, E, k, S, C, lse, ws)
 #define MOE_BAL_LPT(L) do { if (vec) MOE_BAL(L, true); else MOE_BAL(L, false); } while (0)
-  if (E <= 32) MOE_BAL_LPT(8);
-  else if (E <= 64) MOE_BAL_LPT(16);
-  else if (E <= 128) MOE_BAL_LPT(32);
-  else MOE_BAL_LPT(64);
+  switch (lanes_per_token(E)) {
+    case 8: MOE_BAL_LPT(8); break;
+    case 16: MOE_BAL_LPT(16); break;
+    case 32: MOE_BAL_LPT(32); break;
+    default: MOE_BAL_LPT(64);
+  }
 #undef MOE_BAL_LPT
 #undef MOE_BAL
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  balance_sum_kernel<<<S * ((E + 31) / 32), kBalThreads, 0, s>>>(seq_offsets, T, E, k, S, C, cb, cz,
+  balance_sum_kernel<<<S * ((E + 31) / 32), kSumThreads, 0, s>>>(seq_offsets, T, E, k, S, C, cb, cz,
                                                                 ws, counts, prob_sum, tokens, loss);
   return hipGetLastError();
 }
@@ -392,15 +515,16 @@ hipError_t launch_balance_loss_bwd(const float* logits, const float* lse, const 
   const bool vec = E % 4 == 0 && (((uintptr_t)logits | (uintptr_t)d_logits) & 15) == 0;
   ProfScope ps(MOE_KERNEL_BALANCE_BWD, s);
 #define MOE_BAL(L, V)                                                                          \
-  balance_bwd_kernel<L, V><<<(T + kBalWaves * (kWave / L) - 1) / (kBalWaves * (kWave / L)),    \
-                             kBalThreads, 0, s>>>(logits, lse, counts, tokens, seq_offsets,    \
+  balance_bwd_kernel<L, V><<<(T + bal_batch(L) - 1) / bal_batch(L), kBalThreads, 0, s>>>(logits, lse, counts, tokens, seq_offsets,    \
                                                   mask, d_loss, T, E, k, S, cb, cz,            \
                                                   accumulate ? 1 : 0, d_logits)
 #define MOE_BAL_LPT(L) do { if (vec) MOE_BAL(L, true); else MOE_BAL(L, false); } while (0)
-  if (E <= 32) MOE_BAL_LPT(8);
-  else if (E <= 64) MOE_BAL_LPT(16);
-  else if (E <= 128) MOE_BAL_LPT(32);
-  else MOE_BAL_LPT(64);
+  switch (lanes_per_token(E)) {
+    case 8: MOE_BAL_LPT(8); break;
+    case 16: MOE_BAL_LPT(16); break;
+    case 32: MOE_BAL_LPT(32); break;
+    default: MOE_BAL_LPT(64);
+  }
 #undef MOE_BAL_LPT
 #undef MOE_BAL
   return hipGetLastError();
