@@ -503,42 +503,208 @@ hipError_t launch_adapter(AdapterArgs p, hipStream_t s) {
 // weight gradients
 // ---------------------------------------------------------------------------
 
-// Row chunks of the weight gradients: the rows of one adapter (in row order)
-// are cut into chunks of `chunk`; an adapter of one chunk (or no row) writes
-// its gradient whole, one of more writes fp32 partials that a second pass adds
-// in chunk order.  plan[0] = number of chunks; then {id, begin, end, slot}.
+// Rows of one adapter in row order, cut into chunks of `chunk`: an adapter of
+// one chunk (or no row) writes its gradient whole, one of more writes fp32
+// partials that a second pass adds in chunk order.  count = chunks in all, each
+// {id, begin, end, slot}.
 struct ChunkPlan {
-  int32_t* count;   // chunks in all
-  int32_t* chunks;  // [upper][4]
-  int32_t* first;   // [n_ids] first slot of an id of several chunks
+  int32_t* count;
+  int32_t* chunks;   // [upper][4]
+  int32_t* first;    // [n_ids] first slot of an id of several chunks
+  int32_t* offsets;  // [n_ids + 1] rows of an id in the order list
 };
 
-__global__ __launch_bounds__(kMaxE) void adapter_plan_kernel(const int32_t* __restrict__ offsets,
-                                                             int n_ids, int chunk, ChunkPlan plan) {
-  __shared__ int s_n[kMaxE], s_m[kMaxE];
-  const int i = threadIdx.x;
-  const int a = i < n_ids ? offsets[i] : 0, b = i < n_ids ? offsets[i + 1] : 0;
-  const int n = i < n_ids ? max(1, (b - a + chunk - 1) / chunk) : 0;
-  const int m = n > 1 ? n : 0;
-  s_n[i] = n;
-  s_m[i] = m;
-  __syncthreads();
-  for (int o = 1; o < kMaxE; o <<= 1) {
-    const int x = i >= o ? s_n[i - o] : 0, y = i >= o ? s_m[i - o] : 0;
+// The adapter of row r, or -1, by the forward's rule.
+struct RowIds {
+  const int32_t* row_id;
+  const int32_t* src_row;
+  int R, x_rows, n_ids;
+  __device__ __forceinline__ int operator()(int r) const {
+    const int a = row_id[r], s = src_row != nullptr ? src_row[r] : r;
+    return a >= 0 && a < n_ids && s >= 0 && s < x_rows ? a : -1;
+  }
+};
+
+constexpr int kSortBlocks = 128;  // at most, so that a block adds few counts
+int sort_rows(int R) { return max(1024, ((R + kSortBlocks - 1) / kSortBlocks + 255) / 256 * 256); }
+
+// First launch of the backward, two independent parts.
+//  - Both transposed weights, A [ids][rank][K] -> [ids][K][rank] and
+//    B [ids][N][rank] -> [ids][rank][N]: a thread turns a block of 16 bytes of
+//    ranks x CW columns in registers, so both sides move whole lane-contiguous
+//    words.
+//  - Counts of the rows of each adapter in blocks of rows, for the order list.
+template <bool BF16>
+__global__ __launch_bounds__(256) void adapter_prepare_kernel(const char* __restrict__ A,
+                                                              const char* __restrict__ B, int rank,
+                                                              int K, int N, char* __restrict__ At,
+                                                              char* __restrict__ Bt, int tblocks,
+                                                              RowIds ids, int per,
+                                                              int32_t* __restrict__ counts) {
+  using E = Elem<BF16>;
+  constexpr int CW = 4 / E::EB;  // columns of one 4-byte word
+  if ((int)blockIdx.x >= tblocks) {
+    __shared__ int s_n[kMaxE];
+    for (int i = threadIdx.x; i < ids.n_ids; i += 256) s_n[i] = 0;
     __syncthreads();
-    s_n[i] += x;
-    s_m[i] += y;
+    const int b = blockIdx.x - tblocks, r1 = min(ids.R, (b + 1) * per);
+    for (int r = b * per + threadIdx.x; r < r1; r += 256) {
+      const int a = ids(r);
+      if (a >= 0) atomicAdd(&s_n[a], 1);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ids.n_ids; i += 256) counts[(size_t)b * ids.n_ids + i] = s_n[i];
+    return;
+  }
+  const int ka = K / CW, kn = N / CW, rc = rank / E::CE;  // words, chunks
+  const long unit = (long)blockIdx.x * 256 + threadIdx.x;
+  const long each = (long)(ka + kn) * rc;
+  if (unit >= each * ids.n_ids) return;
+  const long id = unit / each;
+  int i = (int)(unit - id * each);
+  const bool second = i >= ka * rc;
+  if (second) i -= ka * rc;
+  const int cols = second ? N : K, cw = second ? kn : ka;
+  const int j = i / cw * E::CE, c = i % cw * CW;  // first rank value, first column
+  const size_t base = (size_t)id * rank * cols * E::EB;
+  // wide[c]: 16 bytes of ranks of column c (rows of B and of A^T);
+  // word[j]: 4 bytes of columns of rank value j (rows of A and of B^T)
+  u32x4_t wide[CW];
+  uint32_t word[E::CE];
+  const char* src = (second ? B : A) + base;
+  char* dst = (second ? Bt : At) + base;
+  if (second) {
+#pragma unroll
+    for (int u = 0; u < CW; ++u) wide[u] = load16(src + ((size_t)(c + u) * rank + j) * E::EB);
+  } else {
+#pragma unroll
+    for (int u = 0; u < E::CE; ++u)
+      word[u] = *reinterpret_cast<const uint32_t*>(src + ((size_t)(j + u) * cols + c) * E::EB);
+  }
+  if constexpr (BF16) {
+    if (second) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t x = wide[0][u / 2] >> (16 * (u % 2)), y = wide[1][u / 2] >> (16 * (u % 2));
+        word[u] = (x & 0xffffu) | (y << 16);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        wide[0][u] = (word[2 * u] & 0xffffu) | (word[2 * u + 1] << 16);
+        wide[1][u] = (word[2 * u] >> 16) | (word[2 * u + 1] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (second) word[u] = wide[0][u]; else wide[0][u] = word[u];
+    }
+  }
+  if (second) {
+#pragma unroll
+    for (int u = 0; u < E::CE; ++u)
+      *reinterpret_cast<uint32_t*>(dst + ((size_t)(j + u) * cols + c) * E::EB) = word[u];
+  } else {
+#pragma unroll
+    for (int u = 0; u < CW; ++u)
+      *reinterpret_cast<u32x4_t*>(dst + ((size_t)(c + u) * rank + j) * E::EB) = wide[u];
+  }
+}
+
+// The rows in adapter order, rows of one adapter in row order: every block adds
+// the counts of the blocks before it (and all, for the adapters' offsets), its
+// four waves take a quarter of its rows each, 64 at a time, and a row's place
+// is its wave's cursor for the adapter plus the lanes before it that have the
+// same.  The first block also writes the chunks.
+__global__ __launch_bounds__(256) void adapter_order_kernel(RowIds ids, int per, int nblk,
+                                                            const int32_t* __restrict__ counts,
+                                                            int chunk, ChunkPlan plan,
+                                                            int32_t* __restrict__ order) {
+  __shared__ int s_cur[4][kMaxE], s_t[kMaxE], s_m[kMaxE];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = lane_id();
+  const int b = blockIdx.x;
+  int before = 0, all = 0;
+  if (tid < ids.n_ids) {
+#pragma unroll 8
+    for (int i = 0; i < nblk; ++i) {
+      const int c = counts[(size_t)i * ids.n_ids + tid];
+      before += i < b ? c : 0;
+      all += c;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) s_cur[w][tid] = 0;
+  s_t[tid] = all;
+  __syncthreads();
+  const int q = (per + 3) / 4;  // rows of a wave
+  const int r0 = b * per + wave * q, r1 = min(min(ids.R, (b + 1) * per), r0 + q);
+  for (int r = r0 + lane; r < r1; r += kWave) {
+    const int a = ids(r);
+    if (a >= 0) atomicAdd(&s_cur[wave][a], 1);
+  }
+  for (int o = 1; o < kMaxE; o <<= 1) {  // totals to ends
+    const int x = tid >= o ? s_t[tid - o] : 0;
+    __syncthreads();
+    s_t[tid] += x;
     __syncthreads();
   }
-  if (i == kMaxE - 1) *plan.count = s_n[i];
-  if (i >= n_ids) return;
-  const int at = s_n[i] - n, slot = s_m[i] - m;
-  plan.first[i] = slot;
+  const int end = s_t[tid], begin = end - all;
+  int at = begin + before;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {  // counts of the waves to their cursors
+    const int n = s_cur[w][tid];
+    s_cur[w][tid] = at;
+    at += n;
+  }
+  __syncthreads();
+  for (int rb = r0; rb < r1; rb += kWave) {
+    const int r = rb + lane;
+    const int a = r < r1 ? ids(r) : -1;
+    int rank = 0, same_n = 0;
+    for (uint64_t todo = __ballot(a >= 0); todo != 0;) {
+      const int cur = __builtin_amdgcn_readlane(a, __builtin_ctzll(todo));
+      const uint64_t same = __ballot(a == cur);
+      todo &= ~same;
+      if (a == cur) {
+        rank = __popcll(same & ((1ull << lane) - 1ull));
+        same_n = __popcll(same);
+      }
+    }
+    const int from = a >= 0 ? s_cur[wave][a] : 0;
+    asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
+    if (a >= 0) {
+      order[from + rank] = r;
+      if (rank == 0) s_cur[wave][a] = from + same_n;
+    }
+    asm volatile("" ::: "memory");
+  }
+  if (b != 0) return;
+  // the chunks, and the slots of adapters of several
+  const int n = tid < ids.n_ids ? max(1, (all + chunk - 1) / chunk) : 0;
+  const int m = n > 1 ? n : 0;
+  __syncthreads();
+  s_t[tid] = n;
+  s_m[tid] = m;
+  __syncthreads();
+  for (int o = 1; o < kMaxE; o <<= 1) {
+    const int x = tid >= o ? s_t[tid - o] : 0, y = tid >= o ? s_m[tid - o] : 0;
+    __syncthreads();
+    s_t[tid] += x;
+    s_m[tid] += y;
+    __syncthreads();
+  }
+  if (tid == kMaxE - 1) *plan.count = s_t[tid];
+  if (tid >= ids.n_ids) return;
+  plan.offsets[tid] = begin;
+  if (tid == ids.n_ids - 1) plan.offsets[tid + 1] = end;
+  const int slot = s_m[tid] - m;
+  plan.first[tid] = slot;
   for (int c = 0; c < n; ++c) {
-    int32_t* e = plan.chunks + 4 * (size_t)(at + c);
-    e[0] = i;
-    e[1] = a + c * chunk;
-    e[2] = min(b, a + (c + 1) * chunk);
+    int32_t* e = plan.chunks + 4 * (size_t)(s_t[tid] - n + c);
+    e[0] = tid;
+    e[1] = begin + c * chunk;
+    e[2] = min(end, begin + (c + 1) * chunk);
     e[3] = n > 1 ? slot + c : -1;
   }
 }
@@ -554,116 +720,176 @@ struct WgradArgs {
   long ldq[2];
   int C[2];                  // K, N
   int nb0;                   // 256-column blocks of the first product
-  int x_rows, rank, accumulate;
+  int rank, accumulate;
 };
 
 constexpr int kWgMaxChunk = 1024;
 
-// One fp32 value as three bf16 parts whose sum is the value (24 bits).
-__device__ __forceinline__ void split3(const float* v, u32x4_t* f) {
-  float h[8], m[8], o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    h[i] = bf2f(f2bf(v[i]));
-    const float r = v[i] - h[i];
-    m[i] = bf2f(f2bf(r));
-    o[i] = r - m[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[0][i] = pack_bf2(h[2 * i], h[2 * i + 1]);
-    f[1][i] = pack_bf2(m[2 * i], m[2 * i + 1]);
-    f[2][i] = pack_bf2(o[2 * i], o[2 * i + 1]);
-  }
-}
+// G = sum over a chunk's rows of p_r q_r^T: the rows are the summed axis.
+//
+// The wide factor: a wave holds 64 columns, lane l the columns 4 l .. 4 l + 3
+// of the rows of its 16-lane group g; loaded row by row (128 contiguous bytes
+// of a bf16 row per group, the next step's while this one is multiplied), the
+// eight rows of a lane are put together per column by 16-bit permutes.
+// The narrow fp32 factor: SB rows at a time, turned to [value][row] in LDS
+// once for the four waves.  bf16 takes it as three bf16 parts (24 bits), so the
+// products are exact and the sums fp32 like those of the fp32 path.
+// Bound by the reads of the wide factor (HBM, and the L2 for gathered rows).
+template <bool BF16, int RT>
+struct WgradLds {
+  static constexpr int SB = RT <= 2 ? 128 : RT == 4 ? 64 : 32;  // rows of a staged block
+  static constexpr int NP = BF16 ? 3 : 1;
+  static constexpr int PITCH = SB * (BF16 ? 2 : 4) + 16;        // bytes of one value's rows
+  static constexpr int BYTES = NP * 16 * RT * PITCH;
+};
 
-// G = sum over a chunk's rows of p_r q_r^T: the rows are the summed axis.  A
-// wave holds 64 columns, lane l the columns 4 l .. 4 l + 3 of the rows of its
-// 16-lane group g; loaded row by row (128 contiguous bytes of a bf16 row per
-// group), the eight rows of a lane are put together per column by 16-bit
-// permutes, without LDS.  bf16 takes the fp32 factor as three bf16 parts, so
-// the products are exact and the sums fp32 like those of the fp32 path.
 template <bool BF16, int RT>
 __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
+  using S = WgradLds<BF16, RT>;
   constexpr int SR = BF16 ? 32 : 16;  // rows of one step
   constexpr int LR = SR / 4;          // rows of a lane
-  __shared__ int s_row[kWgMaxChunk], s_q[kWgMaxChunk];
+  constexpr int SB = S::SB;
+  constexpr int IT = 16 * RT * SB / 8 / 256;  // (value, 8 rows) pairs of a thread
+  typedef uint32_t word_t __attribute__((ext_vector_type(BF16 ? 2 : 4)));
+  __shared__ __align__(16) int s_row[kWgMaxChunk], s_q[kWgMaxChunk];
+  __shared__ __align__(16) char s_p[2][S::BYTES];
   if ((int)blockIdx.x >= *a.plan.count) return;
   const int32_t* e = a.plan.chunks + 4 * (size_t)blockIdx.x;
-  const int id = e[0], begin = e[1], end = e[2], slot = e[3];
+  const int id = e[0], begin = e[1], n = e[2] - e[1], slot = e[3];
   const int z = (int)blockIdx.y >= a.nb0 ? 1 : 0;
   const int C = a.C[z];
-  const int lane = lane_id(), wave = threadIdx.x >> 6, l = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, l = lane & 15, g = lane >> 4;
   const int c0 = 256 * ((int)blockIdx.y - z * a.nb0) + 64 * wave + 4 * l;
-  const int n = end - begin;
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int r = a.order[begin + i];
-    int q = a.src_row != nullptr ? a.src_row[r] : r;
-    if (q < 0 || q >= a.x_rows) q = -1;  // a row that the forward left alone too
-    else if (z == 1) q = r;
-    s_row[i] = r;
-    s_q[i] = q;
-  }
-  __syncthreads();
   const float* P = a.p[z];
-  const char* Q = a.q[z];
-  const long ldq = a.ldq[z];
-  const bool in = c0 < C;
+  const char* Q = a.q[z] + (size_t)min(c0, C - 4) * (BF16 ? 2 : 4);
+  const size_t ldq = (size_t)a.ldq[z] * (BF16 ? 2 : 4);
   f32x4_t acc[RT][4];  // tile q: columns 4 l' + q
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[r][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < n; i0 += SR) {
-    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-    u32x2_t raw[LR];
-    u32x4_t rawf[LR];
-    float pv[RT][LR];
-#pragma unroll
-    for (int i = 0; i < LR; ++i) {
-      const int at = i0 + LR * g + i;
-      const int row = at < n ? s_row[at] : -1, qr = at < n ? s_q[at] : -1;
-      if constexpr (BF16)
-        raw[i] = in && qr >= 0 ? *reinterpret_cast<const u32x2_t*>(Q + ((size_t)qr * ldq + c0) * 2) : u32x2_t{};
-      else
-        rawf[i] = in && qr >= 0 ? load16(Q + ((size_t)qr * ldq + c0) * 4) : u32x4_t{};
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int j = 16 * r + l;
-        pv[r][i] = qr >= 0 && j < a.rank ? P[(size_t)row * a.rank + j] : 0.f;
-      }
+  if (n > 0) {
+    // the list to a whole staged block, the last row again behind the end
+    const int np = (n + SB - 1) / SB * SB;
+    for (int i = tid; i < np; i += 256) {
+      const int r = a.order[begin + min(i, n - 1)];
+      s_row[i] = r;
+      s_q[i] = z == 0 && a.src_row != nullptr ? a.src_row[r] : r;
     }
-    if constexpr (BF16) {
-      u32x4_t col[4];
+    __syncthreads();
+    float pv[IT][8];
+    auto load_p = [&](int i0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int t = 0; t < IT; ++t) {
+        const int j = (tid + 256 * t) % (16 * RT), o = (tid + 256 * t) / (16 * RT) * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x = raw[2 * i][h], y = raw[2 * i + 1][h];
-          col[2 * h][i] = (x & 0xffffu) | (y << 16);
-          col[2 * h + 1][i] = (x >> 16) | (y & 0xffff0000u);
-        }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        u32x4_t f[3];
-        split3(pv[r], f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int s = 0; s < 3; ++s) acc[r][q] = step<true>(f[s], col[q], acc[r][q]);
+        for (int i = 0; i < 8; ++i)
+          pv[t][i] = P[(size_t)s_row[i0 + o + i] * a.rank + min(j, a.rank - 1)];
       }
-    } else {
+    };
+    auto store_p = [&](int i0, char* to) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+      for (int t = 0; t < IT; ++t) {
+        const int j = (tid + 256 * t) % (16 * RT), o = (tid + 256 * t) / (16 * RT) * 8;
+        float v[8], h[8], m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i0 + o + i < n ? pv[t][i] : 0.f;
+        char* at = to + j * S::PITCH;
+        if constexpr (BF16) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            h[i] = bf2f(f2bf(v[i]));
+            const float r = v[i] - h[i];
+            m[i] = bf2f(f2bf(r));
+            v[i] = r - m[i];
+          }
+          const float* parts[3] = {h, m, v};
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            *reinterpret_cast<u32x4_t*>(at + p * 16 * RT * S::PITCH + o * 2) =
+                u32x4_t{pack_bf2(parts[p][0], parts[p][1]), pack_bf2(parts[p][2], parts[p][3]),
+                        pack_bf2(parts[p][4], parts[p][5]), pack_bf2(parts[p][6], parts[p][7])};
+        } else {
+          *reinterpret_cast<f32x4_t*>(at + o * 4) = f32x4_t{v[0], v[1], v[2], v[3]};
+          *reinterpret_cast<f32x4_t*>(at + o * 4 + 16) = f32x4_t{v[4], v[5], v[6], v[7]};
+        }
+      }
+    };
+    auto load_q = [&](word_t (&raw)[LR], int i0) {
+#pragma unroll
+      for (int i = 0; i < LR; ++i)
+        raw[i] = *reinterpret_cast<const word_t*>(Q + (size_t)s_q[i0 + LR * g + i] * ldq);
+    };
+    auto multiply = [&](word_t (&raw)[LR], int i0, const char* sp) {
+      if (i0 + SR > n)  // rows behind the end: zeros on both sides
 #pragma unroll
         for (int i = 0; i < LR; ++i)
+          if (i0 + LR * g + i >= n) raw[i] = word_t{};
+      const char* at = sp + l * S::PITCH + (i0 % SB + LR * g) * (BF16 ? 2 : 4);
+      if constexpr (BF16) {
+        u32x4_t col[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            acc[r][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(pv[r][i], __uint_as_float(rawf[i][q]),
-                                                             acc[r][q], 0, 0, 0);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = raw[2 * i][h], y = raw[2 * i + 1][h];
+            col[2 * h][i] = __builtin_amdgcn_perm(y, x, 0x05040100u);      // the low halves
+            col[2 * h + 1][i] = __builtin_amdgcn_perm(y, x, 0x07060302u);  // the high halves
+          }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            const u32x4_t f = load16(at + (p * RT + r) * 16 * S::PITCH);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[r][q] = step<true>(f, col[q], acc[r][q]);
+          }
+      } else {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const f32x4_t f = *reinterpret_cast<const f32x4_t*>(at + r * 16 * S::PITCH);
+#pragma unroll
+          for (int i = 0; i < LR; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              acc[r][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[i], __uint_as_float(raw[i][q]),
+                                                               acc[r][q], 0, 0, 0);
+        }
+      }
+    };
+    word_t q0[LR], q1[LR];
+    load_p(0);
+    load_q(q0, 0);
+    store_p(0, s_p[0]);
+    __syncthreads();
+    for (int b0 = 0; b0 < np; b0 += SB) {
+      const char* sp = s_p[b0 / SB & 1];
+      const bool more = b0 + SB < np;
+      if (more) load_p(b0 + SB);
+#pragma unroll
+      for (int u = 0; u < SB / SR; u += 2) {
+        const int i0 = b0 + u * SR;
+        if (SB / SR > 1) {
+          load_q(q1, i0 + SR);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(q0, i0, sp);
+          if (u + 2 < SB / SR || more) load_q(q0, i0 + 2 * SR);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(q1, i0 + SR, sp);
+        } else {
+          if (more) load_q(q1, i0 + SR);
+          multiply(q0, i0, sp);
+#pragma unroll
+          for (int i = 0; i < LR; ++i) q0[i] = q1[i];
+        }
+      }
+      if (more) {
+        store_p(b0 + SB, s_p[(b0 / SB + 1) & 1]);
+        __syncthreads();
+      }
     }
   }
-  if (!in) return;
+  if (c0 >= C) return;
   // acc[r][q][i]: rank value 16 r + 4 g + i, column c0 + q
   float* out;
   const bool add = slot < 0 && a.accumulate;
@@ -694,10 +920,10 @@ __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
 
 // Gradients of the adapters of several chunks: their partials in chunk order.
 __global__ __launch_bounds__(256) void adapter_wgrad_sum_kernel(
-    const int32_t* __restrict__ offsets, int chunk, ChunkPlan plan, const f32x4_t* __restrict__ part,
-    int rank, int K, int N, int accumulate, f32x4_t* __restrict__ dA, f32x4_t* __restrict__ dB) {
+    int chunk, ChunkPlan plan, const f32x4_t* __restrict__ part, int rank, int K, int N,
+    int accumulate, f32x4_t* __restrict__ dA, f32x4_t* __restrict__ dB) {
   const int id = blockIdx.y;
-  const int n = (offsets[id + 1] - offsets[id] + chunk - 1) / chunk;
+  const int n = (plan.offsets[id + 1] - plan.offsets[id] + chunk - 1) / chunk;
   if (n <= 1) return;
   const int ka = rank * K / 4, all = rank * (K + N) / 4;  // 16-byte groups
   const int i = blockIdx.x * 256 + threadIdx.x;
@@ -707,30 +933,6 @@ __global__ __launch_bounds__(256) void adapter_wgrad_sum_kernel(
   const f32x4_t* q = part + (size_t)plan.first[id] * all + i;
   for (int c = 0; c < n; ++c) v += q[(size_t)c * all];
   *o = v;
-}
-
-// Both transposed weights: A [ids][rank][K] -> [ids][K][rank] and
-// B [ids][N][rank] -> [ids][rank][N], 32x32 tiles through LDS.
-template <typename U>
-__global__ __launch_bounds__(256) void adapter_transpose_kernel(const U* __restrict__ A,
-                                                                const U* __restrict__ B, int rank,
-                                                                int K, int N, U* __restrict__ At,
-                                                                U* __restrict__ Bt) {
-  __shared__ U tile[32][33];
-  const int ktiles = (K + 31) / 32;
-  const bool second = (int)blockIdx.x >= ktiles;
-  const int rows = second ? N : rank, cols = second ? rank : K;
-  const int c0 = 32 * (second ? (int)blockIdx.y : (int)blockIdx.x);
-  const int r0 = 32 * (second ? (int)blockIdx.x - ktiles : (int)blockIdx.y);
-  const size_t base = (size_t)blockIdx.z * rows * cols;
-  const U* src = (second ? B : A) + base;
-  U* dst = (second ? Bt : At) + base;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  for (int i = ty; i < 32; i += 8)
-    if (r0 + i < rows && c0 + tx < cols) tile[i][tx] = src[(size_t)(r0 + i) * cols + c0 + tx];
-  __syncthreads();
-  for (int i = ty; i < 32; i += 8)
-    if (c0 + i < cols && r0 + tx < rows) dst[(size_t)(c0 + i) * rows + r0 + tx] = tile[tx][i];
 }
 
 // Adapter of grouped row r: that of its token, of its expert.
@@ -767,7 +969,7 @@ int wgrad_chunk(int R, int K, int N) {
 }
 
 struct BwdLayout {
-  size_t at, bt, w, sort, counts, offsets, dest, order, count, chunks, first, part, total;
+  size_t at, bt, w, counts, order, count, chunks, first, offsets, part, total;
   int chunk, upper;
 };
 
@@ -780,14 +982,12 @@ BwdLayout bwd_layout(int R, int K, int N, int n_ids, int rank, int eb) {
   l.at = take((size_t)n_ids * rank * K * eb);
   l.bt = take((size_t)n_ids * rank * N * eb);
   l.w = take((size_t)R * rank * 4);
-  l.sort = take(permute_ws_bytes(R, 1, n_ids));
-  l.counts = take((size_t)n_ids * 4);
-  l.offsets = take((size_t)(n_ids + 1) * 4);
-  l.dest = take((size_t)R * 4);
+  l.counts = take((size_t)((R + sort_rows(R) - 1) / sort_rows(R)) * n_ids * 4);
   l.order = take((size_t)R * 4);
   l.count = take(4);
   l.chunks = take((size_t)l.upper * 16);
   l.first = take((size_t)n_ids * 4);
+  l.offsets = take((size_t)(n_ids + 1) * 4);
   l.part = take((size_t)(2 * (R / l.chunk)) * rank * (K + N) * 4);
   l.total = at;
   return l;
@@ -840,17 +1040,20 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
   const int eb = d.bf16 ? 2 : 4;
   const BwdLayout l = bwd_layout(d.R, d.K, d.N, d.n_ids, d.rank, eb);
   char* w = (char*)ws;
+  const RowIds ids = {row_id, src_row, d.R, d.x_rows, d.n_ids};
+  const int per = sort_rows(d.R), nblk = dA != nullptr ? (d.R + per - 1) / per : 0;
   hipError_t e = hipSuccess;
   if (d.R > 0) {
-    const dim3 grid((d.K + 31) / 32 + (d.N + 31) / 32, (d.rank + 31) / 32, d.n_ids);
+    const long units = (long)d.n_ids * (d.rank * eb / 16) * ((d.K + d.N) * eb / 4);
+    const int tblocks = (int)((units + 255) / 256);
     if (d.bf16)
-      adapter_transpose_kernel<uint16_t><<<grid, 256, 0, s>>>(
-          (const uint16_t*)A, (const uint16_t*)B, d.rank, d.K, d.N, (uint16_t*)(w + l.at),
-          (uint16_t*)(w + l.bt));
+      adapter_prepare_kernel<true><<<tblocks + nblk, 256, 0, s>>>(
+          (const char*)A, (const char*)B, d.rank, d.K, d.N, w + l.at, w + l.bt, tblocks, ids, per,
+          (int32_t*)(w + l.counts));
     else
-      adapter_transpose_kernel<uint32_t><<<grid, 256, 0, s>>>(
-          (const uint32_t*)A, (const uint32_t*)B, d.rank, d.K, d.N, (uint32_t*)(w + l.at),
-          (uint32_t*)(w + l.bt));
+      adapter_prepare_kernel<false><<<tblocks + nblk, 256, 0, s>>>(
+          (const char*)A, (const char*)B, d.rank, d.K, d.N, w + l.at, w + l.bt, tblocks, ids, per,
+          (int32_t*)(w + l.counts));
     if ((e = hipGetLastError()) != hipSuccess) return e;
     // the data part: the forward from dy's rows to dx's on the transposed weights
     AdapterArgs p{};
@@ -875,14 +1078,10 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
     if (e != hipSuccess) return e;
   }
   if (dA == nullptr) return e;
-  // rows in adapter order (a stable sort by adapter: the permutation of
-  // routed rows with one slot per row), then the chunks of each adapter
-  int32_t* offsets = (int32_t*)(w + l.offsets);
-  e = launch_permute(nullptr, row_id, d.R, d.K, 1, 0, d.n_ids, eb, (int32_t*)(w + l.counts), offsets,
-                     (int32_t*)(w + l.dest), (int32_t*)(w + l.order), nullptr, w + l.sort, s);
-  if (e != hipSuccess) return e;
-  const ChunkPlan plan = {(int32_t*)(w + l.count), (int32_t*)(w + l.chunks), (int32_t*)(w + l.first)};
-  adapter_plan_kernel<<<1, kMaxE, 0, s>>>(offsets, d.n_ids, l.chunk, plan);
+  const ChunkPlan plan = {(int32_t*)(w + l.count), (int32_t*)(w + l.chunks), (int32_t*)(w + l.first),
+                          (int32_t*)(w + l.offsets)};
+  adapter_order_kernel<<<max(nblk, 1), 256, 0, s>>>(ids, per, nblk, (const int32_t*)(w + l.counts),
+                                                    l.chunk, plan, (int32_t*)(w + l.order));
   if ((e = hipGetLastError()) != hipSuccess) return e;
   WgradArgs a{};
   a.p[0] = (const float*)(w + l.w);
@@ -900,7 +1099,6 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
   a.C[0] = d.K;
   a.C[1] = d.N;
   a.nb0 = (d.K + 255) / 256;
-  a.x_rows = d.x_rows;
   a.rank = d.rank;
   a.accumulate = accumulate ? 1 : 0;
   const dim3 grid(l.upper, a.nb0 + (d.N + 255) / 256);
@@ -921,8 +1119,8 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (d.R <= l.chunk) return e;  // no adapter has more than one chunk
   adapter_wgrad_sum_kernel<<<dim3((d.rank * (d.K + d.N) / 4 + 255) / 256, d.n_ids), 256, 0, s>>>(
-      offsets, l.chunk, plan, (const f32x4_t*)(w + l.part), d.rank, d.K, d.N, accumulate ? 1 : 0,
-      (f32x4_t*)dA, (f32x4_t*)dB);
+      l.chunk, plan, (const f32x4_t*)(w + l.part), d.rank, d.K, d.N, accumulate ? 1 : 0, (f32x4_t*)dA,
+      (f32x4_t*)dB);
   return hipGetLastError();
 }
 
