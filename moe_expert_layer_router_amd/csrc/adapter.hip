@@ -82,7 +82,7 @@ struct AdapterLds {
   static constexpr int DL = 68;                             // pitch of the results (floats)
   static constexpr int DELTA = 16 * DL * 4;                 // 16 rows x 64 columns
   static constexpr int JB = (BF16 ? 2 : 4) * RT;            // KB of 64 columns of B at most
-  static constexpr bool TWO = JB <= 4;
+  static constexpr bool TWO = BF16 && RT <= 2;
   static constexpr int B1 = RED + DELTA;
   static constexpr int FIRST = 2 * ST > B1 + 1024 * JB ? 2 * ST : B1 + 1024 * JB;
   static constexpr int B0 = TWO ? FIRST : B1;
@@ -118,13 +118,15 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
   const int tile = bid / p.splits, split = bid % p.splits;
   const int row0 = tile * p.rows;
 
-  // lane i: adapter and x row of the workgroup's row i
+  // lane i: adapter, its scale and x row of the workgroup's row i
   int id = -1, xr = 0;
+  float scale = 1.f;
   if (lane < p.rows && row0 + lane < p.R) {
     id = p.row_id[row0 + lane];
     xr = p.src_row != nullptr ? p.src_row[row0 + lane] : row0 + lane;
     if (id < 0 || id >= p.n_ids || xr < 0 || xr >= p.x_rows) id = -1;
     if (!p.gather) xr = row0 + lane;
+    if (id >= 0 && p.scale != nullptr) scale = p.scale[id];
   }
   const uint64_t live = __ballot(id >= 0);
   if (live == 0) {
@@ -306,13 +308,14 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
   for (int i0 = wave * kWave; i0 < p.rows * 4 * RT; i0 += NW * kWave) {
     const int i = i0 + lane;
     const int row = min(i / (4 * RT), p.rows - 1), j = 4 * (i % (4 * RT));
-    const int a = __shfl(id, row, kWave);
+    const float f = __shfl(scale, row, kWave);
+    const bool on = (live >> row & 1) != 0;
     if (i >= p.rows * 4 * RT) continue;
     float* r0 = reinterpret_cast<float*>(lds) + row * RL + j;
     f32x4_t s = *reinterpret_cast<f32x4_t*>(r0);
 #pragma unroll
     for (int w = 1; w < NW; ++w) s += *reinterpret_cast<f32x4_t*>(r0 + w * S::WAVE / 4);
-    s = a < 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : s * (p.scale != nullptr ? p.scale[a] : 1.f);
+    s = on ? s * f : f32x4_t{0.f, 0.f, 0.f, 0.f};
     if (p.v != nullptr && split == 0 && row0 + row < p.R && j < p.rank)
       *reinterpret_cast<f32x4_t*>(p.v + (size_t)(row0 + row) * p.rank + j) = s;
     *reinterpret_cast<f32x4_t*>(r0) = s;
