@@ -579,6 +579,28 @@ int moe_adapter_bwd(const void* dy, const void* x, const int32_t* src_row, const
 int moe_adapter_rows(const int32_t* offsets, const int32_t* src_row, const int32_t* token_adapter,
                      int E_l, int T, int n_adapters, int R_cap, int32_t* row_id, void* stream);
 
+/* moe_grouped_ffn_fwd (src_row NULL: x holds the grouped rows [R_cap,H]) or
+ * moe_grouped_ffn_fwd_gather (src_row given, bf16: x [x_rows,H] holds the token
+ * rows) with low-rank adapters on the expert projections:
+ *   g, u  = the products, each + its adapter's (moe_adapter_fwd on the stored,
+ *           rounded product)                                  -> gu [R_cap,2I]
+ *   h     = SiLU(g) * u, for rows with an adapter from the stored g, u -> h_perm
+ *   y     = the down product + its adapter's on h_perm               -> y_perm
+ * Rows without an adapter get the bits of the call without adapters.
+ *   row_id [R_cap] from moe_adapter_rows (rows past offsets[E_l]: -1);
+ *   a_gate, a_up [n_ids,rank,H], b_gate, b_up [n_ids,I,rank], a_down
+ *   [n_ids,rank,I], b_down [n_ids,H,rank] dtype (a pair may be NULL: no adapter
+ *   on that projection), scale [n_ids] fp32 or NULL
+ *   gu is required; ws MOE_OP_FFN_FWD.  Limits of both calls apply (fp32:
+ *   I % 4 == 0). */
+int moe_grouped_ffn_fwd_adapter(const void* x, const int32_t* src_row, const int32_t* offsets,
+                                const int32_t* row_id, int E_l, int R_cap, int x_rows, int H, int I,
+                                const void* w_gate, const void* w_up, const void* w_down,
+                                const void* a_gate, const void* b_gate, const void* a_up,
+                                const void* b_up, const void* a_down, const void* b_down,
+                                const float* scale, int n_ids, int rank, int dtype, void* gu,
+                                void* h_perm, void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
 /* Kernel timing hook (benchmarks and profilers).  After this call the library
  * records start_events[i] and stop_events[i] (each a hipEvent_t created by
  * the caller) on the launch stream immediately before and after the i-th

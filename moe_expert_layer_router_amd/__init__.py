@@ -16,7 +16,7 @@ moe_quantize_fp8_group_t, moe_grouped_ffn_wgrad_fp8, and its two halves
 moe_grouped_ffn_wgrad_fp8_begin / _end; around the layer: the router's
 auxiliary losses moe_balance_loss / _bwd with moe_route_bwd_add, and the combine
 with dropout moe_combine_dropout / _bwd, and low-rank adapters moe_adapter_fwd /
-_bwd with moe_adapter_rows) and return
+_bwd with moe_adapter_rows and moe_grouped_ffn_fwd_adapter) and return
 freshly allocated torch tensors; each also accepts preallocated outputs via
 ``out=`` dictionaries so that steady-state loops allocate nothing.
 """
@@ -92,6 +92,8 @@ def _load():
         "moe_adapter_fwd": ([P] * 6 + [I32] * 9 + [P, P, P], I32),
         "moe_adapter_ws_bytes": ([I32] * 6, I64),
         "moe_adapter_bwd": ([P] * 8 + [I32] * 10 + [P, P, P, I32, P, SZ, P], I32),
+        "moe_grouped_ffn_fwd_adapter": ([P] * 4 + [I32] * 5 + [P] * 10 + [I32] * 3 + [P, P, P, P, SZ, P],
+                                        I32),
         "moe_adapter_rows": ([P, P, P, I32, I32, I32, I32, P, P], I32),
         "moe_profile_kernel": ([I32, ctypes.POINTER(P), ctypes.POINTER(P), I32], I32),
         "moe_profile_recorded": ([], I32),
@@ -688,6 +690,48 @@ def moe_adapter_rows(offsets: torch.Tensor, src_row: torch.Tensor, token_adapter
                                 n_adapters, R_cap, _into(o, "row_id", (R_cap,), i32, dev), _raw_stream(dev)),
            "moe_adapter_rows")
     return o["row_id"]
+
+
+def moe_grouped_ffn_fwd_adapter(x: torch.Tensor, src_row: Optional[torch.Tensor],
+                                offsets: torch.Tensor, row_id: torch.Tensor, w_gate: torch.Tensor,
+                                w_up: torch.Tensor, w_down: torch.Tensor,
+                                adapters: Dict[str, tuple], scale: Optional[torch.Tensor] = None,
+                                ws: Optional[torch.Tensor] = None,
+                                out: Optional[Dict[str, torch.Tensor]] = None):
+    """Grouped SwiGLU FFN forward with low-rank adapters on the expert projections.  x: the
+    grouped rows (src_row None) or, bf16, the token rows with moe_permute's src_row; row_id from
+    moe_adapter_rows; adapters: {"gate"|"up"|"down": (A, B)}, A [n_ids, rank, in] and B [n_ids,
+    out, rank] of one n_ids and rank.  Returns dict h_perm, y_perm, gu."""
+    dev = _device(x)
+    dt = _row_type(x, "x")
+    x_rows, H = _shape2(x, "x")
+    E_l, I = w_gate.shape[:2]
+    R_cap = row_id.numel()
+    i32 = torch.int32
+    unknown = set(adapters) - {"gate", "up", "down"}
+    if unknown or not adapters:
+        raise ValueError(f"adapters must name some of gate, up, down, got {sorted(adapters)}")
+    n_ids, rank = next(iter(adapters.values()))[0].shape[:2]
+    ab = []
+    for name, k, n in (("gate", H, I), ("up", H, I), ("down", I, H)):
+        pair = adapters.get(name)
+        ab += [None, None] if pair is None else [
+            _arg(pair[0], f"A of {name}", dt, (n_ids, rank, k), dev),
+            _arg(pair[1], f"B of {name}", dt, (n_ids, n, rank), dev)]
+    a = [_arg(x, "x", dt, (x_rows, H), dev), _arg(src_row, "src_row", i32, (R_cap,), dev, optional=True),
+         _arg(offsets, "offsets", i32, (E_l + 1,), dev), _arg(row_id, "row_id", i32, (R_cap,), dev)]
+    w = [_arg(w_gate, "w_gate", dt, (E_l, I, H), dev), _arg(w_up, "w_up", dt, (E_l, I, H), dev),
+         _arg(w_down, "w_down", dt, (E_l, H, I), dev)]
+    o = dict(out or {})
+    code = _dtype_code(x)
+    ws = _ws(workspace_bytes(MOE_OP_FFN_FWD, R_cap, H, I, E_l, 1, 0, E_l, code), dev, ws)
+    _check(lib.moe_grouped_ffn_fwd_adapter(
+        *a, E_l, R_cap, x_rows, H, I, *w, *ab,
+        _arg(scale, "scale", torch.float32, (n_ids,), dev, optional=True), n_ids, rank, code,
+        _into(o, "gu", (R_cap, 2 * I), dt, dev), _into(o, "h_perm", (R_cap, I), dt, dev),
+        _into(o, "y_perm", (R_cap, H), dt, dev), _ptr(ws), _nbytes(ws), _raw_stream(dev)),
+        "moe_grouped_ffn_fwd_adapter")
+    return o
 
 
 from .layer import MoELayer  # noqa: E402,F401

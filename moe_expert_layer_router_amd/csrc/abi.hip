@@ -1135,4 +1135,68 @@ int moe_adapter_rows(const int32_t* offsets, const int32_t* src_row, const int32
                     fn);
 }
 
+int moe_grouped_ffn_fwd_adapter(const void* x, const int32_t* src_row, const int32_t* offsets,
+                                const int32_t* row_id, int E_l, int R_cap, int x_rows, int H, int I,
+                                const void* w_gate, const void* w_up, const void* w_down,
+                                const void* a_gate, const void* b_gate, const void* a_up,
+                                const void* b_up, const void* a_down, const void* b_down,
+                                const float* scale, int n_ids, int rank, int dtype, void* gu,
+                                void* h_perm, void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_grouped_ffn_fwd_adapter";
+  if (int rc = check_dtype(dtype, fn)) return rc;
+  const bool bf16 = dtype == MOE_BF16;
+  if (int rc = check_ffn_shape(E_l, R_cap, H, I, dtype, fn)) return rc;
+  if (int rc = check_adapter(R_cap, H, I, n_ids, rank, dtype, 1 << 20, fn)) return rc;
+  if (src_row != nullptr && !bf16) return fail(MOE_EUNSUPPORTED, "%s: src_row is bf16 only", fn);
+  if (x_rows < 0 || (src_row == nullptr && x_rows != R_cap))
+    return fail(MOE_EINVAL, "%s: x_rows=%d (without src_row the R_cap=%d grouped rows)", fn, x_rows, R_cap);
+  if (bf16)
+    if (int rc = check_range((int64_t)x_rows * H * 2, "x", fn)) return rc;
+  if (int rc = check_ptr(offsets, "offsets", fn)) return rc;
+  if (int rc = check_ptr(w_gate, "w_gate", fn, true)) return rc;
+  if (int rc = check_ptr(w_up, "w_up", fn, true)) return rc;
+  if (int rc = check_ptr(w_down, "w_down", fn, true)) return rc;
+  const void* ab[3][2] = {{a_gate, b_gate}, {a_up, b_up}, {a_down, b_down}};
+  const char* names[3] = {"gate", "up", "down"};
+  for (int i = 0; i < 3; ++i) {
+    if ((ab[i][0] == nullptr) != (ab[i][1] == nullptr))
+      return fail(MOE_EINVAL, "%s: a_%s and b_%s must be given together", fn, names[i], names[i]);
+    if (!aligned16(ab[i][0]) || !aligned16(ab[i][1]))
+      return fail(MOE_EINVAL, "%s: a_%s and b_%s must be 16-byte aligned", fn, names[i], names[i]);
+  }
+  if (R_cap > 0) {
+    if (int rc = check_ptr(x, "x", fn, true)) return rc;
+    if (int rc = check_ptr(row_id, "row_id", fn)) return rc;
+    if (int rc = check_ptr(gu, "gu", fn, true)) return rc;
+    if (int rc = check_ptr(h_perm, "h_perm", fn, true)) return rc;
+    if (int rc = check_ptr(y_perm, "y_perm", fn, true)) return rc;
+  }
+  if (int rc = check_ws(ws, ws_bytes, ws_ffn_fwd(R_cap, E_l, dtype), fn)) return rc;
+  if (R_cap == 0) return MOE_OK;
+  hipStream_t s = begin_launch(stream);
+  auto ffn = [&](int products) {
+    return bf16 ? launch_ffn_fwd_bf16((const bf16_t*)x, offsets, E_l, R_cap, H, I,
+                                      (const bf16_t*)w_gate, (const bf16_t*)w_up,
+                                      (const bf16_t*)w_down, (bf16_t*)gu, (bf16_t*)h_perm,
+                                      (bf16_t*)y_perm, ws, s, src_row, x_rows, products)
+                : launch_ffn_fwd_f32((const float*)x, offsets, E_l, R_cap, H, I,
+                                     (const float*)w_gate, (const float*)w_up, (const float*)w_down,
+                                     (float*)gu, (float*)h_perm, (float*)y_perm, s, products);
+  };
+  hipError_t e = ffn(kFfnGateUp);
+  const AdapterShape in = {bf16, R_cap, x_rows, H, I, n_ids, rank, H, 2 * I};
+  char* u = (char*)gu + (size_t)I * elem_bytes(dtype);
+  if (e == hipSuccess && a_gate != nullptr)
+    e = launch_adapter_fwd(in, x, src_row, row_id, a_gate, b_gate, scale, gu, nullptr, s);
+  if (e == hipSuccess && a_up != nullptr)
+    e = launch_adapter_fwd(in, x, src_row, row_id, a_up, b_up, scale, u, nullptr, s);
+  if (e == hipSuccess && (a_gate != nullptr || a_up != nullptr))
+    e = launch_adapter_swiglu(gu, row_id, src_row, R_cap, x_rows, n_ids, I, bf16, h_perm, s);
+  if (e == hipSuccess) e = ffn(kFfnDown);
+  const AdapterShape out = {bf16, R_cap, R_cap, I, H, n_ids, rank, I, H};
+  if (e == hipSuccess && a_down != nullptr)
+    e = launch_adapter_fwd(out, h_perm, nullptr, row_id, a_down, b_down, scale, y_perm, nullptr, s);
+  return hip_status(e, fn);
+}
+
 }  // extern "C"

@@ -962,6 +962,33 @@ __global__ __launch_bounds__(256) void adapter_rows_kernel(const int32_t* __rest
   row_id[r] = id;
 }
 
+// h[r] = SiLU(g[r]) u[r] from the g, u that the adapters changed (bf16: the
+// stored, rounded ones); rows without an adapter keep the product's h.
+template <bool BF16>
+__global__ __launch_bounds__(256) void adapter_swiglu_kernel(const char* __restrict__ gu, RowIds ids,
+                                                             int I, char* __restrict__ h) {
+  using E = Elem<BF16>;
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= ids.R || ids(r) < 0) return;
+  const char* g = gu + (size_t)r * 2 * I * E::EB;
+  const char* u = g + (size_t)I * E::EB;
+  char* o = h + (size_t)r * I * E::EB;
+  auto act = [](float a, float b) { return a / (1.f + expf(-a)) * b; };
+  for (int c = lane_id() * 16; c < I * E::EB; c += kWave * 16) {
+    const u32x4_t a = load16(g + c), b = load16(u + c);
+    u32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BF16)
+        v[i] = pack_bf2(act(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16)),
+                        act(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u)));
+      else
+        v[i] = __float_as_uint(act(__uint_as_float(a[i]), __uint_as_float(b[i])));
+    }
+    *reinterpret_cast<u32x4_t*>(o + c) = v;
+  }
+}
+
 // Rows of a chunk: about 2048 workgroups of the weight gradients, in powers of
 // two between 128 rows (a workgroup's fixed cost) and what its LDS lists.
 int wgrad_chunk(int R, int K, int N) {
@@ -1007,6 +1034,17 @@ hipError_t launch_adapter_rows(const int32_t* offsets, const int32_t* src_row,
                                int R_cap, int32_t* row_id, hipStream_t s) {
   adapter_rows_kernel<<<(R_cap + 255) / 256, 256, 0, s>>>(offsets, src_row, token_adapter, E_l, T,
                                                           n_adapters, R_cap, row_id);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_swiglu(const void* gu, const int32_t* row_id, const int32_t* src_row,
+                                 int R, int x_rows, int n_ids, int I, bool bf16, void* h,
+                                 hipStream_t s) {
+  const RowIds ids = {row_id, src_row, R, x_rows, n_ids};
+  if (bf16)
+    adapter_swiglu_kernel<true><<<(R + 3) / 4, 256, 0, s>>>((const char*)gu, ids, I, (char*)h);
+  else
+    adapter_swiglu_kernel<false><<<(R + 3) / 4, 256, 0, s>>>((const char*)gu, ids, I, (char*)h);
   return hipGetLastError();
 }
 

@@ -219,6 +219,11 @@ struct AdapterShape {
 hipError_t launch_adapter_rows(const int32_t* offsets, const int32_t* src_row,
                                const int32_t* token_adapter, int E_l, int T, int n_adapters,
                                int R_cap, int32_t* row_id, hipStream_t s);
+// h = SiLU(g) u again on the rows that have an adapter (row_id in [0, n_ids),
+// src_row null or in [0, x_rows)), gu [R][2I], h [R][I]
+hipError_t launch_adapter_swiglu(const void* gu, const int32_t* row_id, const int32_t* src_row,
+                                 int R, int x_rows, int n_ids, int I, bool bf16, void* h,
+                                 hipStream_t s);
 hipError_t launch_adapter_fwd(const AdapterShape& d, const void* x, const int32_t* src_row,
                               const int32_t* row_id, const void* A, const void* B,
                               const float* scale, void* y, float* v, hipStream_t s);
@@ -238,11 +243,15 @@ size_t ffn_sched_bytes(int R_cap, int E_l);
 // The weight gradients' split plans and partial slots (FFN backward workspace).
 size_t ffn_wgrad_split_bytes(int E_l, int H, int I);
 // x_rows null: x_perm holds the grouped rows; else x_perm is the token matrix
-// x [T, H] and grouped row r is its row x_rows[r] (the permutation's src_row)
+// x [T, H] and grouped row r is its row x_rows[r] (the permutation's src_row).
+// products: both, or one of them (the down product finds the other's tile
+// schedule in ws).
+constexpr int kFfnGateUp = 1, kFfnDown = 2;
 hipError_t launch_ffn_fwd_bf16(const bf16_t* x_perm, const int32_t* offsets, int E_l, int R_cap,
                                int H, int I, const bf16_t* w_gate, const bf16_t* w_up,
                                const bf16_t* w_down, bf16_t* gu, bf16_t* h_perm, bf16_t* y_perm,
-                               void* ws, hipStream_t s, const int32_t* x_rows = nullptr, int T = 0);
+                               void* ws, hipStream_t s, const int32_t* x_rows = nullptr, int T = 0,
+                               int products = kFfnGateUp | kFfnDown);
 // The same with the tile table in the library's static per-GPU scratch (no
 // workspace argument); R_cap <= kNoAllocMaxRows.
 constexpr int kNoAllocMaxRows = 1 << 20;
@@ -338,7 +347,7 @@ hipError_t launch_router_dx(const bf16_t* dz_hilo, const bf16_t* w_router, int T
 hipError_t launch_ffn_fwd_f32(const float* x_perm, const int32_t* offsets, int E_l, int R_cap,
                               int H, int I, const float* w_gate, const float* w_up,
                               const float* w_down, float* gu, float* h_perm, float* y_perm,
-                              hipStream_t s);
+                              hipStream_t s, int products = kFfnGateUp | kFfnDown);
 hipError_t launch_ffn_bwd_f32(const float* dy_perm, const float* x_perm, const float* gu,
                               const float* h_perm, const int32_t* offsets, int E_l, int R_cap,
                               int H, int I, const float* w_gate, const float* w_up,

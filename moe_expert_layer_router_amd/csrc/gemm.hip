@@ -2010,12 +2010,16 @@ static hipError_t launch_gemm(const GemmArgs& a, int work_upper, int kernel_id, 
 hipError_t launch_ffn_fwd_bf16(const bf16_t* x_perm, const int32_t* offsets, int E_l, int R_cap,
                                int H, int I, const bf16_t* w_gate, const bf16_t* w_up,
                                const bf16_t* w_down, bf16_t* gu, bf16_t* h_perm, bf16_t* y_perm,
-                               void* ws, hipStream_t s, const int32_t* x_rows, int T) {
+                               void* ws, hipStream_t s, const int32_t* x_rows, int T,
+                               int products) {
   int32_t* sched = (int32_t*)ws;
-  ffn_sched_kernel<<<1, kMaxE, 0, s>>>(offsets, E_l, kBmGrouped, sched, nullptr);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+  hipError_t err;
   const int mt_upper = R_cap / kBmGrouped + E_l;
+  if (products & kFfnGateUp) {
+    ffn_sched_kernel<<<1, kMaxE, 0, s>>>(offsets, E_l, kBmGrouped, sched, nullptr);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
 
   GemmArgs g{};
   g.a = x_perm;
@@ -2034,8 +2038,11 @@ hipError_t launch_ffn_fwd_bf16(const bf16_t* x_perm, const int32_t* offsets, int
   g.c0 = h_perm;
   g.ldc = I;
   g.c1 = gu;
-  err = launch_gemm<K_GATEUP_FWD, kBmGrouped, false, kWideGrouped>(g, mt_upper * g.n_ntiles, MOE_KERNEL_FFN_GATEUP, s);
-  if (err != hipSuccess) return err;
+  if (products & kFfnGateUp) {
+    err = launch_gemm<K_GATEUP_FWD, kBmGrouped, false, kWideGrouped>(g, mt_upper * g.n_ntiles, MOE_KERNEL_FFN_GATEUP, s);
+    if (err != hipSuccess) return err;
+  }
+  if (!(products & kFfnDown)) return hipSuccess;
 
   GemmArgs d{};
   d.a = h_perm;

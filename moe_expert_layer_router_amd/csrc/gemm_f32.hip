@@ -108,15 +108,15 @@ static inline unsigned nblocks(long n) { return (unsigned)((n + 255) / 256); }
 hipError_t launch_ffn_fwd_f32(const float* x_perm, const int32_t* offsets, int E_l, int R_cap,
                               int H, int I, const float* w_gate, const float* w_up,
                               const float* w_down, float* gu, float* h_perm, float* y_perm,
-                              hipStream_t s) {
-  {
+                              hipStream_t s, int products) {
+  if (products & kFfnGateUp) {
     ProfScope ps(MOE_KERNEL_FFN_GATEUP, s);
     gateup_f32_kernel<<<nblocks((long)R_cap * I), 256, 0, s>>>(x_perm, offsets, E_l, R_cap, H, I,
                                                              w_gate, w_up, gu, h_perm);
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  {
+  if (products & kFfnDown) {
     ProfScope ps(MOE_KERNEL_FFN_DOWN, s);
     down_f32_kernel<<<nblocks((long)R_cap * H), 256, 0, s>>>(h_perm, offsets, E_l, R_cap, H, I,
                                                            w_down, y_perm);

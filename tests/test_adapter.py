@@ -387,3 +387,25 @@ def test_binding_refusals():
         moe.moe_adapter_fwd(**{**a, "y": torch.zeros(20, 73, dtype=torch.bfloat16, device=DEV)[:, :72]})
     with pytest.raises(moe.MoEError, match="rank"):
         moe.moe_adapter_fwd(s["x"], s["ids"], s["A"][:, :12].contiguous(), s["B"][..., :12].contiguous(), s["y"])
+
+
+def test_ffn_adapter_refusals():
+    f = L.moe_grouped_ffn_fwd_adapter
+    ok = [A, N, A, A, 4, 16, 16, 64, 64, A, A, A, A, A, N, N, A, A, N, 8, 16, BF16, A, A, A, A, 1 << 30, STREAM]
+
+    def call(**kw):
+        a = list(ok)
+        for i, v in kw.items():
+            a[int(i[1:])] = v
+        return f(*a)
+
+    assert call(_6=15) == EINVAL and "x_rows" in _err()
+    assert call(_1=A, _21=F32) == EUNSUP and "bf16 only" in _err()
+    assert call(_7=96) == EUNSUP and call(_20=20) == EUNSUP and call(_19=0) == EINVAL
+    assert call(_13=N) == EINVAL and "together" in _err()
+    assert call(_12=U) == EINVAL and "aligned" in _err()
+    for i, name in ((0, "x"), (2, "offsets"), (3, "row_id"), (9, "w_gate"), (10, "w_up"), (11, "w_down"),
+                    (22, "gu"), (23, "h_perm"), (24, "y_perm")):
+        assert call(**{f"_{i}": N}) == EINVAL and name in _err()
+    assert call(_25=N) == EWS and call(_26=16) == EWS
+    assert call(_5=0, _6=0, _0=N, _3=N, _22=N, _23=N, _24=N) == OK
