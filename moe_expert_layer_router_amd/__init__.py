@@ -599,6 +599,8 @@ def moe_combine_dropout_bwd(dy: torch.Tensor, y_perm: torch.Tensor, topk_w: torc
 
 def _rows_arg(t: torch.Tensor, name: str, dtype, rows: int, cols: int, dev):
     """(pointer, row pitch) of a matrix whose rows are dense, at any pitch."""
+    if t.dtype is dtype and t.shape == (rows, cols) and t.device == dev and t.is_contiguous():
+        return t.data_ptr(), cols
     if t.dtype != dtype or t.shape != (rows, cols) or t.device != dev:
         raise ValueError(f"{name} must be {dtype} [{rows}, {cols}] on {dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -609,6 +611,28 @@ def _rows_arg(t: torch.Tensor, name: str, dtype, rows: int, cols: int, dev):
 
 
 def _adapter_args(x, row_id, A, B, scale, src_row):
+    """Checked arguments that moe_adapter_fwd and _bwd share.  One expression holds every
+    condition (a decode step's call takes about as long as its kernel); where it fails, the
+    checks one by one name the argument."""
+    d, dt, i32 = row_id.get_device(), A.dtype, torch.int32
+    if A.dim() == 3 and B.dim() == 3 and x.dim() == 2:
+        n_ids, rank, K = A.shape
+        N, R, x_rows = B.shape[1], row_id.numel(), x.shape[0]
+        if (d >= 0 and d == torch._C._cuda_getDevice()
+                and (dt is torch.bfloat16 or dt is torch.float32)
+                and A.get_device() == d and A.is_contiguous()
+                and B.dtype is dt and B.get_device() == d and B.shape == (n_ids, N, rank)
+                and B.is_contiguous()
+                and row_id.dtype is i32 and row_id.dim() == 1 and row_id.is_contiguous()
+                and x.dtype is dt and x.get_device() == d and x.shape[1] == K and x.is_contiguous()
+                and (scale is None or scale.dtype is torch.float32 and scale.get_device() == d
+                     and scale.shape == (n_ids,) and scale.is_contiguous())
+                and (x_rows == R if src_row is None else
+                     src_row.dtype is i32 and src_row.get_device() == d
+                     and src_row.shape == (R,) and src_row.is_contiguous())):
+            return (row_id.device, dt, n_ids, rank, K, N, R, x_rows, x.data_ptr(), K,
+                    (None if src_row is None else src_row.data_ptr(), row_id.data_ptr(),
+                     A.data_ptr(), B.data_ptr()), None if scale is None else scale.data_ptr())
     dev = _device(row_id)
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be [n_ids, rank, K] and B [n_ids, N, rank]")
@@ -618,7 +642,6 @@ def _adapter_args(x, row_id, A, B, scale, src_row):
     x_rows = _shape2(x, "x")[0]
     if src_row is None and x_rows != R:
         raise ValueError(f"x has {x_rows} rows, row_id {R} (src_row maps one to the other)")
-    i32 = torch.int32
     ptrs = (_arg(src_row, "src_row", i32, (R,), dev, optional=True), _arg(row_id, "row_id", i32, (R,), dev),
             _arg(A, "A", dt, (n_ids, rank, K), dev), _arg(B, "B", dt, (n_ids, N, rank), dev))
     sc = _arg(scale, "scale", torch.float32, (n_ids,), dev, optional=True)
@@ -637,11 +660,16 @@ def moe_adapter_fwd(x: torch.Tensor, row_id: torch.Tensor, A: torch.Tensor, B: t
     dev, dt, n_ids, rank, K, N, R, x_rows, xp, ldx, (src, ids, a, b), sc = \
         _adapter_args(x, row_id, A, B, scale, src_row)
     yp, ldy = _rows_arg(y, "y", dt, R, N, dev)
-    o = {"v": out}
-    v = _into(o, "v", (R, rank), torch.float32, dev) if want_v else None
-    _check(lib.moe_adapter_fwd(xp, src, ids, a, b, sc, R, x_rows, K, N, ldx, ldy, n_ids, rank,
-                               _dtype_code(A), yp, v, _raw_stream(dev)), "moe_adapter_fwd")
-    return o["v"] if want_v else None
+    v = None
+    if want_v:
+        if out is None:
+            out = torch.empty((R, rank), dtype=torch.float32, device=dev)
+        v = _arg(out, "out", torch.float32, (R, rank), dev)
+    rc = lib.moe_adapter_fwd(xp, src, ids, a, b, sc, R, x_rows, K, N, ldx, ldy, n_ids, rank,
+                             MOE_BF16 if dt is torch.bfloat16 else MOE_F32, yp, v, _raw_stream(dev))
+    if rc != 0:
+        _check(rc, "moe_adapter_fwd")
+    return out if want_v else None
 
 
 def moe_adapter_bwd(dy: torch.Tensor, x: torch.Tensor, row_id: torch.Tensor, A: torch.Tensor,

@@ -225,6 +225,8 @@ CASES = [  # dtype, R, K, N, n_ids, rank, order, gather, pitch, scaled
     ("bf16", 20000, 64, 72, 3, 32, "range", False, 0, True), ("bf16", 33000, 64, 64, 2, 16, "one", True, 0, True),
     ("f32", 20001, 64, 40, 6, 8, "sorted", False, 0, True), ("bf16", 17000, 96, 64, 5, 120, "sorted", False, 0, True),
     ("f32", 33333, 32, 36, 256, 16, "mixed", False, 0, True), ("bf16", 40000, 200, 128, 8, 64, "mixed", False, 0, True),
+    ("bf16", 3000, 64, 72, 255, 16, "mixed", True, 0, True), ("bf16", 9001, 72, 136, 40, 128, "mixed", False, 0, True),
+    ("f32", 1800, 40, 36, 100, 120, "mixed", True, 0, True),
 ]
 
 
@@ -261,6 +263,19 @@ def test_one_request_never_reaches_another():
     for n in ("dA", "dB"):
         for a in (0, 1, 3):
             assert torch.equal(got[n][a], clean[n][a])
+
+
+@gpu
+@pytest.mark.parametrize("dtype,rank", [("bf16", 16), ("f32", 16), ("bf16", 72)])
+def test_row_order_changes_no_bit(dtype, rank):
+    """Rows sorted by adapter, and the same rows mixed (which are regrouped)."""
+    s = make(dtype, 4000, 136, 200, 37, rank, "sorted", False, 12)
+    perm = torch.randperm(4000, device=DEV)
+    y = s["y"][perm].contiguous()
+    v = moe.moe_adapter_fwd(s["x"], s["ids"], s["A"], s["B"], s["y"], scale=s["scale"], want_v=True)
+    w = moe.moe_adapter_fwd(s["x"][perm].contiguous(), s["ids"][perm].contiguous(), s["A"], s["B"], y,
+                            scale=s["scale"], want_v=True)
+    assert torch.equal(s["y"][perm], y) and torch.equal(v[perm], w)
 
 
 @gpu
