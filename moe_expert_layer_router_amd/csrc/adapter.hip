@@ -94,97 +94,87 @@ constexpr int kWindow = 512;      // rows regrouped together
 constexpr int kWindowKeys = 256;  // adapters (at most 255) and the rows without one
 
 // Rows in mixed order: every adapter among a workgroup's rows is a pass of its
-// own, so 16 rows of 16 adapters cost 16 passes.  The workgroups of `window`
-// rows each look at the adapters of all of them and, where runs of one adapter
-// are shorter than 8 rows on average, share the rows out sorted by adapter (a
-// stable counting sort in LDS, the same in every workgroup).  Which workgroup
-// takes a row changes no bit of its result.  Returns whether lane i < p.rows
-// got another row than row0 + i.  8191 rows of 64 adapters, mixed: 75 us
-// without; sorted rows pay one LDS round.
+// own, so 16 rows of 16 adapters cost 16 passes.  Where 64 neighbours sampled
+// from a window of rows say that runs of one adapter are shorter than 8 rows on
+// average (mixed_rows: every wave asks the same 128 rows, so all workgroups of
+// the window agree), the window's workgroups share its rows out sorted by
+// adapter, by a stable counting sort in LDS that each of them does alike.
+// Which workgroup takes a row changes no bit of its result.  8191 rows of 64
+// adapters, mixed: 39 us, 75 without.
+__device__ __forceinline__ bool mixed_rows(const AdapterArgs& p, int row0) {
+  const int r = min(row0 / kWindow * kWindow + kWindow / kWave * lane_id(), p.R - 1);
+  return __popcll(__ballot(p.row_id[r] != p.row_id[min(r + 1, p.R - 1)])) > kWave / 8;
+}
+
 template <int NW>
-__device__ __forceinline__ bool regroup(const AdapterArgs& p, int row0, char* lds, int& row) {
+__device__ __forceinline__ void regroup(const AdapterArgs& p, int row0, char* lds, int& row) {
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int base = row0 / kWindow * kWindow;
   constexpr int Q = kWindow / NW;  // rows of a wave
   uint16_t* s_ord = reinterpret_cast<uint16_t*>(lds);
   int* s_cur = reinterpret_cast<int*>(lds + 2 * kWindow);  // [NW][kWindowKeys]
-  int* s_runs = s_cur + NW * kWindowKeys;
-  int key[Q / kWave], runs = 0;
+  int key[Q / kWave];
 #pragma unroll
   for (int j = 0; j < Q / kWave; ++j) {
     const int r = base + wave * Q + j * kWave + lane;
     const int a = r < p.R ? p.row_id[r] : -1;
     key[j] = a >= 0 && a < p.n_ids ? a : kWindowKeys - 1;
   }
+  for (int i = threadIdx.x; i < NW * kWindowKeys; i += NW * kWave) s_cur[i] = 0;
+  lds_barrier();
+#pragma unroll
+  for (int j = 0; j < Q / kWave; ++j) atomicAdd(&s_cur[wave * kWindowKeys + key[j]], 1);
+  lds_barrier();
+  if (wave == 0) {  // counts to cursors, by key and then by wave
+    constexpr int KL = kWindowKeys / kWave;
+    int n[KL], sum = 0;
+#pragma unroll
+    for (int i = 0; i < KL; ++i) {
+      n[i] = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) n[i] += s_cur[w * kWindowKeys + KL * lane + i];
+      sum += n[i];
+    }
+    int end = sum;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int x = __shfl_up(end, o, kWave);
+      end += lane >= o ? x : 0;
+    }
+    int at = end - sum;
+#pragma unroll
+    for (int i = 0; i < KL; ++i)
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        int* c = &s_cur[w * kWindowKeys + KL * lane + i];
+        const int m = *c;
+        *c = at;
+        at += m;
+      }
+  }
+  lds_barrier();
 #pragma unroll
   for (int j = 0; j < Q / kWave; ++j) {
-    const int before = __shfl_up(key[j], 1, kWave);
-    runs += __popcll(__ballot(lane > 0 && key[j] != before));
+    int rank = 0, same_n = 0;
+    for (uint64_t todo = ~0ull; todo != 0;) {
+      const int cur = __builtin_amdgcn_readlane(key[j], __builtin_ctzll(todo));
+      const uint64_t same = __ballot(key[j] == cur);
+      todo &= ~same;
+      if (key[j] == cur) {
+        rank = __popcll(same & ((1ull << lane) - 1ull));
+        same_n = __popcll(same);
+      }
+    }
+    int* c = &s_cur[wave * kWindowKeys + key[j]];
+    const int from = *c;
+    asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
+    s_ord[from + rank] = (uint16_t)(wave * Q + j * kWave + lane);
+    if (rank == 0) *c = from + same_n;
+    asm volatile("" ::: "memory");
   }
-  if (lane == 0) s_runs[wave] = runs;
   lds_barrier();
-  int all = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) all += s_runs[w];
-  const bool mixed = all > kWindow / 8;
-  if (mixed) {
-    for (int i = threadIdx.x; i < NW * kWindowKeys; i += NW * kWave) s_cur[i] = 0;
-    lds_barrier();
-#pragma unroll
-    for (int j = 0; j < Q / kWave; ++j) atomicAdd(&s_cur[wave * kWindowKeys + key[j]], 1);
-    lds_barrier();
-    if (wave == 0) {  // counts to cursors, by key and then by wave
-      constexpr int KL = kWindowKeys / kWave;
-      int n[KL], sum = 0;
-#pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        n[i] = 0;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) n[i] += s_cur[w * kWindowKeys + KL * lane + i];
-        sum += n[i];
-      }
-      int end = sum;
-#pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const int x = __shfl_up(end, o, kWave);
-        end += lane >= o ? x : 0;
-      }
-      int at = end - sum;
-#pragma unroll
-      for (int i = 0; i < KL; ++i)
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          int* c = &s_cur[w * kWindowKeys + KL * lane + i];
-          const int m = *c;
-          *c = at;
-          at += m;
-        }
-    }
-    lds_barrier();
-#pragma unroll
-    for (int j = 0; j < Q / kWave; ++j) {
-      int rank = 0, same_n = 0;
-      for (uint64_t todo = ~0ull; todo != 0;) {
-        const int cur = __builtin_amdgcn_readlane(key[j], __builtin_ctzll(todo));
-        const uint64_t same = __ballot(key[j] == cur);
-        todo &= ~same;
-        if (key[j] == cur) {
-          rank = __popcll(same & ((1ull << lane) - 1ull));
-          same_n = __popcll(same);
-        }
-      }
-      int* c = &s_cur[wave * kWindowKeys + key[j]];
-      const int from = *c;
-      asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
-      s_ord[from + rank] = (uint16_t)(wave * Q + j * kWave + lane);
-      if (rank == 0) *c = from + same_n;
-      asm volatile("" ::: "memory");
-    }
-    lds_barrier();
-    if (lane < p.rows) row = base + s_ord[row0 - base + lane];
-  }
+  if (lane < p.rows) row = base + s_ord[row0 - base + lane];
   lds_barrier();  // read by all before the LDS is used otherwise
-  return mixed;
 }
 
 // A workgroup of NW waves takes `rows` <= 16 MT rows and one of `splits`
@@ -226,7 +216,10 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
     xr = p.src_row != nullptr ? p.src_row[row] : row;
   };
   look();
-  if (p.window && regroup<NW>(p, row0, lds, row)) look();
+  if (p.window && mixed_rows(p, row0)) {
+    regroup<NW>(p, row0, lds, row);
+    look();
+  }
   if (id < 0 || id >= p.n_ids || xr < 0 || xr >= p.x_rows) id = -1;
   if (!p.gather) xr = row;
   if (id >= 0 && p.scale != nullptr) scale = p.scale[id];
@@ -722,6 +715,21 @@ __global__ __launch_bounds__(256) void adapter_prepare_kernel(const char* __rest
   }
 }
 
+// Inclusive prefix sum over the 256 threads of a workgroup (s: 4 words).
+__device__ __forceinline__ int block_scan(int v, int* s) {
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int x = __shfl_up(v, o, kWave);
+    v += lane >= o ? x : 0;
+  }
+  if (lane == kWave - 1) s[wave] = v;
+  lds_barrier();
+#pragma unroll
+  for (int w = 0; w < 3; ++w) v += w < wave ? s[w] : 0;
+  return v;
+}
+
 // The rows in adapter order, rows of one adapter in row order: every block adds
 // the counts of the blocks before it (and all, for the adapters' offsets), its
 // four waves take a quarter of its rows each, 64 at a time, and a row's place
@@ -731,7 +739,7 @@ __global__ __launch_bounds__(256) void adapter_order_kernel(RowIds ids, int per,
                                                             const int32_t* __restrict__ counts,
                                                             int chunk, ChunkPlan plan,
                                                             int32_t* __restrict__ order) {
-  __shared__ int s_cur[4][kMaxE], s_t[kMaxE], s_m[kMaxE];
+  __shared__ int s_cur[4][kMaxE], s_t[4], s_n[4], s_m[4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = lane_id();
   const int b = blockIdx.x;
   int before = 0, all = 0;
@@ -745,7 +753,6 @@ __global__ __launch_bounds__(256) void adapter_order_kernel(RowIds ids, int per,
   }
 #pragma unroll
   for (int w = 0; w < 4; ++w) s_cur[w][tid] = 0;
-  s_t[tid] = all;
   __syncthreads();
   const int q = (per + 3) / 4;  // rows of a wave
   const int r0 = b * per + wave * q, r1 = min(min(ids.R, (b + 1) * per), r0 + q);
@@ -753,13 +760,7 @@ __global__ __launch_bounds__(256) void adapter_order_kernel(RowIds ids, int per,
     const int a = ids(r);
     if (a >= 0) atomicAdd(&s_cur[wave][a], 1);
   }
-  for (int o = 1; o < kMaxE; o <<= 1) {  // totals to ends
-    const int x = tid >= o ? s_t[tid - o] : 0;
-    __syncthreads();
-    s_t[tid] += x;
-    __syncthreads();
-  }
-  const int end = s_t[tid], begin = end - all;
+  const int end = block_scan(all, s_t), begin = end - all;
   int at = begin + before;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {  // counts of the waves to their cursors
@@ -793,25 +794,15 @@ __global__ __launch_bounds__(256) void adapter_order_kernel(RowIds ids, int per,
   // the chunks, and the slots of adapters of several
   const int n = tid < ids.n_ids ? max(1, (all + chunk - 1) / chunk) : 0;
   const int m = n > 1 ? n : 0;
-  __syncthreads();
-  s_t[tid] = n;
-  s_m[tid] = m;
-  __syncthreads();
-  for (int o = 1; o < kMaxE; o <<= 1) {
-    const int x = tid >= o ? s_t[tid - o] : 0, y = tid >= o ? s_m[tid - o] : 0;
-    __syncthreads();
-    s_t[tid] += x;
-    s_m[tid] += y;
-    __syncthreads();
-  }
-  if (tid == kMaxE - 1) *plan.count = s_t[tid];
+  const int n_end = block_scan(n, s_n), m_end = block_scan(m, s_m);
+  if (tid == kMaxE - 1) *plan.count = n_end;
   if (tid >= ids.n_ids) return;
   plan.offsets[tid] = begin;
   if (tid == ids.n_ids - 1) plan.offsets[tid + 1] = end;
-  const int slot = s_m[tid] - m;
+  const int slot = m_end - m;
   plan.first[tid] = slot;
   for (int c = 0; c < n; ++c) {
-    int32_t* e = plan.chunks + 4 * (size_t)(s_t[tid] - n + c);
+    int32_t* e = plan.chunks + 4 * (size_t)(n_end - n + c);
     e[0] = tid;
     e[1] = begin + c * chunk;
     e[2] = min(end, begin + (c + 1) * chunk);
