@@ -431,7 +431,7 @@ def _device(t: torch.Tensor) -> torch.device:
     stream the call is enqueued on)."""
     if not t.is_cuda:
         raise ValueError(f"expected tensors on a GPU, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {t.device} while cuda:{torch.cuda.current_device()} is the "
                          f"current device")
     return t.device
@@ -565,15 +565,18 @@ def moe_combine_dropout(y_perm: torch.Tensor, topk_w: Optional[torch.Tensor], de
     if T < 0 or dest_row.numel() % max(T, 1):
         raise ValueError(f"dest_row has {dest_row.numel()} entries, not a multiple of T = {T}")
     k = dest_row.numel() // T if T > 0 else 1
-    o = {"y": out}
-    a = [_arg(y_perm, "y_perm", dt, (R_cap, H), dev),
-         _arg(topk_w, "topk_w", torch.float32, (T, k), dev, optional=True),
-         _arg(dest_row, "dest_row", torch.int32, (T * k,), dev),
-         _arg(residual, "residual", dt, (T, H), dev, optional=True)]
-    _check(lib.moe_combine_dropout(*a, p, _arg(rng, "rng", torch.int64, (2,), dev), T, H, k,
-                                   _dtype_code(y_perm), _into(o, "y", (T, H), dt, dev), _raw_stream(dev)),
-           "moe_combine_dropout")
-    return o["y"]
+    if out is None:
+        out = torch.empty((T, H), dtype=dt, device=dev)
+    rc = lib.moe_combine_dropout(
+        _arg(y_perm, "y_perm", dt, (R_cap, H), dev),
+        None if topk_w is None else _arg(topk_w, "topk_w", torch.float32, (T, k), dev),
+        _arg(dest_row, "dest_row", torch.int32, (T * k,), dev),
+        None if residual is None else _arg(residual, "residual", dt, (T, H), dev), p,
+        _arg(rng, "rng", torch.int64, (2,), dev), T, H, k,
+        MOE_BF16 if dt is torch.bfloat16 else MOE_F32, _arg(out, "out", dt, (T, H), dev), _raw_stream(dev))
+    if rc != 0:
+        _check(rc, "moe_combine_dropout")
+    return out
 
 
 def moe_combine_dropout_bwd(dy: torch.Tensor, y_perm: torch.Tensor, topk_w: torch.Tensor,

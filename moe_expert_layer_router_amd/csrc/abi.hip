@@ -919,8 +919,18 @@ int moe_route_bwd_add(const float* d_topk_w, const float* topk_w, const int32_t*
 }
 
 namespace {
+// Row counts of the operators around the layer: their kernels step past the
+// last row by less than this before they stop.
+constexpr int kMaxRows = 0x7fff0000;
+int check_rows(int rows, const char* name, const char* fn) {
+  if (rows < 0) return fail(MOE_EINVAL, "%s: %s must be >= 0 (got %d)", fn, name, rows);
+  if (rows > kMaxRows) return fail(MOE_EUNSUPPORTED, "%s: %s=%d above %d", fn, name, rows, kMaxRows);
+  return MOE_OK;
+}
+
 int check_balance(int T, int E, int k, int S, const int32_t* seq_offsets, const char* fn) {
   if (int rc = check_routing_shape(T, E, k, fn)) return rc;
+  if (int rc = check_rows(T, "T", fn)) return rc;
   if (S < 1 || S > (1 << 20)) return fail(MOE_EINVAL, "%s: S=%d outside [1, 2^20]", fn, S);
   if (seq_offsets == nullptr && S != 1)
     return fail(MOE_EINVAL, "%s: S=%d sequences need seq_offsets", fn, S);
@@ -930,9 +940,10 @@ int check_balance(int T, int E, int k, int S, const int32_t* seq_offsets, const 
 
 int64_t moe_balance_ws_bytes(int T, int E, int S) {
   const char* fn = "moe_balance_ws_bytes";
-  if (T < 0 || E < 1 || E > kMaxE || S < 1 || S > (1 << 20))
-    return fail(MOE_EINVAL, "%s: need T >= 0, E in [1, %d] and S in [1, 2^20] (T=%d, E=%d, S=%d)",
-                fn, kMaxE, T, E, S);
+  if (int rc = check_rows(T, "T", fn)) return rc;
+  if (E < 1 || E > kMaxE || S < 1 || S > (1 << 20))
+    return fail(MOE_EINVAL, "%s: need E in [1, %d] and S in [1, 2^20] (E=%d, S=%d)", fn,
+                kMaxE, E, S);
   return (int64_t)balance_ws_bytes(T, E, S);
 }
 
@@ -981,7 +992,7 @@ int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* c
 namespace {
 int check_dropout(double p, const uint64_t* rng, int T, int H, int k, int dtype, const char* fn) {
   if (int rc = check_dtype(dtype, fn)) return rc;
-  if (T < 0) return fail(MOE_EINVAL, "%s: T must be >= 0", fn);
+  if (int rc = check_rows(T, "T", fn)) return rc;
   if (k < 1 || k > kMaxK) return fail(MOE_EINVAL, "%s: k=%d outside [1, %d]", fn, k, kMaxK);
   if (int rc = check_row_width(H, dtype, fn)) return rc;
   if (!(p >= 0.0 && p < 1.0)) return fail(MOE_EINVAL, "%s: p=%g outside [0, 1)", fn, p);
@@ -1031,7 +1042,7 @@ constexpr int kAdapterMaxWidth = 1 << 20;
 
 int check_adapter(int R, int K, int N, int n_ids, int rank, int dtype, int most_ids, const char* fn) {
   if (int rc = check_dtype(dtype, fn)) return rc;
-  if (R < 0) return fail(MOE_EINVAL, "%s: R must be >= 0 (got %d)", fn, R);
+  if (int rc = check_rows(R, "R", fn)) return rc;
   const int q = dtype == MOE_BF16 ? 8 : 4;
   if (K <= 0 || N <= 0 || K % q != 0 || N % q != 0)
     return fail(MOE_EINVAL, "%s: K=%d and N=%d must be positive multiples of %d for this dtype", fn, K, N, q);
@@ -1121,7 +1132,8 @@ int moe_adapter_rows(const int32_t* offsets, const int32_t* src_row, const int32
                      int E_l, int T, int n_adapters, int R_cap, int32_t* row_id, void* stream) {
   const char* fn = "moe_adapter_rows";
   if (E_l < 1 || E_l > kMaxE) return fail(MOE_EINVAL, "%s: E_l=%d outside [1, %d]", fn, E_l, kMaxE);
-  if (T < 0 || R_cap < 0) return fail(MOE_EINVAL, "%s: T and R_cap must be >= 0", fn);
+  if (T < 0) return fail(MOE_EINVAL, "%s: T must be >= 0", fn);
+  if (int rc = check_rows(R_cap, "R_cap", fn)) return rc;
   if (n_adapters < 0 || (long long)n_adapters * E_l > 0x7fffffffLL)
     return fail(MOE_EINVAL, "%s: n_adapters=%d is negative, or n_adapters * E_l overflows int32", fn,
                 n_adapters);

@@ -102,6 +102,7 @@ class MoELayer:
         b["h_perm"] = torch.empty((R, I), dtype=dtype, device=dev)
         b["y_perm"] = torch.empty((R, H), dtype=dtype, device=dev)
         b["gu"] = torch.empty((R, 2 * I), dtype=dtype, device=dev) if train or adapters else None
+        b["no_rng"] = torch.zeros(2, dtype=torch.int64, device=dev)
         if adapters:
             b["row_id"] = torch.empty(R, dtype=i32, device=dev)
         if self.aux:
@@ -215,7 +216,7 @@ class MoELayer:
         self._drop = None
         if self.dropout > 0.0 or residual is not None:
             if rng is None:  # no dropout: the numbers do not matter
-                rng = b.setdefault("no_rng", torch.zeros(2, dtype=torch.int64, device=x.device))
+                rng = b["no_rng"]
             self._drop = rng if self.dropout > 0.0 else None
             moe_combine_dropout(b["y_perm"], b["topk_w"], b["dest_row"], T, self.dropout, rng,
                                 residual=residual, out=b["y"])

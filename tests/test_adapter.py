@@ -148,6 +148,7 @@ def test_refusals():
         return f(*a)
 
     assert fwd(_6=-1) == EINVAL and fwd(_7=-1) == EINVAL
+    assert fwd(_6=2 ** 31 - 1, _7=2 ** 31 - 1) == EUNSUP
     assert fwd(_8=0) == EINVAL and fwd(_8=60) == EINVAL and fwd(_9=63) == EINVAL
     assert fwd(_10=56) == EINVAL and "ldx" in _err()
     assert fwd(_10=65) == EINVAL and fwd(_11=60) == EINVAL and "ldy" in _err()

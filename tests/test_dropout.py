@@ -62,6 +62,7 @@ def test_refusals():
     assert f(A, A, A, N, 0.1, rng, 8, 68, 2, BF16, A, STREAM) == EINVAL
     assert f(A, A, A, N, 0.1, rng, 8, 64, 33, F32, A, STREAM) == EINVAL
     assert f(A, A, A, N, 0.1, rng, -8, 64, 2, F32, A, STREAM) == EINVAL
+    assert f(A, A, A, N, 0.1, rng, 2 ** 31 - 1, 64, 1, F32, A, STREAM) == -2
     assert f(A, A, A, N, 0.1, rng, 8, 64, 2, 7, A, STREAM) == EINVAL
     assert f(N, N, N, N, 0.1, N, 0, 64, 2, F32, N, STREAM) == OK
     g = L.moe_combine_dropout_bwd
