@@ -930,7 +930,8 @@ int check_rows(int rows, const char* name, const char* fn) {
 
 int check_balance(int T, int E, int k, int S, const int32_t* seq_offsets, const char* fn) {
   if (int rc = check_routing_shape(T, E, k, fn)) return rc;
-  if (int rc = check_rows(T, "T", fn)) return rc;
+  if ((long long)T * k > kMaxRows)
+    return fail(MOE_EUNSUPPORTED, "%s: T * k = %lld above %d", fn, (long long)T * k, kMaxRows);
   if (S < 1 || S > (1 << 20)) return fail(MOE_EINVAL, "%s: S=%d outside [1, 2^20]", fn, S);
   if (seq_offsets == nullptr && S != 1)
     return fail(MOE_EINVAL, "%s: S=%d sequences need seq_offsets", fn, S);

@@ -102,6 +102,7 @@ def test_refusals():
         return f(*a)
 
     assert call(_4=-1) == EINVAL
+    assert call(_4=2 ** 26 - 1, _5=64, _6=32) == -2 and "T * k" in _err()
     assert call(_4=2 ** 31 - 1, _5=1, _6=1) == -2 and L.moe_balance_ws_bytes(2 ** 31 - 1, 1, 1) == -2
     assert call(_5=257) == EINVAL and call(_5=0) == EINVAL
     assert call(_6=0) == EINVAL and call(_6=9) == EINVAL
