@@ -64,7 +64,7 @@ __device__ __forceinline__ u32x4_t keep_mask(uint32_t bits) {
   return m;
 }
 
-template <bool BF16>
+template <bool BF16, int CU, int SG>
 __global__ __launch_bounds__(256) void combine_dropout_kernel(
     const void* __restrict__ y_perm, const float* __restrict__ topk_w,
     const int32_t* __restrict__ dest_row, const void* residual,
@@ -84,21 +84,22 @@ __global__ __launch_bounds__(256) void combine_dropout_kernel(
   float wc;
   const int n = pack_slots(d, w, dc, wc, jc);
   const int nch = H / R::N;
-  for (int c0 = 0; c0 < nch; c0 += kWave * kCU) {
-    float acc[kCU][R::N];
-    u32x4_t res[kCU];
+  for (int c0 = 0; c0 < nch; c0 += kWave * CU) {
+    float acc[CU][R::N];
+    u32x4_t res[CU];
 #pragma unroll
-    for (int u = 0; u < kCU; ++u) {
+    for (int u = 0; u < CU; ++u) {
       const int c = c0 + u * kWave + lane;
       res[u] = residual != nullptr && c < nch ? R::ld_s(residual, (size_t)t * H + (size_t)c * R::N)
                                               : u32x4_t{};
 #pragma unroll
       for (int i = 0; i < R::N; ++i) acc[u][i] = 0.f;
     }
-    gather_rows<BF16, true>(y_perm, H, nch, c0, n, dc, wc, acc);
+    gather_rows<BF16, true, CU, SG>(y_perm, H, nch, c0, n, dc, wc, acc);
 #pragma unroll
-    for (int u = 0; u < kCU; ++u) {
+    for (int u = 0; u < CU; ++u) {
       const int c = c0 + u * kWave + lane;
+      if (c0 + u * kWave >= nch) break;  // the whole wave
       if (c >= nch) continue;
       const size_t e = (size_t)t * H + (size_t)c * R::N;
       const uint32_t keep = n > 0 ? keep_bits<R::N>(e, offset, seed, thr) : 0;
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(256) void combine_dropout_kernel(
 }
 
 // g = keep / (1 - p) dy;  dy_perm[dest_j] = w_j g[t];  d_topk_w[t,j] = <g[t], y_perm[dest_j]>
-template <bool BF16>
+template <bool BF16, int CU, int SG>
 __global__ __launch_bounds__(256) void combine_dropout_bwd_kernel(
     const void* __restrict__ dy, const void* __restrict__ y_perm, const float* __restrict__ topk_w,
     const int32_t* __restrict__ dest_row, const uint64_t* __restrict__ rng, uint32_t thr,
@@ -133,38 +134,50 @@ __global__ __launch_bounds__(256) void combine_dropout_bwd_kernel(
   float wc;
   const int n = pack_slots(d, w, dc, wc, jc);
   const int nch = H / R::N;
-  for (int j0 = 0; j0 < n; j0 += kSG) {
-    int dj[kSG];
-    float wj[kSG], dot[kSG];
+  // this lane's kept elements, for the slots after the first ones (rows of up
+  // to 64 elements a lane; longer ones compute them again)
+  const bool keeps = nch <= kWave * (64 / R::N);
+  uint64_t kept = 0;
+  for (int j0 = 0; j0 < n; j0 += SG) {
+    int dj[SG];
+    float wj[SG], dot[SG];
 #pragma unroll
-    for (int s = 0; s < kSG; ++s) {
+    for (int s = 0; s < SG; ++s) {
       dj[s] = __shfl(dc, j0 + s, kWave);
       wj[s] = __shfl(wc, j0 + s, kWave);
       dot[s] = 0.f;
     }
-    for (int c0 = 0; c0 < nch; c0 += kWave * kCU) {
-      u32x4_t g[kCU], raw[kSG][kCU];
+    for (int c0 = 0; c0 < nch; c0 += kWave * CU) {
+      u32x4_t g[CU], raw[SG][CU];
 #pragma unroll
-      for (int u = 0; u < kCU; ++u) {
+      for (int u = 0; u < CU; ++u) {
         const int c = c0 + u * kWave + lane;
         g[u] = c < nch ? R::ld_s(dy, (size_t)t * H + (size_t)c * R::N) : u32x4_t{};
 #pragma unroll
-        for (int s = 0; s < kSG; ++s)
+        for (int s = 0; s < SG; ++s)
           raw[s][u] = (j0 + s < n && c < nch) ? R::ld_s(y_perm, (size_t)dj[s] * H + (size_t)c * R::N)
                                               : u32x4_t{};
       }
 #pragma unroll
-      for (int u = 0; u < kCU; ++u) {
+      for (int u = 0; u < CU; ++u) {
         const int c = c0 + u * kWave + lane;
+        if (c0 + u * kWave >= nch) break;  // the whole wave
+        const int at = (c0 / kWave + u) * R::N;
+        uint32_t bits;
+        if (j0 == 0 || !keeps) {
+          bits = keep_bits<R::N>((size_t)t * H + (size_t)c * R::N, offset, seed, thr);
+          if (keeps) kept |= (uint64_t)bits << at;
+        } else {
+          bits = (uint32_t)(kept >> at);
+        }
         // dropped elements leave both factors, so an infinity there is no NaN
-        const u32x4_t m =
-            keep_mask<BF16>(keep_bits<R::N>((size_t)t * H + (size_t)c * R::N, offset, seed, thr));
+        const u32x4_t m = keep_mask<BF16>(bits);
         float gf[R::N];
         R::to_f32(g[u] & m, gf);
 #pragma unroll
         for (int i = 0; i < R::N; ++i) gf[i] *= scale;
 #pragma unroll
-        for (int s = 0; s < kSG; ++s) {
+        for (int s = 0; s < SG; ++s) {
           float v[R::N], o[R::N];
           R::to_f32(raw[s][u] & m, v);
 #pragma unroll
@@ -177,7 +190,7 @@ __global__ __launch_bounds__(256) void combine_dropout_bwd_kernel(
       }
     }
 #pragma unroll
-    for (int s = 0; s < kSG; ++s) {
+    for (int s = 0; s < SG; ++s) {
       const float sum = wave_sum(dot[s]);
       const int js = __shfl(jc, j0 + s, kWave);
       if (lane == 0 && j0 + s < n) d_topk_w[(size_t)t * k + js] = sum;
@@ -200,12 +213,17 @@ hipError_t launch_combine_dropout(const void* y_perm, const float* topk_w, const
   const Drop d = drop_of(p);
   const int blocks = (T + 3) / 4;
   ProfScope ps(MOE_KERNEL_COMBINE_DROPOUT, s);
-  if (bf16)
-    combine_dropout_kernel<true><<<blocks, 256, 0, s>>>(y_perm, topk_w, dest_row, residual, rng,
-                                                        d.thr, d.scale, T, H, k, y);
-  else
-    combine_dropout_kernel<false><<<blocks, 256, 0, s>>>(y_perm, topk_w, dest_row, residual, rng,
-                                                         d.thr, d.scale, T, H, k, y);
+  // Two slots' rows in flight; four chunks of each for long rows (16384 tokens
+  // of 2048, top-8: 112 us, 124 with two), two for short ones, whose chunks do
+  // not fill four (of 512: 28 us, 33 with four).
+#define MOE_DF(B, CU) \
+  combine_dropout_kernel<B, CU, 2><<<blocks, 256, 0, s>>>(y_perm, topk_w, dest_row, residual, rng, d.thr, d.scale, T, H, k, y)
+  if (bf16) {
+    if (H > 2 * kWave * 8) MOE_DF(true, 4); else MOE_DF(true, 2);
+  } else {
+    if (H > 2 * kWave * 4) MOE_DF(false, 4); else MOE_DF(false, 2);
+  }
+#undef MOE_DF
   return hipGetLastError();
 }
 
@@ -216,14 +234,14 @@ hipError_t launch_combine_dropout_bwd(const void* dy, const void* y_perm, const 
   const Drop d = drop_of(p);
   const int blocks = (T + 3) / 4;
   ProfScope ps(MOE_KERNEL_COMBINE_DROPOUT_BWD, s);
+  // Four slots, two chunks of each: enough in flight with more waves on a CU
+  // than four chunks allow (8192 tokens with one local slot: 22 us for 24).
   if (bf16)
-    combine_dropout_bwd_kernel<true><<<blocks, 256, 0, s>>>(dy, y_perm, topk_w, dest_row, rng,
-                                                            d.thr, d.scale, T, H, k, dy_perm,
-                                                            d_topk_w);
+    combine_dropout_bwd_kernel<true, 2, 4><<<blocks, 256, 0, s>>>(
+        dy, y_perm, topk_w, dest_row, rng, d.thr, d.scale, T, H, k, dy_perm, d_topk_w);
   else
-    combine_dropout_bwd_kernel<false><<<blocks, 256, 0, s>>>(dy, y_perm, topk_w, dest_row, rng,
-                                                             d.thr, d.scale, T, H, k, dy_perm,
-                                                             d_topk_w);
+    combine_dropout_bwd_kernel<false, 2, 4><<<blocks, 256, 0, s>>>(
+        dy, y_perm, topk_w, dest_row, rng, d.thr, d.scale, T, H, k, dy_perm, d_topk_w);
   return hipGetLastError();
 }
 

@@ -72,31 +72,31 @@ __device__ __forceinline__ int pack_slots(int d, float w, int& dc, float& wc, in
 // out[c] = sum over packed slots j < n (ascending) of wc_j * rows[dc_j][c] for
 // this lane's chunks c0 + u * 64 + lane; fp32 accumulation.  STREAM: the rows
 // are read once (streaming loads).
-template <bool BF16, bool STREAM>
+template <bool BF16, bool STREAM, int CU = kCU, int SG = kSG>
 __device__ __forceinline__ void gather_rows(const void* __restrict__ rows, int H, int nch, int c0,
                                             int n, int dc, float wc,
-                                            float (&acc)[kCU][Row<BF16>::N]) {
+                                            float (&acc)[CU][Row<BF16>::N]) {
   using R = Row<BF16>;
   const int lane = lane_id();
-  for (int j0 = 0; j0 < n; j0 += kSG) {
-    u32x4_t raw[kSG][kCU];
-    float wj[kSG];
+  for (int j0 = 0; j0 < n; j0 += SG) {
+    u32x4_t raw[SG][CU];
+    float wj[SG];
 #pragma unroll
-    for (int s = 0; s < kSG; ++s) {
+    for (int s = 0; s < SG; ++s) {
       const int j = j0 + s;  // < 36: a valid lane index
       const int dj = __shfl(dc, j, kWave);
       wj[s] = (j < n) ? __shfl(wc, j, kWave) : 0.f;
 #pragma unroll
-      for (int u = 0; u < kCU; ++u) {
+      for (int u = 0; u < CU; ++u) {
         const int c = c0 + u * kWave + lane;
         const size_t e = (size_t)dj * H + (size_t)c * R::N;
         raw[s][u] = (j < n && c < nch) ? (STREAM ? R::ld_s(rows, e) : R::ld(rows, e)) : u32x4_t{};
       }
     }
 #pragma unroll
-    for (int s = 0; s < kSG; ++s)
+    for (int s = 0; s < SG; ++s)
 #pragma unroll
-      for (int u = 0; u < kCU; ++u) {
+      for (int u = 0; u < CU; ++u) {
         float v[R::N];
         R::to_f32(raw[s][u], v);
 #pragma unroll
