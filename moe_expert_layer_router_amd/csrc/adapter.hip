@@ -824,7 +824,7 @@ struct WgradArgs {
   int rank, accumulate;
 };
 
-constexpr int kWgMaxChunk = 768;
+constexpr int kWgMaxChunk = 1024;
 
 // G = sum over a chunk's rows of p_r q_r^T: the rows are the summed axis.
 //
