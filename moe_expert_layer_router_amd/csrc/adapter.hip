@@ -629,34 +629,167 @@ struct RowIds {
 };
 
 constexpr int kSortBlocks = 128;  // at most, so that a block adds few counts
-int sort_rows(int R) { return max(1024, ((R + kSortBlocks - 1) / kSortBlocks + 255) / 256 * 256); }
+int sort_rows(int R) {
+  return R <= 2048 ? (R + 255) / 256 * 256 + 256 * (R == 0) : max(1024, ((R + kSortBlocks - 1) / kSortBlocks + 255) / 256 * 256);
+}
+
+// Inclusive prefix sum over the 256 threads of a workgroup (s: 4 words).
+__device__ __forceinline__ int block_scan(int v, int* s) {
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int x = __shfl_up(v, o, kWave);
+    v += lane >= o ? x : 0;
+  }
+  if (lane == kWave - 1) s[wave] = v;
+  lds_barrier();
+#pragma unroll
+  for (int w = 0; w < 3; ++w) v += w < wave ? s[w] : 0;
+  return v;
+}
+
+// What the backward needs to order the rows by adapter.
+struct RowOrder {
+  RowIds ids;
+  int per, nblk;    // rows of a block, blocks
+  int32_t* counts;  // [nblk][n_ids] rows of each adapter (more than one block)
+  int chunk;
+  ChunkPlan plan;
+  int32_t* order;   // out
+};
+
+// The rows in adapter order, rows of one adapter in row order: every block adds
+// the counts of the blocks before it (and all, for the adapters' offsets), its
+// four waves take a quarter of its rows each, 64 at a time, and a row's place
+// is its wave's cursor for the adapter plus the lanes before it that have the
+// same.  The first block also writes the chunks.
+__device__ __forceinline__ void order_block(const RowOrder& o, int b) {
+  __shared__ int s_cur[4][kMaxE], s_t[4], s_n[4], s_m[4];
+  const RowIds& ids = o.ids;
+  const ChunkPlan& plan = o.plan;
+  const int per = o.per, nblk = o.nblk, chunk = o.chunk;
+  const int32_t* counts = o.counts;
+  int32_t* order = o.order;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = lane_id();
+  int before = 0, all = 0;
+  if (nblk > 1 && tid < ids.n_ids) {
+#pragma unroll 8
+    for (int i = 0; i < nblk; ++i) {
+      const int c = counts[(size_t)i * ids.n_ids + tid];
+      before += i < b ? c : 0;
+      all += c;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) s_cur[w][tid] = 0;
+  __syncthreads();
+  const int q = (per + 3) / 4;  // rows of a wave
+  const int r0 = b * per + wave * q, r1 = min(min(ids.R, (b + 1) * per), r0 + q);
+  constexpr int KR = 8;  // 64-row steps of a wave whose adapters stay in registers
+  int keep[KR];
+#pragma unroll
+  for (int j = 0; j < KR; ++j) {
+    const int r = r0 + j * kWave + lane;
+    keep[j] = r < r1 ? ids(r) : -1;
+  }
+#pragma unroll
+  for (int j = 0; j < KR; ++j)
+    if (keep[j] >= 0) atomicAdd(&s_cur[wave][keep[j]], 1);
+  for (int r = r0 + KR * kWave + lane; r < r1; r += kWave) {
+    const int a = ids(r);
+    if (a >= 0) atomicAdd(&s_cur[wave][a], 1);
+  }
+  if (nblk <= 1) {
+    lds_barrier();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) all += s_cur[w][tid];
+  }
+  const int end = block_scan(all, s_t), begin = end - all;
+  int at = begin + before;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {  // counts of the waves to their cursors
+    const int n = s_cur[w][tid];
+    s_cur[w][tid] = at;
+    at += n;
+  }
+  __syncthreads();
+  auto place = [&](int r, int a) {
+    int rank = 0, same_n = 0;
+    for (uint64_t todo = __ballot(a >= 0); todo != 0;) {
+      const int cur = __builtin_amdgcn_readlane(a, __builtin_ctzll(todo));
+      const uint64_t same = __ballot(a == cur);
+      todo &= ~same;
+      if (a == cur) {
+        rank = __popcll(same & ((1ull << lane) - 1ull));
+        same_n = __popcll(same);
+      }
+    }
+    const int from = a >= 0 ? s_cur[wave][a] : 0;
+    asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
+    if (a >= 0) {
+      order[from + rank] = r;
+      if (rank == 0) s_cur[wave][a] = from + same_n;
+    }
+    asm volatile("" ::: "memory");
+  };
+#pragma unroll
+  for (int j = 0; j < KR; ++j)
+    if (r0 + j * kWave < r1) place(r0 + j * kWave + lane, keep[j]);
+  for (int rb = r0 + KR * kWave; rb < r1; rb += kWave)
+    place(rb + lane, rb + lane < r1 ? ids(rb + lane) : -1);
+  if (b != 0) return;
+  // the chunks, and the slots of adapters of several
+  const int n = tid < ids.n_ids ? max(1, (all + chunk - 1) / chunk) : 0;
+  const int m = n > 1 ? n : 0;
+  const int n_end = block_scan(n, s_n), m_end = block_scan(m, s_m);
+  if (tid == kMaxE - 1) *plan.count = n_end;
+  if (tid >= ids.n_ids) return;
+  plan.offsets[tid] = begin;
+  if (tid == ids.n_ids - 1) plan.offsets[tid + 1] = end;
+  const int slot = m_end - m;
+  plan.first[tid] = slot;
+  for (int c = 0; c < n; ++c) {
+    int32_t* e = plan.chunks + 4 * (size_t)(n_end - n + c);
+    e[0] = tid;
+    e[1] = begin + c * chunk;
+    e[2] = min(end, begin + (c + 1) * chunk);
+    e[3] = n > 1 ? slot + c : -1;
+  }
+}
+
+__global__ __launch_bounds__(256) void adapter_order_kernel(RowOrder o) {
+  order_block(o, blockIdx.x);
+}
 
 // First launch of the backward, two independent parts.
 //  - Both transposed weights, A [ids][rank][K] -> [ids][K][rank] and
 //    B [ids][N][rank] -> [ids][rank][N]: a thread turns a block of 16 bytes of
 //    ranks x CW columns in registers, so both sides move whole lane-contiguous
 //    words.
-//  - Counts of the rows of each adapter in blocks of rows, for the order list.
+//  - Counts of the rows of each adapter in blocks of rows, for the order list;
+//    or the list itself where the rows are one block (1003 rows: one launch of
+//    5 us less).
 template <bool BF16>
 __global__ __launch_bounds__(256) void adapter_prepare_kernel(const char* __restrict__ A,
                                                               const char* __restrict__ B, int rank,
                                                               int K, int N, char* __restrict__ At,
                                                               char* __restrict__ Bt, int tblocks,
-                                                              RowIds ids, int per,
-                                                              int32_t* __restrict__ counts) {
+                                                              RowOrder o) {
   using E = Elem<BF16>;
   constexpr int CW = 4 / E::EB;  // columns of one 4-byte word
+  const RowIds& ids = o.ids;
   if ((int)blockIdx.x >= tblocks) {
+    if (o.nblk == 1) return order_block(o, 0);
     __shared__ int s_n[kMaxE];
     for (int i = threadIdx.x; i < ids.n_ids; i += 256) s_n[i] = 0;
     __syncthreads();
-    const int b = blockIdx.x - tblocks, r1 = min(ids.R, (b + 1) * per);
-    for (int r = b * per + threadIdx.x; r < r1; r += 256) {
+    const int b = blockIdx.x - tblocks, r1 = min(ids.R, (b + 1) * o.per);
+    for (int r = b * o.per + threadIdx.x; r < r1; r += 256) {
       const int a = ids(r);
       if (a >= 0) atomicAdd(&s_n[a], 1);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < ids.n_ids; i += 256) counts[(size_t)b * ids.n_ids + i] = s_n[i];
+    for (int i = threadIdx.x; i < ids.n_ids; i += 256) o.counts[(size_t)b * ids.n_ids + i] = s_n[i];
     return;
   }
   const int ka = K / CW, kn = N / CW, rc = rank / E::CE;  // words, chunks
@@ -712,101 +845,6 @@ __global__ __launch_bounds__(256) void adapter_prepare_kernel(const char* __rest
 #pragma unroll
     for (int u = 0; u < CW; ++u)
       *reinterpret_cast<u32x4_t*>(dst + ((size_t)(c + u) * rank + j) * E::EB) = wide[u];
-  }
-}
-
-// Inclusive prefix sum over the 256 threads of a workgroup (s: 4 words).
-__device__ __forceinline__ int block_scan(int v, int* s) {
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int x = __shfl_up(v, o, kWave);
-    v += lane >= o ? x : 0;
-  }
-  if (lane == kWave - 1) s[wave] = v;
-  lds_barrier();
-#pragma unroll
-  for (int w = 0; w < 3; ++w) v += w < wave ? s[w] : 0;
-  return v;
-}
-
-// The rows in adapter order, rows of one adapter in row order: every block adds
-// the counts of the blocks before it (and all, for the adapters' offsets), its
-// four waves take a quarter of its rows each, 64 at a time, and a row's place
-// is its wave's cursor for the adapter plus the lanes before it that have the
-// same.  The first block also writes the chunks.
-__global__ __launch_bounds__(256) void adapter_order_kernel(RowIds ids, int per, int nblk,
-                                                            const int32_t* __restrict__ counts,
-                                                            int chunk, ChunkPlan plan,
-                                                            int32_t* __restrict__ order) {
-  __shared__ int s_cur[4][kMaxE], s_t[4], s_n[4], s_m[4];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = lane_id();
-  const int b = blockIdx.x;
-  int before = 0, all = 0;
-  if (tid < ids.n_ids) {
-#pragma unroll 8
-    for (int i = 0; i < nblk; ++i) {
-      const int c = counts[(size_t)i * ids.n_ids + tid];
-      before += i < b ? c : 0;
-      all += c;
-    }
-  }
-#pragma unroll
-  for (int w = 0; w < 4; ++w) s_cur[w][tid] = 0;
-  __syncthreads();
-  const int q = (per + 3) / 4;  // rows of a wave
-  const int r0 = b * per + wave * q, r1 = min(min(ids.R, (b + 1) * per), r0 + q);
-  for (int r = r0 + lane; r < r1; r += kWave) {
-    const int a = ids(r);
-    if (a >= 0) atomicAdd(&s_cur[wave][a], 1);
-  }
-  const int end = block_scan(all, s_t), begin = end - all;
-  int at = begin + before;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {  // counts of the waves to their cursors
-    const int n = s_cur[w][tid];
-    s_cur[w][tid] = at;
-    at += n;
-  }
-  __syncthreads();
-  for (int rb = r0; rb < r1; rb += kWave) {
-    const int r = rb + lane;
-    const int a = r < r1 ? ids(r) : -1;
-    int rank = 0, same_n = 0;
-    for (uint64_t todo = __ballot(a >= 0); todo != 0;) {
-      const int cur = __builtin_amdgcn_readlane(a, __builtin_ctzll(todo));
-      const uint64_t same = __ballot(a == cur);
-      todo &= ~same;
-      if (a == cur) {
-        rank = __popcll(same & ((1ull << lane) - 1ull));
-        same_n = __popcll(same);
-      }
-    }
-    const int from = a >= 0 ? s_cur[wave][a] : 0;
-    asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
-    if (a >= 0) {
-      order[from + rank] = r;
-      if (rank == 0) s_cur[wave][a] = from + same_n;
-    }
-    asm volatile("" ::: "memory");
-  }
-  if (b != 0) return;
-  // the chunks, and the slots of adapters of several
-  const int n = tid < ids.n_ids ? max(1, (all + chunk - 1) / chunk) : 0;
-  const int m = n > 1 ? n : 0;
-  const int n_end = block_scan(n, s_n), m_end = block_scan(m, s_m);
-  if (tid == kMaxE - 1) *plan.count = n_end;
-  if (tid >= ids.n_ids) return;
-  plan.offsets[tid] = begin;
-  if (tid == ids.n_ids - 1) plan.offsets[tid + 1] = end;
-  const int slot = m_end - m;
-  plan.first[tid] = slot;
-  for (int c = 0; c < n; ++c) {
-    int32_t* e = plan.chunks + 4 * (size_t)(n_end - n + c);
-    e[0] = tid;
-    e[1] = begin + c * chunk;
-    e[2] = min(end, begin + (c + 1) * chunk);
-    e[3] = n > 1 ? slot + c : -1;
   }
 }
 
@@ -1187,20 +1225,26 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
   const int eb = d.bf16 ? 2 : 4;
   const BwdLayout l = bwd_layout(d.R, d.K, d.N, d.n_ids, d.rank, eb);
   char* w = (char*)ws;
-  const RowIds ids = {row_id, src_row, d.R, d.x_rows, d.n_ids};
-  const int per = sort_rows(d.R), nblk = dA != nullptr ? (d.R + per - 1) / per : 0;
+  const int per = sort_rows(d.R);
+  const RowOrder o = {{row_id, src_row, d.R, d.x_rows, d.n_ids},
+                      per,
+                      dA != nullptr ? (d.R + per - 1) / per : 0,
+                      (int32_t*)(w + l.counts),
+                      l.chunk,
+                      {(int32_t*)(w + l.count), (int32_t*)(w + l.chunks), (int32_t*)(w + l.first),
+                       (int32_t*)(w + l.offsets)},
+                      (int32_t*)(w + l.order)};
   hipError_t e = hipSuccess;
   if (d.R > 0) {
     const long units = (long)d.n_ids * (d.rank * eb / 16) * ((d.K + d.N) * eb / 4);
     const int tblocks = (int)((units + 255) / 256);
+    const int grid = tblocks + o.nblk;
     if (d.bf16)
-      adapter_prepare_kernel<true><<<tblocks + nblk, 256, 0, s>>>(
-          (const char*)A, (const char*)B, d.rank, d.K, d.N, w + l.at, w + l.bt, tblocks, ids, per,
-          (int32_t*)(w + l.counts));
+      adapter_prepare_kernel<true><<<grid, 256, 0, s>>>((const char*)A, (const char*)B, d.rank, d.K,
+                                                        d.N, w + l.at, w + l.bt, tblocks, o);
     else
-      adapter_prepare_kernel<false><<<tblocks + nblk, 256, 0, s>>>(
-          (const char*)A, (const char*)B, d.rank, d.K, d.N, w + l.at, w + l.bt, tblocks, ids, per,
-          (int32_t*)(w + l.counts));
+      adapter_prepare_kernel<false><<<grid, 256, 0, s>>>((const char*)A, (const char*)B, d.rank, d.K,
+                                                         d.N, w + l.at, w + l.bt, tblocks, o);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     // the data part: the forward from dy's rows to dx's on the transposed weights
     AdapterArgs p{};
@@ -1225,11 +1269,10 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
     if (e != hipSuccess) return e;
   }
   if (dA == nullptr) return e;
-  const ChunkPlan plan = {(int32_t*)(w + l.count), (int32_t*)(w + l.chunks), (int32_t*)(w + l.first),
-                          (int32_t*)(w + l.offsets)};
-  adapter_order_kernel<<<max(nblk, 1), 256, 0, s>>>(ids, per, nblk, (const int32_t*)(w + l.counts),
-                                                    l.chunk, plan, (int32_t*)(w + l.order));
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (o.nblk != 1) {  // (no rows at all: the chunks alone)
+    adapter_order_kernel<<<max(o.nblk, 1), 256, 0, s>>>(o);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   WgradArgs a{};
   a.p[0] = (const float*)(w + l.w);
   a.p[1] = v;
@@ -1240,7 +1283,7 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
   a.out[0] = dA;
   a.out[1] = dB;
   a.part = (float*)(w + l.part);
-  a.plan = plan;
+  a.plan = o.plan;
   a.ldq[0] = d.ldx;
   a.ldq[1] = d.ldy;
   a.C[0] = d.K;
@@ -1266,7 +1309,7 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (d.R <= l.chunk) return e;  // no adapter has more than one chunk
   adapter_wgrad_sum_kernel<<<dim3((d.rank * (d.K + d.N) / 4 + 255) / 256, d.n_ids), 256, 0, s>>>(
-      l.chunk, plan, (const f32x4_t*)(w + l.part), d.rank, d.K, d.N, accumulate ? 1 : 0, (f32x4_t*)dA,
+      l.chunk, o.plan, (const f32x4_t*)(w + l.part), d.rank, d.K, d.N, accumulate ? 1 : 0, (f32x4_t*)dA,
       (f32x4_t*)dB);
   return hipGetLastError();
 }
