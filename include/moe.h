@@ -546,7 +546,8 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
  *   v [R,rank] fp32 or NULL (kept for moe_adapter_bwd)
  * K, N, ldx, ldy multiples of 8 (bf16) or 4 (fp32), at most 2^20; rank a
  * multiple of 8, at most 128 (else MOE_EUNSUPPORTED); 1 <= n_ids <= 2^20; row
- * data 16-byte aligned.  R = 0 enqueues nothing. */
+ * data 16-byte aligned; x and y must not share elements (columns of one wider
+ * matrix are fine).  R = 0 enqueues nothing. */
 int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id, const void* A,
                     const void* B, const float* scale, int R, int x_rows, int K, int N, int ldx,
                     int ldy, int n_ids, int rank, int dtype, void* y, float* v, void* stream);
@@ -563,7 +564,8 @@ int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id
  *             the bf16 products whole (three bf16 parts).
  *   ws      moe_adapter_ws_bytes(R, K, N, n_ids, rank, dtype) bytes (transposed
  *           weights, w, the rows in adapter order, partial sums)
- * Limits as moe_adapter_fwd, with n_ids <= 256 (else MOE_EUNSUPPORTED). */
+ * Limits as moe_adapter_fwd, with n_ids <= 256 (else MOE_EUNSUPPORTED); dx
+ * shares no elements with dy or x. */
 int64_t moe_adapter_ws_bytes(int R, int K, int N, int n_ids, int rank, int dtype);
 int moe_adapter_bwd(const void* dy, const void* x, const int32_t* src_row, const int32_t* row_id,
                     const void* A, const void* B, const float* v, const float* scale, int R,

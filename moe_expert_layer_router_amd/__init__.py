@@ -445,6 +445,13 @@ def _into(o: Dict[str, torch.Tensor], name: str, shape, dtype, dev) -> int:
     return _arg(o[name], name, dtype, shape, dev)
 
 
+def _work(nbytes: int, dev, ws: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """_ws with the caller's workspace checked for the device as well."""
+    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {dev}, got one on {ws.device}")
+    return _ws(nbytes, dev, ws)
+
+
 def _row_type(t: torch.Tensor, name: str) -> torch.dtype:
     if t.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
@@ -482,7 +489,7 @@ def moe_route_bwd_add(d_topk_w: torch.Tensor, topk_w: torch.Tensor, topk_idx: to
     if not want_dw:
         o["dw_router"] = None
     code = _dtype_code(x)
-    ws = _ws(workspace_bytes(MOE_OP_ROUTE_BWD, T, H, 1, E, k, 0, E, code), dev, ws)
+    ws = _work(workspace_bytes(MOE_OP_ROUTE_BWD, T, H, 1, E, k, 0, E, code), dev, ws)
     _check(lib.moe_route_bwd_add(*a, T, H, E, k, code, d_logits, dx, dw, _ptr(ws), _nbytes(ws),
                                  _raw_stream(dev)), "moe_route_bwd_add")
     return o
@@ -516,7 +523,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
     nb = lib.moe_balance_ws_bytes(T, E, S)
     if nb < 0:
         _check(int(nb), "moe_balance_ws_bytes")
-    o["ws"] = _ws(int(nb), dev, ws)
+    o["ws"] = _work(int(nb), dev, ws)
     _check(lib.moe_balance_loss(*a, T, E, k, S, balance_coef, z_coef,
                                 _into(o, "counts", (S, E), i32, dev),
                                 _into(o, "prob_sum", (S, E), f32, dev),
@@ -700,7 +707,7 @@ def moe_adapter_bwd(dy: torch.Tensor, x: torch.Tensor, row_id: torch.Tensor, A: 
     nb = lib.moe_adapter_ws_bytes(R, K, N, n_ids, rank, _dtype_code(A))
     if nb < 0:
         _check(int(nb), "moe_adapter_ws_bytes")
-    o["ws"] = _ws(int(nb), dev, ws)
+    o["ws"] = _work(int(nb), dev, ws)
     _check(lib.moe_adapter_bwd(dyp, xp, src, ids, a, b, vp, sc, R, x_rows, K, N, ldx, ldy, lddx,
                                n_ids, rank, _dtype_code(A), dxp, dA, dB, 1 if accumulate else 0,
                                _ptr(o["ws"]), _nbytes(o["ws"]), _raw_stream(dev)), "moe_adapter_bwd")
@@ -755,7 +762,7 @@ def moe_grouped_ffn_fwd_adapter(x: torch.Tensor, src_row: Optional[torch.Tensor]
          _arg(w_down, "w_down", dt, (E_l, H, I), dev)]
     o = dict(out or {})
     code = _dtype_code(x)
-    ws = _ws(workspace_bytes(MOE_OP_FFN_FWD, R_cap, H, I, E_l, 1, 0, E_l, code), dev, ws)
+    ws = _work(workspace_bytes(MOE_OP_FFN_FWD, R_cap, H, I, E_l, 1, 0, E_l, code), dev, ws)
     _check(lib.moe_grouped_ffn_fwd_adapter(
         *a, E_l, R_cap, x_rows, H, I, *w, *ab,
         _arg(scale, "scale", torch.float32, (n_ids,), dev, optional=True), n_ids, rank, code,

@@ -1063,6 +1063,20 @@ int check_pitch(int ld, int width, int dtype, const char* name, const char* fn) 
     return fail(MOE_EINVAL, "%s: %s=%d must be a multiple of %d and at least %d", fn, name, ld, q, width);
   return MOE_OK;
 }
+
+// Whether the first `cols` columns of two matrices (rows at a pitch, in
+// elements) share memory.  At one pitch they may be columns of one wider
+// matrix, like gate and up.
+bool rows_overlap(const void* a, int64_t a_rows, int lda, int a_cols, const void* b, int64_t b_rows,
+                  int ldb, int b_cols, int eb) {
+  if (a_rows == 0 || b_rows == 0) return false;
+  const intptr_t a0 = (intptr_t)a, b0 = (intptr_t)b;
+  if (a0 >= b0 + ((b_rows - 1) * ldb + b_cols) * eb || b0 >= a0 + ((a_rows - 1) * lda + a_cols) * eb)
+    return false;
+  if (lda != ldb) return true;
+  const int64_t pitch = (int64_t)lda * eb, at = ((b0 - a0) % pitch + pitch) % pitch;
+  return at < (int64_t)a_cols * eb || at + (int64_t)b_cols * eb > pitch;
+}
 }  // namespace
 
 int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id, const void* A,
@@ -1074,12 +1088,15 @@ int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id
   if (int rc = check_pitch(ldx, K, dtype, "ldx", fn)) return rc;
   if (int rc = check_pitch(ldy, N, dtype, "ldy", fn)) return rc;
   if (R == 0) return MOE_OK;
-  if (int rc = check_ptr(x, "x", fn, true)) return rc;
+  if (x_rows > 0)
+    if (int rc = check_ptr(x, "x", fn, true)) return rc;
   if (int rc = check_ptr(row_id, "row_id", fn)) return rc;
   if (int rc = check_ptr(A, "A", fn, true)) return rc;
   if (int rc = check_ptr(B, "B", fn, true)) return rc;
   if (int rc = check_ptr(y, "y", fn, true)) return rc;
   if (v != nullptr && !aligned16(v)) return fail(MOE_EINVAL, "%s: v must be 16-byte aligned", fn);
+  if (rows_overlap(x, x_rows, ldx, K, y, R, ldy, N, elem_bytes(dtype)))
+    return fail(MOE_EINVAL, "%s: x and y overlap", fn);
   const AdapterShape d = {dtype == MOE_BF16, R, x_rows, K, N, n_ids, rank, ldx, ldy};
   return hip_status(launch_adapter_fwd(d, x, src_row, row_id, A, B, scale, y, v, begin_launch(stream)), fn);
 }
@@ -1117,12 +1134,18 @@ int moe_adapter_bwd(const void* dy, const void* x, const int32_t* src_row, const
     if (int rc = check_ptr(A, "A", fn, true)) return rc;
     if (int rc = check_ptr(B, "B", fn, true)) return rc;
     if (dA != nullptr) {
-      if (int rc = check_ptr(x, "x", fn, true)) return rc;
+      if (x_rows > 0)
+        if (int rc = check_ptr(x, "x", fn, true)) return rc;
       if (int rc = check_ptr(v, "v", fn, true)) return rc;
     }
   }
   if (int rc = check_ws(ws, ws_bytes, adapter_bwd_ws_bytes(R, K, N, n_ids, rank, elem_bytes(dtype)), fn))
     return rc;
+  const int eb = elem_bytes(dtype);
+  if (dx != nullptr && rows_overlap(dy, R, ldy, N, dx, R, lddx, K, eb))
+    return fail(MOE_EINVAL, "%s: dy and dx overlap", fn);
+  if (dx != nullptr && dA != nullptr && rows_overlap(x, R > 0 ? x_rows : 0, ldx, K, dx, R, lddx, K, eb))
+    return fail(MOE_EINVAL, "%s: x and dx overlap", fn);
   const AdapterShape d = {dtype == MOE_BF16, R, x_rows, K, N, n_ids, rank, ldx, ldy};
   return hip_status(launch_adapter_bwd(d, dy, x, src_row, row_id, A, B, v, scale, dx, lddx, dA, dB,
                                        accumulate != 0, ws, begin_launch(stream)),

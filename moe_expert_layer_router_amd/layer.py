@@ -173,9 +173,9 @@ class MoELayer:
     def forward(self, x, w_router, w_gate, w_up, w_down, bias=None, save_logits=True, residual=None,
                 rng=None, seq_offsets=None, token_mask=None, adapters=None):
         """residual [T,H]: added to the combined rows.  rng [2] int64 on the GPU (seed, offset):
-        the dropout's numbers, still in it when backward() repeats them.  seq_offsets [S+1] int32 and token_mask
-        [T] uint8: the sequences and padding of the auxiliary losses (S = max_sequences; None: one
-        sequence).  adapters: dict token_adapter [T] int32 (-1: none), n, gate / up / down: (A, B)
+        the dropout's numbers, still in it when backward() repeats them.  seq_offsets [S+1] int32 and
+        token_mask [T] uint8: the sequences and padding of the auxiliary losses (S = max_sequences,
+        fewer with empty ones behind the last; None: one sequence).  adapters: dict token_adapter [T] int32 (-1: none), n, gate / up / down: (A, B)
         with A [n, E_l, rank, in] and B [n, E_l, out, rank], scale [n, E_l] fp32 (optional)."""
         b, T, H, I, E, k = self.buf, self.T, self.H, self.I, self.E, self.k
         if self.dropout > 0.0 and rng is None:

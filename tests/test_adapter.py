@@ -192,6 +192,25 @@ def test_refusals():
     assert r(N, N, N, 4, 8, 2, 0, N, STREAM) == OK
 
 
+def test_shared_memory_is_refused():
+    """x and y (dy and dx, x and dx) that share an element; columns of one wider matrix do not."""
+    at = lambda n: A.value + n
+    fwd = lambda x, ldx, y, ldy, K=64, N_=64, R=16: L.moe_adapter_fwd(
+        x, N, A, A, A, N, R, R, K, N_, ldx, ldy, 4, 16, BF16, y, N, STREAM)
+    assert fwd(A, 64, A, 64) == EINVAL and "overlap" in _err()
+    assert fwd(A, 64, at(16 * 64 * 2 - 16), 64) == EINVAL and "overlap" in _err()
+    assert fwd(A, 128, at(112), 128) == EINVAL and "overlap" in _err()       # columns 0..63 and 56..119
+    assert fwd(A, 128, at(144), 128) == EINVAL and "overlap" in _err()       # y's last columns in the next row
+    assert fwd(A, 128, at(256 * 3 + 16), 128) == EINVAL and "overlap" in _err()
+    assert fwd(A, 72, at(128), 136) == EINVAL and "overlap" in _err()        # two pitches
+    big = 1 << 40
+    bwd = lambda dy, x, dx: L.moe_adapter_bwd(dy, x, N, A, A, A, A, N, 16, 16, 64, 64, 64, 64, 64, 4, 16,
+                                              BF16, dx, A, A, 0, A, big, STREAM)
+    far = at(1 << 20)
+    assert bwd(A, far, A) == EINVAL and "dy and dx" in _err()
+    assert bwd(far, A, at(32)) == EINVAL and "x and dx" in _err()
+
+
 def test_definition_gradient_matches_differences():
     """dA, dB, dx of the definition against central differences of <dy, y> in 64 bits."""
     g = torch.Generator().manual_seed(1)
@@ -388,6 +407,35 @@ def test_adapter_rows():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_columns_of_one_matrix(dtype):
+    """x and y as neighbouring columns of one matrix give the bits of separate ones."""
+    s = make(dtype, 37, 64, 72, 3, 16, "mixed", False, 1)
+    want = s["y"].clone()
+    moe.moe_adapter_fwd(s["x"], s["ids"], s["A"], s["B"], want)
+    wide = torch.cat([s["x"], s["y"], s["x"]], 1)
+    moe.moe_adapter_fwd(wide[:, :64], s["ids"], s["A"], s["B"], wide[:, 64:136])
+    assert torch.equal(wide[:, 64:136], want)
+    assert torch.equal(wide[:, :64], s["x"]) and torch.equal(wide[:, 136:], s["x"])
+    wide = torch.cat([s["y"], s["x"]], 1)  # y before x
+    moe.moe_adapter_fwd(wide[:, 72:], s["ids"], s["A"], s["B"], wide[:, :72])
+    assert torch.equal(wide[:, :72], want)
+
+
+@gpu
+def test_no_token_rows():
+    """x without rows: every src_row is outside, no row has an adapter."""
+    s = make("bf16", 20, 64, 72, 3, 16, "mixed", False, 1)
+    none = dict(x=s["x"][:0], src_row=torch.zeros(20, dtype=torch.int32, device=DEV))
+    y = s["y"].clone()
+    v = moe.moe_adapter_fwd(row_id=s["ids"], A=s["A"], B=s["B"], y=y, want_v=True, **none)
+    assert torch.equal(y, s["y"]) and not v.any()
+    dx = torch.ones(20, 64, dtype=torch.bfloat16, device=DEV)
+    o = moe.moe_adapter_bwd(s["y"], row_id=s["ids"], A=s["A"], B=s["B"], v=v, dx=dx, **none)
+    assert (dx == 1).all() and not o["dA"].any() and not o["dB"].any()
+
+
+@gpu
 def test_binding_refusals():
     s = make("bf16", 20, 64, 72, 3, 16, "mixed", False, 1)
     a = dict(x=s["x"], row_id=s["ids"], A=s["A"], B=s["B"], y=s["y"])
@@ -403,6 +451,11 @@ def test_binding_refusals():
         moe.moe_adapter_fwd(**{**a, "y": torch.zeros(20, 73, dtype=torch.bfloat16, device=DEV)[:, :72]})
     with pytest.raises(moe.MoEError, match="rank"):
         moe.moe_adapter_fwd(s["x"], s["ids"], s["A"][:, :12].contiguous(), s["B"][..., :12].contiguous(), s["y"])
+    v = moe.moe_adapter_fwd(**a, want_v=True)
+    ws = moe.moe_adapter_bwd(s["y"], s["x"], s["ids"], s["A"], s["B"], v, None)["ws"]
+    for bad in (ws.cpu(), ws[:64], torch.stack([ws, ws], 1)[:, 0]):
+        with pytest.raises(ValueError, match="ws|workspace"):
+            moe.moe_adapter_bwd(s["y"], s["x"], s["ids"], s["A"], s["B"], v, None, ws=bad)
 
 
 def test_ffn_adapter_refusals():
