@@ -8,7 +8,8 @@
 //   d total / d z[t,e] = p[t,e] (cb E/(k N n_s) (c[s,e] - sum_j p[t,j] c[s,j])
 //                                + cz 2 lse_t / N)
 //
-// Forward, two launches.  The token axis is cut into chunks of C tokens, one
+// Forward, two launches (one for few tokens, balance_one).  The token axis is
+// cut into chunks of C tokens, one
 // workgroup each; the part of sequence s in chunk b is summed into partial row
 // b + s (walking the tokens in order, b or s grows at every new pair, so the
 // sum names the pair, and no plan of the ragged lengths is needed).  The
@@ -20,18 +21,32 @@ namespace moe {
 
 namespace {
 
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+
 constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / kWave;
 
-// Tokens a workgroup takes at once: U for every group of LPT lanes.
-constexpr int kBalU = 4;
-constexpr int bal_batch(int LPT) { return kBalWaves * (kWave / LPT) * kBalU; }
-int lanes_per_token(int E) { return E <= 32 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64; }
+// LPT lanes hold V groups of four logits of a token each, and U tokens at once.
+// Two groups share the token's reductions, logarithm and reciprocal among twice
+// as many logits (a third fewer instructions than one group on twice the lanes).
+constexpr int bal_u(int V) { return V == 1 ? 4 : 2; }
+constexpr int bal_batch(int LPT, int V) { return kBalWaves * (kWave / LPT) * bal_u(V); }
+int lanes_per_token(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : 32; }
+int batch_of(int E) { return bal_batch(lanes_per_token(E), E <= 32 ? 1 : 2); }
+
+// Few tokens in few sequences: one workgroup does all in one launch, 1.4 .. 1.9
+// us a batch and 1.2 us a sequence's end against 8.3 .. 10 us for two launches
+// (256 tokens of 8 experts in 3 sequences: 8.9 us for 9.9, and 9.5 for 12 where
+// the host enqueues every call; 4 batches in 3 sequences: 12.5 for 9.7).
+bool balance_one(int T, int E, int S) {
+  const int b = batch_of(E);
+  return ((long)T + b - 1) / b + S <= 5;
+}
 
 // Tokens per chunk: whole batches, at most 1024 chunks, so that the second
 // launch has few partial rows to add.
 int balance_chunk(int T, int E) {
-  const int b = bal_batch(lanes_per_token(E));
+  const int b = batch_of(E);
   return ((T + 1023) / 1024 + b - 1) / b * b + (T == 0 ? b : 0);
 }
 
@@ -61,7 +76,7 @@ __device__ __forceinline__ int seq_find(const int32_t* off, int S, int t, int T)
 
 // Reductions over the LPT lanes that hold one token: within 16 lanes by data
 // moves of the vector unit (neighbour, pair, half-row and row mirrored), the
-// last one or two steps by shuffles.
+// last step by a shuffle.
 template <int CTRL>
 __device__ __forceinline__ float moved(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
@@ -73,7 +88,6 @@ __device__ __forceinline__ float group_reduce(float v, F f) {
   v = f(v, moved<0x141>(v));  // mirror of 8
   if (LPT > 8) v = f(v, moved<0x140>(v));  // mirror of 16
   if (LPT > 16) v = f(v, __shfl_xor(v, 16, kWave));
-  if (LPT > 32) v = f(v, __shfl_xor(v, 32, kWave));
   return v;
 }
 template <int LPT>
@@ -96,17 +110,40 @@ __device__ __forceinline__ float exp_neg(float d) {
   return fmaf(e, lo * 0.693147181f, e);
 }
 
-// The four values of columns 4 h .. 4 h + 3 of a row of E; VEC: one 16-byte load.
+// 1 / s for s >= 1 (NaN stays NaN): v_rcp_f32 and a step of Newton's method.
+__device__ __forceinline__ float reciprocal(float s) {
+  const float r = __builtin_amdgcn_rcpf(s);
+  return fmaf(fmaf(-s, r, 1.f), r, r);
+}
+
+// The values of columns e .. e + 3 of a row of E (VEC: one 16-byte load); behind
+// the end the last ones again, which the caller replaces (in_row).
 template <bool VEC>
-__device__ __forceinline__ f32x4_t load4(const float* row, int e, int E, float fill) {
+__device__ __forceinline__ f32x4_t load4(const float* row, int e, int E) {
   if constexpr (VEC) {
-    return e < E ? *reinterpret_cast<const f32x4_t*>(row + e) : f32x4_t{fill, fill, fill, fill};
+    return *reinterpret_cast<const f32x4_t*>(row + min(e, E - 4));
   } else {
     f32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = row[min(e + i, E - 1)];
+    return v;
+  }
+}
+// The same with `fill` behind the end.
+template <bool VEC, typename T4, typename T>
+__device__ __forceinline__ T4 load4_or(const T* row, int e, int E, T fill) {
+  if constexpr (VEC) {
+    return e < E ? *reinterpret_cast<const T4*>(row + e) : T4{fill, fill, fill, fill};
+  } else {
+    T4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = e + i < E ? row[e + i] : fill;
     return v;
   }
+}
+template <bool VEC>
+__device__ __forceinline__ bool in_row(int e, int i, int E) {
+  return VEC ? e < E : e + i < E;
 }
 
 // Partial rows of the first launch: [slots][E] counts, [slots][E] probability
@@ -121,74 +158,112 @@ struct BalWs {
   double* zterms;  // [S] sums of lse^2
 };
 
+// The call's results.
+struct BalOut {
+  int32_t* counts;   // [S][E]
+  float* prob_sum;   // [S][E]
+  int32_t* tokens;   // [S + 1]
+  float* loss;       // [3]
+};
+
+// loss from the sum over sequences of (1/n_s) sum_e c q, that of lse^2, and N.
+__device__ __forceinline__ void write_loss(double bal, double z, int N, int E, int k, int S, float cb,
+                                           float cz, const BalOut& o) {
+  bal = N > 0 ? bal * E / ((double)k * N) : 0.0;
+  z = N > 0 ? z / N : 0.0;
+  o.tokens[S] = N;
+  o.loss[0] = (float)bal;
+  o.loss[1] = (float)z;
+  o.loss[2] = (float)(cb * bal + cz * z);
+}
+
 // A workgroup goes through its chunk in batches, the next batch's logits on
 // their way while it computes, with the running sums of the current sequence in
 // registers; where a sequence ends inside the chunk, and at the chunk's end,
-// the sums go out.
-template <int LPT, bool VEC>
+// the sums go out.  ONE: the only workgroup, whose sums are the results.
+template <int LPT, int V, bool VEC, bool ONE>
 __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const int32_t* __restrict__ seq_offsets, const uint8_t* __restrict__ mask, int T, int E, int k,
-    int S, int C, float* __restrict__ lse_out, BalWs ws) {
+    int S, int C, float* __restrict__ lse_out, BalWs ws, float cb, float cz, BalOut out) {
   constexpr int G = kWave / LPT;          // tokens a wave holds at once
   constexpr int NG = kBalWaves * G;       // tokens a workgroup holds at once
-  constexpr int U = kBalU;                // of them for each group
+  constexpr int U = bal_u(V);             // of them for each group
   constexpr int BT = NG * U;
   __shared__ int s_cnt[kMaxE];
-  __shared__ f32x4_t s_p[NG][LPT];
+  __shared__ f32x4_t s_p[NG][V * LPT];
   __shared__ float s_z[NG];
   __shared__ int s_n[NG];
   const int tid = threadIdx.x, lane = lane_id();
   const int h = lane % LPT, g = (tid >> 6) * G + lane / LPT;
-  const int t0 = blockIdx.x * C, t1 = min(T, t0 + C);
-  if (blockIdx.x == 0 && tid == 0) *ws.ticket = 0;
-  if (t0 >= t1) return;
-  const f32x4_t none4 = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  const int t0 = ONE ? 0 : blockIdx.x * C, t1 = ONE ? T : min(T, t0 + C);
+  if constexpr (!ONE) {
+    if (blockIdx.x == 0 && tid == 0) *ws.ticket = 0;
+    if (t0 >= t1) return;
+  }
   constexpr int IQ = 4;  // choices of a thread loaded ahead (a batch has BT k)
-  f32x4_t z[U];
+  f32x4_t z[U][V];
   uint8_t mk[U];
   int pick[IQ];
-  auto choice = [&](int i, int te) {  // -1: not live
-    if (i >= te * k) return -1;
-    const int e = topk_idx[i];
-    return mask == nullptr || mask[i / k] != 0 ? e : -1;
-  };
-  auto fetch = [&](int tb) {
+  uint8_t mp[IQ];
+  int tok[IQ];  // the choices' tokens in a batch
 #pragma unroll
-    for (int q = 0; q < IQ; ++q) pick[q] = choice(tb * k + q * kBalThreads + tid, min(t1, tb + BT));
+  for (int q = 0; q < IQ; ++q) tok[q] = (q * kBalThreads + tid) / k;
+  auto fetch = [&](int tb) {  // (t1 > 0: clamped where a batch ends behind it)
+#pragma unroll
+    for (int q = 0; q < IQ; ++q) {
+      pick[q] = topk_idx[min(tb * k + q * kBalThreads + tid, t1 * k - 1)];
+      mp[q] = mask != nullptr ? mask[min(tb + tok[q], t1 - 1)] : (uint8_t)1;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = tb + u * NG + g;
-      mk[u] = t < t1 ? (mask != nullptr ? mask[t] : (uint8_t)1) : (uint8_t)0;
-      z[u] = t < t1 ? load4<VEC>(logits + (size_t)t * E, 4 * h, E, -INFINITY) : none4;
+      const int t = min(tb + u * NG + g, t1 - 1);
+      mk[u] = mask != nullptr ? mask[t] : (uint8_t)1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) z[u][v] = load4<VEC>(logits + (size_t)t * E, 4 * (h + v * LPT), E);
     }
   };
-  fetch(t0);
+  if (t0 < t1) fetch(t0);
   for (int e = tid; e < E; e += kBalThreads) s_cnt[e] = 0;
-  int s = seq_find(seq_offsets, S, t0, T);
+  int s = ONE ? 0 : seq_find(seq_offsets, S, t0, T);
   int a = s < S ? seq_off(seq_offsets, s, T) : T, b = s < S ? seq_off(seq_offsets, s + 1, T) : T;
   __syncthreads();
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc[V] = {};
   float z2 = 0.f;
   int n = 0;
+  double bal = 0.0, zsum = 0.0;  // ONE, thread 0: the sums over sequences
+  int N = 0;
+  __shared__ double s_term[kBalWaves];
   auto flush = [&]() {
-    s_p[g][h] = acc;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s_p[g][h + v * LPT] = acc[v];
+      acc[v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
     if (h == 0) {
       s_z[g] = z2;
       s_n[g] = n;
     }
-    acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
     z2 = 0.f;
     n = 0;
     __syncthreads();
-    const size_t slot = (size_t)blockIdx.x + s;
-    for (int e = tid; e < E; e += kBalThreads) {
+    const size_t slot = ONE ? s : (size_t)blockIdx.x + s;
+    double term = 0.0;
+    static_assert(kMaxE <= kBalThreads, "a thread per expert");
+    if (const int e = tid; e < E) {
       float q = 0.f;
 #pragma unroll
       for (int i = 0; i < NG; ++i) q += s_p[i][e / 4][e % 4];
-      ws.psum[slot * E + e] = q;
-      ws.counts[slot * E + e] = s_cnt[e];
+      (ONE ? out.prob_sum : ws.psum)[slot * E + e] = q;
+      (ONE ? out.counts : ws.counts)[slot * E + e] = s_cnt[e];
+      if (ONE) term = (double)s_cnt[e] * (double)q;
       s_cnt[e] = 0;
+    }
+    if constexpr (ONE) {
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) term += __shfl_xor(term, o, kWave);
+      if (lane == 0) s_term[tid >> 6] = term;
+      __syncthreads();
     }
     if (tid == 0) {
       float zs = 0.f;
@@ -197,48 +272,83 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
         zs += s_z[i];
         ns += s_n[i];
       }
-      ws.zsum[slot] = zs;
-      ws.tokens[slot] = ns;
+      if constexpr (ONE) {
+        double t = 0.0;
+        for (int i = 0; i < kBalWaves; ++i) t += s_term[i];
+        out.tokens[s] = ns;
+        bal += ns > 0 ? t / ns : 0.0;
+        zsum += zs;
+        N += ns;
+      } else {
+        ws.zsum[slot] = zs;
+        ws.tokens[slot] = ns;
+      }
     }
     __syncthreads();
   };
+  auto empty = [&]() {  // ONE: a sequence without rows
+    if (tid < E) {
+      out.counts[(size_t)s * E + tid] = 0;
+      out.prob_sum[(size_t)s * E + tid] = 0.f;
+    }
+    if (tid == 0) out.tokens[s] = 0;
+  };
   for (int tb = t0; tb < t1; tb += BT) {
-    f32x4_t p[U];
+    f32x4_t p[U][V];
     float lse[U];
     bool live[U];
+    const int te = min(t1, tb + BT);
+    int now[IQ];  // -1: not an expert, or not live
+#pragma unroll
+    for (int q = 0; q < IQ; ++q) now[q] = mp[q] != 0 && (uint32_t)pick[q] < (uint32_t)E ? pick[q] : -1;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       // a row that does not count, whatever it holds, as a row of -inf
-      live[u] = mk[u] != 0;
-      const f32x4_t v = live[u] ? z[u] : none4;
-      const float top = group_max<LPT>(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+      live[u] = mk[u] != 0 && tb + u * NG + g < t1;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p[u][v][i] = live[u] && in_row<VEC>(4 * (h + v * LPT), i, E) ? z[u][v][i] : -INFINITY;
+    }
+    if (tb + BT < t1) fetch(tb + BT);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        top = fmaxf(top, fmaxf(fmaxf(p[u][v][0], p[u][v][1]), fmaxf(p[u][v][2], p[u][v][3])));
+      top = group_max<LPT>(top);
       // a row of -inf alone: probabilities 0 and lse 0.  (A NaN leaves top
       // unless all are NaN; it comes back with the exponentials' sum.)
       const bool none = top == -INFINITY;
+      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[u][i] = none ? (v[i] == v[i] ? 0.f : v[i]) : exp_neg(v[i] - top);
-      const float sum = group_sum<LPT>((p[u][0] + p[u][1]) + (p[u][2] + p[u][3]));
-      const float inv = none ? (sum == sum ? 0.f : sum) : 1.f / sum;
+      for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[u][i] *= inv;
-      lse[u] = none ? inv : top + logf(sum);
+        for (int i = 0; i < 4; ++i) {
+          const float x = p[u][v][i];
+          p[u][v][i] = exp_neg(none ? (x == x ? -INFINITY : x) : x - top);
+        }
+        sum += (p[u][v][0] + p[u][v][1]) + (p[u][v][2] + p[u][v][3]);
+      }
+      sum = group_sum<LPT>(sum);
+      const float inv = none ? sum : reciprocal(sum);
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[u][v] *= inv;
+      lse[u] = none ? sum : top + __builtin_amdgcn_logf(sum) * 0.693147181f;
     }
-    const int te = min(t1, tb + BT);
-    int now[IQ];
-#pragma unroll
-    for (int q = 0; q < IQ; ++q) now[q] = pick[q];
-    if (tb + BT < t1) fetch(tb + BT);
     uint32_t counted = 0;  // tokens of this batch that a sequence has taken
     while (s < S && a < te) {
       const int pa = max(a, tb), pb = min(b, te);
 #pragma unroll
       for (int q = 0; q < IQ; ++q) {
-        const int i = tb * k + q * kBalThreads + tid;
-        if (i >= pa * k && i < pb * k && now[q] >= 0 && now[q] < E) atomicAdd(&s_cnt[now[q]], 1);
+        const int t = tb + tok[q];
+        if (t >= pa && t < pb && now[q] >= 0) atomicAdd(&s_cnt[now[q]], 1);
       }
       for (int i = max(pa * k, tb * k + IQ * kBalThreads) + tid; i < pb * k; i += kBalThreads) {
-        const int e = choice(i, te);
-        if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+        const int e = topk_idx[i];
+        if ((mask == nullptr || mask[i / k] != 0) && e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -246,13 +356,15 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
         const bool in = t >= pa && t < pb;
         if (in) counted |= 1u << u;
         if (in && live[u]) {
-          acc += p[u];
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] += p[u][v];
           z2 = fmaf(lse[u], lse[u], z2);
           ++n;
         }
       }
       if (b > te) break;  // it goes on
       if (max(a, t0) < b) flush();
+      else if (ONE) empty();
       ++s;
       a = b;
       b = s < S ? seq_off(seq_offsets, s + 1, T) : T;
@@ -263,7 +375,12 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
       if (t < t1 && h == 0) lse_out[t] = (counted >> u & 1) && live[u] ? lse[u] : 0.f;
     }
   }
-  if (s < S && a < t1) flush();  // the sequence that goes on in the next chunk
+  if constexpr (ONE) {
+    for (; s < S; ++s) empty();
+    if (tid == 0) write_loss(bal, zsum, N, E, k, S, cb, cz, out);
+  } else {
+    if (s < S && a < t1) flush();  // the sequence that goes on in the next chunk
+  }
 }
 
 // One workgroup per (sequence, 16 experts): 64 threads of a column each add
@@ -285,8 +402,7 @@ __device__ __forceinline__ V published(V* from) {
 
 __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
     const int32_t* __restrict__ seq_offsets, int T, int E, int k, int S, int C, float cb, float cz,
-    BalWs ws, int32_t* __restrict__ counts, float* __restrict__ prob_sum, int32_t* tokens,
-    float* __restrict__ loss) {
+    BalWs ws, BalOut out) {
   __shared__ float s_q[kSumWaves][kSumCols], s_z[kSumWaves];
   __shared__ int s_c[kSumWaves][kSumCols], s_n[kSumWaves];
   const int nb = (E + kSumCols - 1) / kSumCols;
@@ -349,8 +465,8 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
       z2 += s_z[i];
     }
     if (e < E) {
-      counts[(size_t)s * E + e] = c;
-      prob_sum[(size_t)s * E + e] = q;
+      out.counts[(size_t)s * E + e] = c;
+      out.prob_sum[(size_t)s * E + e] = q;
     }
     double term = e < E && n > 0 ? (double)c * (double)q / n : 0.0;
 #pragma unroll
@@ -363,7 +479,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
       publish(&ws.terms[blockIdx.x], term);
       if (eb == 0) {
         publish(&ws.zterms[s], z2);
-        publish(&tokens[s], n);
+        publish(&out.tokens[s], n);
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       last = __hip_atomic_fetch_add(ws.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
@@ -379,7 +495,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
     bal += published(&ws.terms[i]);
   for (int i = tid; i < S; i += kWave) {
     z += published(&ws.zterms[i]);
-    N += published(&tokens[i]);
+    N += published(&out.tokens[i]);
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
@@ -387,36 +503,31 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
     z += __shfl_xor(z, o, kWave);
     N += __shfl_xor(N, o, kWave);
   }
-  if (tid == 0) {
-    bal = N > 0 ? bal * E / ((double)k * N) : 0.0;
-    z = N > 0 ? z / N : 0.0;
-    tokens[S] = N;
-    loss[0] = (float)bal;
-    loss[1] = (float)z;
-    loss[2] = (float)(cb * bal + cz * z);
-  }
+  if (tid == 0) write_loss(bal, z, N, E, k, S, cb, cz, out);
 }
 
 // U tokens of every group at once, their logits loaded before their sequence
 // (the wave's first by search, then by walking) is known.
-template <int LPT, bool VEC>
+template <int LPT, int V, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
     const float* __restrict__ logits, const float* __restrict__ lse,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
     const int32_t* __restrict__ seq_offsets, const uint8_t* __restrict__ mask,
     const float* __restrict__ d_loss, int T, int E, int k, int S, float cb, float cz, int accumulate,
     float* d_logits) {
-  constexpr int G = kWave / LPT, U = kBalU;
+  constexpr int G = kWave / LPT, U = bal_u(V);
   const int lane = lane_id(), h = lane % LPT;
   const int tw = (blockIdx.x * kBalWaves + (threadIdx.x >> 6)) * G * U;  // the wave's first token
   if (tw >= T) return;
-  f32x4_t z[U];
+  f32x4_t z[U][V];
   float l[U];
   bool live[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int t = min(tw + u * G + lane / LPT, T - 1);
-    z[u] = load4<VEC>(logits + (size_t)t * E, 4 * h, E, -INFINITY);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      z[u][v] = load4_or<VEC, f32x4_t>(logits + (size_t)t * E, 4 * (h + v * LPT), E, -INFINITY);
     l[u] = lse[t];
     live[u] = mask == nullptr || mask[t] != 0;
   }
@@ -424,7 +535,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
   const float N = (float)tokens[S];
   // the current sequence of the lane's group: its rows [a, b), counts, factor
   int s = seq_find(seq_offsets, S, tw, T), a = T, b = T;
-  float c[4] = {0.f, 0.f, 0.f, 0.f}, kb = 0.f;
+  float c[V][4] = {}, kb = 0.f;
   auto enter = [&]() {
     if (s >= S) {
       a = b = T;
@@ -434,7 +545,11 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
     b = seq_off(seq_offsets, s + 1, T);
     const int32_t* cs = counts + (size_t)s * E;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = (float)cs[min(4 * h + i, E - 1)];
+    for (int v = 0; v < V; ++v) {
+      const i32x4_t n = load4_or<VEC, i32x4_t>(cs, 4 * (h + v * LPT), E, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[v][i] = (float)n[i];
+    }
     kb = cb * (float)E / ((float)k * N) / (float)tokens[s];
   };
   enter();
@@ -446,27 +561,35 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
       ++s;
       enter();
     }
-    f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+    f32x4_t d[V] = {};
     if (live[u] && t >= a && t < b) {  // the same in a token's lanes
-      float p[4], dot = 0.f;
+      float p[V][4], dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = exp_neg(z[u][i] - l[u]);
-        dot = fmaf(p[i], c[i], dot);
-      }
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[v][i] = exp_neg(z[u][v][i] - l[u]);
+          dot = fmaf(p[v][i], c[v][i], dot);
+        }
       dot = group_sum<LPT>(dot);
       const float kz = cz * 2.f * l[u] / N;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = gl * p[i] * fmaf(kb, c[i] - dot, kz);
-    }
-    float* out = d_logits + (size_t)t * E;
-    if (accumulate) d += load4<VEC>(out, 4 * h, E, 0.f);
-    if constexpr (VEC) {
-      if (4 * h < E) *reinterpret_cast<f32x4_t*>(out + 4 * h) = d;
-    } else {
+      for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (4 * h + i < E) out[4 * h + i] = d[i];
+        for (int i = 0; i < 4; ++i) d[v][i] = gl * p[v][i] * fmaf(kb, c[v][i] - dot, kz);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = 4 * (h + v * LPT);
+      float* out = d_logits + (size_t)t * E;
+      if (accumulate) d[v] += load4_or<VEC, f32x4_t>(out, e, E, 0.f);
+      if constexpr (VEC) {
+        if (e < E) *reinterpret_cast<f32x4_t*>(out + e) = d[v];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (e + i < E) out[e + i] = d[v][i];
+      }
     }
   }
 }
@@ -508,26 +631,31 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
   const BalWs ws = {(int32_t*)(w + l.counts), (float*)(w + l.psum), (int32_t*)(w + l.tokens),
                     (float*)(w + l.zsum), (uint32_t*)(w + l.ticket), (double*)(w + l.terms),
                     (double*)(w + l.zterms)};
+  const BalOut out = {counts, prob_sum, tokens, loss};
   const int C = balance_chunk(T, E);
-  // one workgroup at least: it also clears the second launch's ticket
-  const int grid = T > 0 ? (T + C - 1) / C : 1;
+  const bool one = balance_one(T, E, S);
+  // (no tokens in many sequences: the first workgroup clears the ticket)
+  const int grid = one ? 1 : max(1, (T + C - 1) / C);
   const bool vec = E % 4 == 0 && ((uintptr_t)logits & 15) == 0;
   ProfScope ps(MOE_KERNEL_BALANCE, s);
-#define MOE_BAL(L, V) \
-  balance_part_kernel<L, V><<<grid, kBalThreads, 0, s>>>(logits, topk_idx, seq_offsets, mask, T, E, k, S, C, lse, ws)
-#define MOE_BAL_LPT(L) do { if (vec) MOE_BAL(L, true); else MOE_BAL(L, false); } while (0)
-  switch (lanes_per_token(E)) {
-    case 8: MOE_BAL_LPT(8); break;
-    case 16: MOE_BAL_LPT(16); break;
-    case 32: MOE_BAL_LPT(32); break;
-    default: MOE_BAL_LPT(64);
-  }
+#define MOE_BAL(L, V, A, O)                                                                          \
+  balance_part_kernel<L, V, A, O><<<grid, kBalThreads, 0, s>>>(logits, topk_idx, seq_offsets, mask, T, \
+                                                               E, k, S, C, lse, ws, cb, cz, out)
+#define MOE_BAL_LPT(L, V)                                                             \
+  do {                                                                                \
+    if (one) { if (vec) MOE_BAL(L, V, true, true); else MOE_BAL(L, V, false, true); } \
+    else { if (vec) MOE_BAL(L, V, true, false); else MOE_BAL(L, V, false, false); }   \
+  } while (0)
+  if (E <= 32) MOE_BAL_LPT(8, 1);
+  else if (E <= 64) MOE_BAL_LPT(8, 2);
+  else if (E <= 128) MOE_BAL_LPT(16, 2);
+  else MOE_BAL_LPT(32, 2);
 #undef MOE_BAL_LPT
 #undef MOE_BAL
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  balance_sum_kernel<<<S * ((E + kSumCols - 1) / kSumCols), kSumThreads, 0, s>>>(seq_offsets, T, E, k, S, C, cb, cz,
-                                                                ws, counts, prob_sum, tokens, loss);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || one) return e;
+  balance_sum_kernel<<<S * ((E + kSumCols - 1) / kSumCols), kSumThreads, 0, s>>>(
+      seq_offsets, T, E, k, S, C, cb, cz, ws, out);
   return hipGetLastError();
 }
 
@@ -536,19 +664,18 @@ hipError_t launch_balance_loss_bwd(const float* logits, const float* lse, const 
                                    const uint8_t* mask, const float* d_loss, int T, int E, int k,
                                    int S, float cb, float cz, bool accumulate, float* d_logits,
                                    hipStream_t s) {
-  const bool vec = E % 4 == 0 && (((uintptr_t)logits | (uintptr_t)d_logits) & 15) == 0;
+  const bool vec = E % 4 == 0 && (((uintptr_t)logits | (uintptr_t)counts | (uintptr_t)d_logits) & 15) == 0;
   ProfScope ps(MOE_KERNEL_BALANCE_BWD, s);
-#define MOE_BAL(L, V)                                                                          \
-  balance_bwd_kernel<L, V><<<(T + bal_batch(L) - 1) / bal_batch(L), kBalThreads, 0, s>>>(logits, lse, counts, tokens, seq_offsets,    \
-                                                  mask, d_loss, T, E, k, S, cb, cz,            \
-                                                  accumulate ? 1 : 0, d_logits)
-#define MOE_BAL_LPT(L) do { if (vec) MOE_BAL(L, true); else MOE_BAL(L, false); } while (0)
-  switch (lanes_per_token(E)) {
-    case 8: MOE_BAL_LPT(8); break;
-    case 16: MOE_BAL_LPT(16); break;
-    case 32: MOE_BAL_LPT(32); break;
-    default: MOE_BAL_LPT(64);
-  }
+  const int batch = batch_of(E), grid = (T + batch - 1) / batch;
+#define MOE_BAL(L, V, A)                                                                       \
+  balance_bwd_kernel<L, V, A><<<grid, kBalThreads, 0, s>>>(logits, lse, counts, tokens,        \
+                                                           seq_offsets, mask, d_loss, T, E, k, \
+                                                           S, cb, cz, accumulate ? 1 : 0, d_logits)
+#define MOE_BAL_LPT(L, V) do { if (vec) MOE_BAL(L, V, true); else MOE_BAL(L, V, false); } while (0)
+  if (E <= 32) MOE_BAL_LPT(8, 1);
+  else if (E <= 64) MOE_BAL_LPT(8, 2);
+  else if (E <= 128) MOE_BAL_LPT(16, 2);
+  else MOE_BAL_LPT(32, 2);
 #undef MOE_BAL_LPT
 #undef MOE_BAL
   return hipGetLastError();

@@ -253,6 +253,41 @@ def test_nothing_live():
 
 
 @gpu
+@pytest.mark.parametrize("E,T", [(8, 511), (32, 512), (32, 513), (33, 256), (64, 257), (65, 31), (128, 129),
+                                 (132, 64), (256, 65), (256, 3)])
+@pytest.mark.parametrize("gaps", [False, True])
+def test_few_tokens(E, T, gaps):
+    """Both sides of where one workgroup does the whole loss; sequences that are empty, first, last
+    and in the middle, and rows before the first and behind the last."""
+    rng = np.random.default_rng(E * T)
+    z = rng.standard_normal((T, E)).astype(np.float32) * 3
+    k = min(E, 5)
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :k].astype(np.int32)
+    idx[T // 2] = -1
+    live = rng.random(T) >= 0.2
+    cut = max(1, T // 3)
+    off = np.array([1, 1, cut, T - 1, T - 1] if gaps else [0, T], np.int32)
+    ref = reference(z, idx, k, off, live, 0.02, 0.003)
+    f = moe.moe_balance_loss(dev(z), dev(idx), 0.02, 0.003, seq_offsets=dev(off),
+                             token_mask=dev(live.astype(np.uint8)))
+    d = moe.moe_balance_loss_bwd(dev(z), f, k, 0.02, 0.003, seq_offsets=dev(off),
+                                 token_mask=dev(live.astype(np.uint8)))
+    compare(f, d, ref, E)
+
+
+@gpu
+@pytest.mark.parametrize("S", [1, 3, 40])
+def test_no_tokens(S):
+    z, idx = torch.zeros(0, 12, device=DEV), torch.zeros(0, 2, dtype=torch.int32, device=DEV)
+    off = torch.zeros(S + 1, dtype=torch.int32, device=DEV)
+    out = {n: torch.full(shape, 7, dtype=dt, device=DEV) for n, shape, dt in (
+        ("counts", (S, 12), torch.int32), ("prob_sum", (S, 12), torch.float32),
+        ("tokens", (S + 1,), torch.int32), ("loss", (3,), torch.float32))}
+    f = moe.moe_balance_loss(z, idx, 1.0, 1.0, seq_offsets=off, out=out)
+    assert not any(f[n].any() for n in out)
+
+
+@gpu
 def test_no_gradient_without_imbalance():
     """Even counts: the balance gradient is p (c - c) = 0 up to rounding of sum p."""
     E = 16
