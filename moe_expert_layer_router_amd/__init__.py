@@ -23,6 +23,7 @@ freshly allocated torch tensors; each also accepts preallocated outputs via
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional
 
@@ -400,7 +401,10 @@ def moe_route_bwd(d_topk_w: torch.Tensor, topk_w: torch.Tensor, topk_idx: torch.
 
 # ---------------------------------------------------------------------------
 # Auxiliary losses, dropout.  Their arguments are checked here for device, type
-# and shape (the library sees plain pointers).
+# and shape (the library sees plain pointers).  A call of a small batch takes no
+# longer on the GPU than on the host, so each function first asks in one
+# expression whether everything fits; where it does not (an output to allocate,
+# a mistake), the checks one by one allocate or name the argument.
 # ---------------------------------------------------------------------------
 
 def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, dev, optional: bool = False):
@@ -443,6 +447,14 @@ def _into(o: Dict[str, torch.Tensor], name: str, shape, dtype, dev) -> int:
         o[name] = torch.empty(shape, dtype=dtype, device=dev)
         return o[name].data_ptr()
     return _arg(o[name], name, dtype, shape, dev)
+
+
+@functools.lru_cache(maxsize=64)
+def _balance_ws_bytes(T: int, E: int, S: int) -> int:
+    nb = lib.moe_balance_ws_bytes(T, E, S)
+    if nb < 0:
+        _check(int(nb), "moe_balance_ws_bytes")
+    return int(nb)
 
 
 def _work(nbytes: int, dev, ws: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
@@ -512,18 +524,51 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
     Returns dict loss [3] (balance, z, balance_coef * balance + z_coef * z), counts [S,E] int32,
     prob_sum [S,E], tokens [S+1] int32 (live rows of each sequence, then of all), lse [T], and the
     workspace ws used (pass it and the dict back in to allocate nothing)."""
+    f32, i32, d = torch.float32, torch.int32, logits.get_device()
+    o = dict(out) if out else {}
+    if len(o) >= 5 and ws is not None and logits.dim() == 2 and topk_idx.dim() == 2:
+        T, E = logits.shape
+        k = topk_idx.shape[1]
+        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        cnt, q, n, lse, loss = map(o.get, ("counts", "prob_sum", "tokens", "lse", "loss"))
+        if (d >= 0 and d == torch._C._cuda_getDevice() and S > 0
+                and cnt is not None and q is not None and n is not None and lse is not None
+                and loss is not None
+                and logits.dtype is f32 and logits.is_contiguous()
+                and topk_idx.dtype is i32 and topk_idx.get_device() == d
+                and topk_idx.shape[0] == T and topk_idx.is_contiguous()
+                and (seq_offsets is None or seq_offsets.dtype is i32 and seq_offsets.get_device() == d
+                     and seq_offsets.dim() == 1 and seq_offsets.is_contiguous())
+                and (token_mask is None or token_mask.dtype is torch.uint8
+                     and token_mask.get_device() == d and token_mask.shape == (T,)
+                     and token_mask.is_contiguous())
+                and cnt.dtype is i32 and cnt.get_device() == d and cnt.shape == (S, E)
+                and cnt.is_contiguous()
+                and q.dtype is f32 and q.get_device() == d and q.shape == (S, E) and q.is_contiguous()
+                and n.dtype is i32 and n.get_device() == d and n.shape == (S + 1,) and n.is_contiguous()
+                and lse.dtype is f32 and lse.get_device() == d and lse.shape == (T,)
+                and lse.is_contiguous()
+                and loss.dtype is f32 and loss.get_device() == d and loss.shape == (3,)
+                and loss.is_contiguous()
+                and ws.get_device() == d and ws.is_contiguous()
+                and ws.nbytes >= _balance_ws_bytes(T, E, S)):
+            rc = lib.moe_balance_loss(
+                logits.data_ptr(), topk_idx.data_ptr(),
+                None if seq_offsets is None else seq_offsets.data_ptr(),
+                None if token_mask is None else token_mask.data_ptr(), T, E, k, S, balance_coef, z_coef,
+                cnt.data_ptr(), q.data_ptr(), n.data_ptr(), lse.data_ptr(), loss.data_ptr(),
+                ws.data_ptr(), ws.nbytes, torch._C._cuda_getCurrentRawStream(d))
+            if rc != 0:
+                _check(rc, "moe_balance_loss")
+            o["ws"] = ws
+            return o
     dev = _device(logits)
     T, E = _shape2(logits, "logits")
     k = _shape2(topk_idx, "topk_idx")[1]
     S, off = _sequences(seq_offsets, dev)
-    f32, i32 = torch.float32, torch.int32
-    o = dict(out or {})
     a = [_arg(logits, "logits", f32, (T, E), dev), _arg(topk_idx, "topk_idx", i32, (T, k), dev), off,
          _arg(token_mask, "token_mask", torch.uint8, (T,), dev, optional=True)]
-    nb = lib.moe_balance_ws_bytes(T, E, S)
-    if nb < 0:
-        _check(int(nb), "moe_balance_ws_bytes")
-    o["ws"] = _work(int(nb), dev, ws)
+    o["ws"] = _work(_balance_ws_bytes(T, E, S), dev, ws)
     _check(lib.moe_balance_loss(*a, T, E, k, S, balance_coef, z_coef,
                                 _into(o, "counts", (S, E), i32, dev),
                                 _into(o, "prob_sum", (S, E), f32, dev),
@@ -542,10 +587,39 @@ def moe_balance_loss_bwd(logits: torch.Tensor, fwd: Dict[str, torch.Tensor], k: 
     """Gradient of loss[2] wrt the logits; fwd: moe_balance_loss's dict (lse, counts, tokens) for
     the same logits, k, seq_offsets and token_mask; d_loss [1] fp32: the upstream gradient (None:
     1).  Returns d_logits [T,E] (out, added to with accumulate=True)."""
+    f32, i32, d = torch.float32, torch.int32, logits.get_device()
+    if out is not None and logits.dim() == 2:
+        T, E = logits.shape
+        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        lse, cnt, n = fwd["lse"], fwd["counts"], fwd["tokens"]
+        if (d >= 0 and d == torch._C._cuda_getDevice() and S > 0
+                and logits.dtype is f32 and logits.is_contiguous()
+                and lse.dtype is f32 and lse.get_device() == d and lse.shape == (T,)
+                and lse.is_contiguous()
+                and cnt.dtype is i32 and cnt.get_device() == d and cnt.shape == (S, E)
+                and cnt.is_contiguous()
+                and n.dtype is i32 and n.get_device() == d and n.shape == (S + 1,) and n.is_contiguous()
+                and (seq_offsets is None or seq_offsets.dtype is i32 and seq_offsets.get_device() == d
+                     and seq_offsets.dim() == 1 and seq_offsets.is_contiguous())
+                and (token_mask is None or token_mask.dtype is torch.uint8
+                     and token_mask.get_device() == d and token_mask.shape == (T,)
+                     and token_mask.is_contiguous())
+                and (d_loss is None or d_loss.dtype is f32 and d_loss.get_device() == d
+                     and d_loss.shape == (1,))
+                and out.dtype is f32 and out.get_device() == d and out.shape == (T, E)
+                and out.is_contiguous()):
+            rc = lib.moe_balance_loss_bwd(
+                logits.data_ptr(), lse.data_ptr(), cnt.data_ptr(), n.data_ptr(),
+                None if seq_offsets is None else seq_offsets.data_ptr(),
+                None if token_mask is None else token_mask.data_ptr(),
+                None if d_loss is None else d_loss.data_ptr(), T, E, k, S, balance_coef, z_coef,
+                1 if accumulate else 0, out.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
+            if rc != 0:
+                _check(rc, "moe_balance_loss_bwd")
+            return out
     dev = _device(logits)
     T, E = _shape2(logits, "logits")
     S, off = _sequences(seq_offsets, dev)
-    f32, i32 = torch.float32, torch.int32
     if accumulate and out is None:
         raise ValueError("accumulate=True needs out")
     o = {"d_logits": out}
@@ -566,6 +640,29 @@ def moe_combine_dropout(y_perm: torch.Tensor, topk_w: Optional[torch.Tensor], de
     """moe_combine with dropout (probability p) and the residual [T,H] added.  rng [2] int64 on the
     GPU: seed and offset of the counter-based generator; the same rng goes to
     moe_combine_dropout_bwd.  Returns y [T,H] (out may be residual)."""
+    dt, d = y_perm.dtype, y_perm.get_device()
+    if out is not None and topk_w is not None and y_perm.dim() == 2 and topk_w.dim() == 2:
+        H, k = y_perm.shape[1], topk_w.shape[1]
+        if (d >= 0 and d == torch._C._cuda_getDevice()
+                and (dt is torch.bfloat16 or dt is torch.float32) and y_perm.is_contiguous()
+                and topk_w.dtype is torch.float32 and topk_w.get_device() == d
+                and topk_w.shape[0] == T and topk_w.is_contiguous()
+                and dest_row.dtype is torch.int32 and dest_row.get_device() == d
+                and dest_row.shape == (T * k,) and dest_row.is_contiguous()
+                and (residual is None or residual.dtype is dt and residual.get_device() == d
+                     and residual.shape == (T, H) and residual.is_contiguous())
+                and rng.dtype is torch.int64 and rng.get_device() == d and rng.shape == (2,)
+                and rng.is_contiguous()
+                and out.dtype is dt and out.get_device() == d and out.shape == (T, H)
+                and out.is_contiguous()):
+            rc = lib.moe_combine_dropout(
+                y_perm.data_ptr(), topk_w.data_ptr(), dest_row.data_ptr(),
+                None if residual is None else residual.data_ptr(), p, rng.data_ptr(), T, H, k,
+                MOE_BF16 if dt is torch.bfloat16 else MOE_F32, out.data_ptr(),
+                torch._C._cuda_getCurrentRawStream(d))
+            if rc != 0:
+                _check(rc, "moe_combine_dropout")
+            return out
     dev = _device(y_perm)
     R_cap, H = _shape2(y_perm, "y_perm")
     dt = _row_type(y_perm, "y_perm")
@@ -591,12 +688,39 @@ def moe_combine_dropout_bwd(dy: torch.Tensor, y_perm: torch.Tensor, topk_w: torc
                             out: Optional[Dict[str, torch.Tensor]] = None):
     """Backward of moe_combine_dropout under its p and rng (the residual's gradient is dy).
     Returns dict dy_perm [R_cap,H], d_topk_w [T,k]."""
+    dt, f32, d = dy.dtype, torch.float32, dy.get_device()
+    o = dict(out) if out else {}
+    dyp, dw = o.get("dy_perm"), o.get("d_topk_w")
+    if (dyp is not None and dw is not None and dy.dim() == 2 and topk_w.dim() == 2
+            and y_perm.dim() == 2):
+        T, H = dy.shape
+        k = topk_w.shape[1]
+        if (d >= 0 and d == torch._C._cuda_getDevice()
+                and (dt is torch.bfloat16 or dt is torch.float32) and dy.is_contiguous()
+                and y_perm.dtype is dt and y_perm.get_device() == d and y_perm.shape[1] == H
+                and y_perm.is_contiguous()
+                and topk_w.dtype is f32 and topk_w.get_device() == d and topk_w.shape[0] == T
+                and topk_w.is_contiguous()
+                and dest_row.dtype is torch.int32 and dest_row.get_device() == d
+                and dest_row.shape == (T * k,) and dest_row.is_contiguous()
+                and rng.dtype is torch.int64 and rng.get_device() == d and rng.shape == (2,)
+                and rng.is_contiguous()
+                and dyp.dtype is dt and dyp.get_device() == d and dyp.shape == y_perm.shape
+                and dyp.is_contiguous()
+                and dw.dtype is f32 and dw.get_device() == d and dw.shape == (T, k)
+                and dw.is_contiguous()):
+            rc = lib.moe_combine_dropout_bwd(
+                dy.data_ptr(), y_perm.data_ptr(), topk_w.data_ptr(), dest_row.data_ptr(), p,
+                rng.data_ptr(), T, H, k, MOE_BF16 if dt is torch.bfloat16 else MOE_F32,
+                dyp.data_ptr(), dw.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
+            if rc != 0:
+                _check(rc, "moe_combine_dropout_bwd")
+            return o
     dev = _device(dy)
     T, H = _shape2(dy, "dy")
     k = _shape2(topk_w, "topk_w")[1]
     R_cap = _shape2(y_perm, "y_perm")[0]
-    dt, f32 = _row_type(dy, "dy"), torch.float32
-    o = dict(out or {})
+    dt = _row_type(dy, "dy")
     a = [_arg(dy, "dy", dt, (T, H), dev), _arg(y_perm, "y_perm", dt, (R_cap, H), dev),
          _arg(topk_w, "topk_w", f32, (T, k), dev),
          _arg(dest_row, "dest_row", torch.int32, (T * k,), dev)]

@@ -399,3 +399,45 @@ def test_route_bwd_add(dtype, T, H, E, k):
     zero = moe.moe_route_bwd_add(dev(dw), dev(gate), dev(idx), torch.zeros_like(a2), x, w)
     if not (dtype == "bf16" and E % 4):
         assert torch.equal(zero["d_logits"], moe.moe_route_bwd(dev(dw), dev(gate), dev(idx), x, w)["d_logits"])
+
+
+@gpu
+def test_binding_refusals_of_whole_calls():
+    """Calls that give every tensor: as they are they pass, with any one tensor of another type, shape,
+    device or order they are refused."""
+    z = torch.randn(6, 8, device=DEV)
+    a = dict(logits=z, topk_idx=z.topk(2, dim=1).indices.int(), balance_coef=0.1, z_coef=0.2,
+             seq_offsets=torch.tensor([0, 2, 6], dtype=torch.int32, device=DEV),
+             token_mask=torch.ones(6, dtype=torch.uint8, device=DEV))
+    want = moe.moe_balance_loss(**a)
+    out = {n: torch.empty_like(t) for n, t in want.items() if n != "ws"}
+    a.update(ws=want["ws"], out=out)
+    got = moe.moe_balance_loss(**a)
+    assert got["ws"] is a["ws"] and all(got[n] is out[n] and torch.equal(got[n], want[n]) for n in out)
+    b = {n: a[n] for n in ("logits", "balance_coef", "z_coef", "seq_offsets", "token_mask")}
+    b.update(fwd=got, k=2, d_loss=torch.ones(1, device=DEV), out=torch.empty(6, 8, device=DEV))
+    d = moe.moe_balance_loss_bwd(**{**b, "out": None})
+    assert moe.moe_balance_loss_bwd(**b) is b["out"] and torch.equal(b["out"], d)
+
+    def bad(t):
+        yield t.cpu()
+        yield t.double()
+        yield t[1:]
+        if t.numel() > 1:  # (one element is dense at any stride)
+            yield torch.stack([t, t], -1)[..., 0]
+        yield t.unsqueeze(0)
+
+    def refused(call, args):
+        with pytest.raises(ValueError):
+            call(**args)
+
+    for call, args, inner in ((moe.moe_balance_loss, a, "out"), (moe.moe_balance_loss_bwd, b, "fwd")):
+        for name, t in args.items():
+            if torch.is_tensor(t) and name != "ws":
+                for u in bad(t):
+                    refused(call, {**args, name: u})
+        for name in ("lse", "counts", "tokens") + (("loss", "prob_sum") if inner == "out" else ()):
+            for u in bad(args[inner][name]):
+                refused(call, {**args, inner: {**args[inner], name: u}})
+    for u in (a["ws"].cpu(), a["ws"][:16], torch.stack([a["ws"]] * 2, -1)[:, 0]):
+        refused(moe.moe_balance_loss, {**a, "ws": u})

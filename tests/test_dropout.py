@@ -249,3 +249,40 @@ def test_binding_refusals():
         moe.moe_combine_dropout(**{**a, "p": 1.0})
     with pytest.raises(ValueError, match="GPU"):
         moe.moe_combine_dropout(yp.cpu(), w, dest, 4, 0.1, state)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_binding_refusals_of_whole_calls(dtype):
+    """Calls that give every tensor: as they are they pass, with any one tensor of another type, shape,
+    device or order they are refused."""
+    rand = lambda *s: torch.randn(*s, device=DEV).to(dtype)
+    a = dict(y_perm=rand(8, 16), topk_w=torch.rand(4, 2, device=DEV),
+             dest_row=torch.arange(8, dtype=torch.int32, device=DEV), T=4, p=0.1,
+             rng=torch.tensor([3, 5], device=DEV), residual=rand(4, 16), out=rand(4, 16))
+    want = moe.moe_combine_dropout(**{**a, "out": None})
+    assert moe.moe_combine_dropout(**a) is a["out"] and torch.equal(a["out"], want)
+    b = {n: a[n] for n in ("y_perm", "topk_w", "dest_row", "p", "rng")}
+    b.update(dy=rand(4, 16), out=dict(dy_perm=rand(8, 16), d_topk_w=torch.zeros(4, 2, device=DEV)))
+    fresh = moe.moe_combine_dropout_bwd(**{**b, "out": None})
+    got = moe.moe_combine_dropout_bwd(**b)
+    assert all(got[n] is b["out"][n] and torch.equal(got[n], fresh[n]) for n in b["out"])
+
+    def bad(t):
+        yield t.cpu()
+        yield t.double()
+        yield t[1:]
+        if t.numel() > 1:  # (one element is dense at any stride)
+            yield torch.stack([t, t], -1)[..., 0]
+        yield t.unsqueeze(0)
+
+    for call, args in ((moe.moe_combine_dropout, a), (moe.moe_combine_dropout_bwd, b)):
+        for name, t in args.items():
+            if torch.is_tensor(t):
+                for u in bad(t):
+                    with pytest.raises(ValueError):
+                        call(**{**args, name: u})
+    for name, t in b["out"].items():
+        for u in bad(t):
+            with pytest.raises(ValueError):
+                moe.moe_combine_dropout_bwd(**{**b, "out": {**b["out"], name: u}})
