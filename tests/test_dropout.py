@@ -271,7 +271,8 @@ def test_binding_refusals_of_whole_calls(dtype):
     def bad(t):
         yield t.cpu()
         yield t.double()
-        yield t[1:]
+        if t is not a["y_perm"]:  # (whose row count no other tensor gives)
+            yield t[1:]
         if t.numel() > 1:  # (one element is dense at any stride)
             yield torch.stack([t, t], -1)[..., 0]
         yield t.unsqueeze(0)
