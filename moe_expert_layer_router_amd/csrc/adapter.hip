@@ -46,6 +46,179 @@ __device__ __forceinline__ f32x4_t step(u32x4_t a, u32x4_t b, f32x4_t d) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// rows in adapter order (for the weight gradients)
+// ---------------------------------------------------------------------------
+
+// Rows of one adapter in row order, cut into chunks of `chunk`: an adapter of
+// one chunk (or no row) writes its gradient whole, one of more writes fp32
+// partials that a second pass adds in chunk order.  count = chunks in all, each
+// {id, begin, end, slot}.
+struct ChunkPlan {
+  int32_t* count;
+  int32_t* chunks;   // [upper][4]
+  int32_t* first;    // [n_ids] first slot of an id of several chunks
+  int32_t* offsets;  // [n_ids + 1] rows of an id in the order list
+};
+
+// The adapter of row r, or -1, by the forward's rule.
+struct RowIds {
+  const int32_t* row_id;
+  const int32_t* src_row;
+  int R, x_rows, n_ids;
+  __device__ __forceinline__ int operator()(int r) const {
+    const int a = row_id[r], s = src_row != nullptr ? src_row[r] : r;
+    return a >= 0 && a < n_ids && s >= 0 && s < x_rows ? a : -1;
+  }
+};
+
+constexpr int kSortBlocks = 128;  // at most, so that a block adds few counts
+int sort_rows(int R) {
+  return R <= 2048 ? (R + 255) / 256 * 256 + 256 * (R == 0) : max(1024, ((R + kSortBlocks - 1) / kSortBlocks + 255) / 256 * 256);
+}
+
+// Inclusive prefix sum over the first 256 threads of a workgroup (s: a word per
+// wave).
+__device__ __forceinline__ int block_scan(int v, int* s) {
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int x = __shfl_up(v, o, kWave);
+    v += lane >= o ? x : 0;
+  }
+  if (lane == kWave - 1) s[wave] = v;
+  lds_barrier();
+#pragma unroll
+  for (int w = 0; w < 3; ++w) v += w < wave ? s[w] : 0;
+  return v;
+}
+
+// What the backward needs to order the rows by adapter.
+struct RowOrder {
+  RowIds ids;
+  int per, nblk;    // rows of a block, blocks
+  int32_t* counts;  // [nblk][n_ids] rows of each adapter (more than one block)
+  int chunk;
+  ChunkPlan plan;
+  int32_t* order;   // out
+};
+
+// The rows in adapter order, rows of one adapter in row order: every block adds
+// the counts of the blocks before it (and all, for the adapters' offsets), its
+// four waves take a quarter of its rows each, 64 at a time, and a row's place
+// is its wave's cursor for the adapter plus the lanes before it that have the
+// same.  The first block also writes the chunks.  Waves after the fourth only
+// keep the barriers; mem: kOrderLds bytes of LDS.
+constexpr int kOrderLds = 4 * (4 * kMaxE + 3 * 8);
+static_assert(kMaxE == 256, "a thread per adapter");
+__device__ __forceinline__ void order_block(const RowOrder& o, int b, char* mem) {
+  int(*s_cur)[kMaxE] = reinterpret_cast<int(*)[kMaxE]>(mem);
+  int *s_t = reinterpret_cast<int*>(mem) + 4 * kMaxE, *s_n = s_t + 8, *s_m = s_n + 8;
+  const RowIds& ids = o.ids;
+  const ChunkPlan& plan = o.plan;
+  const int per = o.per, nblk = o.nblk, chunk = o.chunk;
+  const int32_t* counts = o.counts;
+  int32_t* order = o.order;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = lane_id();
+  int before = 0, all = 0;
+  if (nblk > 1 && tid < ids.n_ids) {
+#pragma unroll 8
+    for (int i = 0; i < nblk; ++i) {
+      const int c = counts[(size_t)i * ids.n_ids + tid];
+      before += i < b ? c : 0;
+      all += c;
+    }
+  }
+  const bool key = tid < kMaxE;  // this thread's adapter is tid
+  if (key)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s_cur[w][tid] = 0;
+  __syncthreads();
+  const int q = (per + 3) / 4;  // rows of a wave
+  const int r0 = b * per + wave * q, r1 = wave < 4 ? min(min(ids.R, (b + 1) * per), r0 + q) : r0;
+  constexpr int KR = 8;  // 64-row steps of a wave whose adapters stay in registers
+  int keep[KR];
+#pragma unroll
+  for (int j = 0; j < KR; ++j) {
+    const int r = r0 + j * kWave + lane;
+    keep[j] = r < r1 ? ids(r) : -1;
+  }
+#pragma unroll
+  for (int j = 0; j < KR; ++j)
+    if (keep[j] >= 0) atomicAdd(&s_cur[wave][keep[j]], 1);
+  for (int r = r0 + KR * kWave + lane; r < r1; r += kWave) {
+    const int a = ids(r);
+    if (a >= 0) atomicAdd(&s_cur[wave][a], 1);
+  }
+  if (nblk <= 1) {
+    lds_barrier();
+    if (key)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) all += s_cur[w][tid];
+  }
+  const int end = block_scan(all, s_t), begin = end - all;
+  int at = begin + before;
+  if (key)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {  // counts of the waves to their cursors
+      const int n = s_cur[w][tid];
+      s_cur[w][tid] = at;
+      at += n;
+    }
+  __syncthreads();
+  auto place = [&](int r, int a) {
+    int rank = 0, same_n = 0;
+    for (uint64_t todo = __ballot(a >= 0); todo != 0;) {
+      const int cur = __builtin_amdgcn_readlane(a, __builtin_ctzll(todo));
+      const uint64_t same = __ballot(a == cur);
+      todo &= ~same;
+      if (a == cur) {
+        rank = __popcll(same & ((1ull << lane) - 1ull));
+        same_n = __popcll(same);
+      }
+    }
+    const int from = a >= 0 ? s_cur[wave][a] : 0;
+    asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
+    if (a >= 0) {
+      order[from + rank] = r;
+      if (rank == 0) s_cur[wave][a] = from + same_n;
+    }
+    asm volatile("" ::: "memory");
+  };
+#pragma unroll
+  for (int j = 0; j < KR; ++j)
+    if (r0 + j * kWave < r1) place(r0 + j * kWave + lane, keep[j]);
+  for (int rb = r0 + KR * kWave; rb < r1; rb += kWave)
+    place(rb + lane, rb + lane < r1 ? ids(rb + lane) : -1);
+  if (b != 0) return;
+  // the chunks, and the slots of adapters of several
+  const int n = tid < ids.n_ids ? max(1, (all + chunk - 1) / chunk) : 0;
+  const int m = n > 1 ? n : 0;
+  const int n_end = block_scan(n, s_n), m_end = block_scan(m, s_m);
+  if (tid == kMaxE - 1) *plan.count = n_end;
+  if (tid >= ids.n_ids) return;
+  plan.offsets[tid] = begin;
+  if (tid == ids.n_ids - 1) plan.offsets[tid + 1] = end;
+  const int slot = m_end - m;
+  plan.first[tid] = slot;
+  for (int c = 0; c < n; ++c) {
+    int32_t* e = plan.chunks + 4 * (size_t)(n_end - n + c);
+    e[0] = tid;
+    e[1] = begin + c * chunk;
+    e[2] = min(end, begin + (c + 1) * chunk);
+    e[3] = n > 1 ? slot + c : -1;
+  }
+}
+
+__global__ __launch_bounds__(256) void adapter_order_kernel(RowOrder o) {
+  __shared__ __align__(16) char mem[kOrderLds];
+  order_block(o, blockIdx.x, mem);
+}
+
+// ---------------------------------------------------------------------------
+// forward and data gradients
+// ---------------------------------------------------------------------------
+
 struct AdapterArgs {
   const char* x;            // [x_rows][ldx]
   const int32_t* src_row;   // token row of row r, or null: r
@@ -194,15 +367,26 @@ __device__ __forceinline__ void regroup(const AdapterArgs& p, int row0, char* ld
 // c ^ (r % 8): fragment reads hit all banks), y into registers, where the
 // second product's results meet it through LDS.  No barrier: only the wave
 // that loaded reads.
-template <bool BF16, int RT, int MT, int NW>
-__global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
+//
+// ORDER, in a backward with weight gradients: the first `oblocks` workgroups (a
+// multiple of 8, the XCDs) order the rows by adapter instead, for the launches
+// after this one (8285 rows: one launch of 5 us less).
+template <bool BF16, int RT, int MT, int NW, bool ORDER>
+__global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p, int oblocks, RowOrder o) {
   using E = Elem<BF16>;
   using S = AdapterLds<BF16, RT, MT>;
   constexpr int RL = S::RL;
   extern __shared__ __align__(16) char lds[];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 15, g = lane >> 4;
-  const int bid = xcd_remap(blockIdx.x, gridDim.x);
+  if constexpr (ORDER) {
+    if ((int)blockIdx.x < oblocks) {
+      if ((int)blockIdx.x < o.nblk) order_block(o, blockIdx.x, lds);
+      return;
+    }
+  }
+  const int nob = ORDER ? oblocks : 0;
+  const int bid = xcd_remap(blockIdx.x - nob, gridDim.x - nob);
   const int tile = bid / p.splits, split = bid % p.splits;
   const int row0 = tile * p.rows;
 
@@ -546,11 +730,18 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p) {
 }
 
 template <bool BF16, int RT, int MT, int NW>
-hipError_t launch_one(const AdapterArgs& p, hipStream_t s) {
+hipError_t launch_one(const AdapterArgs& p, const RowOrder& o, hipStream_t s) {
   constexpr int lds = NW * AdapterLds<BF16, RT, MT>::WAVE;
   static_assert(lds <= 160 * 1024, "the LDS of one CU");
+  static_assert(NW < 4 || lds >= kOrderLds, "the order's LDS");
   const int tiles = (p.R + p.rows - 1) / p.rows;
-  adapter_kernel<BF16, RT, MT, NW><<<tiles * p.splits, NW * kWave, lds, s>>>(p);
+  if (NW >= 4 && o.nblk > 1) {
+    const int oblocks = (o.nblk + 7) / 8 * 8;
+    adapter_kernel<BF16, RT, MT, NW, NW >= 4><<<oblocks + tiles * p.splits, NW * kWave, lds, s>>>(p, oblocks, o);
+    return hipGetLastError();
+  }
+  adapter_kernel<BF16, RT, MT, NW, false><<<tiles * p.splits, NW * kWave, lds, s>>>(p, 0, o);
+  if (o.nblk > 1) adapter_order_kernel<<<o.nblk, 256, 0, s>>>(o);
   return hipGetLastError();
 }
 
@@ -568,7 +759,7 @@ hipError_t launch_one(const AdapterArgs& p, hipStream_t s) {
 // where two workgroups of eight do not fit its LDS (8191 rows of rank 64: 29 us
 // for 34).
 template <bool BF16>
-hipError_t launch_adapter(AdapterArgs p, hipStream_t s) {
+hipError_t launch_adapter(AdapterArgs p, const RowOrder& o, hipStream_t s) {
   const int most = p.rank > 64 ? 32 : 16;
   double best = 0.0;
   for (int rows = 1; rows <= most; rows *= 2)
@@ -592,8 +783,8 @@ hipError_t launch_adapter(AdapterArgs p, hipStream_t s) {
     constexpr int wave = AdapterLds<BF16, RT, mt>::WAVE;                                        \
     if constexpr (8 * wave <= 160 * 1024)                                                       \
       if (wgs <= (8 * wave <= 80 * 1024 ? 4 : 1) * kCUs)                                        \
-        return launch_one<BF16, RT, mt, 8>(p, s);                                               \
-    return launch_one<BF16, RT, mt, 4 * wave <= 160 * 1024 ? 4 : 2>(p, s);                      \
+        return launch_one<BF16, RT, mt, 8>(p, o, s);                                               \
+    return launch_one<BF16, RT, mt, 4 * wave <= 160 * 1024 ? 4 : 2>(p, o, s);                      \
   } while (0)
   if (rt <= 1) MOE_AD(1);
   else if (rt <= 2) MOE_AD(2);
@@ -605,161 +796,6 @@ hipError_t launch_adapter(AdapterArgs p, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // weight gradients
 // ---------------------------------------------------------------------------
-
-// Rows of one adapter in row order, cut into chunks of `chunk`: an adapter of
-// one chunk (or no row) writes its gradient whole, one of more writes fp32
-// partials that a second pass adds in chunk order.  count = chunks in all, each
-// {id, begin, end, slot}.
-struct ChunkPlan {
-  int32_t* count;
-  int32_t* chunks;   // [upper][4]
-  int32_t* first;    // [n_ids] first slot of an id of several chunks
-  int32_t* offsets;  // [n_ids + 1] rows of an id in the order list
-};
-
-// The adapter of row r, or -1, by the forward's rule.
-struct RowIds {
-  const int32_t* row_id;
-  const int32_t* src_row;
-  int R, x_rows, n_ids;
-  __device__ __forceinline__ int operator()(int r) const {
-    const int a = row_id[r], s = src_row != nullptr ? src_row[r] : r;
-    return a >= 0 && a < n_ids && s >= 0 && s < x_rows ? a : -1;
-  }
-};
-
-constexpr int kSortBlocks = 128;  // at most, so that a block adds few counts
-int sort_rows(int R) {
-  return R <= 2048 ? (R + 255) / 256 * 256 + 256 * (R == 0) : max(1024, ((R + kSortBlocks - 1) / kSortBlocks + 255) / 256 * 256);
-}
-
-// Inclusive prefix sum over the 256 threads of a workgroup (s: 4 words).
-__device__ __forceinline__ int block_scan(int v, int* s) {
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int x = __shfl_up(v, o, kWave);
-    v += lane >= o ? x : 0;
-  }
-  if (lane == kWave - 1) s[wave] = v;
-  lds_barrier();
-#pragma unroll
-  for (int w = 0; w < 3; ++w) v += w < wave ? s[w] : 0;
-  return v;
-}
-
-// What the backward needs to order the rows by adapter.
-struct RowOrder {
-  RowIds ids;
-  int per, nblk;    // rows of a block, blocks
-  int32_t* counts;  // [nblk][n_ids] rows of each adapter (more than one block)
-  int chunk;
-  ChunkPlan plan;
-  int32_t* order;   // out
-};
-
-// The rows in adapter order, rows of one adapter in row order: every block adds
-// the counts of the blocks before it (and all, for the adapters' offsets), its
-// four waves take a quarter of its rows each, 64 at a time, and a row's place
-// is its wave's cursor for the adapter plus the lanes before it that have the
-// same.  The first block also writes the chunks.
-__device__ __forceinline__ void order_block(const RowOrder& o, int b) {
-  __shared__ int s_cur[4][kMaxE], s_t[4], s_n[4], s_m[4];
-  const RowIds& ids = o.ids;
-  const ChunkPlan& plan = o.plan;
-  const int per = o.per, nblk = o.nblk, chunk = o.chunk;
-  const int32_t* counts = o.counts;
-  int32_t* order = o.order;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = lane_id();
-  int before = 0, all = 0;
-  if (nblk > 1 && tid < ids.n_ids) {
-#pragma unroll 8
-    for (int i = 0; i < nblk; ++i) {
-      const int c = counts[(size_t)i * ids.n_ids + tid];
-      before += i < b ? c : 0;
-      all += c;
-    }
-  }
-#pragma unroll
-  for (int w = 0; w < 4; ++w) s_cur[w][tid] = 0;
-  __syncthreads();
-  const int q = (per + 3) / 4;  // rows of a wave
-  const int r0 = b * per + wave * q, r1 = min(min(ids.R, (b + 1) * per), r0 + q);
-  constexpr int KR = 8;  // 64-row steps of a wave whose adapters stay in registers
-  int keep[KR];
-#pragma unroll
-  for (int j = 0; j < KR; ++j) {
-    const int r = r0 + j * kWave + lane;
-    keep[j] = r < r1 ? ids(r) : -1;
-  }
-#pragma unroll
-  for (int j = 0; j < KR; ++j)
-    if (keep[j] >= 0) atomicAdd(&s_cur[wave][keep[j]], 1);
-  for (int r = r0 + KR * kWave + lane; r < r1; r += kWave) {
-    const int a = ids(r);
-    if (a >= 0) atomicAdd(&s_cur[wave][a], 1);
-  }
-  if (nblk <= 1) {
-    lds_barrier();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) all += s_cur[w][tid];
-  }
-  const int end = block_scan(all, s_t), begin = end - all;
-  int at = begin + before;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {  // counts of the waves to their cursors
-    const int n = s_cur[w][tid];
-    s_cur[w][tid] = at;
-    at += n;
-  }
-  __syncthreads();
-  auto place = [&](int r, int a) {
-    int rank = 0, same_n = 0;
-    for (uint64_t todo = __ballot(a >= 0); todo != 0;) {
-      const int cur = __builtin_amdgcn_readlane(a, __builtin_ctzll(todo));
-      const uint64_t same = __ballot(a == cur);
-      todo &= ~same;
-      if (a == cur) {
-        rank = __popcll(same & ((1ull << lane) - 1ull));
-        same_n = __popcll(same);
-      }
-    }
-    const int from = a >= 0 ? s_cur[wave][a] : 0;
-    asm volatile("" ::: "memory");  // a wave's LDS accesses complete in order
-    if (a >= 0) {
-      order[from + rank] = r;
-      if (rank == 0) s_cur[wave][a] = from + same_n;
-    }
-    asm volatile("" ::: "memory");
-  };
-#pragma unroll
-  for (int j = 0; j < KR; ++j)
-    if (r0 + j * kWave < r1) place(r0 + j * kWave + lane, keep[j]);
-  for (int rb = r0 + KR * kWave; rb < r1; rb += kWave)
-    place(rb + lane, rb + lane < r1 ? ids(rb + lane) : -1);
-  if (b != 0) return;
-  // the chunks, and the slots of adapters of several
-  const int n = tid < ids.n_ids ? max(1, (all + chunk - 1) / chunk) : 0;
-  const int m = n > 1 ? n : 0;
-  const int n_end = block_scan(n, s_n), m_end = block_scan(m, s_m);
-  if (tid == kMaxE - 1) *plan.count = n_end;
-  if (tid >= ids.n_ids) return;
-  plan.offsets[tid] = begin;
-  if (tid == ids.n_ids - 1) plan.offsets[tid + 1] = end;
-  const int slot = m_end - m;
-  plan.first[tid] = slot;
-  for (int c = 0; c < n; ++c) {
-    int32_t* e = plan.chunks + 4 * (size_t)(n_end - n + c);
-    e[0] = tid;
-    e[1] = begin + c * chunk;
-    e[2] = min(end, begin + (c + 1) * chunk);
-    e[3] = n > 1 ? slot + c : -1;
-  }
-}
-
-__global__ __launch_bounds__(256) void adapter_order_kernel(RowOrder o) {
-  order_block(o, blockIdx.x);
-}
 
 // First launch of the backward, two independent parts.
 //  - Both transposed weights, A [ids][rank][K] -> [ids][K][rank] and
@@ -779,8 +815,9 @@ __global__ __launch_bounds__(256) void adapter_prepare_kernel(const char* __rest
   constexpr int CW = 4 / E::EB;  // columns of one 4-byte word
   const RowIds& ids = o.ids;
   if ((int)blockIdx.x >= tblocks) {
-    if (o.nblk == 1) return order_block(o, 0);
-    __shared__ int s_n[kMaxE];
+    __shared__ __align__(16) char mem[kOrderLds];
+    if (o.nblk == 1) return order_block(o, 0, mem);
+    int* s_n = reinterpret_cast<int*>(mem);
     for (int i = threadIdx.x; i < ids.n_ids; i += 256) s_n[i] = 0;
     __syncthreads();
     const int b = blockIdx.x - tblocks, r1 = min(ids.R, (b + 1) * o.per);
@@ -1214,7 +1251,8 @@ hipError_t launch_adapter_fwd(const AdapterShape& d, const void* x, const int32_
   p.n_ids = d.n_ids;
   p.rank = d.rank;
   ProfScope ps(MOE_KERNEL_ADAPTER, s);
-  return d.bf16 ? launch_adapter<true>(p, s) : launch_adapter<false>(p, s);
+  const RowOrder none{};
+  return d.bf16 ? launch_adapter<true>(p, none, s) : launch_adapter<false>(p, none, s);
 }
 
 hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void* x,
@@ -1265,12 +1303,12 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
     p.n_ids = d.n_ids;
     p.rank = d.rank;
     ProfScope ps(MOE_KERNEL_ADAPTER_DGRAD, s);
-    e = d.bf16 ? launch_adapter<true>(p, s) : launch_adapter<false>(p, s);
+    e = d.bf16 ? launch_adapter<true>(p, o, s) : launch_adapter<false>(p, o, s);
     if (e != hipSuccess) return e;
   }
   if (dA == nullptr) return e;
-  if (o.nblk != 1) {  // (no rows at all: the chunks alone)
-    adapter_order_kernel<<<max(o.nblk, 1), 256, 0, s>>>(o);
+  if (d.R == 0) {  // the chunks alone
+    adapter_order_kernel<<<1, 256, 0, s>>>(o);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   WgradArgs a{};

@@ -407,7 +407,7 @@ def test_adapter_rows():
 
 
 @gpu
-@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_columns_of_one_matrix(dtype):
     """x and y as neighbouring columns of one matrix give the bits of separate ones."""
     s = make(dtype, 37, 64, 72, 3, 16, "mixed", False, 1)
