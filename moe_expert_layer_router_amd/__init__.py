@@ -745,34 +745,13 @@ def _rows_arg(t: torch.Tensor, name: str, dtype, rows: int, cols: int, dev):
 
 
 def _adapter_args(x, row_id, A, B, scale, src_row):
-    """Checked arguments that moe_adapter_fwd and _bwd share.  One expression holds every
-    condition (a decode step's call takes about as long as its kernel); where it fails, the
-    checks one by one name the argument."""
-    d, dt, i32 = row_id.get_device(), A.dtype, torch.int32
-    if A.dim() == 3 and B.dim() == 3 and x.dim() == 2:
-        n_ids, rank, K = A.shape
-        N, R, x_rows = B.shape[1], row_id.numel(), x.shape[0]
-        if (d >= 0 and d == torch._C._cuda_getDevice()
-                and (dt is torch.bfloat16 or dt is torch.float32)
-                and A.get_device() == d and A.is_contiguous()
-                and B.dtype is dt and B.get_device() == d and B.shape == (n_ids, N, rank)
-                and B.is_contiguous()
-                and row_id.dtype is i32 and row_id.dim() == 1 and row_id.is_contiguous()
-                and x.dtype is dt and x.get_device() == d and x.shape[1] == K and x.is_contiguous()
-                and (scale is None or scale.dtype is torch.float32 and scale.get_device() == d
-                     and scale.shape == (n_ids,) and scale.is_contiguous())
-                and (x_rows == R if src_row is None else
-                     src_row.dtype is i32 and src_row.get_device() == d
-                     and src_row.shape == (R,) and src_row.is_contiguous())):
-            return (row_id.device, dt, n_ids, rank, K, N, R, x_rows, x.data_ptr(), K,
-                    (None if src_row is None else src_row.data_ptr(), row_id.data_ptr(),
-                     A.data_ptr(), B.data_ptr()), None if scale is None else scale.data_ptr())
+    """Checked arguments that moe_adapter_fwd and _bwd share."""
     dev = _device(row_id)
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be [n_ids, rank, K] and B [n_ids, N, rank]")
     n_ids, rank, K = A.shape
     N, R = B.shape[1], row_id.numel()
-    dt = _row_type(A, "A")
+    dt, i32 = _row_type(A, "A"), torch.int32
     x_rows = _shape2(x, "x")[0]
     if src_row is None and x_rows != R:
         raise ValueError(f"x has {x_rows} rows, row_id {R} (src_row maps one to the other)")
@@ -791,6 +770,33 @@ def moe_adapter_fwd(x: torch.Tensor, row_id: torch.Tensor, A: torch.Tensor, B: t
     scale[a] * B[a] (A[a] x[src_row[r]]), a = row_id[r] (-1: none).  A [n_ids,rank,K],
     B [n_ids,N,rank]; rows of x and y may lie at any pitch.  Returns v [R,rank] fp32 for
     moe_adapter_bwd with want_v=True (written to out if given), else None."""
+    d, dt, i32 = row_id.get_device(), A.dtype, torch.int32
+    if A.dim() == 3 and B.dim() == 3 and x.dim() == 2 and (not want_v or out is not None):
+        n_ids, rank, K = A.shape
+        N, R, x_rows = B.shape[1], row_id.numel(), x.shape[0]
+        if (d >= 0 and d == torch._C._cuda_getDevice()
+                and (dt is torch.bfloat16 or dt is torch.float32)
+                and A.get_device() == d and A.is_contiguous()
+                and B.dtype is dt and B.get_device() == d and B.shape == (n_ids, N, rank)
+                and B.is_contiguous()
+                and row_id.dtype is i32 and row_id.dim() == 1 and row_id.is_contiguous()
+                and x.dtype is dt and x.get_device() == d and x.shape[1] == K and x.is_contiguous()
+                and y.dtype is dt and y.get_device() == d and y.shape == (R, N) and y.is_contiguous()
+                and (scale is None or scale.dtype is torch.float32 and scale.get_device() == d
+                     and scale.shape == (n_ids,) and scale.is_contiguous())
+                and (x_rows == R if src_row is None else
+                     src_row.dtype is i32 and src_row.get_device() == d
+                     and src_row.shape == (R,) and src_row.is_contiguous())
+                and (not want_v or out.dtype is torch.float32 and out.get_device() == d
+                     and out.shape == (R, rank) and out.is_contiguous())):
+            rc = lib.moe_adapter_fwd(
+                x.data_ptr(), None if src_row is None else src_row.data_ptr(), row_id.data_ptr(),
+                A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr(), R, x_rows, K, N,
+                K, N, n_ids, rank, MOE_BF16 if dt is torch.bfloat16 else MOE_F32, y.data_ptr(),
+                out.data_ptr() if want_v else None, torch._C._cuda_getCurrentRawStream(d))
+            if rc != 0:
+                _check(rc, "moe_adapter_fwd")
+            return out if want_v else None
     dev, dt, n_ids, rank, K, N, R, x_rows, xp, ldx, (src, ids, a, b), sc = \
         _adapter_args(x, row_id, A, B, scale, src_row)
     yp, ldy = _rows_arg(y, "y", dt, R, N, dev)
