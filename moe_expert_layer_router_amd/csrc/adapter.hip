@@ -909,6 +909,11 @@ constexpr int kWgMaxChunk = 1024;
 // once for the four waves.  bf16 takes it as three bf16 parts (24 bits), so the
 // products are exact and the sums fp32 like those of the fp32 path.
 // Bound by the reads of the wide factor (HBM, and the L2 for gathered rows).
+//
+// SPLIT, for up to kWgMaxChunk rows in all (every adapter is one chunk) and rank
+// up to 32: the four waves of a workgroup hold the same 64 columns and take the
+// steps of a staged block in turn; their sums meet in LDS, in wave order.  As
+// many waves as chunks of 128 rows give, without the second launch.
 template <bool BF16, int RT>
 struct WgradLds {
   static constexpr int SB = RT <= 2 ? 128 : RT == 4 ? 64 : 32;  // rows of a staged block
@@ -917,7 +922,7 @@ struct WgradLds {
   static constexpr int BYTES = NP * 16 * RT * PITCH;
 };
 
-template <bool BF16, int RT>
+template <bool BF16, int RT, bool SPLIT>
 __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
   using S = WgradLds<BF16, RT>;
   constexpr int SR = BF16 ? 32 : 16;  // rows of one step
@@ -933,7 +938,8 @@ __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
   const int z = (int)blockIdx.y >= a.nb0 ? 1 : 0;
   const int C = a.C[z];
   const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, l = lane & 15, g = lane >> 4;
-  const int c0 = 256 * ((int)blockIdx.y - z * a.nb0) + 64 * wave + 4 * l;
+  const int c0 = SPLIT ? 64 * ((int)blockIdx.y - z * a.nb0) + 4 * l
+                       : 256 * ((int)blockIdx.y - z * a.nb0) + 64 * wave + 4 * l;
   const float* P = a.p[z];
   const char* Q = a.q[z] + (size_t)min(c0, C - 4) * (BF16 ? 2 : 4);
   const size_t ldq = (size_t)a.ldq[z] * (BF16 ? 2 : 4);
@@ -1031,37 +1037,100 @@ __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
         }
       }
     };
-    word_t q0[LR], q1[LR];
-    load_p(0);
-    load_q(q0, 0);
-    store_p(0, s_p[0]);
-    __syncthreads();
-    for (int b0 = 0; b0 < np; b0 += SB) {
-      const char* sp = s_p[b0 / SB & 1];
-      const bool more = b0 + SB < np;
-      if (more) load_p(b0 + SB);
+    if constexpr (SPLIT) {
+      constexpr int NS = SB / SR / 4;  // a wave's steps of a staged block
+      static_assert(NS * SR * 4 == SB, "the waves share a block's steps out evenly");
+      word_t q0[NS][LR], q1[NS][LR];
+      auto load = [&](word_t (&q)[NS][LR], int b0) {
 #pragma unroll
-      for (int u = 0; u < SB / SR; u += 2) {
-        const int i0 = b0 + u * SR;
-        if (SB / SR > 1) {
-          load_q(q1, i0 + SR);
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(q0, i0, sp);
-          if (u + 2 < SB / SR || more) load_q(q0, i0 + 2 * SR);
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(q1, i0 + SR, sp);
-        } else {
-          if (more) load_q(q1, i0 + SR);
-          multiply(q0, i0, sp);
+        for (int i = 0; i < NS; ++i) load_q(q[i], b0 + (wave + 4 * i) * SR);
+      };
+      auto block = [&](word_t (&q)[NS][LR], word_t (&next)[NS][LR], int b0) {
+        const bool more = b0 + SB < np;
+        if (more) {
+          load_p(b0 + SB);
+          load(next, b0 + SB);
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < LR; ++i) q0[i] = q1[i];
+        for (int i = 0; i < NS; ++i) multiply(q[i], b0 + (wave + 4 * i) * SR, s_p[b0 / SB & 1]);
+        if (more) store_p(b0 + SB, s_p[(b0 / SB + 1) & 1]);
+        __syncthreads();
+      };
+      load_p(0);
+      load(q0, 0);
+      store_p(0, s_p[0]);
+      __syncthreads();
+      for (int b0 = 0; b0 < np; b0 += 2 * SB) {
+        block(q0, q1, b0);
+        if (b0 + SB < np) block(q1, q0, b0 + SB);
+      }
+    } else {
+      word_t q0[LR], q1[LR];
+      load_p(0);
+      load_q(q0, 0);
+      store_p(0, s_p[0]);
+      __syncthreads();
+      for (int b0 = 0; b0 < np; b0 += SB) {
+        const char* sp = s_p[b0 / SB & 1];
+        const bool more = b0 + SB < np;
+        if (more) load_p(b0 + SB);
+#pragma unroll
+        for (int u = 0; u < SB / SR; u += 2) {
+          const int i0 = b0 + u * SR;
+          if (SB / SR > 1) {
+            load_q(q1, i0 + SR);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(q0, i0, sp);
+            if (u + 2 < SB / SR || more) load_q(q0, i0 + 2 * SR);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(q1, i0 + SR, sp);
+          } else {
+            if (more) load_q(q1, i0 + SR);
+            multiply(q0, i0, sp);
+#pragma unroll
+            for (int i = 0; i < LR; ++i) q0[i] = q1[i];
+          }
+        }
+        if (more) {
+          store_p(b0 + SB, s_p[(b0 / SB + 1) & 1]);
+          __syncthreads();
         }
       }
-      if (more) {
-        store_p(b0 + SB, s_p[(b0 / SB + 1) & 1]);
-        __syncthreads();
-      }
     }
+  }
+  if constexpr (SPLIT) {
+    // acc of wave w: [w][r][q][i][lane], of which each wave adds a quarter
+    static_assert(4 * 16 * RT * kWave * 4 <= sizeof(s_p), "the sums of four waves");
+    float* sum = reinterpret_cast<float*>(s_p) + lane;
+    auto at = [&](int w, int r, int q, int i) -> float& {
+      return sum[(((w * RT + r) * 4 + q) * 4 + i) * kWave];
+    };
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at(wave, r, q, i) = acc[r][q][i];
+    lds_barrier();
+    if (c0 >= C) return;
+    float* out = a.out[z] + (size_t)id * a.rank * C;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int j = 16 * r + 4 * g;
+      if (j >= a.rank) continue;
+      // z = 0, [rank][K]: four columns of rank value j + wave
+      // z = 1, [N][rank]: four rank values of column c0 + wave
+      float* o = z == 0 ? out + (size_t)(j + wave) * C + c0 : out + (size_t)(c0 + wave) * a.rank + j;
+      f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += z == 0 ? at(w, r, i, wave) : at(w, r, wave, i);
+      if (a.accumulate) v += *reinterpret_cast<const f32x4_t*>(o);
+      *reinterpret_cast<f32x4_t*>(o) = v;
+    }
+    return;
   }
   if (c0 >= C) return;
   // acc[r][q][i]: rank value 16 r + 4 g + i, column c0 + q
@@ -1171,7 +1240,11 @@ __global__ __launch_bounds__(256) void adapter_swiglu_kernel(const char* __restr
 // Rows of a chunk, whole staged blocks: about 700 workgroups of the weight
 // gradients, so that a CU has a few and the partial sums stay few (32768 rows
 // of one adapter: 159 us for the backward, 204 with a third of the rows).
-int wgrad_chunk(int R, int K, int N) {
+// Up to kWgMaxChunk rows in all and rank up to 32: one chunk for every adapter
+// (wgrad_split).
+bool wgrad_split(int R, int rank) { return R <= kWgMaxChunk && rank <= 32; }
+int wgrad_chunk(int R, int K, int N, int rank) {
+  if (wgrad_split(R, rank)) return kWgMaxChunk;
   const long blocks = (K + 255) / 256 + (N + 255) / 256;
   const long c = (R * blocks / 700 + 127) / 128 * 128;
   return (int)min(max(c, 128L), (long)kWgMaxChunk);
@@ -1186,7 +1259,7 @@ BwdLayout bwd_layout(int R, int K, int N, int n_ids, int rank, int eb) {
   BwdLayout l;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t was = at; at += up256(bytes); return was; };
-  l.chunk = wgrad_chunk(R, K, N);
+  l.chunk = wgrad_chunk(R, K, N, rank);
   l.upper = R / l.chunk + n_ids;
   l.at = take((size_t)n_ids * rank * K * eb);
   l.bt = take((size_t)n_ids * rank * N * eb);
@@ -1324,22 +1397,25 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
   a.ldq[1] = d.ldy;
   a.C[0] = d.K;
   a.C[1] = d.N;
-  a.nb0 = (d.K + 255) / 256;
+  const bool split = wgrad_split(d.R, d.rank);
+  const int cols = split ? 64 : 256;  // of a workgroup
+  a.nb0 = (d.K + cols - 1) / cols;
   a.rank = d.rank;
   a.accumulate = accumulate ? 1 : 0;
-  const dim3 grid(l.upper, a.nb0 + (d.N + 255) / 256);
+  const dim3 grid(l.upper, a.nb0 + (d.N + cols - 1) / cols);
   const int rt = (d.rank + 15) / 16;
   {
     ProfScope ps(MOE_KERNEL_ADAPTER_WGRAD, s);
-#define MOE_WG(RT)                                                       \
-  do {                                                                   \
-    if (d.bf16) adapter_wgrad_kernel<true, RT><<<grid, 256, 0, s>>>(a);  \
-    else adapter_wgrad_kernel<false, RT><<<grid, 256, 0, s>>>(a);        \
+#define MOE_WG(RT, SP)                                                       \
+  do {                                                                       \
+    if (d.bf16) adapter_wgrad_kernel<true, RT, SP><<<grid, 256, 0, s>>>(a);  \
+    else adapter_wgrad_kernel<false, RT, SP><<<grid, 256, 0, s>>>(a);        \
   } while (0)
-    if (rt <= 1) MOE_WG(1);
-    else if (rt <= 2) MOE_WG(2);
-    else if (rt <= 4) MOE_WG(4);
-    else MOE_WG(8);
+    if (split) { if (rt <= 1) MOE_WG(1, true); else MOE_WG(2, true); }
+    else if (rt <= 1) MOE_WG(1, false);
+    else if (rt <= 2) MOE_WG(2, false);
+    else if (rt <= 4) MOE_WG(4, false);
+    else MOE_WG(8, false);
 #undef MOE_WG
   }
   if ((e = hipGetLastError()) != hipSuccess) return e;

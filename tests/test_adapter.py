@@ -259,6 +259,17 @@ def test_against_definition(dtype, R, K, N_, n_ids, rank, order, gather, pitch, 
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,n_ids,rank,order", [(1024, 1, 16, "one"), (1024, 3, 32, "mixed"), (1023, 2, 24, "range"),
+                                                (129, 256, 8, "mixed"), (128, 1, 32, "one"), (5, 3, 8, "sorted"),
+                                                (1025, 1, 16, "one"), (1024, 2, 40, "mixed")])
+def test_gradients_of_few_rows(dtype, R, n_ids, rank, order):
+    """Both sides of where an adapter's rows are one sum (1024 rows, rank 32)."""
+    for accumulate in (False, True):
+        check(make(dtype, R, 72, 136, n_ids, rank, order, R % 2 == 1, R + rank), accumulate=accumulate)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_accumulated_gradients(dtype):
     check(make(dtype, 3001, 64, 136, 4, 16, "sorted", False, 7), accumulate=True)
     check(make(dtype, 90, 64, 136, 4, 16, "mixed", True, 8), accumulate=True)
