@@ -910,7 +910,7 @@ constexpr int kWgMaxChunk = 1024;
 // products are exact and the sums fp32 like those of the fp32 path.
 // Bound by the reads of the wide factor (HBM, and the L2 for gathered rows).
 //
-// SPLIT, for up to kWgMaxChunk rows in all (every adapter is one chunk) and rank
+// SPLIT (wgrad_split), for up to kWgMaxChunk rows in all (every adapter is one chunk) and rank
 // up to 32: the four waves of a workgroup hold the same 64 columns and take the
 // steps of a staged block in turn; their sums meet in LDS, in wave order.  As
 // many waves as chunks of 128 rows give, without the second launch.
@@ -1237,14 +1237,25 @@ __global__ __launch_bounds__(256) void adapter_swiglu_kernel(const char* __restr
   }
 }
 
+// Workgroups of the weight gradients with one chunk for every adapter.
+long wgrad_units(int K, int N, int n_ids) { return (long)n_ids * ((K + 255) / 256 + (N + 255) / 256); }
+
+// Few rows and too few workgroups: the waves of a workgroup share an adapter's
+// rows out.  (Backward of 1024 rows of 5 adapters, 2048 x 2048, rank 16: 20 us,
+// 23 in chunks; 600 rows of rank 8, 512 x 256: 14.4 for 16.8.  With one adapter of
+// 1024 rows 21 for 18.6, with 64 adapters, whose workgroups are many, 43 for 38.)
+bool wgrad_split(int R, int K, int N, int n_ids, int rank) {
+  return R <= kWgMaxChunk && R <= 512L * n_ids && rank <= 32 && wgrad_units(K, N, n_ids) < 256;
+}
+
 // Rows of a chunk, whole staged blocks: about 700 workgroups of the weight
 // gradients, so that a CU has a few and the partial sums stay few (32768 rows
-// of one adapter: 159 us for the backward, 204 with a third of the rows).
-// Up to kWgMaxChunk rows in all and rank up to 32: one chunk for every adapter
-// (wgrad_split).
-bool wgrad_split(int R, int rank) { return R <= kWgMaxChunk && rank <= 32; }
-int wgrad_chunk(int R, int K, int N, int rank) {
-  if (wgrad_split(R, rank)) return kWgMaxChunk;
+// of one adapter: 159 us for the backward, 204 with a third of the rows).  Up to
+// 512 rows of enough adapters are not cut, which spares the second launch (512
+// rows of 32 adapters, 2048 x 2048: 27 us for 29).
+int wgrad_chunk(int R, int K, int N, int n_ids, int rank) {
+  if (wgrad_split(R, K, N, n_ids, rank)) return kWgMaxChunk;
+  if (R <= 512 && wgrad_units(K, N, n_ids) >= 256) return 512;
   const long blocks = (K + 255) / 256 + (N + 255) / 256;
   const long c = (R * blocks / 700 + 127) / 128 * 128;
   return (int)min(max(c, 128L), (long)kWgMaxChunk);
@@ -1259,7 +1270,7 @@ BwdLayout bwd_layout(int R, int K, int N, int n_ids, int rank, int eb) {
   BwdLayout l;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t was = at; at += up256(bytes); return was; };
-  l.chunk = wgrad_chunk(R, K, N, rank);
+  l.chunk = wgrad_chunk(R, K, N, n_ids, rank);
   l.upper = R / l.chunk + n_ids;
   l.at = take((size_t)n_ids * rank * K * eb);
   l.bt = take((size_t)n_ids * rank * N * eb);
@@ -1397,7 +1408,7 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
   a.ldq[1] = d.ldy;
   a.C[0] = d.K;
   a.C[1] = d.N;
-  const bool split = wgrad_split(d.R, d.rank);
+  const bool split = wgrad_split(d.R, d.K, d.N, d.n_ids, d.rank);
   const int cols = split ? 64 : 256;  // of a workgroup
   a.nb0 = (d.K + cols - 1) / cols;
   a.rank = d.rank;
