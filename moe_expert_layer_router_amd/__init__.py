@@ -457,6 +457,14 @@ def _balance_ws_bytes(T: int, E: int, S: int) -> int:
     return int(nb)
 
 
+@functools.lru_cache(maxsize=64)
+def _adapter_ws_bytes(R: int, K: int, N: int, n_ids: int, rank: int, dtype: int) -> int:
+    nb = lib.moe_adapter_ws_bytes(R, K, N, n_ids, rank, dtype)
+    if nb < 0:
+        _check(int(nb), "moe_adapter_ws_bytes")
+    return int(nb)
+
+
 def _work(nbytes: int, dev, ws: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     """_ws with the caller's workspace checked for the device as well."""
     if ws is not None and (ws.device != dev or not ws.is_contiguous()):
@@ -821,12 +829,51 @@ def moe_adapter_bwd(dy: torch.Tensor, x: torch.Tensor, row_id: torch.Tensor, A: 
     """Backward of moe_adapter_fwd for dy [R,N] and the forward's v: dx [R,K] (None: not wanted)
     is added to in place.  Returns dict dA [n_ids,rank,K], dB [n_ids,N,rank] fp32 (None with
     want_dw=False; added to with accumulate=True) and the workspace ws used."""
+    d, dt, i32, f32 = row_id.get_device(), A.dtype, torch.int32, torch.float32
+    o = dict(out) if out else {}
+    dA, dB = o.get("dA"), o.get("dB")
+    if (dA is not None and dB is not None and want_dw and ws is not None and v is not None
+            and A.dim() == 3 and B.dim() == 3 and x.dim() == 2):
+        n_ids, rank, K = A.shape
+        N, R, x_rows = B.shape[1], row_id.numel(), x.shape[0]
+        code = MOE_BF16 if dt is torch.bfloat16 else MOE_F32
+        if (d >= 0 and d == torch._C._cuda_getDevice()
+                and (dt is torch.bfloat16 or dt is torch.float32)
+                and A.get_device() == d and A.is_contiguous()
+                and B.dtype is dt and B.get_device() == d and B.shape == (n_ids, N, rank)
+                and B.is_contiguous()
+                and row_id.dtype is i32 and row_id.dim() == 1 and row_id.is_contiguous()
+                and x.dtype is dt and x.get_device() == d and x.shape[1] == K and x.is_contiguous()
+                and dy.dtype is dt and dy.get_device() == d and dy.shape == (R, N) and dy.is_contiguous()
+                and (dx is None or dx.dtype is dt and dx.get_device() == d and dx.shape == (R, K)
+                     and dx.is_contiguous())
+                and v.dtype is f32 and v.get_device() == d and v.shape == (R, rank) and v.is_contiguous()
+                and dA.dtype is f32 and dA.get_device() == d and dA.shape == A.shape
+                and dA.is_contiguous()
+                and dB.dtype is f32 and dB.get_device() == d and dB.shape == B.shape
+                and dB.is_contiguous()
+                and (scale is None or scale.dtype is f32 and scale.get_device() == d
+                     and scale.shape == (n_ids,) and scale.is_contiguous())
+                and (x_rows == R if src_row is None else
+                     src_row.dtype is i32 and src_row.get_device() == d
+                     and src_row.shape == (R,) and src_row.is_contiguous())
+                and ws.get_device() == d and ws.is_contiguous()
+                and ws.nbytes >= _adapter_ws_bytes(R, K, N, n_ids, rank, code)):
+            rc = lib.moe_adapter_bwd(
+                dy.data_ptr(), x.data_ptr(), None if src_row is None else src_row.data_ptr(),
+                row_id.data_ptr(), A.data_ptr(), B.data_ptr(), v.data_ptr(),
+                None if scale is None else scale.data_ptr(), R, x_rows, K, N, K, N, K, n_ids, rank, code,
+                None if dx is None else dx.data_ptr(), dA.data_ptr(), dB.data_ptr(),
+                1 if accumulate else 0, ws.data_ptr(), ws.nbytes,
+                torch._C._cuda_getCurrentRawStream(d))
+            if rc != 0:
+                _check(rc, "moe_adapter_bwd")
+            o["ws"] = ws
+            return o
     dev, dt, n_ids, rank, K, N, R, x_rows, xp, ldx, (src, ids, a, b), sc = \
         _adapter_args(x, row_id, A, B, scale, src_row)
     dyp, ldy = _rows_arg(dy, "dy", dt, R, N, dev)
     dxp, lddx = _rows_arg(dx, "dx", dt, R, K, dev) if dx is not None else (None, K)
-    f32 = torch.float32
-    o = dict(out or {})
     if accumulate and want_dw and (o.get("dA") is None or o.get("dB") is None):
         raise ValueError("accumulate=True needs out with dA and dB")
     dA = _into(o, "dA", (n_ids, rank, K), f32, dev) if want_dw else None
@@ -834,10 +881,7 @@ def moe_adapter_bwd(dy: torch.Tensor, x: torch.Tensor, row_id: torch.Tensor, A: 
     if not want_dw:
         o["dA"] = o["dB"] = None
     vp = _arg(v, "v", f32, (R, rank), dev, optional=not want_dw)
-    nb = lib.moe_adapter_ws_bytes(R, K, N, n_ids, rank, _dtype_code(A))
-    if nb < 0:
-        _check(int(nb), "moe_adapter_ws_bytes")
-    o["ws"] = _work(int(nb), dev, ws)
+    o["ws"] = _work(_adapter_ws_bytes(R, K, N, n_ids, rank, _dtype_code(A)), dev, ws)
     _check(lib.moe_adapter_bwd(dyp, xp, src, ids, a, b, vp, sc, R, x_rows, K, N, ldx, ldy, lddx,
                                n_ids, rank, _dtype_code(A), dxp, dA, dB, 1 if accumulate else 0,
                                _ptr(o["ws"]), _nbytes(o["ws"]), _raw_stream(dev)), "moe_adapter_bwd")

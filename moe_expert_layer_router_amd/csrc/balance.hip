@@ -383,12 +383,11 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
   }
 }
 
-// One workgroup per (sequence, 16 experts): 64 threads of a column each add
-// every 64th partial row, then the 64 in a fixed order.  The workgroup that
-// finishes last adds the losses over sequences in order.
+// One workgroup per (sequence, COLS experts): 1024 / COLS threads of a column add
+// every such partial row each, then their sums in a fixed order.  The workgroup
+// that finishes last adds the losses over sequences in order.
 constexpr int kSumThreads = 1024;
-constexpr int kSumCols = 16;
-constexpr int kSumParts = kSumThreads / kSumCols;
+constexpr int kSumU = 8;  // partial rows of a thread in flight
 constexpr int kSumWaves = kSumThreads / kWave;
 
 template <typename V>
@@ -400,26 +399,27 @@ __device__ __forceinline__ V published(V* from) {
   return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+template <int COLS>
 __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
     const int32_t* __restrict__ seq_offsets, int T, int E, int k, int S, int C, float cb, float cz,
     BalWs ws, BalOut out) {
-  __shared__ float s_q[kSumWaves][kSumCols], s_z[kSumWaves];
-  __shared__ int s_c[kSumWaves][kSumCols], s_n[kSumWaves];
-  const int nb = (E + kSumCols - 1) / kSumCols;
+  __shared__ float s_q[kSumWaves][COLS], s_z[kSumWaves];
+  __shared__ int s_c[kSumWaves][COLS], s_n[kSumWaves];
+  const int nb = (E + COLS - 1) / COLS;
   const int s = blockIdx.x / nb, eb = blockIdx.x % nb;
-  const int tid = threadIdx.x, col = tid % kSumCols, part = tid / kSumCols;
-  const int e = kSumCols * eb + col;
+  const int tid = threadIdx.x, col = tid % COLS, part = tid / COLS;
+  const int e = COLS * eb + col;
   const int a = seq_off(seq_offsets, s, T), b = seq_off(seq_offsets, s + 1, T);
   const int b0 = a / C, b1 = b > a ? (b - 1) / C + 1 : b0;
-  constexpr int U = 8;  // partial rows of a thread in flight
+  constexpr int U = kSumU, PARTS = kSumThreads / COLS;
   float q = 0.f, zs = 0.f;
   int c = 0, n = 0;
-  for (int i0 = b0 + part; i0 < b1; i0 += U * kSumParts) {
+  for (int i0 = b0 + part; i0 < b1; i0 += U * PARTS) {
     float qv[U], zv[U];
     int cv[U], nv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kSumParts;
+      const int i = i0 + u * PARTS;
       const size_t slot = (size_t)min(i, b1 - 1) + s;
       const int ec = min(e, E - 1);
       qv[u] = ws.psum[slot * E + ec];
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u * kSumParts >= b1) continue;
+      if (i0 + u * PARTS >= b1) continue;
       q += qv[u];
       c += cv[u];
       zs += zv[u];
@@ -437,13 +437,13 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
     }
   }
 #pragma unroll
-  for (int o = kSumCols; o < kWave; o <<= 1) {
+  for (int o = COLS; o < kWave; o <<= 1) {
     q += __shfl_xor(q, o, kWave);
     c += __shfl_xor(c, o, kWave);
     zs += __shfl_xor(zs, o, kWave);
     n += __shfl_xor(n, o, kWave);
   }
-  if (lane_id() < kSumCols) {
+  if (lane_id() < COLS) {
     s_q[tid / kWave][col] = q;
     s_c[tid / kWave][col] = c;
     if (col == 0) {
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
   }
   __syncthreads();
   int last = 0;
-  if (tid < kSumCols) {
+  if (tid < COLS) {
     q = 0.f;
     c = n = 0;
     double z2 = 0.0;
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(
     }
     double term = e < E && n > 0 ? (double)c * (double)q / n : 0.0;
 #pragma unroll
-    for (int o = kSumCols / 2; o > 0; o >>= 1) term += __shfl_xor(term, o, kSumCols);
+    for (int o = COLS / 2; o > 0; o >>= 1) term += __shfl_xor(term, o, COLS);
     if (tid == 0) {
       // Everything the last workgroup reads of the others goes through
       // agent-scope atomics, performed where all XCDs see them, and this
@@ -611,7 +611,7 @@ BalLayout balance_layout(int T, int E, int S) {
   l.tokens = take(slots * 4);
   l.zsum = take(slots * 4);
   l.ticket = take(4);
-  l.terms = take((size_t)S * ((E + kSumCols - 1) / kSumCols) * 8);
+  l.terms = take((size_t)S * ((E + 15) / 16) * 8);
   l.zterms = take((size_t)S * 8);
   l.total = at;
   return l;
@@ -654,8 +654,14 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
 #undef MOE_BAL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || one) return e;
-  balance_sum_kernel<<<S * ((E + kSumCols - 1) / kSumCols), kSumThreads, 0, s>>>(
-      seq_offsets, T, E, k, S, C, cb, cz, ws, out);
+  // 64 columns a workgroup where a sequence has at most a partial row (grid / S on
+  // average) for each of its 16 threads of a column: 236 tokens of 255 experts in
+  // 38 sequences 5.9 us, 12 with 16; 16384 x 128 in 4 sequences 9.4 us, 6.4 with 16
+#define MOE_BAL_SUM(COLS)                                                                      \
+  balance_sum_kernel<COLS><<<S * ((E + COLS - 1) / COLS), kSumThreads, 0, s>>>(seq_offsets, T, \
+                                                                               E, k, S, C, cb, cz, ws, out)
+  if (E > 16 && grid / S <= kSumThreads / 64) MOE_BAL_SUM(64); else MOE_BAL_SUM(16);
+#undef MOE_BAL_SUM
   return hipGetLastError();
 }
 

@@ -489,3 +489,43 @@ def test_ffn_adapter_refusals():
         assert call(**{f"_{i}": N}) == EINVAL and name in _err()
     assert call(_25=N) == EWS and call(_26=16) == EWS
     assert call(_5=0, _6=0, _0=N, _3=N, _22=N, _23=N, _24=N) == OK
+
+
+@gpu
+def test_binding_refusals_of_whole_calls():
+    """Calls that give every tensor: as they are they pass, with any one tensor of another type, shape,
+    device or order they are refused."""
+    s = make("bf16", 20, 64, 72, 3, 16, "mixed", True, 1)
+    a = dict(x=s["x"], row_id=s["ids"], A=s["A"], B=s["B"], y=s["y"], scale=s["scale"], src_row=s["src"],
+             want_v=True, out=torch.zeros(20, 16, device=DEV))
+    v = moe.moe_adapter_fwd(**a)
+    assert v is a["out"]
+    b = {n: a[n] for n in ("x", "row_id", "A", "B", "scale", "src_row")}
+    b.update(dy=torch.randn(20, 72, device=DEV).bfloat16(), v=v, dx=torch.zeros(20, 64, device=DEV).bfloat16())
+    fresh = moe.moe_adapter_bwd(**{**b, "dx": b["dx"].clone()})
+    b.update(ws=fresh["ws"], out={n: torch.zeros_like(fresh[n]) for n in ("dA", "dB")})
+    got = moe.moe_adapter_bwd(**b)
+    assert all(got[n] is b["out"][n] and torch.equal(got[n], fresh[n]) for n in b["out"])
+
+    def bad(t):
+        yield t.cpu()
+        yield t.double()
+        if t is not a["x"]:  # (with src_row, x may have any number of rows)
+            yield t[1:]
+        if t is not a["x"] and t is not a["y"] and t is not b["dy"] and t is not b["dx"]:  # (rows at a pitch)
+            yield torch.stack([t, t], -1)[..., 0]
+        yield t.unsqueeze(0)
+
+    for call, args in ((moe.moe_adapter_fwd, a), (moe.moe_adapter_bwd, b)):
+        for name, t in args.items():
+            if torch.is_tensor(t) and name != "ws":
+                for u in bad(t):
+                    with pytest.raises(ValueError):
+                        call(**{**args, name: u})
+    for name, t in b["out"].items():
+        for u in bad(t):
+            with pytest.raises(ValueError):
+                moe.moe_adapter_bwd(**{**b, "out": {**b["out"], name: u}})
+    for u in (b["ws"].cpu(), b["ws"][:64], torch.stack([b["ws"]] * 2, -1)[:, 0]):
+        with pytest.raises(ValueError):
+            moe.moe_adapter_bwd(**{**b, "ws": u})
