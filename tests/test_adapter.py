@@ -363,8 +363,9 @@ def test_gradients_not_wanted():
 
 
 @gpu
-def test_captured_and_on_another_stream():
-    s = make("bf16", 900, 128, 136, 12, 16, "mixed", True, 11)
+@pytest.mark.parametrize("R", [900, 2500, 5000])
+def test_captured_and_on_another_stream(R):
+    s = make("bf16", R, 128, 136, 12, 16, "mixed", True, 11)
     s["src"].clamp_(0, s["x"].shape[0] - 1)
     y0, dx0 = s["y"].clone(), s["dx"].clone()
     fwd = lambda y, v=None: moe.moe_adapter_fwd(s["x"], s["ids"], s["A"], s["B"], y, scale=s["scale"],

@@ -321,10 +321,11 @@ def test_more_than_2_to_31_bytes_of_logits():
 
 
 @gpu
-def test_captured_and_on_another_stream():
+@pytest.mark.parametrize("T,S", [(3000, 5), (150, 2), (400, 90)])
+def test_captured_and_on_another_stream(T, S):
     rng = np.random.default_rng(9)
-    T, E, k = 3000, 64, 4
-    off = dev(offsets_of(rng, T, 5))
+    E, k = 64, 4
+    off = dev(offsets_of(rng, T, S))
     z = torch.randn(T, E, device=DEV)
     idx = z.topk(k, dim=1).indices.to(torch.int32)
     f = moe.moe_balance_loss(z, idx, 0.1, 0.1, seq_offsets=off)

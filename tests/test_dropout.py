@@ -37,7 +37,7 @@ def keep_mask(seed, offset, T, H, p, t0=0):
 
 
 def test_generator_vectors():
-    """The three vectors published with the generator (Random123's known answers)."""
+    """The three vectors published with the generator (its known answers)."""
     one = lambda c, o, s: [int(v) for v in philox(np.array([c], np.uint64), o, s)[0]]
     full = (1 << 64) - 1
     assert one(0, 0, 0) == [0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8]
