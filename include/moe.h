@@ -536,10 +536,10 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
  * row_id is outside [0, n_ids) (-1: none), or whose src_row is outside
  * [0, x_rows), have no adapter: y is not touched and v is 0.  Rows may be in
  * any order; rows of one adapter next to each other share the reads of its
- * weights.  In bf16, v enters the second product as two bf16 halves (16 bits).
+ * weights.  In bf16, v enters the second product whole (as three bf16 parts).
  * One request's weights and rows never reach another's result, whatever they
  * hold.  (An infinity among a row's own values may come out as NaN: 0 times it
- * is part of a product in halves.)
+ * is part of a product in parts.)
  *   x [x_rows,K] dtype at row pitch ldx, y [R,N] dtype at row pitch ldy (in
  *   elements; columns past N untouched), A [n_ids,rank,K], B [n_ids,N,rank]
  *   dtype, scale [n_ids] fp32 or NULL (1), row_id [R], src_row [R] int32,

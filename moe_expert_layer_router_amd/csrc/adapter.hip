@@ -608,11 +608,12 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p, int o
   lds_barrier();
 
   // The rank values (in the first wave's place) as fragments.  bf16 holds each
-  // fp32 value as two bf16 halves (16 significant bits: their rounding stays
-  // 2^-9 below that of y), two instructions on the same weights.
+  // fp32 value whole as three bf16 parts (8 bits each), three instructions on the
+  // same weights: the products are exact and the sums fp32, like those of the
+  // fp32 path.
   constexpr int KF = BF16 ? (RT + 1) / 2 : RT;  // fragment steps of the rank values
-  constexpr int NH = BF16 ? 2 : 1;
-  u32x4_t vf[NH][MT][KF];
+  constexpr int NP = BF16 ? 3 : 1;
+  u32x4_t vf[NP][MT][KF];
 #pragma unroll
   for (int s = 0; s < KF; ++s)
 #pragma unroll
@@ -627,12 +628,19 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p, int o
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (BF16) {
-          const float h0 = bf2f(f2bf(v[2 * i])), h1 = bf2f(f2bf(v[2 * i + 1]));
-          float l0 = v[2 * i] - h0, l1 = v[2 * i + 1] - h1;
-          l0 = __builtin_isfinite(l0) ? l0 : 0.f;  // an infinity is in the upper half alone
-          l1 = __builtin_isfinite(l1) ? l1 : 0.f;
-          vf[0][m][s][i] = on ? pack_bf2(h0, h1) : 0u;
-          vf[NH - 1][m][s][i] = on ? pack_bf2(l0, l1) : 0u;
+          // an infinity is in the first part alone
+          auto rest = [](float x, float part) {
+            const float r = x - part;
+            return __builtin_isfinite(r) ? r : 0.f;
+          };
+          float r0 = v[2 * i], r1 = v[2 * i + 1];
+#pragma unroll
+          for (int h = 0; h < NP; ++h) {
+            const float p0 = bf2f(f2bf(r0)), p1 = bf2f(f2bf(r1));
+            vf[h][m][s][i] = on ? pack_bf2(p0, p1) : 0u;
+            r0 = rest(r0, p0);
+            r1 = rest(r1, p1);
+          }
         } else {
           vf[0][m][s][i] = on ? __float_as_uint(v[i]) : 0u;
         }
@@ -685,7 +693,7 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p, int o
 #pragma unroll
           for (int s = 0; s < KF; ++s)
 #pragma unroll
-            for (int h = 0; h < NH; ++h) acc = step<BF16>(w[s], vf[h][m][s], acc);
+            for (int h = 0; h < NP; ++h) acc = step<BF16>(w[s], vf[h][m][s], acc);
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[q][m][i] = idm[m] == cur ? acc[i] : d[q][m][i];
         }

@@ -530,3 +530,42 @@ def test_binding_refusals_of_whole_calls():
     for u in (b["ws"].cpu(), b["ws"][:64], torch.stack([b["ws"]] * 2, -1)[:, 0]):
         with pytest.raises(ValueError):
             moe.moe_adapter_bwd(**{**b, "ws": u})
+
+
+def paired(rows, width, n_ids, rank, n_out, g):
+    """Whole numbers for x [rows, width], A [n_ids, rank, width], B [n_ids, n_out, rank]: rank values
+    2 i and 2 i + 1 are sums of 20 bits or so that differ by one element of x alone, and every
+    column of B takes the difference of one such pair.  Every sum is below 2^24 (each product is at
+    most 2^14, at most 512 of them), so fp32 holds them all, and a result is an element of x."""
+    pick = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=DEV).double()
+    x, Aw = pick(-127, 128, rows, width), pick(-127, 128, n_ids, rank, width)
+    Aw[:, 1::2] = Aw[:, ::2]
+    c = torch.randint(0, width, (n_ids, rank // 2, 1), generator=g, device=DEV)
+    Aw[:, 1::2].scatter_add_(2, c, torch.ones_like(c).double())
+    Bw = torch.zeros(n_ids, n_out, rank, dtype=torch.float64, device=DEV)
+    n = torch.arange(n_out, device=DEV)
+    Bw[:, n, 2 * n % rank], Bw[:, n, (2 * n + 1) % rank] = 1.0, -1.0
+    return x, Aw, Bw
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 64, 72, 128])
+def test_rank_values_keep_all_bits(dtype, rank):
+    """Rank values of 20 bits that cancel to 8: exact, forward and data gradients."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device=DEV).manual_seed(rank)
+    R, n_ids, wide, out = 77, 3, 512, 136
+    ids = torch.randint(-1, n_ids, (R,), generator=g, device=DEV, dtype=torch.int32)
+    x, Aw, Bw = paired(R, wide, n_ids, rank, out, g)
+    zero = torch.zeros(R, out, dtype=torch.float64, device=DEV)
+    want = definition(x, None, ids, Aw, Bw, None, zero)[0]["y"]
+    assert want.abs().max() <= 127 and want.any()
+    y = zero.to(dt)
+    moe.moe_adapter_fwd(x.to(dt), ids, Aw.to(dt), Bw.to(dt), y)
+    assert torch.equal(y.double(), want)
+    # the data gradients take dy for x, B^T for A and A^T for B
+    Ab, Bb = Bw.transpose(1, 2).contiguous(), Aw.transpose(1, 2).contiguous()
+    dx = zero.to(dt)
+    moe.moe_adapter_bwd(x.to(dt), zero.to(dt), ids, Ab.to(dt), Bb.to(dt), None, dx, want_dw=False)
+    assert torch.equal(dx.double(), want)
