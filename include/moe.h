@@ -495,7 +495,9 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t
  * whole numbers), for the upstream gradient *d_loss (device scalar; NULL: 1):
  *   d_logits[t,e] = d_loss p[t,e] (balance_coef E / (k N n_s) (counts[s,e] - sum_j p[t,j] counts[s,j])
  *                                  + z_coef 2 lse[t] / N)
- * Rows that are not live get 0.  accumulate != 0 adds to d_logits.  logits,
+ * Rows that are not live get 0.  accumulate != 0 adds to d_logits.  p is formed
+ * again from the logits, relative to their largest (exp(z - lse) would lose the
+ * bits that lse has rounded away).  logits,
  * lse, counts, tokens, seq_offsets and token_mask as given to and written by
  * moe_balance_loss. */
 int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* counts,

@@ -116,6 +116,39 @@ __device__ __forceinline__ float reciprocal(float s) {
   return fmaf(fmaf(-s, r, 1.f), r, r);
 }
 
+// The probabilities of a token's logits p[v][i] (behind the row's end -inf), in
+// their place: exp(p - top) over its sum, so that a shift of the whole row, which
+// a softmax does not depend on, costs no bits.
+struct Top {
+  float top, sum;
+  bool none;  // a row of -inf alone: probabilities and sum 0
+};
+template <int LPT, int V>
+__device__ __forceinline__ Top softmax(f32x4_t (&p)[V]) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    top = fmaxf(top, fmaxf(fmaxf(p[v][0], p[v][1]), fmaxf(p[v][2], p[v][3])));
+  top = group_max<LPT>(top);
+  // (A NaN leaves top unless all are NaN; it comes back with the exponentials' sum.)
+  const bool none = top == -INFINITY;
+  float sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = p[v][i];
+      p[v][i] = exp_neg(none ? (x == x ? -INFINITY : x) : x - top);
+    }
+    sum += (p[v][0] + p[v][1]) + (p[v][2] + p[v][3]);
+  }
+  sum = group_sum<LPT>(sum);
+  const float inv = none ? sum : reciprocal(sum);
+#pragma unroll
+  for (int v = 0; v < V; ++v) p[v] *= inv;
+  return {top, sum, none};
+}
+
 // The values of columns e .. e + 3 of a row of E (VEC: one 16-byte load); behind
 // the end the last ones again, which the caller replaces (in_row).
 template <bool VEC>
@@ -314,29 +347,8 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
     if (tb + BT < t1) fetch(tb + BT);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        top = fmaxf(top, fmaxf(fmaxf(p[u][v][0], p[u][v][1]), fmaxf(p[u][v][2], p[u][v][3])));
-      top = group_max<LPT>(top);
-      // a row of -inf alone: probabilities 0 and lse 0.  (A NaN leaves top
-      // unless all are NaN; it comes back with the exponentials' sum.)
-      const bool none = top == -INFINITY;
-      float sum = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = p[u][v][i];
-          p[u][v][i] = exp_neg(none ? (x == x ? -INFINITY : x) : x - top);
-        }
-        sum += (p[u][v][0] + p[u][v][1]) + (p[u][v][2] + p[u][v][3]);
-      }
-      sum = group_sum<LPT>(sum);
-      const float inv = none ? sum : reciprocal(sum);
-#pragma unroll
-      for (int v = 0; v < V; ++v) p[u][v] *= inv;
-      lse[u] = none ? sum : top + __builtin_amdgcn_logf(sum) * 0.693147181f;
+      const Top t = softmax<LPT, V>(p[u]);
+      lse[u] = t.none ? t.sum : t.top + __builtin_amdgcn_logf(t.sum) * 0.693147181f;
     }
     uint32_t counted = 0;  // tokens of this batch that a sequence has taken
     while (s < S && a < te) {
@@ -563,14 +575,15 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
     }
     f32x4_t d[V] = {};
     if (live[u] && t >= a && t < b) {  // the same in a token's lanes
-      float p[V][4], dot = 0.f;
+      f32x4_t p[V];
+      float dot = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[v] = z[u][v];
+      softmax<LPT, V>(p);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[v][i] = exp_neg(z[u][v][i] - l[u]);
-          dot = fmaf(p[v][i], c[v][i], dot);
-        }
+        for (int i = 0; i < 4; ++i) dot = fmaf(p[v][i], c[v][i], dot);
       dot = group_sum<LPT>(dot);
       const float kz = cz * 2.f * l[u] / N;
 #pragma unroll

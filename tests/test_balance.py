@@ -442,3 +442,28 @@ def test_binding_refusals_of_whole_calls():
                 refused(call, {**args, inner: {**args[inner], name: u}})
     for u in (a["ws"].cpu(), a["ws"][:16], torch.stack([a["ws"]] * 2, -1)[:, 0]):
         refused(moe.moe_balance_loss, {**a, "ws": u})
+
+
+@gpu
+@pytest.mark.parametrize("E", [3, 32, 60, 128, 132, 256])
+@pytest.mark.parametrize("shift", [4096.0, -4096.0])
+def test_gradient_of_shifted_logits(E, shift):
+    """A softmax does not depend on a shift of its row.  Logits that are multiples of 2^-10 below 2^4
+    are shifted by 2^12 without rounding, so without a z loss the gradient has the same bits.  Its own
+    bound: z - top is exact here, exp within 4 u, sums of E terms in a tree of at most 13 levels, p and
+    sum p c then within 24 and 40 u, the factors 16 more: 80 u of the magnitudes."""
+    rng = np.random.default_rng(E)
+    T, k = 300, min(E, 4)
+    z = np.clip(np.round(rng.standard_normal((T, E)) * 2048) / 1024, -15, 15).astype(np.float32)
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :k].astype(np.int32)
+    off = np.array([0, 100, 280, 300], np.int32)
+    cb = np.float32(0.125)
+    d = []
+    for a in (z, z + np.float32(shift)):
+        f = moe.moe_balance_loss(dev(a), dev(idx), 0.125, seq_offsets=dev(off))
+        d.append(moe.moe_balance_loss_bwd(dev(a), f, k, 0.125, seq_offsets=dev(off)))
+    ref = reference(z, idx, k, off, np.ones(T, bool), cb, 0.0)
+    for got in d:
+        err = np.abs(got.cpu().numpy() - ref["d_logits"])
+        assert (err <= 80 * U24 * ref["mag"] + 2.0 ** -126).all(), (err / np.maximum(ref["mag"], 1e-30)).max() / U24
+    assert torch.equal(d[0], d[1])
