@@ -484,7 +484,10 @@ int moe_route_bwd_add(const float* d_topk_w, const float* topk_w, const int32_t*
  *   counts, prob_sum [S,E], tokens [S+1] int32 (n_s, then N), lse [T] fp32 (0
  *   for rows not live), loss [3] fp32
  *   ws       moe_balance_ws_bytes(T, E, S) bytes
- * T = 0 writes zeros to counts, prob_sum, tokens and loss. */
+ * T = 0 writes zeros to counts, prob_sum, tokens and loss.  S <= 2^20 (with more
+ * than 192 experts below that); T k up to 0x7fff0000.  As in the calls below,
+ * sizes that would take a launch of 2^32 threads (2^26 tokens of the dropout,
+ * about 2^28 rows elsewhere) are MOE_EUNSUPPORTED, with nothing enqueued. */
 int64_t moe_balance_ws_bytes(int T, int E, int S);
 int moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
                      const uint8_t* token_mask, int T, int E, int k, int S, float balance_coef,

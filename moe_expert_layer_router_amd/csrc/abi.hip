@@ -907,20 +907,9 @@ int moe_route_bwd(const float* d_topk_w, const float* topk_w, const int32_t* top
                    dtype, d_logits, dx_router, dw_router, ws, ws_bytes, stream);
 }
 
-int moe_route_bwd_add(const float* d_topk_w, const float* topk_w, const int32_t* topk_idx,
-                      const float* d_logits_add, const void* x, const void* w_router, int T, int H,
-                      int E, int k, int dtype, float* d_logits, float* dx_router, float* dw_router,
-                      void* ws, size_t ws_bytes, void* stream) {
-  const char* fn = "moe_route_bwd_add";
-  if (T > 0)
-    if (int rc = check_ptr(d_logits_add, "d_logits_add", fn)) return rc;
-  return route_bwd(fn, d_topk_w, topk_w, topk_idx, d_logits_add, x, w_router, T, H, E, k, dtype,
-                   d_logits, dx_router, dw_router, ws, ws_bytes, stream);
-}
-
 namespace {
-// Row counts of the operators around the layer: their kernels step past the
-// last row by less than this before they stop.
+// Row counts of the operators around the layer: int32 indexes that step past the
+// last row by less than 2^16 before they stop.
 constexpr int kMaxRows = 0x7fff0000;
 int check_rows(int rows, const char* name, const char* fn) {
   if (rows < 0) return fail(MOE_EINVAL, "%s: %s must be >= 0 (got %d)", fn, name, rows);
@@ -928,6 +917,33 @@ int check_rows(int rows, const char* name, const char* fn) {
   return MOE_OK;
 }
 
+// HIP launches fewer than 2^32 threads along an axis; asked before anything of
+// the call is enqueued.
+int check_launch(uint64_t threads, const char* fn) {
+  if (threads >> 32 != 0)
+    return fail(MOE_EUNSUPPORTED, "%s: needs a launch of %llu threads, which have to be below 2^32", fn,
+                (unsigned long long)threads);
+  return MOE_OK;
+}
+
+// Threads of a kernel with a wave for every row, four in a workgroup.
+uint64_t wave_per_row(int rows) { return ((uint64_t)rows + 3) / 4 * 256; }
+}  // namespace
+
+int moe_route_bwd_add(const float* d_topk_w, const float* topk_w, const int32_t* topk_idx,
+                      const float* d_logits_add, const void* x, const void* w_router, int T, int H,
+                      int E, int k, int dtype, float* d_logits, float* dx_router, float* dw_router,
+                      void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_route_bwd_add";
+  if (T > 0)
+    if (int rc = check_launch(wave_per_row(T), fn)) return rc;
+  if (T > 0)
+    if (int rc = check_ptr(d_logits_add, "d_logits_add", fn)) return rc;
+  return route_bwd(fn, d_topk_w, topk_w, topk_idx, d_logits_add, x, w_router, T, H, E, k, dtype,
+                   d_logits, dx_router, dw_router, ws, ws_bytes, stream);
+}
+
+namespace {
 int check_balance(int T, int E, int k, int S, const int32_t* seq_offsets, const char* fn) {
   if (int rc = check_routing_shape(T, E, k, fn)) return rc;
   if ((long long)T * k > kMaxRows)
@@ -945,6 +961,7 @@ int64_t moe_balance_ws_bytes(int T, int E, int S) {
   if (E < 1 || E > kMaxE || S < 1 || S > (1 << 20))
     return fail(MOE_EINVAL, "%s: need E in [1, %d] and S in [1, 2^20] (E=%d, S=%d)", fn,
                 kMaxE, E, S);
+  if (int rc = check_launch(balance_threads(T, E, S), fn)) return rc;
   return (int64_t)balance_ws_bytes(T, E, S);
 }
 
@@ -954,6 +971,7 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t
                      float* loss, void* ws, size_t ws_bytes, void* stream) {
   const char* fn = "moe_balance_loss";
   if (int rc = check_balance(T, E, k, S, seq_offsets, fn)) return rc;
+  if (int rc = check_launch(balance_threads(T, E, S), fn)) return rc;
   if (T > 0) {
     if (int rc = check_ptr(logits, "logits", fn)) return rc;
     if (int rc = check_ptr(topk_idx, "topk_idx", fn)) return rc;
@@ -978,6 +996,7 @@ int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* c
   const char* fn = "moe_balance_loss_bwd";
   if (int rc = check_balance(T, E, k, S, seq_offsets, fn)) return rc;
   if (accumulate != 0 && accumulate != 1) return fail(MOE_EINVAL, "%s: accumulate must be 0 or 1", fn);
+  if (int rc = check_launch(balance_bwd_threads(T, E), fn)) return rc;
   if (T == 0) return MOE_OK;
   if (int rc = check_ptr(logits, "logits", fn)) return rc;
   if (int rc = check_ptr(lse, "lse", fn)) return rc;
@@ -994,6 +1013,7 @@ namespace {
 int check_dropout(double p, const uint64_t* rng, int T, int H, int k, int dtype, const char* fn) {
   if (int rc = check_dtype(dtype, fn)) return rc;
   if (int rc = check_rows(T, "T", fn)) return rc;
+  if (int rc = check_launch(wave_per_row(T), fn)) return rc;
   if (k < 1 || k > kMaxK) return fail(MOE_EINVAL, "%s: k=%d outside [1, %d]", fn, k, kMaxK);
   if (int rc = check_row_width(H, dtype, fn)) return rc;
   if (!(p >= 0.0 && p < 1.0)) return fail(MOE_EINVAL, "%s: p=%g outside [0, 1)", fn, p);
@@ -1088,6 +1108,7 @@ int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id
   if (int rc = check_pitch(ldx, K, dtype, "ldx", fn)) return rc;
   if (int rc = check_pitch(ldy, N, dtype, "ldy", fn)) return rc;
   if (R == 0) return MOE_OK;
+  if (int rc = check_launch(adapter_fwd_threads(dtype == MOE_BF16, R, K, N, n_ids, rank, true), fn)) return rc;
   if (x_rows > 0)
     if (int rc = check_ptr(x, "x", fn, true)) return rc;
   if (int rc = check_ptr(row_id, "row_id", fn)) return rc;
@@ -1129,6 +1150,8 @@ int moe_adapter_bwd(const void* dy, const void* x, const int32_t* src_row, const
     if (int rc = check_ptr(dB, "dB", fn, true)) return rc;
   }
   if (R > 0) {
+    if (int rc = check_launch(adapter_bwd_threads(dtype == MOE_BF16, R, K, N, n_ids, rank, dx != nullptr), fn))
+      return rc;
     if (int rc = check_ptr(dy, "dy", fn, true)) return rc;
     if (int rc = check_ptr(row_id, "row_id", fn)) return rc;
     if (int rc = check_ptr(A, "A", fn, true)) return rc;
@@ -1188,6 +1211,12 @@ int moe_grouped_ffn_fwd_adapter(const void* x, const int32_t* src_row, const int
     return fail(MOE_EINVAL, "%s: x_rows=%d (without src_row the R_cap=%d grouped rows)", fn, x_rows, R_cap);
   if (bf16)
     if (int rc = check_range((int64_t)x_rows * H * 2, "x", fn)) return rc;
+  if (R_cap > 0) {  // the activation, the adapters, and the fp32 products (a thread for each of their elements)
+    const uint64_t up = adapter_fwd_threads(bf16, R_cap, H, I, n_ids, rank, true);
+    const uint64_t down = adapter_fwd_threads(bf16, R_cap, I, H, n_ids, rank, true);
+    const uint64_t f32 = bf16 ? 0 : (uint64_t)R_cap * std::max(H, I) + 255;
+    if (int rc = check_launch(std::max({wave_per_row(R_cap), up, down, f32}), fn)) return rc;
+  }
   if (int rc = check_ptr(offsets, "offsets", fn)) return rc;
   if (int rc = check_ptr(w_gate, "w_gate", fn, true)) return rc;
   if (int rc = check_ptr(w_up, "w_up", fn, true)) return rc;

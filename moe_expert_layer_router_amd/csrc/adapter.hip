@@ -14,6 +14,8 @@
 // the summed axis is right as long as both operands share it.
 #include "common.h"
 
+#include <algorithm>
+
 namespace moe {
 
 namespace {
@@ -767,33 +769,55 @@ hipError_t launch_one(const AdapterArgs& p, const RowOrder& o, hipStream_t s) {
 // four), four where a CU takes several in turn (131072 rows: 222 us for 243) or
 // where two workgroups of eight do not fit its LDS (8191 rows of rank 64: 29 us
 // for 34).
+struct AdapterTiles {
+  int rows, splits, waves;
+  long wgs;
+};
+template <bool BF16, int RT>
+struct AdapterWaves {
+  static constexpr int MT = RT <= 4 ? 1 : 2;
+  static constexpr int WAVE = AdapterLds<BF16, RT, MT>::WAVE;
+  static constexpr bool EIGHT = 8 * WAVE <= 160 * 1024;
+  static constexpr int FEW = 4 * WAVE <= 160 * 1024 ? 4 : 2;
+  static int of(long wgs) { return EIGHT && wgs <= (8 * WAVE <= 80 * 1024 ? 4 : 1) * kCUs ? 8 : FEW; }
+};
 template <bool BF16>
-hipError_t launch_adapter(AdapterArgs p, const RowOrder& o, hipStream_t s) {
-  const int most = p.rank > 64 ? 32 : 16;
+AdapterTiles adapter_tiles(int R, int K, int N, int n_ids, int rank, bool y) {
+  AdapterTiles t{};
+  const int most = rank > 64 ? 32 : 16;
   double best = 0.0;
   for (int rows = 1; rows <= most; rows *= 2)
-    for (int splits = 1; splits <= (p.y == nullptr ? 1 : 8); splits *= 2) {
-      if (splits > 1 && 256 * splits > p.N) break;
-      const long tiles = ((long)p.R + rows - 1) / rows;
-      const double ids = min((double)rows, max(1.0, 2.0 * rows * p.n_ids / p.R)) * p.rank;
-      const double each = (rows + ids) * p.K + (ids + 2.0 * rows) * p.N / splits;
+    for (int splits = 1; splits <= (y ? 8 : 1); splits *= 2) {
+      if (splits > 1 && 256 * splits > N) break;
+      const long tiles = ((long)R + rows - 1) / rows;
+      const double ids = (double)std::clamp(2L * rows * n_ids / R, 1L, (long)rows) * rank;
+      const double each = (rows + ids) * K + (ids + 2.0 * rows) * N / splits;
       const double cost = (double)((tiles * splits + kCUs - 1) / kCUs) * each;
       if (best > 0.0 && cost > best) continue;
       best = cost;
-      p.rows = rows;
-      p.splits = splits;
+      t = {rows, splits, 0, tiles * splits};
     }
-  const int rt = (p.rank + 15) / 16;
+  const int rt = (rank + 15) / 16;
+  t.waves = rt <= 1   ? AdapterWaves<BF16, 1>::of(t.wgs)
+            : rt <= 2 ? AdapterWaves<BF16, 2>::of(t.wgs)
+            : rt <= 4 ? AdapterWaves<BF16, 4>::of(t.wgs)
+                      : AdapterWaves<BF16, 8>::of(t.wgs);
+  return t;
+}
+
+template <bool BF16>
+hipError_t launch_adapter(AdapterArgs p, const RowOrder& o, hipStream_t s) {
+  const AdapterTiles t = adapter_tiles<BF16>(p.R, p.K, p.N, p.n_ids, p.rank, p.y != nullptr);
+  p.rows = t.rows;
+  p.splits = t.splits;
   p.window = p.rows > 1 && p.n_ids > 1 && p.n_ids < kWindowKeys;
-  const long wgs = (long)((p.R + p.rows - 1) / p.rows) * p.splits;
-#define MOE_AD(RT)                                                                              \
-  do {                                                                                          \
-    constexpr int mt = RT <= 4 ? 1 : 2;                                                         \
-    constexpr int wave = AdapterLds<BF16, RT, mt>::WAVE;                                        \
-    if constexpr (8 * wave <= 160 * 1024)                                                       \
-      if (wgs <= (8 * wave <= 80 * 1024 ? 4 : 1) * kCUs)                                        \
-        return launch_one<BF16, RT, mt, 8>(p, o, s);                                               \
-    return launch_one<BF16, RT, mt, 4 * wave <= 160 * 1024 ? 4 : 2>(p, o, s);                      \
+  const int rt = (p.rank + 15) / 16;
+#define MOE_AD(RT)                                                                     \
+  do {                                                                                 \
+    using W = AdapterWaves<BF16, RT>;                                                  \
+    if constexpr (W::EIGHT)                                                            \
+      if (t.waves == 8) return launch_one<BF16, RT, W::MT, 8>(p, o, s);                \
+    return launch_one<BF16, RT, W::MT, W::FEW>(p, o, s);                               \
   } while (0)
   if (rt <= 1) MOE_AD(1);
   else if (rt <= 2) MOE_AD(2);
@@ -1266,7 +1290,12 @@ int wgrad_chunk(int R, int K, int N, int n_ids, int rank) {
   if (R <= 512 && wgrad_units(K, N, n_ids) >= 256) return 512;
   const long blocks = (K + 255) / 256 + (N + 255) / 256;
   const long c = (R * blocks / 700 + 127) / 128 * 128;
-  return (int)min(max(c, 128L), (long)kWgMaxChunk);
+  return (int)std::clamp(c, 128L, (long)kWgMaxChunk);
+}
+
+// Threads of the transposes.
+uint64_t transpose_units(int n_ids, int rank, int K, int N, int eb) {
+  return (uint64_t)n_ids * (rank * eb / 16) * ((K + N) * (long)eb / 4);
 }
 
 struct BwdLayout {
@@ -1295,6 +1324,19 @@ BwdLayout bwd_layout(int R, int K, int N, int n_ids, int rank, int eb) {
 }
 
 }  // namespace
+
+uint64_t adapter_fwd_threads(bool bf16, int R, int K, int N, int n_ids, int rank, bool y) {
+  if (R < 1 << 19) return (uint64_t)R * 8 * 512;  // at most a workgroup for each row and column range
+  const AdapterTiles t = bf16 ? adapter_tiles<true>(R, K, N, n_ids, rank, y)
+                              : adapter_tiles<false>(R, K, N, n_ids, rank, y);
+  return (uint64_t)t.wgs * t.waves * kWave;
+}
+
+uint64_t adapter_bwd_threads(bool bf16, int R, int K, int N, int n_ids, int rank, bool dx) {
+  const uint64_t data = adapter_fwd_threads(bf16, R, N, K, n_ids, rank, dx) + kSortBlocks * 512;
+  const uint64_t prepare = transpose_units(n_ids, rank, K, N, bf16 ? 2 : 4) + 256 * (kSortBlocks + 1);
+  return std::max(data, prepare);  // (HIP's own max takes int)
+}
 
 size_t adapter_bwd_ws_bytes(int R, int K, int N, int n_ids, int rank, int elem_bytes) {
   return bwd_layout(R, K, N, n_ids, rank, elem_bytes).total;
@@ -1364,8 +1406,7 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
                       (int32_t*)(w + l.order)};
   hipError_t e = hipSuccess;
   if (d.R > 0) {
-    const long units = (long)d.n_ids * (d.rank * eb / 16) * ((d.K + d.N) * eb / 4);
-    const int tblocks = (int)((units + 255) / 256);
+    const int tblocks = (int)((transpose_units(d.n_ids, d.rank, d.K, d.N, eb) + 255) / 256);
     const int grid = tblocks + (o.nblk > 1 ? o.nblk : 0);
     if (d.bf16)
       adapter_prepare_kernel<true><<<grid, 256, 0, s>>>((const char*)A, (const char*)B, d.rank, d.K,

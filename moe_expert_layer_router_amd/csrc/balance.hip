@@ -607,6 +607,21 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(
   }
 }
 
+// Workgroups of the first launch (no tokens in many sequences: the first clears
+// the ticket).
+int balance_parts(int T, int E) {
+  const int C = balance_chunk(T, E);
+  return max(1, (int)(((long)T + C - 1) / C));
+}
+
+// Columns of a workgroup of the second launch: 64 where a sequence has at most a
+// partial row (parts / S on average) for each of its 16 threads of a column: 236
+// tokens of 255 experts in 38 sequences 5.9 us, 12 with 16; 16384 x 128 in 4
+// sequences 9.4 us, 6.4 with 16.
+int balance_sum_cols(int T, int E, int S) {
+  return E > 16 && balance_parts(T, E) / S <= kSumThreads / 64 ? 64 : 16;
+}
+
 inline size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 struct BalLayout {
@@ -632,6 +647,15 @@ BalLayout balance_layout(int T, int E, int S) {
 
 }  // namespace
 
+uint64_t balance_threads(int T, int E, int S) {
+  if (balance_one(T, E, S)) return kBalThreads;
+  const int cols = balance_sum_cols(T, E, S);
+  return (uint64_t)S * ((E + cols - 1) / cols) * kSumThreads;
+}
+uint64_t balance_bwd_threads(int T, int E) {
+  return ((uint64_t)T + batch_of(E) - 1) / batch_of(E) * kBalThreads;
+}
+
 size_t balance_ws_bytes(int T, int E, int S) { return balance_layout(T, E, S).total; }
 
 hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
@@ -647,8 +671,7 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
   const BalOut out = {counts, prob_sum, tokens, loss};
   const int C = balance_chunk(T, E);
   const bool one = balance_one(T, E, S);
-  // (no tokens in many sequences: the first workgroup clears the ticket)
-  const int grid = one ? 1 : max(1, (T + C - 1) / C);
+  const int grid = one ? 1 : balance_parts(T, E);
   const bool vec = E % 4 == 0 && ((uintptr_t)logits & 15) == 0;
   ProfScope ps(MOE_KERNEL_BALANCE, s);
 #define MOE_BAL(L, V, A, O)                                                                          \
@@ -667,13 +690,10 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
 #undef MOE_BAL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || one) return e;
-  // 64 columns a workgroup where a sequence has at most a partial row (grid / S on
-  // average) for each of its 16 threads of a column: 236 tokens of 255 experts in
-  // 38 sequences 5.9 us, 12 with 16; 16384 x 128 in 4 sequences 9.4 us, 6.4 with 16
 #define MOE_BAL_SUM(COLS)                                                                      \
   balance_sum_kernel<COLS><<<S * ((E + COLS - 1) / COLS), kSumThreads, 0, s>>>(seq_offsets, T, \
                                                                                E, k, S, C, cb, cz, ws, out)
-  if (E > 16 && grid / S <= kSumThreads / 64) MOE_BAL_SUM(64); else MOE_BAL_SUM(16);
+  if (balance_sum_cols(T, E, S) == 64) MOE_BAL_SUM(64); else MOE_BAL_SUM(16);
 #undef MOE_BAL_SUM
   return hipGetLastError();
 }

@@ -198,7 +198,9 @@ hipError_t launch_combine_dropout_bwd(const void* dy, const void* y_perm, const 
                                       int H, int k, bool bf16, void* dy_perm, float* d_topk_w,
                                       hipStream_t s);
 
-// balance.hip
+// balance.hip (threads: of the largest launch that S or T alone can make too large)
+uint64_t balance_threads(int T, int E, int S);
+uint64_t balance_bwd_threads(int T, int E);
 size_t balance_ws_bytes(int T, int E, int S);
 hipError_t launch_balance_loss(const float* logits, const int32_t* topk_idx,
                                const int32_t* seq_offsets, const uint8_t* mask, int T, int E, int k,
@@ -227,6 +229,9 @@ hipError_t launch_adapter_swiglu(const void* gu, const int32_t* row_id, const in
 hipError_t launch_adapter_fwd(const AdapterShape& d, const void* x, const int32_t* src_row,
                               const int32_t* row_id, const void* A, const void* B,
                               const float* scale, void* y, float* v, hipStream_t s);
+// threads of the largest launch, or a bound on them (R > 0; y, dx: whether they are written)
+uint64_t adapter_fwd_threads(bool bf16, int R, int K, int N, int n_ids, int rank, bool y);
+uint64_t adapter_bwd_threads(bool bf16, int R, int K, int N, int n_ids, int rank, bool dx);
 size_t adapter_bwd_ws_bytes(int R, int K, int N, int n_ids, int rank, int elem_bytes);
 hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void* x,
                               const int32_t* src_row, const int32_t* row_id, const void* A,

@@ -569,3 +569,27 @@ def test_rank_values_keep_all_bits(dtype, rank):
     dx = zero.to(dt)
     moe.moe_adapter_bwd(x.to(dt), zero.to(dt), ids, Ab.to(dt), Bb.to(dt), None, dx, want_dw=False)
     assert torch.equal(dx.double(), want)
+
+
+def test_sizes_past_one_launch_are_refused():
+    """A launch has fewer than 2^32 threads.  The adapter kernel: 256 for 16 rows, 32 above rank 64, 128
+    for these in fp32 (the tile that fits a CU twice); the FFN's activation: 64 for a row."""
+    far = lambda n: A.value + n
+
+    def fwd(R, rank, dtype, K=8):
+        return L.moe_adapter_fwd(A, N, A, A, A, N, R, R, K, K, K, K, 4, rank, dtype, far(1 << 46), N, STREAM)
+
+    for rank, dtype, most in ((16, BF16, (1 << 28) - 16), (64, F32, (1 << 28) - 16), (128, BF16, (1 << 29) - 32),
+                              (128, F32, (1 << 30) - 32)):
+        assert fwd(most + 1, rank, dtype) == EUNSUP and "2^32" in _err(), (rank, dtype)
+    big = 1 << 60
+    R = (1 << 28) - 16 + 1
+    assert L.moe_adapter_bwd(A, A, N, A, A, A, A, N, R, R, 8, 8, 8, 8, 8, 4, 16, BF16, far(1 << 46), A, A, 0, A, big,
+                             STREAM) == EUNSUP and "2^32" in _err()
+    # the transposed weights: a thread for 4 bytes of columns of 16 bytes of ranks
+    w = 1 << 20
+    assert L.moe_adapter_bwd(A, A, N, A, A, A, A, N, 4, 4, w, w, w, w, w, 256, 32, F32, far(1 << 46), A, A, 0, A, big,
+                             STREAM) == EUNSUP and "2^32" in _err()
+    R = (1 << 26) - 3
+    assert L.moe_grouped_ffn_fwd_adapter(A, N, A, A, 4, R, R, 4, 4, A, A, A, A, A, N, N, A, A, N, 8, 16, F32, A, A, A,
+                                         A, big, STREAM) == EUNSUP and "2^32" in _err()

@@ -467,3 +467,20 @@ def test_gradient_of_shifted_logits(E, shift):
         err = np.abs(got.cpu().numpy() - ref["d_logits"])
         assert (err <= 80 * U24 * ref["mag"] + 2.0 ** -126).all(), (err / np.maximum(ref["mag"], 1e-30)).max() / U24
     assert torch.equal(d[0], d[1])
+
+
+def test_sizes_past_one_launch_are_refused():
+    """A launch has fewer than 2^32 threads.  The gradient: 256 for a batch of 128 tokens (up to 32
+    experts), 64, 32 or 16 (above 128).  The sums: 1024 for 64 experts of a sequence.  The router
+    backward: 64 for a token."""
+    big = 1 << 50
+    for E, T in ((33, (1 << 30) - 64), (65, (1 << 29) - 32), (129, (1 << 28) - 16), (256, (1 << 28) - 16)):
+        assert L.moe_balance_loss_bwd(A, A, A, A, N, N, N, T + 1, E, 1, 1, 0.1, 0.1, 0, A, STREAM) == -2, E
+        assert "2^32" in _err()
+    for E in (193, 256):
+        assert L.moe_balance_loss(A, A, A, N, 64, E, 1, 1 << 20, 0.1, 0.1, A, A, A, A, A, A, big, STREAM) == -2
+        assert "2^32" in _err()
+        assert L.moe_balance_ws_bytes(64, E, 1 << 20) == -2 and L.moe_balance_ws_bytes(64, E, (1 << 20) - 1) > 0
+    assert L.moe_balance_ws_bytes(64, 192, 1 << 20) > 0 and L.moe_balance_ws_bytes(64, 8, 1 << 20) > 0
+    assert L.moe_route_bwd_add(A, A, A, A, A, A, (1 << 26) - 3, 4, 1, 1, F32, A, N, N, A, big, STREAM) == -2
+    assert "2^32" in _err()

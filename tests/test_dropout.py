@@ -287,3 +287,10 @@ def test_binding_refusals_of_whole_calls(dtype):
         for u in bad(t):
             with pytest.raises(ValueError):
                 moe.moe_combine_dropout_bwd(**{**b, "out": {**b["out"], name: u}})
+
+
+def test_sizes_past_one_launch_are_refused():
+    """A launch has fewer than 2^32 threads, 64 for a token."""
+    T = (1 << 26) - 3
+    assert L.moe_combine_dropout(A, A, A, N, 0.1, A, T, 8, 1, BF16, A, STREAM) == -2 and "2^32" in _err()
+    assert L.moe_combine_dropout_bwd(A, A, A, A, 0.1, A, T, 8, 1, BF16, A, A, STREAM) == -2 and "2^32" in _err()
