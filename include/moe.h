@@ -549,8 +549,8 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
  *   elements; columns past N untouched), A [n_ids,rank,K], B [n_ids,N,rank]
  *   dtype, scale [n_ids] fp32 or NULL (1), row_id [R], src_row [R] int32,
  *   v [R,rank] fp32 or NULL (kept for moe_adapter_bwd)
- * K, N, ldx, ldy multiples of 8 (bf16) or 4 (fp32), at most 2^20; rank a
- * multiple of 8, at most 128 (else MOE_EUNSUPPORTED); 1 <= n_ids <= 2^20; row
+ * K, N, ldx, ldy multiples of 8 (bf16) or 4 (fp32), K and N at most 2^20 (else
+ * MOE_EUNSUPPORTED), ldx >= K and ldy >= N as far as int goes; rank a multiple of 8, at most 128 (else MOE_EUNSUPPORTED); 1 <= n_ids <= 2^20; row
  * data 16-byte aligned; x and y must not share elements (columns of one wider
  * matrix are fine).  R = 0 enqueues nothing. */
 int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id, const void* A,

@@ -472,6 +472,13 @@ def _work(nbytes: int, dev, ws: Optional[torch.Tensor]) -> Optional[torch.Tensor
     return _ws(nbytes, dev, ws)
 
 
+def _int32(**sizes):
+    """Refuses sizes that do not fit the library's int arguments (ctypes would cut them)."""
+    for name, v in sizes.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name}={v} does not fit 32 bits")
+
+
 def _row_type(t: torch.Tensor, name: str) -> torch.dtype:
     if t.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
@@ -495,6 +502,7 @@ def moe_route_bwd_add(d_topk_w: torch.Tensor, topk_w: torch.Tensor, topk_idx: to
     T, H = _shape2(x, "x")
     E = _shape2(w_router, "w_router")[1]
     k = _shape2(topk_idx, "topk_idx")[1]
+    _int32(T=T, H=H, E=E, k=k)
     dt, f32 = _row_type(x, "x"), torch.float32
     o = dict(out or {})
     a = [_arg(d_topk_w, "d_topk_w", f32, (T, k), dev), _arg(topk_w, "topk_w", f32, (T, k), dev),
@@ -539,7 +547,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
         k = topk_idx.shape[1]
         S = 1 if seq_offsets is None else seq_offsets.numel() - 1
         cnt, q, n, lse, loss = map(o.get, ("counts", "prob_sum", "tokens", "lse", "loss"))
-        if (d >= 0 and d == torch._C._cuda_getDevice() and S > 0
+        if (d >= 0 and d == torch._C._cuda_getDevice() and S > 0 and not (T | E | k | S) >> 31
                 and cnt is not None and q is not None and n is not None and lse is not None
                 and loss is not None
                 and logits.dtype is f32 and logits.is_contiguous()
@@ -574,6 +582,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
     T, E = _shape2(logits, "logits")
     k = _shape2(topk_idx, "topk_idx")[1]
     S, off = _sequences(seq_offsets, dev)
+    _int32(T=T, E=E, k=k, S=S)
     a = [_arg(logits, "logits", f32, (T, E), dev), _arg(topk_idx, "topk_idx", i32, (T, k), dev), off,
          _arg(token_mask, "token_mask", torch.uint8, (T,), dev, optional=True)]
     o["ws"] = _work(_balance_ws_bytes(T, E, S), dev, ws)
@@ -600,7 +609,7 @@ def moe_balance_loss_bwd(logits: torch.Tensor, fwd: Dict[str, torch.Tensor], k: 
         T, E = logits.shape
         S = 1 if seq_offsets is None else seq_offsets.numel() - 1
         lse, cnt, n = fwd["lse"], fwd["counts"], fwd["tokens"]
-        if (d >= 0 and d == torch._C._cuda_getDevice() and S > 0
+        if (d >= 0 and d == torch._C._cuda_getDevice() and S > 0 and not (T | E | k | S) >> 31
                 and logits.dtype is f32 and logits.is_contiguous()
                 and lse.dtype is f32 and lse.get_device() == d and lse.shape == (T,)
                 and lse.is_contiguous()
@@ -628,6 +637,7 @@ def moe_balance_loss_bwd(logits: torch.Tensor, fwd: Dict[str, torch.Tensor], k: 
     dev = _device(logits)
     T, E = _shape2(logits, "logits")
     S, off = _sequences(seq_offsets, dev)
+    _int32(T=T, E=E, k=k, S=S)
     if accumulate and out is None:
         raise ValueError("accumulate=True needs out")
     o = {"d_logits": out}
@@ -651,7 +661,7 @@ def moe_combine_dropout(y_perm: torch.Tensor, topk_w: Optional[torch.Tensor], de
     dt, d = y_perm.dtype, y_perm.get_device()
     if out is not None and topk_w is not None and y_perm.dim() == 2 and topk_w.dim() == 2:
         H, k = y_perm.shape[1], topk_w.shape[1]
-        if (d >= 0 and d == torch._C._cuda_getDevice()
+        if (d >= 0 and d == torch._C._cuda_getDevice() and not (T | H | k) >> 31
                 and (dt is torch.bfloat16 or dt is torch.float32) and y_perm.is_contiguous()
                 and topk_w.dtype is torch.float32 and topk_w.get_device() == d
                 and topk_w.shape[0] == T and topk_w.is_contiguous()
@@ -677,6 +687,7 @@ def moe_combine_dropout(y_perm: torch.Tensor, topk_w: Optional[torch.Tensor], de
     if T < 0 or dest_row.numel() % max(T, 1):
         raise ValueError(f"dest_row has {dest_row.numel()} entries, not a multiple of T = {T}")
     k = dest_row.numel() // T if T > 0 else 1
+    _int32(T=T, H=H, k=k)
     if out is None:
         out = torch.empty((T, H), dtype=dt, device=dev)
     rc = lib.moe_combine_dropout(
@@ -703,7 +714,7 @@ def moe_combine_dropout_bwd(dy: torch.Tensor, y_perm: torch.Tensor, topk_w: torc
             and y_perm.dim() == 2):
         T, H = dy.shape
         k = topk_w.shape[1]
-        if (d >= 0 and d == torch._C._cuda_getDevice()
+        if (d >= 0 and d == torch._C._cuda_getDevice() and not (T | H | k) >> 31
                 and (dt is torch.bfloat16 or dt is torch.float32) and dy.is_contiguous()
                 and y_perm.dtype is dt and y_perm.get_device() == d and y_perm.shape[1] == H
                 and y_perm.is_contiguous()
@@ -728,6 +739,7 @@ def moe_combine_dropout_bwd(dy: torch.Tensor, y_perm: torch.Tensor, topk_w: torc
     T, H = _shape2(dy, "dy")
     k = _shape2(topk_w, "topk_w")[1]
     R_cap = _shape2(y_perm, "y_perm")[0]
+    _int32(T=T, H=H, k=k)
     dt = _row_type(dy, "dy")
     a = [_arg(dy, "dy", dt, (T, H), dev), _arg(y_perm, "y_perm", dt, (R_cap, H), dev),
          _arg(topk_w, "topk_w", f32, (T, k), dev),
@@ -749,6 +761,7 @@ def _rows_arg(t: torch.Tensor, name: str, dtype, rows: int, cols: int, dev):
     ld = t.stride(0) if rows > 1 else cols
     if (cols > 1 and t.stride(1) != 1) or ld < cols:
         raise ValueError(f"{name} must have dense rows that do not overlap, got strides {t.stride()}")
+    _int32(**{f"the row pitch of {name}": ld})
     return t.data_ptr(), ld
 
 
@@ -761,6 +774,7 @@ def _adapter_args(x, row_id, A, B, scale, src_row):
     N, R = B.shape[1], row_id.numel()
     dt, i32 = _row_type(A, "A"), torch.int32
     x_rows = _shape2(x, "x")[0]
+    _int32(R=R, x_rows=x_rows, K=K, N=N, n_ids=n_ids, rank=rank)
     if src_row is None and x_rows != R:
         raise ValueError(f"x has {x_rows} rows, row_id {R} (src_row maps one to the other)")
     ptrs = (_arg(src_row, "src_row", i32, (R,), dev, optional=True), _arg(row_id, "row_id", i32, (R,), dev),
@@ -782,7 +796,7 @@ def moe_adapter_fwd(x: torch.Tensor, row_id: torch.Tensor, A: torch.Tensor, B: t
     if A.dim() == 3 and B.dim() == 3 and x.dim() == 2 and (not want_v or out is not None):
         n_ids, rank, K = A.shape
         N, R, x_rows = B.shape[1], row_id.numel(), x.shape[0]
-        if (d >= 0 and d == torch._C._cuda_getDevice()
+        if (d >= 0 and d == torch._C._cuda_getDevice() and not (R | x_rows | K | N | n_ids | rank) >> 31
                 and (dt is torch.bfloat16 or dt is torch.float32)
                 and A.get_device() == d and A.is_contiguous()
                 and B.dtype is dt and B.get_device() == d and B.shape == (n_ids, N, rank)
@@ -837,7 +851,7 @@ def moe_adapter_bwd(dy: torch.Tensor, x: torch.Tensor, row_id: torch.Tensor, A: 
         n_ids, rank, K = A.shape
         N, R, x_rows = B.shape[1], row_id.numel(), x.shape[0]
         code = MOE_BF16 if dt is torch.bfloat16 else MOE_F32
-        if (d >= 0 and d == torch._C._cuda_getDevice()
+        if (d >= 0 and d == torch._C._cuda_getDevice() and not (R | x_rows | K | N | n_ids | rank) >> 31
                 and (dt is torch.bfloat16 or dt is torch.float32)
                 and A.get_device() == d and A.is_contiguous()
                 and B.dtype is dt and B.get_device() == d and B.shape == (n_ids, N, rank)
@@ -894,6 +908,7 @@ def moe_adapter_rows(offsets: torch.Tensor, src_row: torch.Tensor, token_adapter
     token_adapter[src_row[r]] * E_l + expert of r, or -1."""
     dev = _device(offsets)
     E_l, R_cap, T = offsets.numel() - 1, src_row.numel(), token_adapter.numel()
+    _int32(E_l=E_l, R_cap=R_cap, T=T, n_adapters=n_adapters)
     i32 = torch.int32
     o = {"row_id": out}
     _check(lib.moe_adapter_rows(_arg(offsets, "offsets", i32, (E_l + 1,), dev),
@@ -924,6 +939,7 @@ def moe_grouped_ffn_fwd_adapter(x: torch.Tensor, src_row: Optional[torch.Tensor]
     if unknown or not adapters:
         raise ValueError(f"adapters must name some of gate, up, down, got {sorted(adapters)}")
     n_ids, rank = next(iter(adapters.values()))[0].shape[:2]
+    _int32(E_l=E_l, R_cap=R_cap, x_rows=x_rows, H=H, I=I, n_ids=n_ids, rank=rank)
     ab = []
     for name, k, n in (("gate", H, I), ("up", H, I), ("down", I, H)):
         pair = adapters.get(name)
