@@ -686,7 +686,7 @@ def moe_combine_dropout(y_perm: torch.Tensor, topk_w: Optional[torch.Tensor], de
     dt = _row_type(y_perm, "y_perm")
     if T < 0 or dest_row.numel() % max(T, 1):
         raise ValueError(f"dest_row has {dest_row.numel()} entries, not a multiple of T = {T}")
-    k = dest_row.numel() // T if T > 0 else 1
+    k = topk_w.shape[1] if topk_w is not None and topk_w.dim() == 2 else dest_row.numel() // max(T, 1) or 1
     _int32(T=T, H=H, k=k)
     if out is None:
         out = torch.empty((T, H), dtype=dt, device=dev)

@@ -62,3 +62,14 @@ def test_pitches_past_32_bits(no_gpu, which):
             moe.moe_adapter_fwd(a["x"], w["row_id"], w["A"], w["B"], a["y"])
         else:
             moe.moe_adapter_bwd(a["dy"], a["x"], w["row_id"], w["A"], w["B"], t(f32, 3, 16), a["dx"])
+
+
+@pytest.mark.parametrize("k", [1, 2, 8])
+@pytest.mark.parametrize("given", [False, True])
+def test_dropout_of_no_tokens(no_gpu, k, given):
+    """An empty batch of any number of slots, with the output given or not."""
+    out = t(bf, 0, 16) if given else None
+    y = moe.moe_combine_dropout(t(bf, 0, 16), t(f32, 0, k), t(i32, 0), 0, 0.1, t(i64, 2), out=out)
+    assert y.shape == (0, 16)
+    b = moe.moe_combine_dropout_bwd(t(bf, 0, 16), t(bf, 0, 16), t(f32, 0, k), t(i32, 0), 0.1, t(i64, 2))
+    assert b["dy_perm"].shape == (0, 16) and b["d_topk_w"].shape == (0, k)
