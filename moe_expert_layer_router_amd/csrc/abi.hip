@@ -1091,8 +1091,10 @@ bool rows_overlap(const void* a, int64_t a_rows, int lda, int a_cols, const void
                   int ldb, int b_cols, int eb) {
   if (a_rows == 0 || b_rows == 0) return false;
   const intptr_t a0 = (intptr_t)a, b0 = (intptr_t)b;
-  if (a0 >= b0 + ((b_rows - 1) * ldb + b_cols) * eb || b0 >= a0 + ((a_rows - 1) * lda + a_cols) * eb)
-    return false;
+  // (an x that is gathered from may claim more than 2^63 bytes)
+  const __int128 a1 = a0 + ((__int128)(a_rows - 1) * lda + a_cols) * eb;
+  const __int128 b1 = b0 + ((__int128)(b_rows - 1) * ldb + b_cols) * eb;
+  if (a0 >= b1 || b0 >= a1) return false;
   if (lda != ldb) return true;
   const int64_t pitch = (int64_t)lda * eb, at = ((b0 - a0) % pitch + pitch) % pitch;
   return at < (int64_t)a_cols * eb || at + (int64_t)b_cols * eb > pitch;

@@ -9,6 +9,8 @@ Tolerances (u = 2^-24; e = eps / 2 of the type: half a rounding step relative to
   dA  w's error through x; the sum of n rows of (three times, for the parts) products:
       (3 n + 16) u; dB the same with v
 Values below the normal range of the parts may be lost: 1e-30 absolute."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -593,3 +595,12 @@ def test_sizes_past_one_launch_are_refused():
     R = (1 << 26) - 3
     assert L.moe_grouped_ffn_fwd_adapter(A, N, A, A, 4, R, R, 4, 4, A, A, A, A, A, N, N, A, A, N, 8, 16, F32, A, A, A,
                                          A, big, STREAM) == EUNSUP and "2^32" in _err()
+
+
+def test_overlap_of_the_largest_matrices():
+    """Extents past 2^63 bytes (as the arguments give them) are compared without overflow."""
+    x = ctypes.c_void_p(A.value + (1 << 40))
+    for back in (64, 1 << 30, 1 << 38):
+        y = ctypes.c_void_p(x.value + back)
+        assert L.moe_adapter_fwd(x, A, A, A, A, N, 16, (1 << 31) - 1, 64, 64, (1 << 31) - 8, 64, 4, 16, F32, y, N,
+                                 STREAM) == EINVAL and "overlap" in _err()
