@@ -1095,6 +1095,8 @@ bool rows_overlap(const void* a, int64_t a_rows, int lda, int a_cols, const void
   const __int128 a1 = a0 + ((__int128)(a_rows - 1) * lda + a_cols) * eb;
   const __int128 b1 = b0 + ((__int128)(b_rows - 1) * ldb + b_cols) * eb;
   if (a0 >= b1 || b0 >= a1) return false;
+  if (a_rows == 1) lda = ldb;  // one row lies in any pitch
+  if (b_rows == 1) ldb = lda;
   if (lda != ldb) return true;
   const int64_t pitch = (int64_t)lda * eb, at = ((b0 - a0) % pitch + pitch) % pitch;
   return at < (int64_t)a_cols * eb || at + (int64_t)b_cols * eb > pitch;

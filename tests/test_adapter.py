@@ -597,6 +597,25 @@ def test_sizes_past_one_launch_are_refused():
                                          A, big, STREAM) == EUNSUP and "2^32" in _err()
 
 
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("row", [0, 3, 19])
+def test_one_row_beside_many(dtype, row):
+    """x one row of a matrix, behind the columns that y takes of all its rows: they share nothing."""
+    s = make(dtype, 20, 64, 72, 3, 16, "mixed", False, 1)
+    src = torch.zeros(20, dtype=torch.int32, device=DEV)
+    wide = torch.cat([s["y"], s["x"]], 1)
+    x = s["x"][row:row + 1].contiguous()
+    moe.moe_adapter_fwd(x, s["ids"], s["A"], s["B"], s["y"], src_row=src)
+    moe.moe_adapter_fwd(wide[row:row + 1, 72:], s["ids"], s["A"], s["B"], wide[:, :72], src_row=src)
+    assert torch.equal(wide[:, :72], s["y"]) and torch.equal(wide[:, 72:], s["x"])
+    # one that begins in y's columns, and one that ends in those of the next row
+    for first in (8, 64) + ((80,) if row < 19 else ()):
+        flat = wide.reshape(-1)[row * 136 + first:row * 136 + first + 64].reshape(1, 64)
+        with pytest.raises(moe.MoEError, match="overlap"):
+            moe.moe_adapter_fwd(flat, s["ids"], s["A"], s["B"], wide[:, :72], src_row=src)
+
+
 def test_overlap_of_the_largest_matrices():
     """Extents past 2^63 bytes (as the arguments give them) are compared without overflow."""
     x = ctypes.c_void_p(A.value + (1 << 40))
