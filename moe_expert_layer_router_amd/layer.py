@@ -112,6 +112,8 @@ class MoELayer:
             b["aux_counts"] = torch.empty((S, E), dtype=i32, device=dev)
             b["aux_prob_sum"] = torch.empty((S, E), dtype=f32, device=dev)
             b["aux_tokens"] = torch.empty(S + 1, dtype=i32, device=dev)
+            # all tokens as the first sequence, for a forward without seq_offsets
+            b["aux_one"] = torch.tensor([0] + [T] * S, dtype=i32, device=dev) if S > 1 else None
             nb = lib.moe_balance_ws_bytes(T, E, S)
             if nb < 0:
                 _check(int(nb), "moe_balance_ws_bytes")
@@ -175,8 +177,9 @@ class MoELayer:
         """residual [T,H]: added to the combined rows.  rng [2] int64 on the GPU (seed, offset):
         the dropout's numbers, still in it when backward() repeats them.  seq_offsets [S+1] int32 and
         token_mask [T] uint8: the sequences and padding of the auxiliary losses (S = max_sequences,
-        fewer with empty ones behind the last; None: one sequence).  adapters: dict token_adapter [T] int32 (-1: none), n, gate / up / down: (A, B)
-        with A [n, E_l, rank, in] and B [n, E_l, out, rank], scale [n, E_l] fp32 (optional)."""
+        fewer with empty ones behind the last; None: all tokens are one sequence).  adapters: dict
+        token_adapter [T] int32 (-1: none), n, gate / up / down: (A, B) with A [n, E_l, rank, in] and
+        B [n, E_l, out, rank], scale [n, E_l] fp32 (optional)."""
         b, T, H, I, E, k = self.buf, self.T, self.H, self.I, self.E, self.k
         if self.dropout > 0.0 and rng is None:
             raise ValueError("a layer with dropout needs rng")
@@ -229,9 +232,11 @@ class MoELayer:
         b = self.buf
         if not save_logits:
             raise ValueError("the auxiliary losses read the logits: save_logits must be True")
-        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-        if S != self.max_sequences:
-            raise ValueError(f"{S} sequences given to a layer built for {self.max_sequences}")
+        if seq_offsets is None:
+            seq_offsets = b["aux_one"]
+        elif seq_offsets.numel() - 1 != self.max_sequences:
+            raise ValueError(f"{seq_offsets.numel() - 1} sequences given to a layer built for "
+                             f"{self.max_sequences}")
         self._sequences = (seq_offsets, token_mask)
         moe_balance_loss(b["logits"], b["topk_idx"], self.balance_coef, self.z_coef, seq_offsets,
                          token_mask, ws=self.ws_aux,

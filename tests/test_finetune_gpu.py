@@ -253,3 +253,26 @@ def test_refusals():
     p = moe.moe_permute(t["x"], torch.zeros((8, 1), dtype=torch.int32, device=DEV), 8, 0, 8)
     with pytest.raises(ValueError, match="gate, up, down"):
         moe.moe_grouped_ffn_fwd_adapter(p["x_perm"], None, p["offsets"], p["src_row"], *a[2:], {})
+
+
+def test_one_sequence_in_a_layer_for_several():
+    """Without seq_offsets all tokens are one sequence, in a layer built for more as well."""
+    w = TINY.scaled(name="t", T=90)
+    t = inputs(w, torch.float32)
+    a = (t["x"], t["w_router"], t["w_gate"], t["w_up"], t["w_down"])
+    shape = (w.T, w.H, w.I, w.E, w.k, 0, 8, torch.float32, DEV)
+    one, four = (moe.MoELayer(*shape, balance_coef=0.1, z_coef=0.02, max_sequences=n) for n in (1, 4))
+    mask = (torch.arange(w.T, device=DEV) % 5 != 0).to(torch.uint8)
+    dy = torch.ones(w.T, w.H, device=DEV)
+    got = []
+    for layer in (one, four):
+        layer.forward(*a, token_mask=mask)
+        grads = layer.backward(dy, *a)
+        got.append([grads["d_logits"], grads["dx"], layer.buf["aux_loss"], layer.buf["aux_counts"][0],
+                    layer.buf["aux_prob_sum"][0]])
+    for u, v in zip(*got):
+        assert torch.equal(u, v)
+    assert not four.buf["aux_counts"][1:].any() and not four.buf["aux_prob_sum"][1:].any()
+    assert four.buf["aux_tokens"].tolist() == [72, 0, 0, 0, 72]
+    with pytest.raises(ValueError, match="sequences"):
+        four.forward(*a, seq_offsets=torch.tensor([0, w.T], dtype=torch.int32, device=DEV))
