@@ -928,7 +928,7 @@ def moe_grouped_ffn_fwd_adapter(x: torch.Tensor, src_row: Optional[torch.Tensor]
     """Grouped SwiGLU FFN forward with low-rank adapters on the expert projections.  x: the
     grouped rows (src_row None) or, bf16, the token rows with moe_permute's src_row; row_id from
     moe_adapter_rows; adapters: {"gate"|"up"|"down": (A, B)}, A [n_ids, rank, in] and B [n_ids,
-    out, rank] of one n_ids and rank.  Returns dict h_perm, y_perm, gu."""
+    out, rank] of one n_ids and rank (None: as if not given).  Returns dict h_perm, y_perm, gu."""
     dev = _device(x)
     dt = _row_type(x, "x")
     x_rows, H = _shape2(x, "x")
@@ -936,8 +936,10 @@ def moe_grouped_ffn_fwd_adapter(x: torch.Tensor, src_row: Optional[torch.Tensor]
     R_cap = row_id.numel()
     i32 = torch.int32
     unknown = set(adapters) - {"gate", "up", "down"}
+    adapters = {name: pair for name, pair in adapters.items() if pair is not None}
     if unknown or not adapters:
-        raise ValueError(f"adapters must name some of gate, up, down, got {sorted(adapters)}")
+        raise ValueError(f"adapters must name some of gate, up, down, got "
+                         f"{sorted(unknown.union(adapters))}")
     n_ids, rank = next(iter(adapters.values()))[0].shape[:2]
     _int32(E_l=E_l, R_cap=R_cap, x_rows=x_rows, H=H, I=I, n_ids=n_ids, rank=rank)
     ab = []

@@ -253,7 +253,7 @@ class MoELayer:
         n = adapters["n"]
         moe_adapter_rows(b["offsets"], b["src_row"], adapters["token_adapter"], n, out=b["row_id"])
         flat = {name: tuple(t.view(n * self.E_l, *t.shape[2:]) for t in adapters[name])
-                for name in ("gate", "up", "down") if name in adapters}
+                for name in ("gate", "up", "down") if adapters.get(name) is not None}
         scale = adapters.get("scale")
         moe_grouped_ffn_fwd_adapter(x if self.gather else b["x_perm"],
                                     b["src_row"] if self.gather else None, b["offsets"], b["row_id"],

@@ -276,3 +276,29 @@ def test_one_sequence_in_a_layer_for_several():
     assert four.buf["aux_tokens"].tolist() == [72, 0, 0, 0, 72]
     with pytest.raises(ValueError, match="sequences"):
         four.forward(*a, seq_offsets=torch.tensor([0, w.T], dtype=torch.int32, device=DEV))
+
+
+def test_projections_without_adapters():
+    """A projection given as None is one that is not given, first or last; all of them None is refused."""
+    w = EP_SHARE.scaled(name="l", T=33, H=128, I=64, E=8, k=2, e_lo=0, e_hi=8)
+    t = inputs(w, torch.bfloat16)
+    a = (t["x"], t["w_router"], t["w_gate"], t["w_up"], t["w_down"])
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rnd = lambda *s: (torch.randn(s, generator=g, device=DEV) * 0.2).bfloat16()
+    up = (rnd(2, 8, 8, w.H), rnd(2, 8, w.I, 8))
+    who = torch.randint(-1, 2, (w.T,), generator=g, device=DEV, dtype=torch.int32)
+    layer = moe.MoELayer(w.T, w.H, w.I, w.E, w.k, 0, 8, torch.bfloat16, DEV, train=False, adapters=True)
+    plain = layer.forward(*a).clone()
+    want = layer.forward(*a, adapters=dict(n=2, token_adapter=who, up=up)).clone()
+    got = layer.forward(*a, adapters=dict(n=2, token_adapter=who, gate=None, up=up, down=None))
+    assert torch.equal(got, want) and not torch.equal(got, plain)
+    p = moe.moe_permute(t["x"], layer.buf["topk_idx"], 8, 0, 8)
+    rows = moe.moe_adapter_rows(p["offsets"], p["src_row"], who, 2)
+    call = lambda ad: moe.moe_grouped_ffn_fwd_adapter(p["x_perm"], None, p["offsets"], rows, *a[2:], ad)["y_perm"]
+    flat = tuple(u.reshape(16, *u.shape[2:]) for u in up)
+    n = int(p["offsets"][-1])
+    assert torch.equal(call({"gate": None, "up": flat})[:n], call({"up": flat})[:n])
+    with pytest.raises(ValueError, match="gate, up, down"):
+        call({"gate": None, "down": None})
+    with pytest.raises(ValueError, match="gate, up, down"):
+        layer.forward(*a, adapters=dict(n=2, token_adapter=who))
