@@ -71,19 +71,21 @@ __device__ __forceinline__ int pack_slots(int d, float w, int& dc, float& wc, in
 
 // out[c] = sum over packed slots j < n (ascending) of wc_j * rows[dc_j][c] for
 // this lane's chunks c0 + u * 64 + lane; fp32 accumulation.  STREAM: the rows
-// are read once (streaming loads).
+// are read once (streaming loads).  n <= 64: groups of SG slots that divide the
+// wave never ask a lane behind its last.
 template <bool BF16, bool STREAM, int CU = kCU, int SG = kSG>
 __device__ __forceinline__ void gather_rows(const void* __restrict__ rows, int H, int nch, int c0,
                                             int n, int dc, float wc,
                                             float (&acc)[CU][Row<BF16>::N]) {
   using R = Row<BF16>;
+  static_assert(kWave % SG == 0, "a group of slots ends inside the wave");
   const int lane = lane_id();
   for (int j0 = 0; j0 < n; j0 += SG) {
     u32x4_t raw[SG][CU];
     float wj[SG];
 #pragma unroll
     for (int s = 0; s < SG; ++s) {
-      const int j = j0 + s;  // < 36: a valid lane index
+      const int j = j0 + s;  // < 64: a valid lane index
       const int dj = __shfl(dc, j, kWave);
       wj[s] = (j < n) ? __shfl(wc, j, kWave) : 0.f;
 #pragma unroll
