@@ -623,3 +623,51 @@ def test_overlap_of_the_largest_matrices():
         y = ctypes.c_void_p(x.value + back)
         assert L.moe_adapter_fwd(x, A, A, A, A, N, 16, (1 << 31) - 1, 64, 64, (1 << 31) - 8, 64, 4, 16, F32, y, N,
                                  STREAM) == EINVAL and "overlap" in _err()
+
+
+def whole_numbers(dtype, R, K, N_, n_ids, rank, seed):
+    """make() with -1, 0 and 1 for x, y, dx and dy, and four 1 or -1 in each rank value's column of A
+    and of B: all results are whole numbers that their types hold."""
+    s = make(dtype, R, K, N_, n_ids, rank, "sorted", False, seed, scaled=False)
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    for n in ("x", "y", "dy", "dx"):
+        s[n] = torch.randint(-1, 2, s[n].shape, generator=g, device=DEV).to(s[n].dtype)
+    for n, cols in (("A", K), ("B", N_)):
+        w = torch.zeros(n_ids, rank, cols, device=DEV)
+        at = torch.randint(0, cols, (n_ids, rank, 4), generator=g, device=DEV)
+        w.scatter_(2, at, torch.randint(0, 2, at.shape, generator=g, device=DEV).float() * 2 - 1)
+        s[n] = (w if n == "A" else w.transpose(1, 2)).contiguous().to(s[n].dtype)
+    return s
+
+
+LONG = [  # R, K, N, n_ids, rank: rows of a chunk of the weight gradients, several chunks an adapter
+    (9001, 768, 2048, 16, 16),    # 256
+    (9001, 4096, 4096, 5, 8),     # 512
+    (20011, 4104, 4096, 9, 32),   # 1024
+    (16000, 2048, 1536, 3, 24),   # 384
+    (300001, 64, 64, 7, 8),       # 896; a wave orders more than 512 rows
+    (40000, 256, 256, 5, 64), (33333, 64, 64, 1, 16), (20001, 128, 136, 2, 128),  # 128
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,K,N_,n_ids,rank", LONG)
+def test_no_row_is_lost(dtype, R, K, N_, n_ids, rank):
+    """Sums of whole numbers below 2^24 are exact in any order: a row that is missing or taken twice
+    shows.  |v|, |w| <= 4 and at most R rows: sums of at most 4 R < 2^21."""
+    s = whole_numbers(dtype, R, K, N_, n_ids, rank, R + rank)
+    if dtype == "f32" and R == 9001:
+        s["ids"] = s["ids"][torch.randperm(R, generator=torch.Generator().manual_seed(1)).to(DEV)].contiguous()
+    o, _ = definition(s["x"], None, s["ids"], s["A"], s["B"], None, s["y"], s["dy"], s["dx"])
+    v = moe.moe_adapter_fwd(s["x"], s["ids"], s["A"], s["B"], s["y"], want_v=True)
+    r = moe.moe_adapter_bwd(s["dy"], s["x"], s["ids"], s["A"], s["B"], v, s["dx"])
+    for n, got in (("v", v), ("y", s["y"]), ("dx", s["dx"]), ("dA", r["dA"]), ("dB", r["dB"])):
+        assert torch.equal(got.double(), o[n]), n
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,K,N_,n_ids,rank", LONG[:5])
+def test_long_gradients(dtype, R, K, N_, n_ids, rank):
+    check(make(dtype, R, K, N_, n_ids, rank, "sorted", False, R + rank))

@@ -484,3 +484,22 @@ def test_sizes_past_one_launch_are_refused():
     assert L.moe_balance_ws_bytes(64, 192, 1 << 20) > 0 and L.moe_balance_ws_bytes(64, 8, 1 << 20) > 0
     assert L.moe_route_bwd_add(A, A, A, A, A, A, (1 << 26) - 3, 4, 1, 1, F32, A, N, N, A, big, STREAM) == -2
     assert "2^32" in _err()
+
+
+@gpu
+@pytest.mark.parametrize("T,E,S,drop", [(5000, 128, 1, 0.0), (20000, 256, 40, 0.1), (262144, 64, 3, 0.2),
+                                        (400, 32, 2, 0.3), (6000, 16, 900, 0.0), (33, 1, 1, 0.0)])
+def test_no_row_is_lost(T, E, S, drop):
+    """Rows of equal logits, E a power of two: every probability is 1 / E, and the sums n_s / E are exact
+    in any order."""
+    rng = np.random.default_rng(T)
+    z = np.repeat(rng.standard_normal((T, 1)).astype(np.float32), E, axis=1)
+    idx = rng.integers(0, E, (T, 1)).astype(np.int32)
+    off = offsets_of(rng, T, S) if S > 1 else np.array([0, T], np.int32)
+    live = rng.random(T) >= drop
+    f = moe.moe_balance_loss(dev(z), dev(idx), 1.0, seq_offsets=dev(off), token_mask=dev(live.astype(np.uint8)))
+    n = np.array([live[off[s]:off[s + 1]].sum() for s in range(S)])
+    assert np.array_equal(f["tokens"].cpu().numpy(), np.append(n, n.sum()))
+    assert np.array_equal(f["prob_sum"].cpu().numpy(), np.repeat(n[:, None] / E, E, axis=1).astype(np.float32))
+    want = np.stack([np.bincount(idx[off[s]:off[s + 1], 0][live[off[s]:off[s + 1]]], minlength=E) for s in range(S)])
+    assert np.array_equal(f["counts"].cpu().numpy(), want)
