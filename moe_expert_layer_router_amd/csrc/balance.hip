@@ -229,7 +229,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_part_kernel(
   __shared__ int s_n[NG];
   const int tid = threadIdx.x, lane = lane_id();
   const int h = lane % LPT, g = (tid >> 6) * G + lane / LPT;
-  const int t0 = ONE ? 0 : blockIdx.x * C, t1 = ONE ? T : min(T, t0 + C);
+  const int t0 = ONE ? 0 : blockIdx.x * C, t1 = ONE ? T : t0 + min(C, T - t0);
   if constexpr (!ONE) {
     if (blockIdx.x == 0 && tid == 0) *ws.ticket = 0;
     if (t0 >= t1) return;
@@ -629,8 +629,7 @@ struct BalLayout {
 };
 
 BalLayout balance_layout(int T, int E, int S) {
-  const int C = balance_chunk(T, E);
-  const size_t slots = (size_t)(T + C - 1) / C + S;
+  const size_t slots = (size_t)balance_parts(T, E) + S;
   BalLayout l;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t was = at; at += up256(bytes); return was; };

@@ -503,3 +503,31 @@ def test_no_row_is_lost(T, E, S, drop):
     assert np.array_equal(f["prob_sum"].cpu().numpy(), np.repeat(n[:, None] / E, E, axis=1).astype(np.float32))
     want = np.stack([np.bincount(idx[off[s]:off[s + 1], 0][live[off[s]:off[s + 1]]], minlength=E) for s in range(S)])
     assert np.array_equal(f["counts"].cpu().numpy(), want)
+
+
+def test_workspace_of_the_most_tokens():
+    """1024 chunks and the sequences at most, up to the largest T."""
+    for T in (0x7FFF0000, 0x7FFF0000 - 65536, (1 << 31) - (1 << 21), 1 << 28):
+        for E in (1, 8, 33, 65, 200):
+            assert 0 < L.moe_balance_ws_bytes(T, E, 3) <= 8 * (1030 * (E + 4) + 64 * E), (T, E)
+
+
+@gpu
+def test_the_most_tokens():
+    """T k = 0x7fff0000: the last chunk ends near 2^31.  Equal logits of two experts: p = 1/2, sums of
+    halves exact up to 2^24 a thread and then as multiples of a chunk's."""
+    T = 0x7FFF0000
+    z = torch.zeros((T, 2), device=DEV)
+    idx = torch.zeros((T, 1), dtype=torch.int32, device=DEV)
+    idx[-3:] = 1
+    f = moe.moe_balance_loss(z, idx, 1.0)
+    assert f["counts"].tolist() == [[T - 3, 3]] and f["tokens"].tolist() == [T, T]
+    assert f["prob_sum"].tolist() == [[T / 2, T / 2]]
+    assert abs(float(f["loss"][0]) - 1.0) < 1e-6
+    del f["lse"]
+    f["lse"] = torch.full((T,), 0.6931472, device=DEV)
+    d = moe.moe_balance_loss_bwd(z, f, 1, 1.0)
+    # p (E / (k N n) (c - sum p c)) = 1/2 2 / T^2 (+-)(c0 - c1) / 2
+    want = (T - 6) / 2 / T / T
+    for rows in (d[:2], d[T // 2:T // 2 + 2], d[-2:]):
+        assert ((rows.double() - torch.tensor([want, -want], device=DEV)).abs() <= 8 * U24 * want).all()
