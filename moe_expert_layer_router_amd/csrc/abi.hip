@@ -1129,6 +1129,8 @@ int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id
 int64_t moe_adapter_ws_bytes(int R, int K, int N, int n_ids, int rank, int dtype) {
   const char* fn = "moe_adapter_ws_bytes";
   if (int rc = check_adapter(R, K, N, n_ids, rank, dtype, kMaxE, fn)) return rc;
+  if (R > 0)
+    if (int rc = check_launch(adapter_bwd_threads(dtype == MOE_BF16, R, K, N, n_ids, rank, true), fn)) return rc;
   return (int64_t)adapter_bwd_ws_bytes(R, K, N, n_ids, rank, elem_bytes(dtype));
 }
 
