@@ -56,6 +56,8 @@ def _p(t: Optional[torch.Tensor]):
 
 
 class MoELayer:
+    ADAPTER_KEYS = frozenset(("token_adapter", "n", "gate", "up", "down", "scale"))
+
     def __init__(self, T: int, H: int, I: int, E: int, k: int, e_lo: int, e_hi: int,
                  dtype: torch.dtype, device="cuda", train: bool = True, fp8: bool = False,
                  gather: Optional[bool] = None, balance_coef: float = 0.0, z_coef: float = 0.0,
@@ -185,6 +187,9 @@ class MoELayer:
             raise ValueError("a layer with dropout needs rng")
         if adapters is not None and not self.adapters:
             raise ValueError("the layer was built without adapters")
+        if adapters is not None and not self.ADAPTER_KEYS.issuperset(adapters):
+            raise ValueError(f"adapters has {sorted(set(adapters) - self.ADAPTER_KEYS)}, which are none of "
+                             f"{sorted(self.ADAPTER_KEYS)}")
         s = _stream()
         ws, wsb = _p(self.ws), self.ws_bytes
         if self.fp8:

@@ -302,3 +302,17 @@ def test_projections_without_adapters():
         call({"gate": None, "down": None})
     with pytest.raises(ValueError, match="gate, up, down"):
         layer.forward(*a, adapters=dict(n=2, token_adapter=who))
+
+
+def test_misnamed_projections_are_refused():
+    """A key of the adapters that means nothing would leave its projection without them, in silence."""
+    w = TINY.scaled(name="t", T=8)
+    t = inputs(w, torch.float32)
+    a = (t["x"], t["w_router"], t["w_gate"], t["w_up"], t["w_down"])
+    layer = moe.MoELayer(w.T, w.H, w.I, w.E, w.k, 0, 8, torch.float32, DEV, train=False, adapters=True)
+    who = torch.zeros(w.T, dtype=torch.int32, device=DEV)
+    up = (torch.zeros(1, 8, 8, w.H, device=DEV), torch.zeros(1, 8, w.I, 8, device=DEV))
+    layer.forward(*a, adapters=dict(n=1, token_adapter=who, up=up))
+    for wrong in (dict(gat=up), dict(w_down=up), dict(scales=torch.ones(1, 8, device=DEV))):
+        with pytest.raises(ValueError, match=next(iter(wrong))):
+            layer.forward(*a, adapters=dict(n=1, token_adapter=who, up=up, **wrong))
