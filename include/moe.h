@@ -500,9 +500,8 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t
  *                                  + z_coef 2 lse[t] / N)
  * Rows that are not live get 0.  accumulate != 0 adds to d_logits.  p is formed
  * again from the logits, relative to their largest (exp(z - lse) would lose the
- * bits that lse has rounded away).  logits,
- * lse, counts, tokens, seq_offsets and token_mask as given to and written by
- * moe_balance_loss. */
+ * bits that lse has rounded away).  logits, lse, counts, tokens, seq_offsets and
+ * token_mask as given to and written by moe_balance_loss. */
 int moe_balance_loss_bwd(const float* logits, const float* lse, const int32_t* counts,
                          const int32_t* tokens, const int32_t* seq_offsets,
                          const uint8_t* token_mask, const float* d_loss, int T, int E, int k, int S,
@@ -550,9 +549,10 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
  *   dtype, scale [n_ids] fp32 or NULL (1), row_id [R], src_row [R] int32,
  *   v [R,rank] fp32 or NULL (kept for moe_adapter_bwd)
  * K, N, ldx, ldy multiples of 8 (bf16) or 4 (fp32), K and N at most 2^20 (else
- * MOE_EUNSUPPORTED), ldx >= K and ldy >= N as far as int goes; rank a multiple of 8, at most 128 (else MOE_EUNSUPPORTED); 1 <= n_ids <= 2^20; row
- * data 16-byte aligned; x and y must not share elements (columns of one wider
- * matrix are fine).  R = 0 enqueues nothing. */
+ * MOE_EUNSUPPORTED), ldx >= K and ldy >= N as far as int goes; rank a multiple
+ * of 8, at most 128 (else MOE_EUNSUPPORTED); 1 <= n_ids <= 2^20; row data 16-byte
+ * aligned; x and y must not share elements (columns of one wider matrix are
+ * fine).  R = 0 enqueues nothing. */
 int moe_adapter_fwd(const void* x, const int32_t* src_row, const int32_t* row_id, const void* A,
                     const void* B, const float* scale, int R, int x_rows, int K, int N, int ldx,
                     int ldy, int n_ids, int rank, int dtype, void* y, float* v, void* stream);
@@ -594,7 +594,8 @@ int moe_adapter_rows(const int32_t* offsets, const int32_t* src_row, const int32
  *           rounded product)                                  -> gu [R_cap,2I]
  *   h     = SiLU(g) * u, for rows with an adapter from the stored g, u -> h_perm
  *   y     = the down product + its adapter's on h_perm               -> y_perm
- * Rows without an adapter get the bits of the call without adapters.
+ * Rows without an adapter get the bits of the call without adapters.  Forward
+ * only: the rank values are not kept, and moe_grouped_ffn_bwd knows no adapters.
  *   row_id [R_cap] from moe_adapter_rows (rows past offsets[E_l]: -1);
  *   a_gate, a_up [n_ids,rank,H], b_gate, b_up [n_ids,I,rank], a_down
  *   [n_ids,rank,I], b_down [n_ids,H,rank] dtype (a pair may be NULL: no adapter

@@ -1254,6 +1254,9 @@ int moe_grouped_ffn_fwd_adapter(const void* x, const int32_t* src_row, const int
                                      (const float*)w_gate, (const float*)w_up, (const float*)w_down,
                                      (float*)gu, (float*)h_perm, (float*)y_perm, s, products);
   };
+  // The adapters add to g and u as the product stored them (bf16: rounded, and
+  // rounded again with the adapter's part), so that the product's kernel and the
+  // bits of the rows without adapter stay those of the plain forward.
   hipError_t e = ffn(kFfnGateUp);
   const AdapterShape in = {bf16, R_cap, x_rows, H, I, n_ids, rank, H, 2 * I};
   char* u = (char*)gu + (size_t)I * elem_bytes(dtype);

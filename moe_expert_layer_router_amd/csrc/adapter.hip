@@ -612,7 +612,8 @@ __global__ __launch_bounds__(NW* kWave) void adapter_kernel(AdapterArgs p, int o
   // The rank values (in the first wave's place) as fragments.  bf16 holds each
   // fp32 value whole as three bf16 parts (8 bits each), three instructions on the
   // same weights: the products are exact and the sums fp32, like those of the
-  // fp32 path.
+  // fp32 path.  (Two parts, 16 of the 24 bits, gain 0 to 2 %: 8191 rows of rank 64
+  // 27.6 us for 28.2.)
   constexpr int KF = BF16 ? (RT + 1) / 2 : RT;  // fragment steps of the rank values
   constexpr int NP = BF16 ? 3 : 1;
   u32x4_t vf[NP][MT][KF];

@@ -118,7 +118,8 @@ __device__ __forceinline__ float reciprocal(float s) {
 
 // The probabilities of a token's logits p[v][i] (behind the row's end -inf), in
 // their place: exp(p - top) over its sum, so that a shift of the whole row, which
-// a softmax does not depend on, costs no bits.
+// a softmax does not depend on, costs no bits.  (exp(p - lse) in the gradient, with
+// lse in fp32, is off by half a step of |lse|; 32768 x 128: 8.4 us, 9.2 so.)
 struct Top {
   float top, sum;
   bool none;  // a row of -inf alone: probabilities and sum 0

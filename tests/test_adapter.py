@@ -3,8 +3,8 @@ definitions.
 
 Tolerances (u = 2^-24; e = eps / 2 of the type: half a rounding step relative to the value):
   v   fp32 sum of K products (products of bf16 values are exact) and the scale: (K + 8) u sum |.|
-  y   v's error through B; v held as two bf16 halves, 2^-16 relative (bf16 only); the sum of
-      rank (twice, for the halves) products: (2 rank + 8) u; then one rounding: e |y| + u |y|
+  y   v's error through B; 2^-16 relative for v's own bits (bf16 only; test_rank_values_keep_all_bits
+      asks for all of them); the sum of rank products: (2 rank + 8) u; then one rounding: e |y| + u |y|
   dx  the same with N products in w
   dA  w's error through x; the sum of n rows of (three times, for the parts) products:
       (3 n + 16) u; dB the same with v
