@@ -683,3 +683,27 @@ def test_workspace_of_the_most_rows():
         R = most - 20000
         need = 4 * R * (rank + 1) + R // 512 * rank * 16 * 4 + R // 64
         assert need - (1 << 20) <= w(R, 8, 8, 4, rank, dtype) <= need + (1 << 20)
+
+
+@gpu
+def test_the_most_rows():
+    """Near the 2^28 rows of one launch: rows of zeros but for a few at both ends and in the middle,
+    whole numbers, forward and backward exact (sums of at most 4 * 300)."""
+    R, few = (1 << 28) - 5000, 100
+    s = whole_numbers("bf16", 3 * few, 8, 16, 3, 8, 5)
+    at = torch.cat([torch.arange(few), torch.arange(few) + R // 2, torch.arange(few) + (R - few)]).to(DEV)
+    big = {}
+    for n, cols in (("x", 8), ("dy", 16)):
+        big[n] = torch.zeros((R, cols), dtype=torch.bfloat16, device=DEV)
+        big[n][at] = s[n]
+    ids = torch.ones(R, dtype=torch.int32, device=DEV)
+    ids[at] = s["ids"]
+    y, dx = torch.zeros_like(big["dy"]), torch.zeros_like(big["x"])
+    zero = [torch.zeros_like(s[n]) for n in ("y", "dx")]
+    o, _ = definition(s["x"], None, s["ids"], s["A"], s["B"], None, zero[0], s["dy"], zero[1])
+    v = moe.moe_adapter_fwd(big["x"], ids, s["A"], s["B"], y, want_v=True)
+    r = moe.moe_adapter_bwd(big["dy"], big["x"], ids, s["A"], s["B"], v, dx)
+    for n, got in (("v", v[at]), ("y", y[at]), ("dx", dx[at]), ("dA", r["dA"]), ("dB", r["dB"])):
+        assert torch.equal(got.double(), o[n]), n
+    y[at], dx[at] = 0, 0
+    assert not y.any() and not dx.any()

@@ -294,3 +294,21 @@ def test_sizes_past_one_launch_are_refused():
     T = (1 << 26) - 3
     assert L.moe_combine_dropout(A, A, A, N, 0.1, A, T, 8, 1, BF16, A, STREAM) == -2 and "2^32" in _err()
     assert L.moe_combine_dropout_bwd(A, A, A, A, 0.1, A, T, 8, 1, BF16, A, A, STREAM) == -2 and "2^32" in _err()
+
+
+@gpu
+def test_the_most_tokens():
+    """2^26 - 4 tokens, a wave for each: the last ones' elements lie past 2^29."""
+    H, p, seed, offset = 8, 0.5, 21, 9
+    T = (1 << 26) - 4
+    dest = torch.arange(T, dtype=torch.int32, device=DEV)
+    yp = torch.ones(T, H, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(T, 1, device=DEV)
+    state = torch.tensor([seed, offset], dtype=torch.int64, device=DEV)
+    y = moe.moe_combine_dropout(yp, w, dest, T, p, state)
+    b = moe.moe_combine_dropout_bwd(yp, yp, w, dest, p, state)
+    for t0 in (0, T // 2, T - 500):
+        keep = torch.from_numpy(keep_mask(seed, offset, 500, H, p, t0=t0)).to(DEV)
+        want = torch.where(keep, 2.0, 0.0).bfloat16()
+        assert torch.equal(y[t0:t0 + 500], want) and torch.equal(b["dy_perm"][t0:t0 + 500], want)
+        assert torch.equal(b["d_topk_w"][t0:t0 + 500, 0], want.float().sum(dim=1))
