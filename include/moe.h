@@ -610,6 +610,129 @@ int moe_grouped_ffn_fwd_adapter(const void* x, const int32_t* src_row, const int
                                 const float* scale, int n_ids, int rank, int dtype, void* gu,
                                 void* h_perm, void* y_perm, void* ws, size_t ws_bytes, void* stream);
 
+/* RMS norm before the layer, with the residual update:
+ *   r[t] = x[t] + delta[t]                                 (fp32, stored as dtype)
+ *   n[t] = r[t] / sqrt(mean_h r[t,h]^2 + eps) * weight     (of the stored r; fp32, rounded once)
+ * delta NULL: r is x and is not written.
+ *   x, delta, r, n [T,H] dtype (r may be x or delta), weight [H] fp32
+ * 1 <= H <= 16384 (else MOE_EUNSUPPORTED), eps > 0; row data and weight 16-byte
+ * aligned.  T = 0 enqueues nothing. */
+int moe_norm(const void* x, const void* delta, const float* weight, double eps, int T, int H,
+             int dtype, void* r, void* n, void* stream);
+
+/* Backward of moe_norm for the gradient dn of n and, where r has other readers
+ * (the residual), dr of r (or NULL).  With s = 1 / sqrt(mean r^2 + eps), xh = s r:
+ *   dx[t]   = dr[t] + s (dn weight - xh mean_h(dn weight xh))   [T,H] dtype
+ *   dweight = sum_t dn[t] xh[t]                                 [H] fp32
+ * dx is the gradient of x and of delta.  Nothing of the forward but r is needed.
+ * dweight is overwritten or, with accumulate != 0, added to; its rows are summed
+ * in an order fixed by T and H alone.  dx may be dn or dr.
+ *   ws  moe_norm_ws_bytes(H) bytes.  T = 0 writes (or keeps) dweight only. */
+int64_t moe_norm_ws_bytes(int H);
+int moe_norm_bwd(const void* dn, const void* dr, const void* r, const float* weight, double eps,
+                 int T, int H, int dtype, void* dx, float* dweight, int accumulate, void* ws,
+                 size_t ws_bytes, void* stream);
+
+/* The weighted combine with the RMS norm after the layer, a gate and the scaled
+ * residual, for every token:
+ *   c    = sum_{j: dest_row[t*k+j] >= 0} topk_w[t,j] * y_perm[dest_row[t*k+j]]
+ *   y[t] = residual_scale * residual[t] + gate[t] * (c / sqrt(mean_h c^2 + eps)) * weight
+ * in fp32, rounded once.  A token without a local slot gets residual_scale *
+ * residual[t].  (The norm is of the whole combined row: with experts on several
+ * ranks the parts have to be added up first.)
+ *   gate: MOE_GATE_NONE NULL (1); MOE_GATE_TOKEN [T] fp32; MOE_GATE_FULL [T,H] dtype
+ *   residual [T,H] dtype or NULL (0); y may be residual; weight [H] fp32
+ *   other arguments as moe_combine.  Limits as moe_norm. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_FULL = 2 } moe_gate;
+
+int moe_combine_norm(const void* y_perm, const float* topk_w, const int32_t* dest_row,
+                     const void* residual, double residual_scale, const void* gate, int gate_kind,
+                     const float* weight, double eps, int T, int H, int k, int dtype, void* y,
+                     void* stream);
+
+/* Backward of moe_combine_norm for dy [T,H].  c is formed again from the grouped
+ * rows; with s = 1 / sqrt(mean c^2 + eps), xh = s c, g = dy gate weight:
+ *   dc = s (g - xh mean_h(g xh))                            (fp32, not rounded)
+ *   dy_perm[dest_row[t*k+j]] = topk_w[t,j] * dc             (stored as dtype)
+ *   d_topk_w[t,j] = <dc, y_perm[dest_row[t*k+j]]>           (fp32; 0 for non-local slots)
+ *   dgate  = sum_h dy weight xh [T] fp32, or dy weight xh [T,H] dtype, as the gate
+ *   dweight = sum_t dy gate xh  [H] fp32, overwritten or added to (accumulate)
+ * The residual's gradient is residual_scale * dy.  Sums in a fixed order.
+ *   ws  moe_norm_ws_bytes(H) bytes */
+int moe_combine_norm_bwd(const void* dy, const void* y_perm, const float* topk_w,
+                         const int32_t* dest_row, const void* gate, int gate_kind,
+                         const float* weight, double eps, int T, int H, int k, int dtype,
+                         void* dy_perm, float* d_topk_w, void* dgate, float* dweight,
+                         int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Rows as 8-bit integers: for each group of `group` neighbouring columns of a
+ * row, with a its largest magnitude,
+ *   scale = a / 127,  q = rint(v * (127 / a))   (ties to even), value = q * scale,
+ * every quotient and product one correctly rounded fp32 operation.  a < 2^-100
+ * gives scale 0 and codes 0; a group with an infinity or a NaN has that as its
+ * scale (and comes back as NaN).  Operands of moe_grouped_gemm_i8 and
+ * moe_grouped_ffn_fwd_i8 (group = cols: one scale a row, for weights a channel),
+ * and activation checkpoints (group below cols).
+ *   src [rows,cols] MOE_BF16 or MOE_F32, q [rows,cols] int8, scale
+ *   [rows,cols/group] fp32; rows >= *nrows (device, or NULL) are not written
+ * cols % 16 == 0; group is cols, or 32, 64, 128, 256 or 512 and divides cols;
+ * row data 16-byte aligned. */
+int moe_quantize_i8(const void* src, int rows, int cols, int group, int dtype,
+                    const int32_t* nrows, int8_t* q, float* scale, void* stream);
+
+/* The values of code rows, out[r] = value(q[src_row[r]]) (src_row NULL: q[r]),
+ * rounded to dtype: with src_row of moe_permute the grouped rows of a checkpoint
+ * of token rows.  An entry of src_row outside [0, src_rows) gives a row of 0.
+ *   q [src_rows,cols] int8, scale [src_rows,cols/group] fp32, src_row [rows]
+ *   int32 or NULL (src_rows = rows), out [rows,cols] dtype; nrows, cols as above;
+ *   group a multiple of 16 that divides cols */
+int moe_dequantize_i8(const int8_t* q, const float* scale, const int32_t* src_row, int rows,
+                      int src_rows, int cols, int group, int dtype, const int32_t* nrows,
+                      void* out, void* stream);
+
+/* What moe_grouped_ffn_bwd reads of a forward whose gu_saved was kept as 8-bit
+ * codes alone (moe_quantize_i8 of its rows):
+ *   gu[r] = value(q[r]) rounded to dtype,  h_perm[r] = SiLU(g) * u of those values
+ *   q [rows,2I] int8, scale [rows,2I/group] fp32, gu [rows,2I], h_perm [rows,I]
+ *   dtype; nrows as above; I % 16 == 0, group a multiple of 16 that divides 2I */
+int moe_swiglu_restore_i8(const int8_t* q, const float* scale, int rows, int I, int group,
+                          int dtype, const int32_t* nrows, void* gu, void* h_perm, void* stream);
+
+/* Product of int8 rows with int8 weights, grouped by expert, for the rows r of
+ * expert e in [offsets[e], offsets[e+1]):
+ *   y[r,n] = x_scale[s] * w_scale[e,n] * sum_k x_q[s,k] * w_q[e,n,k],  s = src_row[r]
+ * (src_row NULL: s = r).  The sum is exact; the scales are applied in fp32 and
+ * the result rounded once to bf16, so the bits do not depend on the variant.
+ * Groups may have any size, 0 included; E_l = 1 is an ordinary product.
+ *   x_q [x_rows,K] int8, x_scale [x_rows] fp32, src_row [R_cap] int32 or NULL
+ *   (x_rows = R_cap; entries below offsets[E_l] are clamped into [0,x_rows)),
+ *   w_q [E_l,N,K] int8, w_scale [E_l,N] fp32, y [R_cap,N] bf16 (rows >= R not
+ *   written)
+ * K and N multiples of 16, K <= 65536, x_rows * K and N * K below 2^31 (else
+ * MOE_EUNSUPPORTED); pointers of row data and scales 16-byte aligned. */
+int moe_grouped_gemm_i8(const int8_t* x_q, const float* x_scale, const int32_t* src_row,
+                        const int32_t* offsets, int E_l, int R_cap, int x_rows, int K, int N,
+                        const int8_t* w_q, const float* w_scale, void* y, void* stream);
+
+/* Grouped SwiGLU expert FFN, forward, on int8 codes (serving; the token rows and
+ * each row of the weights quantized by moe_quantize_i8 with group = cols):
+ *   g, u      = the products with wg and wu as moe_grouped_gemm_i8 (fp32, not rounded)
+ *   h_perm[r] = bf16(SiLU(g) * u), its rows quantized as moe_quantize_i8 does
+ *   y_perm[r] = the product of those codes with wd
+ *   x_q [x_rows,H] int8, x_scale [x_rows] fp32, src_row as above,
+ *   wg_q / wu_q [E_l,I,H] int8 with wg_scale / wu_scale [E_l,I] fp32, wd_q
+ *   [E_l,H,I] int8 with wd_scale [E_l,H] fp32, h_perm [R_cap,I], y_perm
+ *   [R_cap,H] bf16
+ *   ws  moe_ffn_i8_ws_bytes(R_cap, I) bytes (codes and scales of h)
+ * H and I multiples of 16, at most 65536; x_rows * H, R_cap * I and I * H below
+ * 2^31 (else MOE_EUNSUPPORTED). */
+int64_t moe_ffn_i8_ws_bytes(int R_cap, int I);
+int moe_grouped_ffn_fwd_i8(const int8_t* x_q, const float* x_scale, const int32_t* src_row,
+                           const int32_t* offsets, int E_l, int R_cap, int x_rows, int H, int I,
+                           const int8_t* wg_q, const float* wg_scale, const int8_t* wu_q,
+                           const float* wu_scale, const int8_t* wd_q, const float* wd_scale,
+                           void* h_perm, void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
 /* Kernel timing hook (benchmarks and profilers).  After this call the library
  * records start_events[i] and stop_events[i] (each a hipEvent_t created by
  * the caller) on the launch stream immediately before and after the i-th
@@ -644,7 +767,16 @@ typedef enum {
   MOE_KERNEL_ADAPTER = 22,           /* moe_adapter_fwd */
   MOE_KERNEL_ADAPTER_DGRAD = 23,     /* moe_adapter_bwd: w and dx */
   MOE_KERNEL_ADAPTER_WGRAD = 24,     /* moe_adapter_bwd: dA and dB, without the partials' sum */
-  MOE_KERNEL_COUNT = 25
+  MOE_KERNEL_NORM = 25,
+  MOE_KERNEL_NORM_BWD = 26,          /* both launches */
+  MOE_KERNEL_COMBINE_NORM = 27,
+  MOE_KERNEL_COMBINE_NORM_BWD = 28,  /* both launches */
+  MOE_KERNEL_QUANTIZE_I8 = 29,
+  MOE_KERNEL_RESTORE_I8 = 30,        /* moe_swiglu_restore_i8 */
+  MOE_KERNEL_GEMM_I8 = 31,           /* moe_grouped_gemm_i8 (both kernels) */
+  MOE_KERNEL_FFN_GATEUP_I8 = 32,
+  MOE_KERNEL_FFN_DOWN_I8 = 33,
+  MOE_KERNEL_COUNT = 34
 } moe_kernel;
 
 int moe_profile_kernel(int kernel_id, void** start_events, void** stop_events, int n);

@@ -96,6 +96,17 @@ def _load():
         "moe_grouped_ffn_fwd_adapter": ([P] * 4 + [I32] * 5 + [P] * 10 + [I32] * 3 + [P, P, P, P, SZ, P],
                                         I32),
         "moe_adapter_rows": ([P, P, P, I32, I32, I32, I32, P, P], I32),
+        "moe_norm": ([P, P, P, F64, I32, I32, I32, P, P, P], I32),
+        "moe_norm_ws_bytes": ([I32], I64),
+        "moe_norm_bwd": ([P, P, P, P, F64, I32, I32, I32, P, P, I32, P, SZ, P], I32),
+        "moe_combine_norm": ([P, P, P, P, F64, P, I32, P, F64, I32, I32, I32, I32, P, P], I32),
+        "moe_combine_norm_bwd": ([P] * 5 + [I32, P, F64] + [I32] * 4 + [P] * 4 + [I32, P, SZ, P], I32),
+        "moe_quantize_i8": ([P, I32, I32, I32, I32, P, P, P, P], I32),
+        "moe_dequantize_i8": ([P, P, P, I32, I32, I32, I32, I32, P, P, P], I32),
+        "moe_swiglu_restore_i8": ([P, P, I32, I32, I32, I32, P, P, P, P], I32),
+        "moe_grouped_gemm_i8": ([P] * 4 + [I32] * 5 + [P] * 4, I32),
+        "moe_ffn_i8_ws_bytes": ([I32, I32], I64),
+        "moe_grouped_ffn_fwd_i8": ([P] * 4 + [I32] * 5 + [P] * 9 + [SZ, P], I32),
         "moe_profile_kernel": ([I32, ctypes.POINTER(P), ctypes.POINTER(P), I32], I32),
         "moe_profile_recorded": ([], I32),
     }
@@ -428,6 +439,16 @@ def _raw_stream(dev: torch.device) -> int:
     """The current stream of a device as a pointer (without building a Stream object, which
     costs as much as a small kernel)."""
     return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _cuda_device() -> int:
+    """Index of the current GPU."""
+    return torch._C._cuda_getDevice()
+
+
+def _cuda_stream(index: int) -> int:
+    """The current stream of the GPU of this index, as a pointer."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _device(t: torch.Tensor) -> torch.device:
@@ -964,6 +985,9 @@ def moe_grouped_ffn_fwd_adapter(x: torch.Tensor, src_row: Optional[torch.Tensor]
     return o
 
 
+from .norm import moe_combine_norm, moe_combine_norm_bwd, moe_norm, moe_norm_bwd  # noqa: E402,F401
+from .int8 import (moe_dequantize_i8, moe_grouped_ffn_fwd_i8, moe_grouped_gemm_i8,  # noqa: E402,F401
+                   moe_quantize_i8, moe_swiglu_restore_i8)
 from .layer import MoELayer  # noqa: E402,F401
 
 

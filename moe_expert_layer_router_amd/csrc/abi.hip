@@ -1273,4 +1273,257 @@ int moe_grouped_ffn_fwd_adapter(const void* x, const int32_t* src_row, const int
   return hip_status(e, fn);
 }
 
+namespace {
+constexpr int kNormMaxWidth = 16384;
+
+int check_norm(int T, int H, int dtype, double eps, const float* weight, const char* fn) {
+  if (int rc = check_dtype(dtype, fn)) return rc;
+  if (int rc = check_rows(T, "T", fn)) return rc;
+  if (int rc = check_row_width(H, dtype, fn)) return rc;
+  if (H > kNormMaxWidth) return fail(MOE_EUNSUPPORTED, "%s: H=%d above %d", fn, H, kNormMaxWidth);
+  // as the kernels hold it: a smaller eps would be 0 in fp32
+  if (!((float)eps >= 1.17549435e-38f && eps <= 3.4028234e38))
+    return fail(MOE_EINVAL, "%s: eps=%g must be a positive normal fp32 number", fn, eps);
+  // a wave for every row, or a workgroup of up to 1024 threads for long ones
+  const uint64_t wide = (uint64_t)H * elem_bytes(dtype) > 16384 ? 1024 : H * elem_bytes(dtype) > 4096 ? 256 : 64;
+  if (int rc = check_launch((uint64_t)T * wide + 255, fn)) return rc;
+  return T == 0 ? MOE_OK : check_ptr(weight, "weight", fn, true);
+}
+
+int check_gate(const void* gate, int kind, const char* name, const char* fn) {
+  if (kind != MOE_GATE_NONE && kind != MOE_GATE_TOKEN && kind != MOE_GATE_FULL)
+    return fail(MOE_EINVAL, "%s: unknown gate_kind %d", fn, kind);
+  if (kind == MOE_GATE_NONE) return MOE_OK;
+  return check_ptr(gate, name, fn, kind == MOE_GATE_FULL);
+}
+
+int check_accumulate(int accumulate, const char* fn) {
+  if (accumulate != 0 && accumulate != 1) return fail(MOE_EINVAL, "%s: accumulate must be 0 or 1", fn);
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_norm(const void* x, const void* delta, const float* weight, double eps, int T, int H,
+             int dtype, void* r, void* n, void* stream) {
+  const char* fn = "moe_norm";
+  if (int rc = check_norm(T, H, dtype, eps, weight, fn)) return rc;
+  if (T == 0) return MOE_OK;
+  if (int rc = check_ptr(x, "x", fn, true)) return rc;
+  if (int rc = check_ptr(n, "n", fn, true)) return rc;
+  if (delta != nullptr) {
+    if (int rc = check_ptr(delta, "delta", fn, true)) return rc;
+    if (int rc = check_ptr(r, "r", fn, true)) return rc;
+  }
+  return hip_status(launch_norm(x, delta, weight, (float)eps, T, H, dtype == MOE_BF16, r, n,
+                                begin_launch(stream)),
+                    fn);
+}
+
+int64_t moe_norm_ws_bytes(int H) {
+  const char* fn = "moe_norm_ws_bytes";
+  if (H <= 0) return fail(MOE_EINVAL, "%s: H must be positive (got %d)", fn, H);
+  if (H > kNormMaxWidth) return fail(MOE_EUNSUPPORTED, "%s: H=%d above %d", fn, H, kNormMaxWidth);
+  return (int64_t)norm_ws_bytes(H);
+}
+
+int moe_norm_bwd(const void* dn, const void* dr, const void* r, const float* weight, double eps,
+                 int T, int H, int dtype, void* dx, float* dweight, int accumulate, void* ws,
+                 size_t ws_bytes, void* stream) {
+  const char* fn = "moe_norm_bwd";
+  if (int rc = check_norm(T, H, dtype, eps, weight, fn)) return rc;
+  if (int rc = check_accumulate(accumulate, fn)) return rc;
+  if (T > 0) {
+    if (int rc = check_ptr(dn, "dn", fn, true)) return rc;
+    if (int rc = check_ptr(r, "r", fn, true)) return rc;
+    if (int rc = check_ptr(dx, "dx", fn, true)) return rc;
+    if (!aligned16(dr)) return fail(MOE_EINVAL, "%s: dr must be 16-byte aligned", fn);
+  }
+  if (int rc = check_ptr(dweight, "dweight", fn)) return rc;
+  if (int rc = check_ws(ws, ws_bytes, norm_ws_bytes(H), fn)) return rc;
+  return hip_status(launch_norm_bwd(dn, dr, r, weight, (float)eps, T, H, dtype == MOE_BF16, dx, dweight,
+                                    accumulate != 0, ws, begin_launch(stream)),
+                    fn);
+}
+
+int moe_combine_norm(const void* y_perm, const float* topk_w, const int32_t* dest_row,
+                     const void* residual, double residual_scale, const void* gate, int gate_kind,
+                     const float* weight, double eps, int T, int H, int k, int dtype, void* y,
+                     void* stream) {
+  const char* fn = "moe_combine_norm";
+  if (int rc = check_norm(T, H, dtype, eps, weight, fn)) return rc;
+  if (k < 1 || k > kMaxK) return fail(MOE_EINVAL, "%s: k=%d outside [1, %d]", fn, k, kMaxK);
+  if (T == 0) return MOE_OK;
+  if (int rc = check_gate(gate, gate_kind, "gate", fn)) return rc;
+  if (int rc = check_ptr(y_perm, "y_perm", fn, true)) return rc;
+  if (int rc = check_ptr(dest_row, "dest_row", fn)) return rc;
+  if (int rc = check_ptr(y, "y", fn, true)) return rc;
+  if (!aligned16(residual)) return fail(MOE_EINVAL, "%s: residual must be 16-byte aligned", fn);
+  return hip_status(launch_combine_norm(y_perm, topk_w, dest_row, residual, (float)residual_scale, gate,
+                                        gate_kind, weight, (float)eps, T, H, k, dtype == MOE_BF16, y,
+                                        begin_launch(stream)),
+                    fn);
+}
+
+int moe_combine_norm_bwd(const void* dy, const void* y_perm, const float* topk_w,
+                         const int32_t* dest_row, const void* gate, int gate_kind,
+                         const float* weight, double eps, int T, int H, int k, int dtype,
+                         void* dy_perm, float* d_topk_w, void* dgate, float* dweight,
+                         int accumulate, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_combine_norm_bwd";
+  if (int rc = check_norm(T, H, dtype, eps, weight, fn)) return rc;
+  if (k < 1 || k > kMaxK) return fail(MOE_EINVAL, "%s: k=%d outside [1, %d]", fn, k, kMaxK);
+  if (int rc = check_accumulate(accumulate, fn)) return rc;
+  if (T > 0) {
+    if (int rc = check_gate(gate, gate_kind, "gate", fn)) return rc;
+    if (int rc = check_gate(dgate, gate_kind, "dgate", fn)) return rc;
+    if (int rc = check_ptr(dy, "dy", fn, true)) return rc;
+    if (int rc = check_ptr(y_perm, "y_perm", fn, true)) return rc;
+    if (int rc = check_ptr(topk_w, "topk_w", fn)) return rc;
+    if (int rc = check_ptr(dest_row, "dest_row", fn)) return rc;
+    if (int rc = check_ptr(dy_perm, "dy_perm", fn, true)) return rc;
+    if (int rc = check_ptr(d_topk_w, "d_topk_w", fn)) return rc;
+  }
+  if (int rc = check_ptr(dweight, "dweight", fn)) return rc;
+  if (int rc = check_ws(ws, ws_bytes, norm_ws_bytes(H), fn)) return rc;
+  return hip_status(launch_combine_norm_bwd(dy, y_perm, topk_w, dest_row, gate, gate_kind, weight,
+                                            (float)eps, T, H, k, dtype == MOE_BF16, dy_perm, d_topk_w,
+                                            dgate, dweight, accumulate != 0, ws, begin_launch(stream)),
+                    fn);
+}
+
+namespace {
+// Rows of `cols` columns whose codes carry a scale for every `group` of them.
+int check_rows_i8(int rows, int cols, int group, int dtype, const char* fn) {
+  if (int rc = check_dtype(dtype, fn)) return rc;
+  if (int rc = check_rows(rows, "rows", fn)) return rc;
+  if (cols <= 0 || cols % 16 != 0)
+    return fail(MOE_EINVAL, "%s: cols=%d must be a positive multiple of 16", fn, cols);
+  if (group <= 0 || group % 16 != 0 || cols % group != 0)
+    return fail(MOE_EINVAL, "%s: group=%d must be a multiple of 16 that divides cols=%d", fn, group, cols);
+  if (int rc = check_launch(rows_i8_threads(rows, cols), fn)) return rc;
+  return check_launch(wave_per_row(rows), fn);
+}
+}  // namespace
+
+int moe_quantize_i8(const void* src, int rows, int cols, int group, int dtype,
+                    const int32_t* nrows, int8_t* q, float* scale, void* stream) {
+  const char* fn = "moe_quantize_i8";
+  if (int rc = check_rows_i8(rows, cols, group, dtype, fn)) return rc;
+  if (group != cols && (group < 32 || group > 512 || (group & (group - 1)) != 0))
+    return fail(MOE_EUNSUPPORTED, "%s: group=%d must be cols or 32, 64, 128, 256 or 512", fn, group);
+  if (rows == 0) return MOE_OK;
+  if (int rc = check_ptr(src, "src", fn, true)) return rc;
+  if (int rc = check_ptr(q, "q", fn, true)) return rc;
+  if (int rc = check_ptr(scale, "scale", fn)) return rc;
+  return hip_status(launch_quantize_i8(src, rows, cols, group, dtype == MOE_BF16, nrows, q, scale,
+                                       begin_launch(stream)),
+                    fn);
+}
+
+int moe_dequantize_i8(const int8_t* q, const float* scale, const int32_t* src_row, int rows,
+                      int src_rows, int cols, int group, int dtype, const int32_t* nrows,
+                      void* out, void* stream) {
+  const char* fn = "moe_dequantize_i8";
+  if (int rc = check_rows_i8(rows, cols, group, dtype, fn)) return rc;
+  if (src_rows < 0 || (src_row == nullptr && src_rows != rows))
+    return fail(MOE_EINVAL, "%s: src_rows=%d (without src_row the rows=%d)", fn, src_rows, rows);
+  if (rows == 0) return MOE_OK;
+  if (src_rows > 0) {
+    if (int rc = check_ptr(q, "q", fn, true)) return rc;
+    if (int rc = check_ptr(scale, "scale", fn)) return rc;
+  }
+  if (int rc = check_ptr(out, "out", fn, true)) return rc;
+  return hip_status(launch_dequantize_i8(q, scale, src_row, rows, src_rows, cols, group,
+                                         dtype == MOE_BF16, nrows, out, begin_launch(stream)),
+                    fn);
+}
+
+int moe_swiglu_restore_i8(const int8_t* q, const float* scale, int rows, int I, int group,
+                          int dtype, const int32_t* nrows, void* gu, void* h_perm, void* stream) {
+  const char* fn = "moe_swiglu_restore_i8";
+  if (I <= 0 || I % 16 != 0 || I > 0x3fffffff)
+    return fail(MOE_EINVAL, "%s: I=%d must be a positive multiple of 16, below 2^30", fn, I);
+  if (int rc = check_rows_i8(rows, 2 * I, group, dtype, fn)) return rc;
+  if (rows == 0) return MOE_OK;
+  if (int rc = check_ptr(q, "q", fn, true)) return rc;
+  if (int rc = check_ptr(scale, "scale", fn)) return rc;
+  if (int rc = check_ptr(gu, "gu", fn, true)) return rc;
+  if (int rc = check_ptr(h_perm, "h_perm", fn, true)) return rc;
+  return hip_status(launch_swiglu_restore_i8(q, scale, rows, I, group, dtype == MOE_BF16, nrows, gu,
+                                             h_perm, begin_launch(stream)),
+                    fn);
+}
+
+namespace {
+// The sums of products of codes (-128 included) stay below 2^31 up to this K.
+constexpr int kGemmI8MaxK = 65536;
+
+int check_gemm_i8(int E_l, int R_cap, int x_rows, bool gathered, int K, int N, const char* k_name,
+                  const char* n_name, const char* fn) {
+  if (E_l < 1 || E_l > kMaxE) return fail(MOE_EINVAL, "%s: E_l=%d outside [1, %d]", fn, E_l, kMaxE);
+  if (int rc = check_rows(R_cap, "R_cap", fn)) return rc;
+  if (K <= 0 || N <= 0 || K % 16 != 0 || N % 16 != 0)
+    return fail(MOE_EINVAL, "%s: %s=%d and %s=%d must be positive multiples of 16", fn, k_name, K, n_name, N);
+  if (K > kGemmI8MaxK) return fail(MOE_EUNSUPPORTED, "%s: %s=%d above %d", fn, k_name, K, kGemmI8MaxK);
+  if (x_rows < 0 || (R_cap > 0 && x_rows == 0) || (!gathered && x_rows != R_cap))
+    return fail(MOE_EINVAL, "%s: x_rows=%d (without src_row the R_cap=%d grouped rows)", fn, x_rows, R_cap);
+  if (int rc = check_range((int64_t)x_rows * K, "x_q", fn)) return rc;
+  if (int rc = check_range((int64_t)N * K, "one expert's weight", fn)) return rc;
+  return check_launch(gemm_i8_threads(R_cap, E_l, N), fn);
+}
+}  // namespace
+
+int moe_grouped_gemm_i8(const int8_t* x_q, const float* x_scale, const int32_t* src_row,
+                        const int32_t* offsets, int E_l, int R_cap, int x_rows, int K, int N,
+                        const int8_t* w_q, const float* w_scale, void* y, void* stream) {
+  const char* fn = "moe_grouped_gemm_i8";
+  if (int rc = check_gemm_i8(E_l, R_cap, x_rows, src_row != nullptr, K, N, "K", "N", fn)) return rc;
+  if (R_cap == 0) return MOE_OK;
+  if (int rc = check_ptr(x_q, "x_q", fn, true)) return rc;
+  if (int rc = check_ptr(x_scale, "x_scale", fn)) return rc;
+  if (int rc = check_ptr(offsets, "offsets", fn)) return rc;
+  if (int rc = check_ptr(w_q, "w_q", fn, true)) return rc;
+  if (int rc = check_ptr(w_scale, "w_scale", fn, true)) return rc;
+  if (int rc = check_ptr(y, "y", fn, true)) return rc;
+  return hip_status(launch_gemm_i8(x_q, x_scale, src_row, x_rows, offsets, E_l, R_cap, K, N, w_q, w_scale,
+                                   (bf16_t*)y, begin_launch(stream)),
+                    fn);
+}
+
+int64_t moe_ffn_i8_ws_bytes(int R_cap, int I) {
+  const char* fn = "moe_ffn_i8_ws_bytes";
+  if (int rc = check_rows(R_cap, "R_cap", fn)) return rc;
+  if (I <= 0 || I % 16 != 0) return fail(MOE_EINVAL, "%s: I=%d must be a positive multiple of 16", fn, I);
+  if (int rc = check_range((int64_t)R_cap * I, "the codes of h", fn)) return rc;
+  return (int64_t)ffn_fwd_i8_ws_bytes(R_cap, I);
+}
+
+int moe_grouped_ffn_fwd_i8(const int8_t* x_q, const float* x_scale, const int32_t* src_row,
+                           const int32_t* offsets, int E_l, int R_cap, int x_rows, int H, int I,
+                           const int8_t* wg_q, const float* wg_scale, const int8_t* wu_q,
+                           const float* wu_scale, const int8_t* wd_q, const float* wd_scale,
+                           void* h_perm, void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_grouped_ffn_fwd_i8";
+  if (int rc = check_gemm_i8(E_l, R_cap, x_rows, src_row != nullptr, H, I, "H", "I", fn)) return rc;
+  if (int rc = check_gemm_i8(E_l, R_cap, R_cap, false, I, H, "I", "H", fn)) return rc;
+  if (int rc = check_launch(wave_per_row(R_cap), fn)) return rc;
+  if (R_cap == 0) return MOE_OK;
+  if (int rc = check_ptr(x_q, "x_q", fn, true)) return rc;
+  if (int rc = check_ptr(x_scale, "x_scale", fn)) return rc;
+  if (int rc = check_ptr(offsets, "offsets", fn)) return rc;
+  if (int rc = check_ptr(wg_q, "wg_q", fn, true)) return rc;
+  if (int rc = check_ptr(wg_scale, "wg_scale", fn, true)) return rc;
+  if (int rc = check_ptr(wu_q, "wu_q", fn, true)) return rc;
+  if (int rc = check_ptr(wu_scale, "wu_scale", fn, true)) return rc;
+  if (int rc = check_ptr(wd_q, "wd_q", fn, true)) return rc;
+  if (int rc = check_ptr(wd_scale, "wd_scale", fn, true)) return rc;
+  if (int rc = check_ptr(h_perm, "h_perm", fn, true)) return rc;
+  if (int rc = check_ptr(y_perm, "y_perm", fn, true)) return rc;
+  if (int rc = check_ws(ws, ws_bytes, ffn_fwd_i8_ws_bytes(R_cap, I), fn)) return rc;
+  return hip_status(launch_ffn_fwd_i8(x_q, x_scale, src_row, x_rows, offsets, E_l, R_cap, H, I, wg_q,
+                                      wg_scale, wu_q, wu_scale, wd_q, wd_scale, (bf16_t*)h_perm,
+                                      (bf16_t*)y_perm, ws, begin_launch(stream)),
+                    fn);
+}
+
 }  // extern "C"

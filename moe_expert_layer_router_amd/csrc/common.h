@@ -239,6 +239,44 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
                               long lddx, float* dA, float* dB, bool accumulate, void* ws,
                               hipStream_t s);
 
+// norm.hip (RMS norms before and after the layer); gate kinds of moe.h
+size_t norm_ws_bytes(int H);
+hipError_t launch_norm(const void* x, const void* delta, const float* weight, float eps, int T, int H,
+                       bool bf16, void* r, void* n, hipStream_t s);
+hipError_t launch_norm_bwd(const void* dn, const void* dr, const void* r, const float* weight, float eps,
+                           int T, int H, bool bf16, void* dx, float* dweight, bool accumulate, void* ws,
+                           hipStream_t s);
+hipError_t launch_combine_norm(const void* y_perm, const float* topk_w, const int32_t* dest_row,
+                               const void* residual, float residual_scale, const void* gate, int gate_kind,
+                               const float* weight, float eps, int T, int H, int k, bool bf16, void* y,
+                               hipStream_t s);
+hipError_t launch_combine_norm_bwd(const void* dy, const void* y_perm, const float* topk_w,
+                                   const int32_t* dest_row, const void* gate, int gate_kind,
+                                   const float* weight, float eps, int T, int H, int k, bool bf16,
+                                   void* dy_perm, float* d_topk_w, void* dgate, float* dweight,
+                                   bool accumulate, void* ws, hipStream_t s);
+
+// rows_i8.hip (rows as 8-bit integers); threads of a launch over rows of cols
+uint64_t rows_i8_threads(int rows, int cols);
+hipError_t launch_quantize_i8(const void* src, int rows, int cols, int group, bool bf16,
+                              const int32_t* nrows, int8_t* q, float* scale, hipStream_t s);
+hipError_t launch_dequantize_i8(const int8_t* q, const float* scale, const int32_t* src_row, int rows,
+                                int src_rows, int cols, int group, bool bf16, const int32_t* nrows,
+                                void* out, hipStream_t s);
+hipError_t launch_swiglu_restore_i8(const int8_t* q, const float* scale, int rows, int I, int group,
+                                    bool bf16, const int32_t* nrows, void* gu, void* h, hipStream_t s);
+
+// gemm_i8.hip (int8 products grouped by expert)
+uint64_t gemm_i8_threads(int R_cap, int E_l, int N);
+hipError_t launch_gemm_i8(const int8_t* x, const float* xs, const int32_t* src, int x_rows,
+                          const int32_t* offsets, int E_l, int R_cap, int K, int N, const int8_t* w,
+                          const float* ws, bf16_t* y, hipStream_t s);
+size_t ffn_fwd_i8_ws_bytes(int R_cap, int I);
+hipError_t launch_ffn_fwd_i8(const int8_t* x, const float* xs, const int32_t* src, int x_rows,
+                             const int32_t* offsets, int E_l, int R_cap, int H, int I, const int8_t* wg,
+                             const float* wgs, const int8_t* wu, const float* wus, const int8_t* wd,
+                             const float* wds, bf16_t* h, bf16_t* y, void* ws, hipStream_t s);
+
 // gemm.hip (bf16 MFMA grouped GEMMs)
 int gemm_tiles(int M, int N);  // output tiles of one M x N product
 // Whether the router weight gradient's split products add their hi and lo
