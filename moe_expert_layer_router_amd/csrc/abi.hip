@@ -1400,7 +1400,7 @@ int check_rows_i8(int rows, int cols, int group, int dtype, const char* fn) {
     return fail(MOE_EINVAL, "%s: cols=%d must be a positive multiple of 16", fn, cols);
   if (group <= 0 || group % 16 != 0 || cols % group != 0)
     return fail(MOE_EINVAL, "%s: group=%d must be a multiple of 16 that divides cols=%d", fn, group, cols);
-  if (int rc = check_launch(rows_i8_threads(rows, cols), fn)) return rc;
+  if (int rc = check_launch(rows_i8_threads(rows, cols, dtype == MOE_BF16 ? 8 : 4), fn)) return rc;
   return check_launch(wave_per_row(rows), fn);
 }
 }  // namespace
@@ -1468,8 +1468,9 @@ int check_gemm_i8(int E_l, int R_cap, int x_rows, bool gathered, int K, int N, c
   if (x_rows < 0 || (R_cap > 0 && x_rows == 0) || (!gathered && x_rows != R_cap))
     return fail(MOE_EINVAL, "%s: x_rows=%d (without src_row the R_cap=%d grouped rows)", fn, x_rows, R_cap);
   if (int rc = check_range((int64_t)x_rows * K, "x_q", fn)) return rc;
-  if (int rc = check_range((int64_t)N * K, "one expert's weight", fn)) return rc;
-  return check_launch(gemm_i8_threads(R_cap, E_l, N), fn);
+  if ((((int64_t)R_cap + 127) / 128 + E_l) * (((int64_t)N + 127) / 128) > kMaxRows)
+    return fail(MOE_EUNSUPPORTED, "%s: R_cap=%d rows of %s=%d are too many tiles", fn, R_cap, n_name, N);
+  return check_range((int64_t)N * K, "one expert's weight", fn);
 }
 }  // namespace
 

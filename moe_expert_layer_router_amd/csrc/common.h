@@ -256,8 +256,9 @@ hipError_t launch_combine_norm_bwd(const void* dy, const void* y_perm, const flo
                                    void* dy_perm, float* d_topk_w, void* dgate, float* dweight,
                                    bool accumulate, void* ws, hipStream_t s);
 
-// rows_i8.hip (rows as 8-bit integers); threads of a launch over rows of cols
-uint64_t rows_i8_threads(int rows, int cols);
+// rows_i8.hip (rows as 8-bit integers); threads of a launch with one for every
+// `per` columns
+uint64_t rows_i8_threads(int rows, int cols, int per);
 hipError_t launch_quantize_i8(const void* src, int rows, int cols, int group, bool bf16,
                               const int32_t* nrows, int8_t* q, float* scale, hipStream_t s);
 hipError_t launch_dequantize_i8(const int8_t* q, const float* scale, const int32_t* src_row, int rows,
@@ -267,7 +268,6 @@ hipError_t launch_swiglu_restore_i8(const int8_t* q, const float* scale, int row
                                     bool bf16, const int32_t* nrows, void* gu, void* h, hipStream_t s);
 
 // gemm_i8.hip (int8 products grouped by expert)
-uint64_t gemm_i8_threads(int R_cap, int E_l, int N);
 hipError_t launch_gemm_i8(const int8_t* x, const float* xs, const int32_t* src, int x_rows,
                           const int32_t* offsets, int E_l, int R_cap, int K, int N, const int8_t* w,
                           const float* ws, bf16_t* y, hipStream_t s);

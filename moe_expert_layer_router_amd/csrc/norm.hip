@@ -287,7 +287,8 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_kernel(
 #pragma unroll
     for (int i = 0; i < R::N; ++i) acc[u][i] = 0.f;
   }
-  gather_rows<BF16, true, NC, NC >= 4 ? 2 : 4>(y_perm, H, nch, at.first - lane_id(), slot.n, slot.dc,
+  constexpr int kAtOnce = NC == 1 ? 8 : NC == 2 ? 4 : 2;  // slots whose rows are in flight
+  gather_rows<BF16, true, NC, kAtOnce>(y_perm, H, nch, at.first - lane_id(), slot.n, slot.dc,
                                                slot.wc, acc);
   float ss[1] = {0.f};
 #pragma unroll
@@ -316,30 +317,25 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_kernel(
 
 // Slots whose rows a lane holds at once; where they are all of a token's, they
 // stay in registers between c and its gradient.
-constexpr int held(int NC) { return NC == 1 ? 8 : 2; }
+constexpr int held(int W, int NC) { return NC > 1 ? 2 : W > 8 ? 4 : 8; }
 
 template <bool BF16, int W, int NC>
-__global__ __launch_bounds__(threads_of(W)) void combine_norm_bwd_kernel(
+__global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
     const void* __restrict__ dy, const void* __restrict__ y_perm, const float* __restrict__ topk_w,
     const int32_t* __restrict__ dest_row, const void* __restrict__ gate, int gate_kind,
     const float* __restrict__ weight, float eps, int T, int H, int k, void* __restrict__ dy_perm,
     float* __restrict__ d_topk_w, void* __restrict__ dgate, float* __restrict__ part) {
   using R = Row<BF16>;
-  constexpr int kHeld = held(NC);
+  constexpr int kHeld = held(W, NC);
   __shared__ float lds[2 * threads_of(W) / kWave], dots[kHeld * threads_of(W) / kWave];
   __shared__ __align__(16) float sums[partial_lds<BF16, W, NC>()];
   const Place<W, NC> at;
   const int nch = H / R::N;
-  float dw[NC][R::N], wt[NC][R::N];
+  float dw[NC][R::N];
 #pragma unroll
-  for (int u = 0; u < NC; ++u) {
-    const int c = at.first + u * kWave;
+  for (int u = 0; u < NC; ++u)
 #pragma unroll
-    for (int i = 0; i < R::N; ++i) {
-      dw[u][i] = 0.f;
-      wt[u][i] = c < nch ? weight[c * R::N + i] : 0.f;
-    }
-  }
+    for (int i = 0; i < R::N; ++i) dw[u][i] = 0.f;
   for (int t0 = blockIdx.x * at.kTeams; t0 < T; t0 += gridDim.x * at.kTeams) {
     const int t = t0 + at.team;
     const Slots slot(dest_row, topk_w, t, T, k);
@@ -392,6 +388,8 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_bwd_kernel(
     float s2[2] = {0.f, 0.f};
 #pragma unroll
     for (int u = 0; u < NC; ++u) {
+      const int c = min(at.first + u * kWave, nch - 1);  // (past the row dy is 0)
+      const float* wt = weight + c * R::N;
       float d[R::N], g[R::N];
       R::to_f32(dyr[u], d);
       R::to_f32(gt[u], g);
@@ -399,7 +397,7 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_bwd_kernel(
       for (int i = 0; i < R::N; ++i) {
         const float ge = gate_kind == kGateFull ? g[i] : 1.f;
         s2[0] = fmaf(c_[u][i], c_[u][i], s2[0]);
-        s2[1] = fmaf(d[i] * ge * wt[u][i], c_[u][i], s2[1]);
+        s2[1] = fmaf(d[i] * ge * wt[i], c_[u][i], s2[1]);
       }
     }
     team_sum<W>(s2, lds);
@@ -407,10 +405,10 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_bwd_kernel(
     const float m = g1 * s2[1] * s / (float)H;  // mean(g xh)
     if (t < T && gate_kind == kGateToken && threadIdx.x % (W * kWave) == 0)
       ((float*)dgate)[t] = s2[1] * s;
-    float dc[NC][R::N];
 #pragma unroll
     for (int u = 0; u < NC; ++u) {
       const int c = at.first + u * kWave;
+      const float* wt = weight + min(c, nch - 1) * R::N;
       float d[R::N], g[R::N], o[R::N];
       R::to_f32(dyr[u], d);
       R::to_f32(gt[u], g);
@@ -419,8 +417,8 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_bwd_kernel(
         const float ge = gate_kind == kGateFull ? g[i] : g1;
         const float xh = c_[u][i] * s;
         dw[u][i] = fmaf(d[i] * ge, xh, dw[u][i]);
-        o[i] = d[i] * (xh * wt[u][i]);
-        dc[u][i] = s * fmaf(-xh, m, d[i] * ge * wt[u][i]);
+        o[i] = d[i] * (xh * wt[i]);
+        c_[u][i] = s * fmaf(-xh, m, d[i] * ge * wt[i]);  // from here on the gradient of c
       }
       if (gate_kind == kGateFull && t < T && c < nch)
         R::st_s(dgate, (size_t)t * H + (size_t)c * R::N, R::from_f32(o));
@@ -440,8 +438,8 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_bwd_kernel(
           R::to_f32(raw[q][u], v);
 #pragma unroll
           for (int i = 0; i < R::N; ++i) {
-            dot[q] = fmaf(dc[u][i], v[i], dot[q]);
-            o[i] = w * dc[u][i];
+            dot[q] = fmaf(c_[u][i], v[i], dot[q]);
+            o[i] = w * c_[u][i];
           }
           if (j0 + q < slot.n && c < nch) R::st_s(dy_perm, (size_t)d * H + (size_t)c * R::N, R::from_f32(o));
         }
@@ -458,6 +456,10 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_bwd_kernel(
   }
   write_partial<BF16, W, NC>(at, nch, H, dw, part, sums);
 }
+
+// Up to this many tokens a token's slots are loaded at once by a team with one
+// chunk a lane: fewer round trips, which is what few tokens wait for.
+constexpr int kFewTokens = 4 * kCUs;
 
 // Partial rows of the weight's gradient: workgroups of the backward.
 constexpr int kNormParts = 1024;
@@ -529,7 +531,11 @@ hipError_t launch_combine_norm(const void* y_perm, const float* topk_w, const in
     combine_norm_kernel<B, W, NC><<<(T + teams - 1) / teams, threads_of(W), 0, s>>>(                  \
         y_perm, topk_w, dest_row, residual, residual_scale, gate, gate_kind, weight, eps, T, H, k, y); \
   }
-  if (bf16) { MOE_NORM_SHAPES(true, MOE_LAUNCH) } else { MOE_NORM_SHAPES(false, MOE_LAUNCH) }
+  if (T <= kFewTokens) {
+    if (bf16) { MOE_NORM_SHAPES1(true, MOE_LAUNCH) } else { MOE_NORM_SHAPES1(false, MOE_LAUNCH) }
+  } else {
+    if (bf16) { MOE_NORM_SHAPES(true, MOE_LAUNCH) } else { MOE_NORM_SHAPES(false, MOE_LAUNCH) }
+  }
 #undef MOE_LAUNCH
   return hipGetLastError();
 }

@@ -9,8 +9,8 @@
 // group with an infinity or a NaN has that as its scale, so that it comes back
 // as NaN rather than as a number.
 //
-// All three kernels move their operands once; a lane holds 16 columns, whose
-// codes are one 16-byte store.
+// All kernels move their operands once; a lane quantizes 16 columns, whose codes
+// are one 16-byte store, and restores as many as fill one.
 #include "rows.h"
 
 namespace moe {
@@ -25,13 +25,6 @@ __device__ __forceinline__ void load16(const void* base, size_t elem, float (&v)
   using R = Row<BF16>;
 #pragma unroll
   for (int i = 0; i < kCols / R::N; ++i) R::to_f32(R::ld_s(base, elem + i * R::N), v + i * R::N);
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store16(void* base, size_t elem, const float (&v)[kCols]) {
-  using R = Row<BF16>;
-#pragma unroll
-  for (int i = 0; i < kCols / R::N; ++i) R::st_s(base, elem + i * R::N, R::from_f32(v + i * R::N));
 }
 
 // The largest magnitude, as bits: the order of the magnitudes of floats is that
@@ -71,11 +64,6 @@ __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
 
 __device__ __forceinline__ u32x4_t codes16(const float (&v)[kCols], float inv) {
   return u32x4_t{codes4(v, inv), codes4(v + 4, inv), codes4(v + 8, inv), codes4(v + 12, inv)};
-}
-
-__device__ __forceinline__ void values16(u32x4_t q, float scale, float (&v)[kCols]) {
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) v[i] = (float)((int)(q[i / 4] << (24 - 8 * (i % 4))) >> 24) * scale;
 }
 
 // Groups of G columns, 32 <= G <= 512 a power of two: G / 16 neighbouring lanes.
@@ -147,6 +135,23 @@ __global__ __launch_bounds__(256) void quantize_rows_i8_kernel(const void* __res
   }
 }
 
+// The codes of the columns whose values fill 16 bytes, so that a wave's stores
+// are one run: 8 of bf16, 4 of fp32.  (With 16 columns a lane each store leaves
+// every second 16 bytes to the next: 324 us for the gate and up of 131072 rows.)
+template <bool BF16>
+__device__ __forceinline__ void values(const int8_t* q, float scale, float (&v)[Row<BF16>::N]) {
+  uint32_t w[Row<BF16>::N / 4];
+  if constexpr (BF16) {
+    const uint2 t = *reinterpret_cast<const uint2*>(q);
+    w[0] = t.x;
+    w[1] = t.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(q);
+  }
+#pragma unroll
+  for (int i = 0; i < Row<BF16>::N; ++i) v[i] = (float)((int)(w[i / 4] << (24 - 8 * (i % 4))) >> 24) * scale;
+}
+
 // out[r] = values of code row src_row[r] (or r); 0 where src_row[r] names none.
 template <bool BF16>
 __global__ __launch_bounds__(256) void dequantize_i8_kernel(const int8_t* __restrict__ q,
@@ -155,18 +160,17 @@ __global__ __launch_bounds__(256) void dequantize_i8_kernel(const int8_t* __rest
                                                             int src_rows, int cols, int group,
                                                             const int32_t* __restrict__ nrows,
                                                             void* __restrict__ out) {
-  const uint32_t per_row = (uint32_t)cols / kCols;
+  using R = Row<BF16>;
+  const uint32_t per_row = (uint32_t)cols / R::N;
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
   const uint32_t row = i / per_row, c = i % per_row;
   if (row >= (uint32_t)rows || (nrows != nullptr && (int)row >= *nrows)) return;
   const int from = src_row != nullptr ? src_row[row] : (int)row;
-  float v[kCols] = {};
-  if (from >= 0 && from < src_rows) {
-    const u32x4_t w = reinterpret_cast<const u32x4_t*>(q)[(size_t)from * per_row + c];
-    const float s = scale[(size_t)from * (uint32_t)(cols / group) + c / (uint32_t)(group / kCols)];
-    values16(w, s, v);
-  }
-  store16<BF16>(out, (size_t)i * kCols, v);
+  float v[R::N] = {};
+  if (from >= 0 && from < src_rows)
+    values<BF16>(q + (size_t)from * cols + c * R::N,
+                 scale[(size_t)from * (uint32_t)(cols / group) + c / (uint32_t)(group / R::N)], v);
+  R::st_s(out, (size_t)i * R::N, R::from_f32(v));
 }
 
 // g and u from the codes of [g | u], and h = SiLU(g) u of the values as stored:
@@ -179,43 +183,41 @@ __global__ __launch_bounds__(256) void swiglu_restore_i8_kernel(const int8_t* __
                                                                 void* __restrict__ gu,
                                                                 void* __restrict__ h) {
   using R = Row<BF16>;
-  const uint32_t half = (uint32_t)I / kCols, per_group = (uint32_t)(group / kCols);
+  const uint32_t half = (uint32_t)I / R::N, per_group = (uint32_t)(group / R::N);
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
   const uint32_t row = i / half, c = i % half;
   if (row >= (uint32_t)rows || (nrows != nullptr && (int)row >= *nrows)) return;
-  const u32x4_t* w = reinterpret_cast<const u32x4_t*>(q) + (size_t)row * 2 * half;
-  const u32x4_t wg = __builtin_nontemporal_load(w + c), wu = __builtin_nontemporal_load(w + half + c);
+  const size_t e = (size_t)row * 2 * I + (size_t)c * R::N;
   const float* sr = scale + (size_t)row * (uint32_t)(2 * I / group);
-  float g[kCols], u[kCols], o[kCols];
-  values16(wg, sr[c / per_group], g);
-  values16(wu, sr[(half + c) / per_group], u);
-  const size_t e = (size_t)row * 2 * I + (size_t)c * kCols;
+  float g[R::N], u[R::N], o[R::N];
+  values<BF16>(q + e, sr[c / per_group], g);
+  values<BF16>(q + e + I, sr[(half + c) / per_group], u);
+  const u32x4_t pg = R::from_f32(g), pu = R::from_f32(u);
+  R::st_s(gu, e, pg);
+  R::st_s(gu, e + I, pu);
+  R::to_f32(pg, g);
+  R::to_f32(pu, u);
 #pragma unroll
-  for (int n = 0; n < kCols; n += R::N) {
-    const u32x4_t pg = R::from_f32(g + n), pu = R::from_f32(u + n);
-    R::st_s(gu, e + n, pg);
-    R::st_s(gu, e + I + n, pu);
-    R::to_f32(pg, g + n);
-    R::to_f32(pu, u + n);
-  }
-#pragma unroll
-  for (int n = 0; n < kCols; ++n) o[n] = g[n] * fast_rcp(1.f + __expf(-g[n])) * u[n];
-  store16<BF16>(h, (size_t)i * kCols, o);
+  for (int n = 0; n < R::N; ++n) o[n] = g[n] * fast_rcp(1.f + __expf(-g[n])) * u[n];
+  R::st_s(h, (size_t)i * R::N, R::from_f32(o));
 }
 
-unsigned blocks_of(int rows, int cols) {
-  return (unsigned)(((uint64_t)rows * (uint64_t)(cols / kCols) + 255) / 256);
+// Workgroups of a launch with a thread for every `per` columns.
+unsigned blocks_of(int rows, int cols, int per) {
+  return (unsigned)(((uint64_t)rows * (uint64_t)(cols / per) + 255) / 256);
 }
 
 }  // namespace
 
-uint64_t rows_i8_threads(int rows, int cols) { return ((uint64_t)rows * (uint64_t)(cols / kCols) + 255) / 256 * 256; }
+uint64_t rows_i8_threads(int rows, int cols, int per) {
+  return ((uint64_t)rows * (uint64_t)(cols / per) + 255) / 256 * 256;
+}
 
 hipError_t launch_quantize_i8(const void* src, int rows, int cols, int group, bool bf16,
                               const int32_t* nrows, int8_t* q, float* scale, hipStream_t s) {
   ProfScope ps(MOE_KERNEL_QUANTIZE_I8, s);
   if (group < cols) {
-    const unsigned blocks = blocks_of(rows, cols);
+    const unsigned blocks = blocks_of(rows, cols, kCols);
     if (bf16)
       quantize_groups_i8_kernel<true><<<blocks, 256, 0, s>>>(src, rows, cols, group / kCols, nrows, q, scale);
     else
@@ -235,7 +237,7 @@ hipError_t launch_quantize_i8(const void* src, int rows, int cols, int group, bo
 hipError_t launch_dequantize_i8(const int8_t* q, const float* scale, const int32_t* src_row, int rows,
                                 int src_rows, int cols, int group, bool bf16, const int32_t* nrows,
                                 void* out, hipStream_t s) {
-  const unsigned blocks = blocks_of(rows, cols);
+  const unsigned blocks = blocks_of(rows, cols, bf16 ? 8 : 4);
   if (bf16)
     dequantize_i8_kernel<true><<<blocks, 256, 0, s>>>(q, scale, src_row, rows, src_rows, cols, group, nrows, out);
   else
@@ -246,7 +248,7 @@ hipError_t launch_dequantize_i8(const int8_t* q, const float* scale, const int32
 hipError_t launch_swiglu_restore_i8(const int8_t* q, const float* scale, int rows, int I, int group, bool bf16,
                                     const int32_t* nrows, void* gu, void* h, hipStream_t s) {
   ProfScope ps(MOE_KERNEL_RESTORE_I8, s);
-  const unsigned blocks = blocks_of(rows, I);
+  const unsigned blocks = blocks_of(rows, I, bf16 ? 8 : 4);
   if (bf16)
     swiglu_restore_i8_kernel<true><<<blocks, 256, 0, s>>>(q, scale, rows, I, group, nrows, gu, h);
   else
