@@ -708,7 +708,7 @@ int moe_swiglu_restore_i8(const int8_t* q, const float* scale, int rows, int I, 
  *   (x_rows = R_cap; entries below offsets[E_l] are clamped into [0,x_rows)),
  *   w_q [E_l,N,K] int8, w_scale [E_l,N] fp32, y [R_cap,N] bf16 (rows >= R not
  *   written)
- * K and N multiples of 16, K <= 65536, x_rows * K and N * K below 2^31 (else
+ * K and N multiples of 16, K <= 65536, N <= 2^20, x_rows * K and N * K below 2^31 (else
  * MOE_EUNSUPPORTED); pointers of row data and scales 16-byte aligned. */
 int moe_grouped_gemm_i8(const int8_t* x_q, const float* x_scale, const int32_t* src_row,
                         const int32_t* offsets, int E_l, int R_cap, int x_rows, int K, int N,

@@ -1457,6 +1457,8 @@ int moe_swiglu_restore_i8(const int8_t* q, const float* scale, int rows, int I, 
 namespace {
 // The sums of products of codes (-128 included) stay below 2^31 up to this K.
 constexpr int kGemmI8MaxK = 65536;
+// A tile's 256 rows of results are stored through a descriptor of 32-bit range.
+constexpr int kGemmI8MaxN = 1 << 20;
 
 int check_gemm_i8(int E_l, int R_cap, int x_rows, bool gathered, int K, int N, const char* k_name,
                   const char* n_name, const char* fn) {
@@ -1465,6 +1467,7 @@ int check_gemm_i8(int E_l, int R_cap, int x_rows, bool gathered, int K, int N, c
   if (K <= 0 || N <= 0 || K % 16 != 0 || N % 16 != 0)
     return fail(MOE_EINVAL, "%s: %s=%d and %s=%d must be positive multiples of 16", fn, k_name, K, n_name, N);
   if (K > kGemmI8MaxK) return fail(MOE_EUNSUPPORTED, "%s: %s=%d above %d", fn, k_name, K, kGemmI8MaxK);
+  if (N > kGemmI8MaxN) return fail(MOE_EUNSUPPORTED, "%s: %s=%d above %d", fn, n_name, N, kGemmI8MaxN);
   if (x_rows < 0 || (R_cap > 0 && x_rows == 0) || (!gathered && x_rows != R_cap))
     return fail(MOE_EINVAL, "%s: x_rows=%d (without src_row the R_cap=%d grouped rows)", fn, x_rows, R_cap);
   if (int rc = check_range((int64_t)x_rows * K, "x_q", fn)) return rc;

@@ -5,12 +5,11 @@
 // int32, so every variant and every split of K gives the same bits; the two
 // scales are applied in fp32 and the result is rounded once.
 //
-// Two kernels share the experts out by their number of rows, which only the
-// device knows:
-//   few rows (skinny_expert): bound by the read of the weights.  A workgroup
-//     owns 32 columns of one expert; its four waves split K and take the weights
-//     straight from memory into MFMA operands, each byte once for up to 64 rows,
-//     and add their sums through LDS.
+// Two kernels, chosen by the rows for an expert on average:
+//   few rows (skinny_i8_kernel): bound by the read of the weights.  A workgroup
+//     owns 32 columns of one expert (64 where K is short); its waves split K and
+//     take the weights straight from memory into MFMA operands, each byte once for
+//     up to 64 rows, and add their sums through LDS.
 //   many rows (tile_i8_kernel): bound by the matrix cores and what feeds them.
 //     Tiles of 256 rows x 256 weight rows in a workgroup of eight waves that stays
 //     on its CU and takes tile after tile; operands through two LDS stages of 128
@@ -22,7 +21,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.h"
+#include "rows_i8.h"
 
 namespace moe {
 
@@ -43,7 +42,8 @@ struct ProductI8 {
   int E_l, K, N;
   const int8_t *w0, *w1;
   const float *s0, *s1;
-  bf16_t* out;  // [rows][N]
+  bf16_t* out;      // [rows][N]
+  const bf16_t* h;  // rows before their quantization (skinny_quantize_i8_kernel)
 };
 
 __device__ __forceinline__ int source_row(const ProductI8& p, int r) {
@@ -55,7 +55,33 @@ __device__ __forceinline__ int source_row(const ProductI8& p, int r) {
 // few rows
 // ---------------------------------------------------------------------------
 
-constexpr int kFew = 64;  // rows of one pass over an expert's weights
+constexpr int kFew = 64;      // rows of one pass over an expert's weights
+constexpr int kFewWaves = 4;  // of a workgroup
+
+// Codes of up to 16 rows of p.h from r0 on, as moe_quantize_i8 makes them, a wave a
+// row.  Ends with a barrier.
+__device__ __forceinline__ void quantize_rows(const ProductI8& p, int r0, int hi, int8_t* codes, float* scales) {
+  using namespace rows_i8;
+  const int lane = lane_id(), per_row = p.K / kCols;
+  for (int r = threadIdx.x >> 6; r0 + r < hi; r += kFewWaves) {
+    const size_t base = (size_t)(r0 + r) * p.K;
+    float v[kCols];
+    uint32_t top = 0;
+    for (int c = lane; c < per_row; c += kWave) {
+      load16<true>(p.h, base + (size_t)c * kCols, v);
+      top = top_bits(v, top);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, kWave));
+    const Scale s(top);
+    if (lane == 0) scales[r] = s.scale;
+    for (int c = lane; c < per_row; c += kWave) {
+      if (per_row > kWave) load16<true>(p.h, base + (size_t)c * kCols, v);
+      *reinterpret_cast<u32x4_t*>(codes + r * p.K + c * kCols) = codes16(v, s.inv);
+    }
+  }
+  __syncthreads();
+}
 
 // The i-th expert that has rows; false if there are fewer.
 __device__ __forceinline__ bool nth_expert(const int32_t* __restrict__ offsets, int E_l, int i, int& e,
@@ -86,38 +112,61 @@ __device__ __forceinline__ bool nth_expert(const int32_t* __restrict__ offsets, 
   return false;
 }
 
-// NB blocks of 16 rows from row r0 on.  Columns: GU: 16 of gate and the same of
-// up; else 32, a lane's 4 + 4 in a run of 8.
-template <bool GU, int NB, int WAVES>
-__device__ __forceinline__ void skinny_rows(const ProductI8& p, int e, int n0, int r0, int hi,
-                                            i32x4_t (*red)[2 * 4][kWave]) {
-  constexpr int U = NB == 1 ? 8 : 4;  // K steps of 64 in flight
+// Columns of a wave: 16 of gate and the same of up, or 32, a lane's 4 + 4 in a run of 8.
+template <bool GU>
+constexpr int few_cols() { return GU ? 16 : 32; }
+
+// NB blocks of 16 rows from row r0 on; every SPLIT waves share K for one wave's
+// columns.  QUANT: the rows are bf16 (p.h), and their codes are made here, in LDS,
+// while the weights are on their way.
+template <bool GU, int NB, int SPLIT, bool QUANT = false>
+__device__ __forceinline__ void skinny_rows(const ProductI8& p, int e, int n_first, int r0, int hi,
+                                            i32x4_t (*red)[2 * 4][kWave], int8_t* codes = nullptr,
+                                            float* scales = nullptr) {
+  static_assert(!QUANT || NB == 1, "codes of one block of rows");
+  constexpr int kCols = few_cols<GU>();
+  constexpr int U = 8 / NB;  // K steps of 64 in flight
   const int lane = lane_id(), wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
-  const int steps = (p.K + 63) / 64;
+  const int steps = (p.K + 63) / 64, n0 = n_first + wave / SPLIT * kCols;
+  int xi[NB];  // rows of x, needed after the weights' loads have been issued
+#pragma unroll
+  for (int m = 0; m < NB; ++m) {
+    const int r = min(r0 + m * 16 + l16, hi - 1);
+    xi[m] = p.src != nullptr ? p.src[r] : r;
+  }
   const int8_t* wr[2];
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int n = GU ? n0 + l16 : n0 + (l16 >> 2) * 8 + b * 4 + (l16 & 3);
     wr[b] = (GU && b == 1 ? p.w1 : p.w0) + ((size_t)e * p.N + min(n, p.N - 1)) * p.K + g * 16;
   }
-  const int8_t* xr[NB];
-#pragma unroll
-  for (int m = 0; m < NB; ++m)
-    xr[m] = p.x + (size_t)source_row(p, min(r0 + m * 16 + l16, hi - 1)) * p.K + g * 16;
   i32x4_t acc[2][NB] = {};
-  for (int s0 = wave; s0 < steps; s0 += WAVES * U) {
+  bool first = true;
+  for (int s0 = wave % SPLIT; s0 < steps || (QUANT && first); s0 += SPLIT * U) {
     i32x4_t a[U][2], b[U][NB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = (s0 + WAVES * u) * 64;
+      const int k = (s0 + SPLIT * u) * 64;
       const bool in = k + g * 16 < p.K;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        a[u][i] = in ? __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(wr[i] + k)) : i32x4_t{};
+        a[u][i] = in ? *reinterpret_cast<const i32x4_t*>(wr[i] + k) : i32x4_t{};
     }
+    const int8_t* xr[NB];
+    if constexpr (QUANT) {
+      if (first) quantize_rows(p, r0, hi, codes, scales);
+      xr[0] = codes + min(l16, hi - 1 - r0) * p.K + g * 16;
+    } else {
+#pragma unroll
+      for (int m = 0; m < NB; ++m) {
+        asm volatile("" : "+v"(xi[m]));  // not before the weights' loads
+        xr[m] = p.x + (size_t)min(max(xi[m], 0), p.x_rows - 1) * p.K + g * 16;
+      }
+    }
+    first = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = (s0 + WAVES * u) * 64;
+      const int k = (s0 + SPLIT * u) * 64;
       const bool in = k + g * 16 < p.K;
 #pragma unroll
       for (int m = 0; m < NB; ++m)
@@ -136,66 +185,65 @@ __device__ __forceinline__ void skinny_rows(const ProductI8& p, int e, int n0, i
 #pragma unroll
     for (int m = 0; m < NB; ++m) red[wave][i * NB + m][lane] = acc[i][m];
   __syncthreads();
-  if (wave < NB) {
+  for (int q = wave; q < NB * (kFewWaves / SPLIT); q += kFewWaves) {  // (block of rows, wave's columns)
+    const int m = q % NB, cg = q / NB;
     i32x4_t sum[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      sum[i] = red[0][i * NB + wave][lane];
+      sum[i] = red[cg * SPLIT][i * NB + m][lane];
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) sum[i] += red[w][i * NB + wave][lane];
+      for (int w = 1; w < SPLIT; ++w) sum[i] += red[cg * SPLIT + w][i * NB + m][lane];
     }
-    const int r = r0 + wave * 16 + l16;
-    if (r < hi) {
-      const float xs = p.xs[source_row(p, r)];
-      if constexpr (GU) {
-        const int n = n0 + g * 4;
-        if (n < p.N) {
-          const f32x4_t sg = *reinterpret_cast<const f32x4_t*>(p.s0 + (size_t)e * p.N + n);
-          const f32x4_t su = *reinterpret_cast<const f32x4_t*>(p.s1 + (size_t)e * p.N + n);
-          float o[4];
+    const int r = r0 + m * 16 + l16, n = n_first + cg * kCols + g * (GU ? 4 : 8);
+    if (r >= hi || n >= p.N) continue;
+    const float xs = QUANT ? scales[l16] : p.xs[source_row(p, r)];
+    const f32x4_t* ws = reinterpret_cast<const f32x4_t*>(p.s0 + (size_t)e * p.N + n);
+    const f32x4_t wa = ws[0], wb = GU ? *reinterpret_cast<const f32x4_t*>(p.s1 + (size_t)e * p.N + n) : ws[1];
+    float o[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = swiglu((float)sum[0][i] * xs * sg[i], (float)sum[1][i] * xs * su[i]);
-          *reinterpret_cast<uint2*>(p.out + (size_t)r * p.N + n) =
-              make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
-        }
-      } else {
-        const int n = n0 + g * 8;
-        if (n < p.N) {
-          const f32x4_t* ws = reinterpret_cast<const f32x4_t*>(p.s0 + (size_t)e * p.N + n);
-          const f32x4_t wa = ws[0], wb = ws[1];
-          float o[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[i] = (float)sum[0][i] * xs * wa[i];
-            o[4 + i] = (float)sum[1][i] * xs * wb[i];
-          }
-          *reinterpret_cast<uint4*>(p.out + (size_t)r * p.N + n) = pack8(o);
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float va = (float)sum[0][i] * xs * wa[i], vb = (float)sum[1][i] * xs * wb[i];
+      o[i] = GU ? swiglu(va, vb) : va;
+      o[4 + i] = vb;
     }
+    bf16_t* to = p.out + (size_t)r * p.N + n;
+    if constexpr (GU) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+    else *reinterpret_cast<uint4*>(to) = pack8(o);
   }
 }
 
-// All rows [lo, hi) of expert e for the columns from n0 on.
-template <bool GU, int WAVES>
-__device__ __forceinline__ void skinny_expert(const ProductI8& p, int e, int n0, int lo, int hi,
-                                              i32x4_t (*red)[2 * 4][kWave]) {
-  for (int r0 = lo; r0 < hi; r0 += kFew) {
-    if (r0 > lo) __syncthreads();  // the last sums have been read
-    const int left = hi - r0;
-    if (left <= 16) skinny_rows<GU, 1, WAVES>(p, e, n0, r0, hi, red);
-    else if (left <= 32) skinny_rows<GU, 2, WAVES>(p, e, n0, r0, hi, red);
-    else skinny_rows<GU, 4, WAVES>(p, e, n0, r0, hi, red);
-  }
-}
-
-template <bool GU>
-__global__ __launch_bounds__(256) void skinny_i8_kernel(ProductI8 p) {
+// Two waves a SIMD at the least: with registers for four the loads in flight spill
+// (64 tokens of the whole layer: 88 us, 63 with these bounds, for 403 MB).
+template <bool GU, int SPLIT>
+__global__ __launch_bounds__(256, 2) void skinny_i8_kernel(ProductI8 p) {
   __shared__ i32x4_t red[4][2 * 4][kWave];
   int e, lo, hi;
   if (!nth_expert(p.offsets, p.E_l, (int)blockIdx.y, e, lo, hi)) return;
-  skinny_expert<GU, 4>(p, e, (int)blockIdx.x * (GU ? 16 : 32), lo, hi, red);
+  const int n0 = (int)blockIdx.x * (kFewWaves / SPLIT * few_cols<GU>());
+  for (int r0 = lo; r0 < hi; r0 += kFew) {
+    if (r0 > lo) __syncthreads();  // the last sums have been read
+    const int left = hi - r0;
+    if (left <= 16) skinny_rows<GU, 1, SPLIT>(p, e, n0, r0, hi, red);
+    else if (left <= 32) skinny_rows<GU, 2, SPLIT>(p, e, n0, r0, hi, red);
+    else skinny_rows<GU, 4, SPLIT>(p, e, n0, r0, hi, red);
+  }
+}
+
+// The product of bf16 rows, each workgroup quantizing those of its expert itself,
+// 16 at a time: for few rows one launch less, and the rows' reads lie under the
+// weights'.
+template <int SPLIT>
+__global__ __launch_bounds__(256, 2) void skinny_quantize_i8_kernel(ProductI8 p) {
+  extern __shared__ __align__(16) char lds[];  // codes of 16 rows
+  __shared__ i32x4_t red[4][2 * 4][kWave];
+  __shared__ float scales[16];
+  int e, lo, hi;
+  if (!nth_expert(p.offsets, p.E_l, (int)blockIdx.y, e, lo, hi)) return;
+  for (int r0 = lo; r0 < hi; r0 += 16) {
+    if (r0 > lo) __syncthreads();  // the last sums and codes have been read
+    skinny_rows<false, 1, SPLIT, true>(p, e, (int)blockIdx.x * (kFewWaves / SPLIT * few_cols<false>()), r0,
+                                       min(hi, r0 + 16), red, (int8_t*)lds, scales);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -206,7 +254,7 @@ constexpr int kTileM = 256;    // most rows of a tile
 constexpr int kTileW = 256;    // weight rows of a tile (128 of gate and 128 of up in the pair)
 constexpr int kTileWaves = 8;  // 2 along the rows, 4 along the weight rows
 constexpr int kStageK = 128;    // bytes of K a stage
-constexpr int kStages = 256 / kStageK;
+constexpr int kStages = 2;
 constexpr int kStageBytes = (kTileM + kTileW) * kStageK;
 constexpr int kRowChunks = kStageK / 16;            // 16-byte chunks of an LDS row
 constexpr int kDmaRows = kWave / kRowChunks;        // LDS rows that one DMA fills
@@ -215,8 +263,21 @@ constexpr int kOutBytes = 32 * 64;  // of a wave: 32 rows of 32 columns on their
 constexpr int kOutAt = kStages * kStageBytes;
 constexpr int kTileLds = kOutAt + kTileWaves * kOutBytes;
 
+// Streaming stores for a product's rows, in whole cache lines: 131072 rows of 768 by
+// 2048 columns 316 -> 260 us, inside the FFN 355 -> 351.  (h, in half lines and read
+// again at once, is stored plainly: 493 us, 503 streamed.)
+constexpr int kStreamed = 2;
+
 template <bool GU>
 constexpr int tile_cols() { return GU ? 128 : 256; }
+
+// Between the LDS accesses of a wave's lanes to each other's values: the hardware
+// keeps them in order, and the compiler, which looks at one lane, is kept from
+// changing it.
+__device__ __forceinline__ void lanes_meet() {
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
 
 __device__ __forceinline__ uint32_t lds_byte_addr(const void* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t*)p);
@@ -246,8 +307,7 @@ struct At {
 struct TileLds {
   int start[kMaxE + 1];  // row tiles before expert e
   int row0[kMaxE], row1[kMaxE];
-  int list[kMaxE];       // experts with few rows
-  int scan[4], few[4], tall[4];
+  int scan[4], tall[4];
   int row[kTileM];       // rows of x of the next tile
   float xs[kTileM], ws[kTileW];  // scales of the tile in work
 };
@@ -286,36 +346,48 @@ struct Feed {
     }
   }
 
-  // The first steps of a tile, into all stages.
-  __device__ __forceinline__ void start(uint32_t to, int wave) const {
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) issue(i, to + i * kStageBytes, wave);
+  // DMA i of K step s (the weights' first) into its ring stage; chunks past K (and
+  // whole steps past the last) are dropped and leave zeros.
+  __device__ __forceinline__ void issue(int i, int s, uint32_t to, int wave) const {
+    const int k = s * kStageK, j = i % kDmas;
+    if (i < kDmas) {
+      const bool in = k + chunk_w(j, wave) * 16 < K && wv[j] != kDmaKill;
+      dma16(wd[GU ? j / (kDmas / 2) : 0], in ? wv[j] + k : kDmaKill, to + j * (kTileWaves * 1024));
+    } else {
+      const bool in = k + chunk_x(j, wave) * 16 < K && xv[j] != kDmaKill;
+      dma16(xd, in ? xv[j] + k : kDmaKill, to + kTileW * kStageK + j * (kTileWaves * 1024));
+    }
   }
-
-  // K step s into its ring stage; chunks past K (and whole steps past the last)
-  // are dropped and leave zeros.
-  __device__ __forceinline__ void issue(int s, uint32_t to, int wave) const {
-    const int k = s * kStageK;
-#pragma unroll
-    for (int i = 0; i < kDmas; ++i) {
-      const bool in = k + chunk_w(i, wave) * 16 < K && wv[i] != kDmaKill;
-      dma16(wd[GU ? i / (kDmas / 2) : 0], in ? wv[i] + k : kDmaKill, to + i * (kTileWaves * 1024));
-    }
-#pragma unroll
-    for (int i = 0; i < kDmas; ++i) {
-      const bool in = k + chunk_x(i, wave) * 16 < K && xv[i] != kDmaKill;
-      dma16(xd, in ? xv[i] + k : kDmaKill, to + kTileW * kStageK + i * (kTileWaves * 1024));
-    }
+  // DMA i of the first two steps, into the first two stages.
+  __device__ __forceinline__ void start(int i, uint32_t to, int wave) const {
+    issue(i % (2 * kDmas), i / (2 * kDmas), to + i / (2 * kDmas) * kStageBytes, wave);
   }
 };
 
-__device__ __forceinline__ void store16(u32x4_t v, u32x4_t* to) {
-#ifdef NTS
-  __builtin_nontemporal_store(v, to);
-#else
-  *to = v;
-#endif
+// The results of a wave with NB blocks of 32 rows leave in blocks of 32 columns, two
+// stores each, and the DMAs of the next tile's first two steps are issued in the
+// first (up to four) of them: the memory counter of a wait for one of the steps has
+// to leave room for what was issued after it, a fixed number of operations.
+template <bool GU, int NB>
+struct Order {
+  static constexpr int kBlocks = NB * (GU ? 1 : 2);
+  static constexpr int kFront = kBlocks < 4 ? kBlocks : 4;
+  static constexpr int kPer = kFront == 0 ? 0 : 4 * kDmas / kFront;  // DMAs in each of the first blocks
+  // operations behind the first step's last DMA, and behind the second's
+  static constexpr int stores_from(int block) { return GU ? 2 * (kBlocks - block) : 4 * ((kBlocks - block + 1) / 2); }
+  static constexpr int kAfter0 = 2 * kDmas + (kFront == 0 ? 0 : stores_from((2 * kDmas - 1) / kPer));
+  static constexpr int kAfter1 = kFront == 0 ? 0 : stores_from(kFront - 1);
+};
+
+// A wait for the second step of a tile, with this many operations behind it.
+__device__ __forceinline__ void wait_second(int after) {
+  if (after == 12) wait_vm<12>();
+  else if (after == 4) wait_vm<4>();
+  else if (after == 2) wait_vm<2>();
+  else wait_vm<0>();
 }
+static_assert(Order<false, 4>::kAfter1 == 12 && Order<false, 2>::kAfter1 == 4 && Order<true, 4>::kAfter1 == 2 &&
+              Order<true, 2>::kAfter1 == 2 && Order<true, 0>::kAfter1 == 0, "the counts that wait_second knows");
 
 template <bool GU>
 struct Wave {
@@ -368,13 +440,14 @@ struct Wave {
     if constexpr (2 + NB > 2 * NB) __builtin_amdgcn_sched_group_barrier(0x100, 2 + NB - 2 * NB, 0);
   }
 
-  // One tile, whose first steps have landed in the stages (every wave has waited for
-  // its part of them).  The products of 64 weight rows with NB blocks of 32 rows,
-  // from row `first` of the tile on; `begin` fetches what the next tile and the
-  // results need; `next` starts the next tile's first steps; then the results.
+  // One tile, whose first step has landed in the first stage and whose second is on
+  // its way, `after` operations behind it.  The products of 64 weight rows with NB
+  // blocks of 32 rows, from row `first` of the tile on; `begin` fetches what the next
+  // tile and the results need; then the results, and the next tile's first steps
+  // between them.  Returns what is behind its second step.
   template <int NB, class Begin, class Next>
-  __device__ __forceinline__ void run(const At& t, const Feed<GU>& feed, int first, const Begin& begin,
-                                      const Next& next) const {
+  __device__ __forceinline__ int run(const At& t, const Feed<GU>& feed, int first, int after,
+                                     const Begin& begin, const Next& next) const {
     constexpr int N1 = NB == 0 ? 1 : NB;
     constexpr int kSub = kStageK / 32;  // operands of a stage
     const int a = l >> 3, h = (l >> 2) & 1, j = l & 3;
@@ -388,16 +461,23 @@ struct Wave {
     }
     i32x16_t acc[2][N1];
     const int steps = (p.K + kStageK - 1) / kStageK;
-    lds_barrier();  // everybody's part of the first steps
+    lds_barrier();  // everybody's part of the first step
     begin();
     Operands<N1> o[2];
     if constexpr (NB > 0) o[0].load(lds + aw[0], lds + ax[0]);
     const auto step = [&](auto first_step, int s) {
       constexpr bool kFirst = decltype(first_step)::value;
-      const char* at = lds + (s & (kStages - 1)) * kStageBytes;
-      const char* after = lds + ((s + 1) & (kStages - 1)) * kStageBytes;
+      const char* at = lds + (s & 1) * kStageBytes;
+      const char* behind = lds + ((s + 1) & 1) * kStageBytes;
 #pragma unroll
       for (int ks = 0; ks < kSub - 1; ++ks) {
+        // A step's DMAs are spread over the products: a wave whose DMAs wait for the
+        // memory pipeline issues no products.  These are the rest of step s + 1.
+        if (!kFirst && ks < 2) {
+#pragma unroll
+          for (int i = 3 + 3 * ks; i < 6 + 2 * ks; ++i)
+            feed.issue(i, s + 1, lds0 + ((s + 1) & 1) * kStageBytes, wave);
+        }
         if constexpr (NB > 0) {
           o[(ks + 1) & 1].load(at + aw[ks + 1], at + ax[ks + 1]);
           if constexpr (kFirst) {
@@ -410,11 +490,13 @@ struct Wave {
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (s >= kStages - 1) wait_vm<2 * kDmas*(kStages - 2)>();  // this wave's part of step s + 1
+      if (kFirst) wait_second(after);  // this wave's part of step s + 1
+      else wait_vm<0>();
       lds_barrier();  // everybody's, and everybody has read step s
-      feed.issue(s + kStages, lds0 + (s & (kStages - 1)) * kStageBytes, wave);  // (dropped past K)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) feed.issue(i, s + 2, lds0 + (s & 1) * kStageBytes, wave);  // (dropped past K)
       if constexpr (NB > 0) {
-        o[0].load(after + aw[0], after + ax[0]);  // (of no use after the last step)
+        o[0].load(behind + aw[0], behind + ax[0]);  // (of no use after the last step)
         multiply<N1, false>(o[(kSub - 1) & 1], acc);
         interleave<N1>();
       }
@@ -424,17 +506,28 @@ struct Wave {
     wait_vm<0>();  // the dropped steps
     next.publish();
     lds_barrier();  // nobody reads the ring any more, and what `begin` fetched is in the LDS
-    next();
-    if constexpr (NB > 0) store<NB>(t, acc, first);
-    else wait_vm<0>();  // the next tile's first steps
+    next.set();
+    store<NB>(t, acc, first, next);
+    wait_vm<Order<GU, NB>::kAfter0>();  // the next tile's first step
+    return Order<GU, NB>::kAfter1;
   }
 
   // The results of a wave go through its own part of the LDS, 32 rows of 32 columns
   // at a time, so that a store writes 64 bytes in a run.
-  template <int NB>
-  __device__ __forceinline__ void store(const At& t, const i32x16_t (&acc)[2][NB], int first) const {
+  template <int NB, class Next, int N1>
+  __device__ __forceinline__ void store(const At& t, const i32x16_t (&acc)[2][N1], int first,
+                                        const Next& next) const {
+    if constexpr (NB == 0) {
+#pragma unroll
+      for (int i = 0; i < 4 * kDmas; ++i) next.start(i);
+      return;
+    }
+    using O = Order<GU, NB>;
     const int lane = lane_id(), chunk = lane & 3;
     char* mine = lds + kOutAt + wave * kOutBytes;
+    const __amdgpu_buffer_rsrc_t to = __builtin_amdgcn_make_buffer_rsrc(
+        p.out + (size_t)t.r0 * p.N, 0, t.rows * p.N * 2, 0x00020000);
+    uint4 held[4];
     f32x4_t ws[2][4];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
@@ -442,40 +535,67 @@ struct Wave {
       for (int q = 0; q < 4; ++q)
         ws[b][q] = *reinterpret_cast<const f32x4_t*>(c.ws + (GU ? b * 128 + wn * 32 : wn * 64 + b * 32) + half * 16 + 4 * q);
 #pragma unroll
-    for (int m = 0; m < NB; ++m) {
+    for (int n = 0; n < O::kBlocks; ++n) {
+      const int m = GU ? n : n / 2, b = GU ? 0 : n % 2;
+      if (n < O::kFront) {
+#pragma unroll
+        for (int i = 0; i < O::kPer; ++i) next.start(n * O::kPer + i);
+      }
       const float xs = c.xs[first + m * 32 + l];
+      const int col = t.n0 + wn * (GU ? 32 : 64) + b * 32;
+      float o[16];
 #pragma unroll
-      for (int b = 0; b < (GU ? 1 : 2); ++b) {
-        const int col = t.n0 + wn * (GU ? 32 : 64) + b * 32;
-        float o[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float v = (float)acc[b][m][i] * xs * ws[b][i / 4][i % 4];
-          o[i] = GU ? swiglu(v, (float)acc[1][m][i] * xs * ws[1][i / 4][i % 4]) : v;
-        }
+      for (int i = 0; i < 16; ++i) {
+        const float v = (float)acc[b][m][i] * xs * ws[b][i / 4][i % 4];
+        o[i] = GU ? swiglu(v, (float)acc[1][m][i] * xs * ws[1][i / 4][i % 4]) : v;
+      }
+      if constexpr (GU) {
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           *reinterpret_cast<uint4*>(mine + (l * 4 + ((half * 2 + q) ^ swizzle_row<4>(l))) * 16) = pack8(o + 8 * q);
-        // The next tile's first steps, before the first store: a wait for them later
-        // would wait for the stores as well.
-        if (m == 0 && b == 0) wait_vm<0>();
+        lanes_meet();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int row = i * 16 + lane / 4;
+          const int row = i * 16 + lane / 4, at = first + m * 32 + row;
           const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + (row * 4 + (chunk ^ swizzle_row<4>(row))) * 16);
-          if (first + m * 32 + row < t.rows && col + chunk * 8 < p.N)
-            store16(v, reinterpret_cast<u32x4_t*>(p.out + (size_t)(t.r0 + first + m * 32 + row) * p.N + col + chunk * 8));
+          const bool in = at < t.rows && col + chunk * 8 < p.N;  // (the others are dropped by the descriptor's range)
+          __builtin_amdgcn_raw_buffer_store_b128(v, to, in ? (at * p.N + col + chunk * 8) * 2 : (int)kDmaKill, 0, 0);
+        }
+        lanes_meet();
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) held[b * 2 + q] = pack8(o + 8 * q);
+        if (b == 1) {  // 16 rows of 64 columns at a time
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if ((l >> 4) == g) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int ch = (q >> 1) * 4 + half * 2 + (q & 1);
+                *reinterpret_cast<uint4*>(mine + ((l & 15) * 8 + (ch ^ swizzle_row<8>(l & 15))) * 16) = held[q];
+              }
+            }
+            lanes_meet();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = i * 8 + lane / 8, at = first + m * 32 + g * 16 + row, ch = lane & 7;
+              const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + (row * 8 + (ch ^ swizzle_row<8>(row))) * 16);
+              const int c0 = t.n0 + wn * 64 + ch * 8;
+              const bool in = at < t.rows && c0 < p.N;
+              __builtin_amdgcn_raw_buffer_store_b128(v, to, in ? (at * p.N + c0) * 2 : (int)kDmaKill, 0, kStreamed);
+            }
+            lanes_meet();
+          }
         }
       }
     }
   }
 };
 
-// Experts with more than kFew rows in tiles, in the order (expert, column tile, row
-// tile); then the other experts, a few columns at a time.  Every workgroup counts
-// the tiles from the offsets and takes its share of them: an XCD a run of the
-// order, in rounds of one tile a workgroup, so that neighbouring tiles (of the same
-// weights, of the same rows) are in work at the same time on one L2.
+// Tiles in the order (expert, column tile, row tile).  Every workgroup counts them
+// from the offsets and takes its share: an XCD a run of the order, in rounds of one
+// tile a workgroup, so that neighbouring tiles (of the same weights, of the same
+// rows) are in work at the same time on one L2.
 template <bool GU>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p) {
   extern __shared__ __align__(16) char lds[];
@@ -485,21 +605,16 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
   int height = kTileM;
   {
     const bool in = tid < p.E_l;
-    const int lo = in ? p.offsets[tid] : 0, hi = in ? p.offsets[tid + 1] : 0, n = hi - lo;
-    const bool is_few = n > 0 && n <= kFew;
-    const uint64_t small = __ballot(is_few);
+    const int lo = in ? p.offsets[tid] : 0, hi = in ? p.offsets[tid + 1] : 0, n = max(hi - lo, 0);
     // row tiles of the full height: with fewer of them than two for a workgroup,
     // tiles of half the height keep more CUs at work
-    int full = n > kFew ? (n + kTileM - 1) / kTileM : 0;
+    int full = (n + kTileM - 1) / kTileM;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) full += __shfl_xor(full, o, kWave);
-    if (lane == 0 && wave < 4) {
-      c.tall[wave] = full;
-      c.few[wave] = __popcll(small);
-    }
+    if (lane == 0 && wave < 4) c.tall[wave] = full;
     __syncthreads();
     if ((c.tall[0] + c.tall[1] + c.tall[2] + c.tall[3]) * cols < 2 * (int)gridDim.x) height = kTileM / 2;
-    const int mine = n > kFew ? (n + height - 1) / height : 0;
+    const int mine = (n + height - 1) / height;
     int sum = mine;  // row tiles up to this thread's expert
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
@@ -509,12 +624,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
     if (lane == 63 && wave < 4) c.scan[wave] = sum;
     __syncthreads();
     if (tid < kMaxE) {
-      int at = __popcll(small & ((1ull << lane) - 1ull)), before = sum - mine;
-      for (int w = 0; w < wave; ++w) {
-        at += c.few[w];
-        before += c.scan[w];
-      }
-      if (is_few) c.list[at] = tid;
+      int before = sum - mine;
+      for (int w = 0; w < wave; ++w) before += c.scan[w];
       c.start[tid] = before;
       c.row0[tid] = lo;
       c.row1[tid] = hi;
@@ -554,8 +665,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
     if (tid < kTileM) c.row[tid] = row;
     __syncthreads();
     feed.set(p, t, c.row, w.wave);
-    feed.start(w.lds0, w.wave);
-    wait_vm<0>();
+#pragma unroll
+    for (int i = 0; i < 4 * kDmas; ++i) feed.start(i, w.lds0, w.wave);
+    wait_vm<2 * kDmas>();
+    int after = 0;  // operations behind the second step
     while (id < to) {
       const At now = t;
       const Feed<GU> f = feed;
@@ -577,7 +690,6 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
         Feed<GU>& feed;
         TileLds& c;
         const Wave<GU>& w;
-        const bool more;
         const int tid;
         const int& row;
         const float& scale;
@@ -589,39 +701,38 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
             c.ws[tid - kTileM] = scale;
           }
         }
-        __device__ void operator()() const {
-          if (!more) return;
-          feed.set(p, t, c.row, w.wave);
-          feed.start(w.lds0, w.wave);
-        }
-      } next = {p, t, feed, c, w, id < to, tid, row, scale};
+        // The last tile's "next" is itself again: its DMAs have to be there for the waits'
+        // counts, and what they fetch is not read.
+        __device__ void set() const { feed.set(p, t, c.row, w.wave); }
+        __device__ void start(int i) const { feed.start(i, w.lds0, w.wave); }
+      } next = {p, t, feed, c, w, tid, row, scale};
       const int first = w.wm * (height / 2);
       const int blocks = min((now.rows - first + 31) / 32, height / 64);  // of this wave that have rows
-      if (blocks > 2) w.template run<4>(now, f, first, begin, next);
-      else if (blocks > 0) w.template run<2>(now, f, first, begin, next);
-      else w.template run<0>(now, f, first, begin, next);
+      if (blocks > 2) after = w.template run<4>(now, f, first, after, begin, next);
+      else if (blocks > 0) after = w.template run<2>(now, f, first, after, begin, next);
+      else after = w.template run<0>(now, f, first, after, begin, next);
     }
-  }
-  const int per = (p.N + (GU ? 15 : 31)) / (GU ? 16 : 32);
-  const int items = (c.few[0] + c.few[1] + c.few[2] + c.few[3]) * per;
-  for (int i = (int)blockIdx.x; i < items; i += (int)gridDim.x) {
-    const int e = __builtin_amdgcn_readfirstlane(c.list[i / per]);
-    __syncthreads();  // the LDS of the last tile or item has been read
-    skinny_expert<GU, kTileWaves>(p, e, (i % per) * (GU ? 16 : 32), c.row0[e], c.row1[e],
-                                  reinterpret_cast<i32x4_t(*)[2 * 4][kWave]>(lds));
+    wait_vm<0>();  // the last "next tile", before the LDS is another workgroup's
   }
 }
 
-// Up to this many rows for an expert on average go without the tiles: the
-// workgroups then need less LDS and stream the weights with more waves a CU.
-constexpr int kSkinnyOnly = 32;
+// Up to this many rows for an expert on average (of the capacity: the host does not
+// know more) go without the tiles.
+constexpr int kSkinnyRows = 16;
+constexpr int kFusedRows = 8, kFusedCols = 1536;
+
+// Waves that share K: where it is short, two, and twice the columns, so that a wave
+// has enough loads in flight (768: 64 tokens of the whole layer 51 -> 39 us).
+int split_of(int K) { return K > 1024 ? 4 : 2; }
 
 template <bool GU>
 hipError_t launch_product(const ProductI8& p, int R_cap, int kernel_id, hipStream_t s) {
   ProfScope ps(kernel_id, s);
-  if ((long)R_cap <= (long)kSkinnyOnly * p.E_l) {
-    const int cols = (p.N + (GU ? 15 : 31)) / (GU ? 16 : 32);
-    skinny_i8_kernel<GU><<<dim3(cols, std::min(p.E_l, R_cap)), 256, 0, s>>>(p);
+  if ((long)R_cap <= (long)kSkinnyRows * p.E_l) {
+    const int split = split_of(p.K), cols = kFewWaves / split * few_cols<GU>();
+    const dim3 grid((p.N + cols - 1) / cols, std::min(p.E_l, R_cap));
+    if (split == 4) skinny_i8_kernel<GU, 4><<<grid, 256, 0, s>>>(p);
+    else skinny_i8_kernel<GU, 2><<<grid, 256, 0, s>>>(p);
   } else {
     tile_i8_kernel<GU><<<kCUs, 64 * kTileWaves, kTileLds, s>>>(p);
   }
@@ -633,7 +744,7 @@ hipError_t launch_product(const ProductI8& p, int R_cap, int kernel_id, hipStrea
 hipError_t launch_gemm_i8(const int8_t* x, const float* xs, const int32_t* src, int x_rows,
                           const int32_t* offsets, int E_l, int R_cap, int K, int N, const int8_t* w,
                           const float* ws, bf16_t* y, hipStream_t s) {
-  const ProductI8 p = {x, xs, src, x_rows, offsets, E_l, K, N, w, nullptr, ws, nullptr, y};
+  const ProductI8 p = {x, xs, src, x_rows, offsets, E_l, K, N, w, nullptr, ws, nullptr, y, nullptr};
   return launch_product<false>(p, R_cap, MOE_KERNEL_GEMM_I8, s);
 }
 
@@ -648,12 +759,21 @@ hipError_t launch_ffn_fwd_i8(const int8_t* x, const float* xs, const int32_t* sr
                              const float* wds, bf16_t* h, bf16_t* y, void* ws, hipStream_t s) {
   int8_t* hq = (int8_t*)ws;
   float* hs = (float*)((char*)ws + (((size_t)R_cap * I + 255) & ~(size_t)255));
-  const ProductI8 up = {x, xs, src, x_rows, offsets, E_l, H, I, wg, wu, wgs, wus, h};
+  const ProductI8 up = {x, xs, src, x_rows, offsets, E_l, H, I, wg, wu, wgs, wus, h, nullptr};
   hipError_t e = launch_product<true>(up, R_cap, MOE_KERNEL_FFN_GATEUP_I8, s);
   if (e != hipSuccess) return e;
+  const ProductI8 down = {hq, hs, nullptr, R_cap, offsets, E_l, I, H, wd, nullptr, wds, nullptr, y, h};
+  // Few rows for an expert on average, short enough for their codes in LDS.
+  if ((long)R_cap <= (long)kFusedRows * E_l && I <= kFusedCols) {
+    ProfScope ps(MOE_KERNEL_FFN_DOWN_I8, s);
+    const int split = split_of(I), cols = kFewWaves / split * few_cols<false>();
+    const dim3 grid((H + cols - 1) / cols, std::min(E_l, R_cap));
+    if (split == 4) skinny_quantize_i8_kernel<4><<<grid, 256, 16 * I, s>>>(down);
+    else skinny_quantize_i8_kernel<2><<<grid, 256, 16 * I, s>>>(down);
+    return hipGetLastError();
+  }
   e = launch_quantize_i8(h, R_cap, I, I, true, offsets + E_l, hq, hs, s);
   if (e != hipSuccess) return e;
-  const ProductI8 down = {hq, hs, nullptr, R_cap, offsets, E_l, I, H, wd, nullptr, wds, nullptr, y};
   return launch_product<false>(down, R_cap, MOE_KERNEL_FFN_DOWN_I8, s);
 }
 

@@ -92,11 +92,11 @@ def test_product_refusals():
     g = [A, A, A, A, 4, 16, 9, 64, 48, A, A, A, STREAM]
     each(L.moe_grouped_gemm_i8, g, [(0, N, EINVAL), (0, U, EINVAL), (1, N, EINVAL), (3, N, EINVAL), (4, 0, EINVAL),
                                     (4, 257, EINVAL), (5, -1, EINVAL), (6, 0, EINVAL), (2, N, EINVAL), (7, 24, EINVAL),
-                                    (7, 0, EINVAL), (7, 65552, EUNSUP), (8, 40, EINVAL), (9, U, EINVAL), (10, N, EINVAL),
+                                    (7, 0, EINVAL), (7, 65552, EUNSUP), (8, 40, EINVAL), (8, (1 << 20) + 16, EUNSUP), (9, U, EINVAL), (10, N, EINVAL),
                                     (10, U, EINVAL), (11, N, EINVAL), (11, U, EINVAL)])
     assert L.moe_grouped_gemm_i8(A, A, A, A, 4, 16, 1 << 20, 2048, 48, A, A, A, STREAM) == EUNSUP and "x_q" in _err()
     assert L.moe_grouped_gemm_i8(A, A, A, A, 4, 16, 9, 65536, 32768, A, A, A, STREAM) == EUNSUP and "weight" in _err()
-    assert L.moe_grouped_gemm_i8(A, A, A, A, 256, 0x7fff0000, 9, 16, 1 << 20, A, A, A, STREAM) == EUNSUP
+    assert L.moe_grouped_gemm_i8(A, A, A, A, 256, 0x7fff0000, 9, 16, 1 << 20, A, A, A, STREAM) == EUNSUP and "tiles" in _err()
     assert L.moe_grouped_gemm_i8(N, N, N, N, 4, 0, 0, 64, 48, N, N, N, STREAM) == OK
     f = [A, A, A, A, 4, 16, 9, 64, 48, A, A, A, A, A, A, A, A, A, 1 << 20, STREAM]
     each(L.moe_grouped_ffn_fwd_i8, f, [(i, N, EINVAL) for i in (0, 1, 3, 9, 10, 11, 12, 13, 14, 15, 16)]
