@@ -621,16 +621,17 @@ int moe_norm(const void* x, const void* delta, const float* weight, double eps, 
              int dtype, void* r, void* n, void* stream);
 
 /* Backward of moe_norm for the gradient dn of n and, where r has other readers
- * (the residual), dr of r (or NULL).  With s = 1 / sqrt(mean r^2 + eps), xh = s r:
- *   dx[t]   = dr[t] + s (dn weight - xh mean_h(dn weight xh))   [T,H] dtype
+ * (the residual), dr of r times dr_scale (or NULL).  With s = 1 / sqrt(mean r^2 + eps),
+ * xh = s r:
+ *   dx[t]   = dr_scale * dr[t] + s (dn weight - xh mean_h(dn weight xh))   [T,H] dtype
  *   dweight = sum_t dn[t] xh[t]                                 [H] fp32
  * dx is the gradient of x and of delta.  Nothing of the forward but r is needed.
  * dweight is overwritten or, with accumulate != 0, added to; its rows are summed
  * in an order fixed by T and H alone.  dx may be dn or dr.
  *   ws  moe_norm_ws_bytes(H) bytes.  T = 0 writes (or keeps) dweight only. */
 int64_t moe_norm_ws_bytes(int H);
-int moe_norm_bwd(const void* dn, const void* dr, const void* r, const float* weight, double eps,
-                 int T, int H, int dtype, void* dx, float* dweight, int accumulate, void* ws,
+int moe_norm_bwd(const void* dn, const void* dr, double dr_scale, const void* r,
+                 const float* weight, double eps, int T, int H, int dtype, void* dx, float* dweight, int accumulate, void* ws,
                  size_t ws_bytes, void* stream);
 
 /* The weighted combine with the RMS norm after the layer, a gate and the scaled

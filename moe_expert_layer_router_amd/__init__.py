@@ -98,7 +98,7 @@ def _load():
         "moe_adapter_rows": ([P, P, P, I32, I32, I32, I32, P, P], I32),
         "moe_norm": ([P, P, P, F64, I32, I32, I32, P, P, P], I32),
         "moe_norm_ws_bytes": ([I32], I64),
-        "moe_norm_bwd": ([P, P, P, P, F64, I32, I32, I32, P, P, I32, P, SZ, P], I32),
+        "moe_norm_bwd": ([P, P, F64, P, P, F64, I32, I32, I32, P, P, I32, P, SZ, P], I32),
         "moe_combine_norm": ([P, P, P, P, F64, P, I32, P, F64, I32, I32, I32, I32, P, P], I32),
         "moe_combine_norm_bwd": ([P] * 5 + [I32, P, F64] + [I32] * 4 + [P] * 4 + [I32, P, SZ, P], I32),
         "moe_quantize_i8": ([P, I32, I32, I32, I32, P, P, P, P], I32),

@@ -1326,8 +1326,8 @@ int64_t moe_norm_ws_bytes(int H) {
   return (int64_t)norm_ws_bytes(H);
 }
 
-int moe_norm_bwd(const void* dn, const void* dr, const void* r, const float* weight, double eps,
-                 int T, int H, int dtype, void* dx, float* dweight, int accumulate, void* ws,
+int moe_norm_bwd(const void* dn, const void* dr, double dr_scale, const void* r,
+                 const float* weight, double eps, int T, int H, int dtype, void* dx, float* dweight, int accumulate, void* ws,
                  size_t ws_bytes, void* stream) {
   const char* fn = "moe_norm_bwd";
   if (int rc = check_norm(T, H, dtype, eps, weight, fn)) return rc;
@@ -1340,8 +1340,8 @@ int moe_norm_bwd(const void* dn, const void* dr, const void* r, const float* wei
   }
   if (int rc = check_ptr(dweight, "dweight", fn)) return rc;
   if (int rc = check_ws(ws, ws_bytes, norm_ws_bytes(H), fn)) return rc;
-  return hip_status(launch_norm_bwd(dn, dr, r, weight, (float)eps, T, H, dtype == MOE_BF16, dx, dweight,
-                                    accumulate != 0, ws, begin_launch(stream)),
+  return hip_status(launch_norm_bwd(dn, dr, dr != nullptr ? (float)dr_scale : 0.f, r, weight, (float)eps, T, H, dtype == MOE_BF16,
+                                    dx, dweight, accumulate != 0, ws, begin_launch(stream)),
                     fn);
 }
 
@@ -1358,8 +1358,9 @@ int moe_combine_norm(const void* y_perm, const float* topk_w, const int32_t* des
   if (int rc = check_ptr(dest_row, "dest_row", fn)) return rc;
   if (int rc = check_ptr(y, "y", fn, true)) return rc;
   if (!aligned16(residual)) return fail(MOE_EINVAL, "%s: residual must be 16-byte aligned", fn);
-  return hip_status(launch_combine_norm(y_perm, topk_w, dest_row, residual, (float)residual_scale, gate,
-                                        gate_kind, weight, (float)eps, T, H, k, dtype == MOE_BF16, y,
+  return hip_status(launch_combine_norm(y_perm, topk_w, dest_row, residual,
+                                        residual != nullptr ? (float)residual_scale : 0.f, gate, gate_kind,
+                                        weight, (float)eps, T, H, k, dtype == MOE_BF16, y,
                                         begin_launch(stream)),
                     fn);
 }

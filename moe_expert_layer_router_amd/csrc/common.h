@@ -243,8 +243,8 @@ hipError_t launch_adapter_bwd(const AdapterShape& d, const void* dy, const void*
 size_t norm_ws_bytes(int H);
 hipError_t launch_norm(const void* x, const void* delta, const float* weight, float eps, int T, int H,
                        bool bf16, void* r, void* n, hipStream_t s);
-hipError_t launch_norm_bwd(const void* dn, const void* dr, const void* r, const float* weight, float eps,
-                           int T, int H, bool bf16, void* dx, float* dweight, bool accumulate, void* ws,
+hipError_t launch_norm_bwd(const void* dn, const void* dr, float dr_scale, const void* r,
+                           const float* weight, float eps, int T, int H, bool bf16, void* dx, float* dweight, bool accumulate, void* ws,
                            hipStream_t s);
 hipError_t launch_combine_norm(const void* y_perm, const float* topk_w, const int32_t* dest_row,
                                const void* residual, float residual_scale, const void* gate, int gate_kind,

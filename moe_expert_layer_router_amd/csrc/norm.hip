@@ -155,11 +155,11 @@ constexpr int partial_lds() {
   return Place<W, NC>::kTeams > 1 ? (Place<W, NC>::kTeams - 1) * W * kWave * NC * Row<BF16>::N : 1;
 }
 
-// dx = dr + s (g - xh mean(g xh)), g = dn w; the rows' dn xh added up per column.
+// dx = rs dr + s (g - xh mean(g xh)), g = dn w; the rows' dn xh added up per column.
 template <bool BF16, int W, int NC>
 __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(
-    const void* dn, const void* dr, const void* __restrict__ r, const float* __restrict__ weight,
-    float eps, int T, int H, void* dx, float* __restrict__ part) {
+    const void* dn, const void* dr, float rs, const void* __restrict__ r,
+    const float* __restrict__ weight, float eps, int T, int H, void* dx, float* __restrict__ part) {
   using R = Row<BF16>;
   __shared__ float lds[2][2 * threads_of(W) / kWave];
   __shared__ __align__(16) float sums[partial_lds<BF16, W, NC>()];
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(
       for (int i = 0; i < R::N; ++i) {
         const float xh = v[i] * s;
         dw[u][i] = fmaf(g[i], xh, dw[u][i]);
-        a[i] = fmaf(s, fmaf(-xh, m, g[i] * wt[u][i]), a[i]);
+        a[i] = fmaf(s, fmaf(-xh, m, g[i] * wt[u][i]), rs * a[i]);
       }
       if (t < T && c < nch) R::st_s(dx, (size_t)t * H + (size_t)c * R::N, R::from_f32(a));
     }
@@ -498,8 +498,8 @@ hipError_t launch_norm(const void* x, const void* delta, const float* weight, fl
   return hipGetLastError();
 }
 
-hipError_t launch_norm_bwd(const void* dn, const void* dr, const void* r, const float* weight, float eps,
-                           int T, int H, bool bf16, void* dx, float* dweight, bool accumulate, void* ws,
+hipError_t launch_norm_bwd(const void* dn, const void* dr, float dr_scale, const void* r,
+                           const float* weight, float eps, int T, int H, bool bf16, void* dx, float* dweight, bool accumulate, void* ws,
                            hipStream_t s) {
   ProfScope ps(MOE_KERNEL_NORM_BWD, s);
   const int nch = H / (bf16 ? 8 : 4);
@@ -508,8 +508,8 @@ hipError_t launch_norm_bwd(const void* dn, const void* dr, const void* r, const 
   {                                                                                                 \
     blocks = bwd_blocks<W>(T);                                                                      \
     if (blocks > 0)                                                                                 \
-      norm_bwd_kernel<B, W, NC><<<blocks, threads_of(W), 0, s>>>(dn, dr, r, weight, eps, T, H, dx,  \
-                                                                 (float*)ws);                       \
+      norm_bwd_kernel<B, W, NC><<<blocks, threads_of(W), 0, s>>>(dn, dr, dr_scale, r, weight, eps,   \
+                                                                 T, H, dx, (float*)ws);             \
   }
   if (bf16) { MOE_NORM_SHAPES(true, MOE_LAUNCH) } else { MOE_NORM_SHAPES(false, MOE_LAUNCH) }
 #undef MOE_LAUNCH

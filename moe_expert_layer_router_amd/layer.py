@@ -27,6 +27,10 @@ second stream from the start of the backward, [dg | du] (with dW_gate and
 dW_up) once the data gradients have produced it.  Routing, combine and the
 router backward stay as in the bf16 layer.
 
+With int8=True (forward only) the expert FFN runs on int8 codes: forward() takes
+each expert weight as the pair (codes, scales) that moe_quantize_i8 made of it
+once, and quantizes the token rows itself.
+
 Options around the layer, in any of its forms unless said otherwise:
  - balance_coef, z_coef: the router's auxiliary losses, in buf["aux_loss"] (and
    the per-expert counts of all E experts in buf["aux_counts"]) after forward();
@@ -36,6 +40,18 @@ Options around the layer, in any of its forms unless said otherwise:
    dropout(combine); the residual's gradient is dy itself and not part of dx.
  - adapters=True (bf16 or fp32, forward only): forward() takes the low-rank
    adapters of the batch's requests on the expert projections.
+ - checkpoint=pool (training, not fp8): what the backward needs of the grouped
+   rows is kept as 8-bit codes (gate and up, and the expert outputs), and the
+   large buffers (x_perm, gu, h_perm, y_perm) are those of the dict `pool`, which
+   layers of the same sizes share: the first one fills it.  forward() leaves the
+   codes, backward() restores the buffers from them and permutes x again, so
+   layers may run forward one after another and backward in the other order.
+ - pre_norm, post_norm (whole layers, [e_lo, e_hi) = [0, E)): with pre_norm the
+   layer takes the residual stream, r = x + delta and n = norm(r) * pre_weight,
+   and y = residual_scale * r + its output; with post_norm the output is
+   gate * norm(combine) * post_weight in place of the combine.  Both are the eps of
+   their norm.  backward() returns the gradient of x (and of delta), which includes
+   the residual's, and dpre_weight, dpost_weight, dgate.
 """
 from __future__ import annotations
 
@@ -48,11 +64,18 @@ from . import (MOE_BF16, MOE_F32, MOE_FP8, MOE_OP_FFN_BWD, MOE_OP_FFN_DGRAD_FP8,
                MOE_OP_FFN_FWD_FP8, MOE_OP_FFN_WGRAD_FP8, MOE_OP_PERMUTE, MOE_OP_QUANTIZE_W_FP8,
                MOE_OP_ROUTE, MOE_OP_ROUTE_BWD, _check, _stream, lib, moe_adapter_rows,
                moe_balance_loss, moe_balance_loss_bwd, moe_combine_dropout, moe_combine_dropout_bwd,
-               moe_grouped_ffn_fwd_adapter, moe_route_bwd_add, workspace_bytes)
+               moe_combine_norm, moe_combine_norm_bwd, moe_dequantize_i8, moe_grouped_ffn_fwd_adapter,
+               moe_grouped_ffn_fwd_i8, moe_norm, moe_norm_bwd, moe_quantize_i8, moe_route_bwd_add,
+               moe_swiglu_restore_i8, workspace_bytes)
 
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _group(*widths: int) -> int:
+    """The largest group of the 8-bit codes that divides every width (0: none does)."""
+    return next((g for g in (128, 64, 32) if all(w % g == 0 for w in widths)), 0)
 
 
 class MoELayer:
@@ -61,15 +84,30 @@ class MoELayer:
     def __init__(self, T: int, H: int, I: int, E: int, k: int, e_lo: int, e_hi: int,
                  dtype: torch.dtype, device="cuda", train: bool = True, fp8: bool = False,
                  gather: Optional[bool] = None, balance_coef: float = 0.0, z_coef: float = 0.0,
-                 max_sequences: int = 1, dropout: float = 0.0, adapters: bool = False):
+                 max_sequences: int = 1, dropout: float = 0.0, adapters: bool = False,
+                 int8: bool = False, checkpoint: Optional[Dict[str, torch.Tensor]] = None,
+                 pre_norm: Optional[float] = None, post_norm: Optional[float] = None):
         if not 0.0 <= dropout < 1.0:
             raise ValueError(f"dropout={dropout} outside [0, 1)")
         if adapters and (fp8 or train):
             raise ValueError("adapters=True needs a layer built for the forward alone (not fp8)")
+        if int8 and (train or fp8 or adapters or dtype != torch.bfloat16 or H % 16 or I % 16):
+            raise ValueError("int8=True needs a bf16 layer built for the forward alone (not fp8, no "
+                             "adapters), H and I multiples of 16")
+        if checkpoint is not None and (not train or fp8 or not _group(I, H)):
+            raise ValueError("checkpoint needs a layer built for training (not fp8), H and I multiples of 32")
+        if (pre_norm is not None or post_norm is not None) and (e_lo, e_hi) != (0, E):
+            raise ValueError("the norms need all experts of the layer: a rank's part of the combined row is "
+                             "not the row")
+        if post_norm is not None and dropout > 0.0:
+            raise ValueError("dropout and post_norm do not go together")
+        self.int8, self.pre_norm, self.post_norm = int8, pre_norm, post_norm
+        self.checkpoint = checkpoint
         self.balance_coef, self.z_coef, self.dropout = balance_coef, z_coef, dropout
         self.aux = balance_coef != 0.0 or z_coef != 0.0
         self.adapters = adapters
         self._drop = None  # the forward's dropout numbers
+        self._norms = (None, None, None, None, 1.0)  # and its residual, norm weights, gate and scale
         if fp8 and (dtype != torch.bfloat16 or H % 128 or I % 128 or I > 2048):
             raise ValueError("the FP8 layer needs bf16 tensors, H % 128 == 0, I % 128 == 0 "
                              "and I <= 2048")
@@ -81,6 +119,9 @@ class MoELayer:
         self.R_cap = T * k
         self.train = train
         dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
         f32, i32 = torch.float32, torch.int32
         R, E_l = self.R_cap, self.E_l
         b = {}
@@ -96,14 +137,42 @@ class MoELayer:
         # copy.  (FP8: the permute writes maps only, its FFN gathers the token
         # code rows the same way; training keeps x_perm for
         # the weight gradients.)
-        can_gather = not train and not fp8 and dtype == torch.bfloat16
+        can_gather = not train and not fp8 and not int8 and dtype == torch.bfloat16
         if gather and not can_gather:
             raise ValueError("gather=True needs a bf16 layer built for the forward alone (not fp8)")
         self.gather = can_gather if gather is None else bool(gather)
-        b["x_perm"] = None if (fp8 or self.gather) else torch.empty((R, H), dtype=dtype, device=dev)
-        b["h_perm"] = torch.empty((R, I), dtype=dtype, device=dev)
-        b["y_perm"] = torch.empty((R, H), dtype=dtype, device=dev)
-        b["gu"] = torch.empty((R, 2 * I), dtype=dtype, device=dev) if train or adapters else None
+        big = self._large if checkpoint is not None else lambda name, shape: torch.empty(
+            shape, dtype=dtype, device=dev)
+        b["x_perm"] = None if (fp8 or int8 or self.gather) else big("x_perm", (R, H))
+        b["h_perm"] = big("h_perm", (R, I))
+        b["y_perm"] = big("y_perm", (R, H))
+        b["gu"] = big("gu", (R, 2 * I)) if train or adapters else None
+        if checkpoint is not None:
+            g = _group(I, H)
+            b["gu_q"] = torch.empty((R, 2 * I), dtype=torch.int8, device=dev)
+            b["gu_s"] = torch.empty((R, 2 * I // g), dtype=f32, device=dev)
+            b["y_q"] = torch.empty((R, H), dtype=torch.int8, device=dev)
+            b["y_s"] = torch.empty((R, H // g), dtype=f32, device=dev)
+        if pre_norm is not None:
+            b["n"] = torch.empty((T, H), dtype=dtype, device=dev)
+            b["r"] = torch.empty((T, H), dtype=dtype, device=dev)
+        if int8:
+            b["x_q"] = torch.empty((T, H), dtype=torch.int8, device=dev)
+            b["x_scale"] = torch.empty(T, dtype=f32, device=dev)
+            nb = lib.moe_ffn_i8_ws_bytes(R, I)
+            if nb < 0:
+                _check(int(nb), "moe_ffn_i8_ws_bytes")
+            self.ws_i8 = torch.empty(max(int(nb), 256), dtype=torch.uint8, device=dev)
+        if train and (pre_norm is not None or post_norm is not None):
+            nb = lib.moe_norm_ws_bytes(H)
+            if nb < 0:
+                _check(int(nb), "moe_norm_ws_bytes")
+            self.ws_norm = torch.empty(int(nb), dtype=torch.uint8, device=dev)
+            if pre_norm is not None:
+                b["dx_in"] = torch.empty((T, H), dtype=dtype, device=dev)
+                b["dpre_weight"] = torch.empty(H, dtype=f32, device=dev)
+            if post_norm is not None:
+                b["dpost_weight"] = torch.empty(H, dtype=f32, device=dev)
         b["no_rng"] = torch.zeros(2, dtype=torch.int64, device=dev)
         if adapters:
             b["row_id"] = torch.empty(R, dtype=i32, device=dev)
@@ -174,15 +243,40 @@ class MoELayer:
         if train or fp8:
             self.side = torch.cuda.Stream(device=dev) if dev.type == "cuda" else None
 
+    def _large(self, name, shape):
+        """A buffer of the pool that layers share: the pool's, or a new one put there."""
+        t = self.checkpoint.get(name)
+        if t is None:
+            t = self.checkpoint[name] = torch.empty(shape, dtype=self.dtype, device=self.device)
+        if tuple(t.shape) != shape or t.dtype != self.dtype or t.device != self.device:
+            raise ValueError(f"the pool's {name} is {t.dtype} {tuple(t.shape)} on {t.device}, this layer needs "
+                             f"{self.dtype} {shape} on {self.device}")
+        return t
+
     def forward(self, x, w_router, w_gate, w_up, w_down, bias=None, save_logits=True, residual=None,
-                rng=None, seq_offsets=None, token_mask=None, adapters=None):
+                rng=None, seq_offsets=None, token_mask=None, adapters=None, delta=None, pre_weight=None,
+                post_weight=None, gate=None, residual_scale=1.0):
         """residual [T,H]: added to the combined rows.  rng [2] int64 on the GPU (seed, offset):
         the dropout's numbers, still in it when backward() repeats them.  seq_offsets [S+1] int32 and
         token_mask [T] uint8: the sequences and padding of the auxiliary losses (S = max_sequences,
         fewer with empty ones behind the last; None: all tokens are one sequence).  adapters: dict
         token_adapter [T] int32 (-1: none), n, gate / up / down: (A, B) with A [n, E_l, rank, in] and
-        B [n, E_l, out, rank], scale [n, E_l] fp32 (optional)."""
+        B [n, E_l, out, rank], scale [n, E_l] fp32 (optional).  pre_weight, post_weight [H] fp32: the
+        norms' weights; delta [T,H] (pre_norm): added to x first; gate [T] fp32 or [T,H]
+        (post_norm); residual_scale (post_norm): of the residual, which with pre_norm is r.  They
+        and x are still as given when backward() reads them.  int8: w_gate, w_up and w_down are
+        (codes, scales)."""
         b, T, H, I, E, k = self.buf, self.T, self.H, self.I, self.E, self.k
+        for name, given, wanted in (("pre_weight", pre_weight, self.pre_norm),
+                                    ("post_weight", post_weight, self.post_norm)):
+            if (given is None) != (wanted is None):
+                raise ValueError(f"{name} goes with a layer built with its norm")
+        if self.pre_norm is None and delta is not None:
+            raise ValueError("delta needs a layer built with pre_norm")
+        if self.pre_norm is not None and residual is not None:
+            raise ValueError("a layer with pre_norm has its residual: r = x + delta")
+        if self.post_norm is None and (gate is not None or residual_scale != 1.0):
+            raise ValueError("gate and residual_scale need a layer built with post_norm")
         if self.dropout > 0.0 and rng is None:
             raise ValueError("a layer with dropout needs rng")
         if adapters is not None and not self.adapters:
@@ -192,6 +286,10 @@ class MoELayer:
                              f"{sorted(self.ADAPTER_KEYS)}")
         s = _stream()
         ws, wsb = _p(self.ws), self.ws_bytes
+        if self.pre_norm is not None:
+            moe_norm(x, pre_weight, self.pre_norm, delta=delta, out={"n": b["n"], "r": b["r"]})
+            residual, x = x if delta is None else b["r"], b["n"]
+        self._norms = (residual, pre_weight, post_weight, gate, residual_scale)
         if self.fp8:
             self._quantize_weights_fp8(w_gate, w_up, w_down)
         _check(lib.moe_route(_p(x), _p(w_router), _p(bias), T, H, E, k, self.dt,
@@ -201,6 +299,8 @@ class MoELayer:
             self._aux_forward(save_logits, seq_offsets, token_mask)
         if self.fp8:
             self._forward_ffn_fp8(x, w_gate, w_up, w_down, ws, wsb, s)
+        elif self.int8:
+            self._forward_ffn_int8(x, w_gate, w_up, w_down, ws, wsb, s)
         elif adapters is not None:
             self._forward_ffn_adapters(x, w_gate, w_up, w_down, adapters, ws, wsb, s)
         elif self.gather:
@@ -221,8 +321,15 @@ class MoELayer:
                                            H, I, _p(w_gate), _p(w_up), _p(w_down), self.dt, _p(b["gu"]),
                                            _p(b["h_perm"]), _p(b["y_perm"]), ws, wsb, s),
                    "moe_grouped_ffn_fwd")
+        if self.checkpoint is not None:  # what the backward restores the pool's buffers from
+            g, n = _group(I, H), b["offsets"][self.E_l:]
+            moe_quantize_i8(b["gu"], group=g, nrows=n, out={"q": b["gu_q"], "scale": b["gu_s"]})
+            moe_quantize_i8(b["y_perm"], group=g, nrows=n, out={"q": b["y_q"], "scale": b["y_s"]})
         self._drop = None
-        if self.dropout > 0.0 or residual is not None:
+        if self.post_norm is not None:
+            moe_combine_norm(b["y_perm"], b["topk_w"], b["dest_row"], T, post_weight, self.post_norm,
+                             residual=residual, residual_scale=residual_scale, gate=gate, out=b["y"])
+        elif self.dropout > 0.0 or residual is not None:
             if rng is None:  # no dropout: the numbers do not matter
                 rng = b["no_rng"]
             self._drop = rng if self.dropout > 0.0 else None
@@ -265,6 +372,28 @@ class MoELayer:
                                     w_gate, w_up, w_down, flat,
                                     scale=None if scale is None else scale.view(-1), ws=self.ws,
                                     out={"gu": b["gu"], "h_perm": b["h_perm"], "y_perm": b["y_perm"]})
+
+    def _forward_ffn_int8(self, x, w_gate, w_up, w_down, ws, wsb, s):
+        """Token rows quantized, the permutation's maps, then the int8 grouped FFN reading the token code
+        rows through src_row."""
+        b, T, H, E, k = self.buf, self.T, self.H, self.E, self.k
+        moe_quantize_i8(x, out={"q": b["x_q"], "scale": b["x_scale"]})
+        _check(lib.moe_permute(None, _p(b["topk_idx"]), T, H, E, k, self.e_lo, self.e_hi, self.dt,
+                               _p(b["counts"]), _p(b["offsets"]), _p(b["dest_row"]), _p(b["src_row"]),
+                               None, ws, wsb, s), "moe_permute")
+        moe_grouped_ffn_fwd_i8(b["x_q"], b["x_scale"], b["src_row"], b["offsets"], w_gate, w_up, w_down,
+                               ws=self.ws_i8, out={"h_perm": b["h_perm"], "y_perm": b["y_perm"]})
+
+    def _restore(self, x, ws, wsb, s):
+        """The pool's buffers as the backward needs them: gu and h, y_perm from the codes, the grouped rows
+        of x again."""
+        b, T, H, E, k = self.buf, self.T, self.H, self.E, self.k
+        n = b["offsets"][self.E_l:]
+        moe_swiglu_restore_i8(b["gu_q"], b["gu_s"], self.dtype, nrows=n, out={"gu": b["gu"], "h_perm": b["h_perm"]})
+        moe_dequantize_i8(b["y_q"], b["y_s"], self.dtype, nrows=n, out=b["y_perm"])
+        _check(lib.moe_permute(_p(x), _p(b["topk_idx"]), T, H, E, k, self.e_lo, self.e_hi, self.dt,
+                               _p(b["counts"]), _p(b["offsets"]), _p(b["dest_row"]), _p(b["src_row"]),
+                               _p(b["x_perm"]), ws, wsb, s), "moe_permute")
 
     def _quantize_rows(self, src, rows, cols, q, scale, s, nrows=None):
         _check(lib.moe_quantize_fp8(_p(src), rows, cols, self.dt, _p(nrows), _p(q), _p(scale), s),
@@ -356,12 +485,26 @@ class MoELayer:
         b, T, H, I, E, k = self.buf, self.T, self.H, self.I, self.E, self.k
         s = _stream()
         ws, wsb = _p(self.ws), self.ws_bytes
+        residual, pre_weight, post_weight, gate, residual_scale = self._norms
+        if self.pre_norm is not None:
+            x = b["n"]
+        if self.checkpoint is not None:
+            self._restore(x, ws, wsb, s)
         # the router weight's transpose while nothing else runs: later, behind
         # the data gradients, its small grid would wait for CUs that the
         # concurrent weight-gradient product holds
         _check(lib.moe_router_weight_t(_p(w_router), H, E, self.dt, _p(b["w_router_t"]), s),
                "moe_router_weight_t")
-        if self._drop is not None:
+        if self.post_norm is not None:
+            out = {"dy_perm": b["dy_perm"], "d_topk_w": b["d_topk_w"], "dweight": b["dpost_weight"]}
+            if gate is not None:
+                g = b.get("dgate")
+                if g is None or g.shape != gate.shape or g.dtype != gate.dtype:
+                    b["dgate"] = torch.empty_like(gate)
+                out["dgate"] = b["dgate"]
+            moe_combine_norm_bwd(dy, b["y_perm"], b["topk_w"], b["dest_row"], post_weight, self.post_norm,
+                                 gate=gate, ws=self.ws_norm, out=out)
+        elif self._drop is not None:
             moe_combine_dropout_bwd(dy, b["y_perm"], b["topk_w"], b["dest_row"], self.dropout, self._drop,
                                     out={"dy_perm": b["dy_perm"], "d_topk_w": b["d_topk_w"]})
         else:
@@ -381,7 +524,8 @@ class MoELayer:
                                                  _p(b["dw_up"]), _p(b["dw_down"]), 0, ws, wsb, s, side),
                    "moe_grouped_ffn_bwd_split")
         if self.aux:
-            return self._backward_aux(x, w_router, d_aux, s)
+            self._backward_aux(x, w_router, d_aux, s)
+            return self._gradients(dy)
         # input gradient: the experts' part and the router's part in one pass
         _check(lib.moe_combine_dx_t(_p(b["dx_perm"]), _p(b["dest_row"]), _p(b["d_topk_w"]),
                                     _p(b["topk_w"]), _p(b["topk_idx"]), _p(b["w_router_t"]), T, H,
@@ -392,8 +536,22 @@ class MoELayer:
             # waits for d_topk_w: the FFN backward forked it after the combine backward)
             self._route_bwd(x, w_router, side)
         main.wait_stream(self.side)
-        return {n: b[n] for n in ("dx", "dw_router", "dw_gate", "dw_up", "dw_down", "d_logits",
-                                  "d_topk_w")}
+        return self._gradients(dy)
+
+    def _gradients(self, dy) -> Dict[str, torch.Tensor]:
+        """The gradients of a backward; with norms, that of x through the one before the layer."""
+        b = self.buf
+        got = {n: b[n] for n in ("dx", "dw_router", "dw_gate", "dw_up", "dw_down", "d_logits", "d_topk_w")}
+        residual, pre_weight, _, gate, residual_scale = self._norms
+        if self.post_norm is not None:
+            got["dpost_weight"] = b["dpost_weight"]
+            if gate is not None:
+                got["dgate"] = b["dgate"]
+        if self.pre_norm is not None:
+            moe_norm_bwd(b["dx"], residual, pre_weight, self.pre_norm, dr=dy, dr_scale=residual_scale,
+                         ws=self.ws_norm, out={"dx": b["dx_in"], "dweight": b["dpre_weight"]})
+            got["dx"], got["dpre_weight"] = b["dx_in"], b["dpre_weight"]
+        return got
 
     def _backward_aux(self, x, w_router, d_aux, s):
         """The end of a backward with auxiliary losses: their logit gradient, dense, joins the gate's,
@@ -409,5 +567,3 @@ class MoELayer:
         _check(lib.moe_combine(_p(b["dx_perm"]), None, _p(b["dest_row"]), _p(b["dx_router"]), T, H, k,
                                self.dt, _p(b["dx"]), s), "moe_combine")
         torch.cuda.current_stream().wait_stream(self.side)
-        return {n: b[n] for n in ("dx", "dw_router", "dw_gate", "dw_up", "dw_down", "d_logits",
-                                  "d_topk_w")}

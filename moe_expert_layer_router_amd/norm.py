@@ -62,9 +62,9 @@ def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, delta: Op
 
 
 def moe_norm_bwd(dn: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
-                 dr: Optional[torch.Tensor] = None, accumulate: bool = False,
+                 dr: Optional[torch.Tensor] = None, dr_scale: float = 1.0, accumulate: bool = False,
                  ws: Optional[torch.Tensor] = None, out: Optional[Dict[str, torch.Tensor]] = None):
-    """Backward of moe_norm for the gradient dn of n and (optional) dr of r.  Returns dict dx [T,H] (of
+    """Backward of moe_norm for the gradient dn of n and (optional) dr_scale * dr of r.  Returns dict dx [T,H] (of
     x and of delta), dweight [H] fp32 (added to with accumulate=True) and the workspace ws used."""
     o = dict(out) if out else {}
     dt, f32, d = dn.dtype, torch.float32, dn.get_device()
@@ -81,7 +81,7 @@ def moe_norm_bwd(dn: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, eps: f
                 and dx.dtype is dt and dx.get_device() == d and dx.shape == dn.shape and dx.is_contiguous()
                 and dw.dtype is f32 and dw.get_device() == d and dw.shape == (H,) and dw.is_contiguous()
                 and ws.get_device() == d and ws.is_contiguous()):
-            rc = lib.moe_norm_bwd(dn.data_ptr(), None if dr is None else dr.data_ptr(), r.data_ptr(),
+            rc = lib.moe_norm_bwd(dn.data_ptr(), None if dr is None else dr.data_ptr(), dr_scale, r.data_ptr(),
                                   weight.data_ptr(), eps, T, H,
                                   MOE_BF16 if dt is torch.bfloat16 else MOE_F32, dx.data_ptr(),
                                   dw.data_ptr(), 1 if accumulate else 0, ws.data_ptr(), ws.nbytes,
@@ -94,7 +94,7 @@ def moe_norm_bwd(dn: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, eps: f
     T, H = _shape2(dn, "dn")
     _int32(T=T, H=H)
     dt = _row_type(dn, "dn")
-    a = [_arg(dn, "dn", dt, (T, H), dev), _arg(dr, "dr", dt, (T, H), dev, optional=True),
+    a = [_arg(dn, "dn", dt, (T, H), dev), _arg(dr, "dr", dt, (T, H), dev, optional=True), dr_scale,
          _arg(r, "r", dt, (T, H), dev), _arg(weight, "weight", f32, (H,), dev)]
     if accumulate and dw is None:
         raise ValueError("accumulate=True needs out with dweight")

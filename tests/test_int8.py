@@ -274,6 +274,38 @@ def test_products(sizes, K, N):
 
 
 @gpu
+@pytest.mark.parametrize("E,rows", [(3, 5), (1, 400), (256, 4200)])
+def test_no_rows_at_all(E, rows):
+    """Every group empty, in both kernels and in the FFN: nothing is written."""
+    K, N = 64, 48
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    x, xs = torch.ones((rows, K), dtype=torch.int8, device=DEV), torch.ones(rows, device=DEV)
+    w, ws = torch.ones((E, N, K), dtype=torch.int8, device=DEV), torch.ones((E, N), device=DEV)
+    d, ds = torch.ones((E, K, N), dtype=torch.int8, device=DEV), torch.ones((E, K), device=DEV)
+    y = torch.full((rows, N), 7.0, dtype=bf, device=DEV)
+    assert (moe.moe_grouped_gemm_i8(x, xs, None, off, w, ws, out=y) == 7).all()
+    o = {"h_perm": y, "y_perm": torch.full((rows, K), 7.0, dtype=bf, device=DEV)}
+    moe.moe_grouped_ffn_fwd_i8(x, xs, None, off, (w, ws), (w, ws), (d, ds), out=o)
+    assert (y == 7).all() and (o["y_perm"] == 7).all()
+
+
+@gpu
+def test_a_row_that_is_no_number_stays_alone():
+    """A token with an infinity and one with a NaN: their rows of the FFN's result are NaN, no other is,
+    in both kernels."""
+    H, I = 128, 96
+    g = torch.Generator(device=DEV).manual_seed(9)
+    ww = [moe.moe_quantize_i8(torch.randn(s, generator=g, device=DEV)) for s in ((2, I, H), (2, I, H), (2, H, I))]
+    for rows in (12, 150):
+        x = torch.randn((rows, H), generator=g, device=DEV).to(bf)
+        x[3, 5], x[7, 1] = float("inf"), float("nan")
+        off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device=DEV)
+        y = moe.moe_grouped_ffn_fwd_i8(*moe.moe_quantize_i8(x), None, off, *ww)["y_perm"]
+        bad = y.isnan()
+        assert bad[3].all() and bad[7].all() and int(bad.sum()) == 2 * H
+
+
+@gpu
 def test_the_split_into_groups_changes_no_bit():
     """1030 rows as one group (tiles), as groups of 1 to 64 rows beside large ones (both kernels), and as
     groups that go without tiles."""
