@@ -690,6 +690,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
         Feed<GU>& feed;
         TileLds& c;
         const Wave<GU>& w;
+        const bool more;
         const int tid;
         const int& row;
         const float& scale;
@@ -701,11 +702,16 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
             c.ws[tid - kTileM] = scale;
           }
         }
-        // The last tile's "next" is itself again: its DMAs have to be there for the waits'
-        // counts, and what they fetch is not read.
-        __device__ void set() const { feed.set(p, t, c.row, w.wave); }
+        // After the last tile every chunk is dropped: the DMAs have to be there for the
+        // waits' counts, and move nothing.
+        __device__ void set() const {
+          feed.set(p, t, c.row, w.wave);
+          if (more) return;
+#pragma unroll
+          for (int i = 0; i < kDmas; ++i) feed.wv[i] = feed.xv[i] = kDmaKill;
+        }
         __device__ void start(int i) const { feed.start(i, w.lds0, w.wave); }
-      } next = {p, t, feed, c, w, tid, row, scale};
+      } next = {p, t, feed, c, w, id < to, tid, row, scale};
       const int first = w.wm * (height / 2);
       const int blocks = min((now.rows - first + 31) / 32, height / 64);  // of this wave that have rows
       if (blocks > 2) after = w.template run<4>(now, f, first, after, begin, next);

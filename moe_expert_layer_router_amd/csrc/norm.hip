@@ -113,15 +113,17 @@ __global__ __launch_bounds__(threads_of(W)) void norm_kernel(
 }
 
 // Adds the column sums that the teams of a workgroup hold (dw, a lane's chunks)
-// in team order and writes them as the workgroup's partial row.
+// in team order and writes them as the workgroup's partial row, or, where it is the
+// only one, as (or to) the sums themselves.
 template <bool BF16, int W, int NC>
 __device__ __forceinline__ void write_partial(const Place<W, NC>& at, int nch, int H,
                                               float (&dw)[NC][Row<BF16>::N], float* __restrict__ part,
-                                              float* lds) {
+                                              float* __restrict__ only, int accumulate, float* lds) {
   constexpr int N = Row<BF16>::N;
   constexpr int kTeams = Place<W, NC>::kTeams;
   constexpr int kRow = W * kWave * NC * N;  // elements a team covers
-  float* row = part + (size_t)blockIdx.x * H;
+  float* row = gridDim.x == 1 ? only : part + (size_t)blockIdx.x * H;
+  const bool add = gridDim.x == 1 && accumulate != 0;
   if constexpr (kTeams > 1) {
     __syncthreads();
     if (at.team > 0) {
@@ -145,7 +147,8 @@ __device__ __forceinline__ void write_partial(const Place<W, NC>& at, int nch, i
 #pragma unroll
       for (int m = 1; m < kTeams; ++m)
         v += *reinterpret_cast<const f32x4_t*>(lds + (m - 1) * kRow + c * N + i);
-      *reinterpret_cast<f32x4_t*>(row + c * N + i) = v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) row[c * N + i + q] = add ? row[c * N + i + q] + v[q] : v[q];
     }
   }
 }
@@ -159,7 +162,8 @@ constexpr int partial_lds() {
 template <bool BF16, int W, int NC>
 __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(
     const void* dn, const void* dr, float rs, const void* __restrict__ r,
-    const float* __restrict__ weight, float eps, int T, int H, void* dx, float* __restrict__ part) {
+    const float* __restrict__ weight, float eps, int T, int H, void* dx, float* __restrict__ part,
+    float* __restrict__ dweight, int accumulate) {
   using R = Row<BF16>;
   __shared__ float lds[2][2 * threads_of(W) / kWave];
   __shared__ __align__(16) float sums[partial_lds<BF16, W, NC>()];
@@ -219,7 +223,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(
       if (t < T && c < nch) R::st_s(dx, (size_t)t * H + (size_t)c * R::N, R::from_f32(a));
     }
   }
-  write_partial<BF16, W, NC>(at, nch, H, dw, part, sums);
+  write_partial<BF16, W, NC>(at, nch, H, dw, part, dweight, accumulate, sums);
 }
 
 // out[h] (+)= sum over the G partial rows, in row order within each of 32 shares
@@ -324,7 +328,8 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
     const void* __restrict__ dy, const void* __restrict__ y_perm, const float* __restrict__ topk_w,
     const int32_t* __restrict__ dest_row, const void* __restrict__ gate, int gate_kind,
     const float* __restrict__ weight, float eps, int T, int H, int k, void* __restrict__ dy_perm,
-    float* __restrict__ d_topk_w, void* __restrict__ dgate, float* __restrict__ part) {
+    float* __restrict__ d_topk_w, void* __restrict__ dgate, float* __restrict__ part,
+    float* __restrict__ dweight, int accumulate) {
   using R = Row<BF16>;
   constexpr int kHeld = held(W, NC);
   __shared__ float lds[2 * threads_of(W) / kWave], dots[kHeld * threads_of(W) / kWave];
@@ -454,7 +459,7 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
     }
     if (W > 1 && most == 0) lds_barrier();  // lds is read before the next token's sums (no slots: no other barrier)
   }
-  write_partial<BF16, W, NC>(at, nch, H, dw, part, sums);
+  write_partial<BF16, W, NC>(at, nch, H, dw, part, dweight, accumulate, sums);
 }
 
 // Up to this many tokens a token's slots are loaded at once by a team with one
@@ -509,13 +514,15 @@ hipError_t launch_norm_bwd(const void* dn, const void* dr, float dr_scale, const
     blocks = bwd_blocks<W>(T);                                                                      \
     if (blocks > 0)                                                                                 \
       norm_bwd_kernel<B, W, NC><<<blocks, threads_of(W), 0, s>>>(dn, dr, dr_scale, r, weight, eps,   \
-                                                                 T, H, dx, (float*)ws);             \
+                                                                 T, H, dx, (float*)ws, dweight,     \
+                                                                 accumulate);                       \
   }
   if (bf16) { MOE_NORM_SHAPES(true, MOE_LAUNCH) } else { MOE_NORM_SHAPES(false, MOE_LAUNCH) }
 #undef MOE_LAUNCH
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  column_sum_kernel<<<(H + 31) / 32, 1024, 0, s>>>((const float*)ws, blocks, H, accumulate, dweight);
+  if (blocks != 1)  // (none: zeros)
+    column_sum_kernel<<<(H + 31) / 32, 1024, 0, s>>>((const float*)ws, blocks, H, accumulate, dweight);
   return hipGetLastError();
 }
 
@@ -554,13 +561,14 @@ hipError_t launch_combine_norm_bwd(const void* dy, const void* y_perm, const flo
     if (blocks > 0)                                                                                  \
       combine_norm_bwd_kernel<B, W, NC><<<blocks, threads_of(W), 0, s>>>(                            \
           dy, y_perm, topk_w, dest_row, gate, gate_kind, weight, eps, T, H, k, dy_perm, d_topk_w,    \
-          dgate, (float*)ws);                                                                        \
+          dgate, (float*)ws, dweight, accumulate);                                                   \
   }
   if (bf16) { MOE_NORM_SHAPES1(true, MOE_LAUNCH) } else { MOE_NORM_SHAPES1(false, MOE_LAUNCH) }
 #undef MOE_LAUNCH
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  column_sum_kernel<<<(H + 31) / 32, 1024, 0, s>>>((const float*)ws, blocks, H, accumulate, dweight);
+  if (blocks != 1)  // (none: zeros)
+    column_sum_kernel<<<(H + 31) / 32, 1024, 0, s>>>((const float*)ws, blocks, H, accumulate, dweight);
   return hipGetLastError();
 }
 
