@@ -305,9 +305,8 @@ struct At {
 
 // What every workgroup finds out from the offsets, and what it keeps of a tile.
 struct TileLds {
-  int start[kMaxE + 1];  // row tiles before expert e
-  int row0[kMaxE], row1[kMaxE];
-  int scan[4], tall[4];
+  int start[kMaxE + 4];  // row tiles before expert e; start[kMaxE]: of all
+  int off[kMaxE + 4];    // the offsets (experts past E_l have no rows)
   int row[kTileM];       // rows of x of the next tile
   float xs[kTileM], ws[kTileW];  // scales of the tile in work
 };
@@ -592,6 +591,17 @@ struct Wave {
   }
 };
 
+// Sums of the lanes up to each (inclusive), by row shifts and broadcasts.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 of a row to the next
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
+  return v;
+}
+
 // Tiles in the order (expert, column tile, row tile).  Every workgroup counts them
 // from the offsets and takes its share: an XCD a run of the order, in rounds of one
 // tile a workgroup, so that neighbouring tiles (of the same weights, of the same
@@ -602,36 +612,36 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
   __shared__ __align__(16) TileLds c;
   const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
   const int cols = (p.N + tile_cols<GU>() - 1) / tile_cols<GU>();
+  // Every wave counts for itself, a lane for four experts, and writes what the others
+  // write: nobody waits for anybody.
   int height = kTileM;
   {
-    const bool in = tid < p.E_l;
-    const int lo = in ? p.offsets[tid] : 0, hi = in ? p.offsets[tid + 1] : 0, n = max(hi - lo, 0);
+    int off[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) off[i] = p.offsets[min(4 * lane + i, p.E_l)];
+    const auto tiles_of = [&](int h, int i) { return (max(off[i + 1] - off[i], 0) + h - 1) / h; };
+    int full = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) full += tiles_of(kTileM, i);
     // row tiles of the full height: with fewer of them than two for a workgroup,
     // tiles of half the height keep more CUs at work
-    int full = (n + kTileM - 1) / kTileM;
+    if (__builtin_amdgcn_readlane(wave_scan(full), 63) * cols < 2 * (int)gridDim.x) height = kTileM / 2;
+    int mine = 0, n[4];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) full += __shfl_xor(full, o, kWave);
-    if (lane == 0 && wave < 4) c.tall[wave] = full;
-    __syncthreads();
-    if ((c.tall[0] + c.tall[1] + c.tall[2] + c.tall[3]) * cols < 2 * (int)gridDim.x) height = kTileM / 2;
-    const int mine = (n + height - 1) / height;
-    int sum = mine;  // row tiles up to this thread's expert
+    for (int i = 0; i < 4; ++i) mine += n[i] = height == kTileM ? tiles_of(kTileM, i) : tiles_of(kTileM / 2, i);
+    const int upto = wave_scan(mine);
+    int before = upto - mine;
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const int up = __shfl_up(sum, o, kWave);
-      if (lane >= o) sum += up;
+    for (int i = 0; i < 4; ++i) {
+      c.start[4 * lane + i] = before;
+      c.off[4 * lane + i] = off[i];
+      before += n[i];
     }
-    if (lane == 63 && wave < 4) c.scan[wave] = sum;
-    __syncthreads();
-    if (tid < kMaxE) {
-      int before = sum - mine;
-      for (int w = 0; w < wave; ++w) before += c.scan[w];
-      c.start[tid] = before;
-      c.row0[tid] = lo;
-      c.row1[tid] = hi;
+    if (lane == 63) {
+      c.start[kMaxE] = upto;
+      c.off[kMaxE] = off[4];
     }
-    if (tid == 0) c.start[kMaxE] = c.scan[0] + c.scan[1] + c.scan[2] + c.scan[3];
-    __syncthreads();
+    lanes_meet();
   }
   const int tiles = c.start[kMaxE] * cols;
   // this XCD's run of the tiles
@@ -645,13 +655,14 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
     int a = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a += __popcll(__ballot(s[i] * cols <= id));
-    const int n = c.start[a + 1] - c.start[a], at = id - c.start[a] * cols;
-    const int r0 = c.row0[a] + at % n * height;
+    const uint32_t n = c.start[a + 1] - c.start[a], at = id - c.start[a] * cols;
+    const uint32_t col = at / n;
+    const int r0 = c.off[a] + (int)(at - col * n) * height;
     At t;
     t.e = __builtin_amdgcn_readfirstlane(a);
-    t.n0 = __builtin_amdgcn_readfirstlane(at / n) * tile_cols<GU>();
+    t.n0 = __builtin_amdgcn_readfirstlane((int)col) * tile_cols<GU>();
     t.r0 = __builtin_amdgcn_readfirstlane(r0);
-    t.rows = __builtin_amdgcn_readfirstlane(min(height, c.row1[a] - r0));
+    t.rows = __builtin_amdgcn_readfirstlane(min(height, c.off[a + 1] - r0));
     return t;
   };
   const Wave<GU> w(p, lds, c);
