@@ -9,12 +9,19 @@
 //   few rows (skinny_i8_kernel): bound by the read of the weights.  A workgroup
 //     owns 32 columns of one expert (64 where K is short); its waves split K and
 //     take the weights straight from memory into MFMA operands, each byte once for
-//     up to 64 rows, and add their sums through LDS.
+//     up to 64 rows, and add their sums through LDS.  64 tokens of the whole layer
+//     (128 experts of 2048 x 768, top-8): gate and up 58 us, down 39, 598 MB together
+//     at 6.2 TB/s.
 //   many rows (tile_i8_kernel): bound by the matrix cores and what feeds them.
 //     Tiles of 256 rows x 256 weight rows in a workgroup of eight waves that stays
 //     on its CU and takes tile after tile; operands through two LDS stages of 128
 //     bytes of K (whole cache lines) filled by DMA, the next tile's first stages on
-//     their way while the results of the last are written.
+//     their way while the results of the last are written.  16384 tokens of the whole
+//     layer: gate and up 473 us (1743 TOP/s), down 357 (1155).  Bound by what fills the
+//     LDS: some 20 bytes a clock and CU arrive (64 lines in flight at 412 clocks each),
+//     1.75 us for the 64 KB of a step, which is 2450 TOP/s in the steady state; the
+//     products alone would take 1.15 us (3740 TOP/s on random operands).  The rest are the
+//     ends of the tiles, for the down product with its 6 steps a tile a third.
 // Weights are the first operand of the MFMA, so that a lane's results are
 // neighbouring columns of one row; which weight row takes which place in the
 // operand is chosen so that they are 16 or 32 in a run.
@@ -58,8 +65,21 @@ __device__ __forceinline__ int source_row(const ProductI8& p, int r) {
 constexpr int kFew = 64;      // rows of one pass over an expert's weights
 constexpr int kFewWaves = 4;  // of a workgroup
 
+// Waves that share K: where it is short, two, and twice the columns, so that a wave
+// has enough loads in flight (768: 64 tokens of the whole layer 51 -> 39 us).
+constexpr int split_of(int K) { return K > 1024 ? 4 : 2; }
+
+// The down product quantizes h itself up to this many rows for an expert on average
+// and this many columns: one launch less, but every workgroup of an expert quantizes
+// all of its rows.  The FFN, a launch more and so: 128 experts of 2048 x 768, 1/16 of
+// a row on average 19.4 and 17.7 us, 1: 67.6 and 66.4, 4: 93.7 and 98.1; 64 experts of
+// 2048 x 1536, 1/2 of a row 52.4 and 55.4.
+constexpr int kFusedRows = 1, kFusedCols = 1024;
+constexpr int kFusedSplit = split_of(kFusedCols);
+static_assert(kFusedCols <= kWave * rows_i8::kCols, "a chunk of a row for each lane");
+
 // Codes of up to 16 rows of p.h from r0 on, as moe_quantize_i8 makes them, a wave a
-// row.  Ends with a barrier.
+// row (of up to 64 * 16 columns).  Ends with a barrier.
 __device__ __forceinline__ void quantize_rows(const ProductI8& p, int r0, int hi, int8_t* codes, float* scales) {
   using namespace rows_i8;
   const int lane = lane_id(), per_row = p.K / kCols;
@@ -67,18 +87,15 @@ __device__ __forceinline__ void quantize_rows(const ProductI8& p, int r0, int hi
     const size_t base = (size_t)(r0 + r) * p.K;
     float v[kCols];
     uint32_t top = 0;
-    for (int c = lane; c < per_row; c += kWave) {
-      load16<true>(p.h, base + (size_t)c * kCols, v);
+    if (lane < per_row) {
+      load16<true>(p.h, base + (size_t)lane * kCols, v);
       top = top_bits(v, top);
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, kWave));
     const Scale s(top);
     if (lane == 0) scales[r] = s.scale;
-    for (int c = lane; c < per_row; c += kWave) {
-      if (per_row > kWave) load16<true>(p.h, base + (size_t)c * kCols, v);
-      *reinterpret_cast<u32x4_t*>(codes + r * p.K + c * kCols) = codes16(v, s.inv);
-    }
+    if (lane < per_row) *reinterpret_cast<u32x4_t*>(codes + r * p.K + lane * kCols) = codes16(v, s.inv);
   }
   __syncthreads();
 }
@@ -232,7 +249,6 @@ __global__ __launch_bounds__(256, 2) void skinny_i8_kernel(ProductI8 p) {
 // The product of bf16 rows, each workgroup quantizing those of its expert itself,
 // 16 at a time: for few rows one launch less, and the rows' reads lie under the
 // weights'.
-template <int SPLIT>
 __global__ __launch_bounds__(256, 2) void skinny_quantize_i8_kernel(ProductI8 p) {
   extern __shared__ __align__(16) char lds[];  // codes of 16 rows
   __shared__ i32x4_t red[4][2 * 4][kWave];
@@ -241,8 +257,8 @@ __global__ __launch_bounds__(256, 2) void skinny_quantize_i8_kernel(ProductI8 p)
   if (!nth_expert(p.offsets, p.E_l, (int)blockIdx.y, e, lo, hi)) return;
   for (int r0 = lo; r0 < hi; r0 += 16) {
     if (r0 > lo) __syncthreads();  // the last sums and codes have been read
-    skinny_rows<false, 1, SPLIT, true>(p, e, (int)blockIdx.x * (kFewWaves / SPLIT * few_cols<false>()), r0,
-                                       min(hi, r0 + 16), red, (int8_t*)lds, scales);
+    skinny_rows<false, 1, kFusedSplit, true>(p, e, (int)blockIdx.x * (kFewWaves / kFusedSplit * few_cols<false>()),
+                                             r0, min(hi, r0 + 16), red, (int8_t*)lds, scales);
   }
 }
 
@@ -253,7 +269,7 @@ __global__ __launch_bounds__(256, 2) void skinny_quantize_i8_kernel(ProductI8 p)
 constexpr int kTileM = 256;    // most rows of a tile
 constexpr int kTileW = 256;    // weight rows of a tile (128 of gate and 128 of up in the pair)
 constexpr int kTileWaves = 8;  // 2 along the rows, 4 along the weight rows
-constexpr int kStageK = 128;    // bytes of K a stage
+constexpr int kStageK = 128;   // bytes of K a stage
 constexpr int kStages = 2;
 constexpr int kStageBytes = (kTileM + kTileW) * kStageK;
 constexpr int kRowChunks = kStageK / 16;            // 16-byte chunks of an LDS row
@@ -286,16 +302,14 @@ __device__ __forceinline__ uint32_t lds_byte_addr(const void* p) {
 // Chunks of 16 bytes of an LDS row are stored at place c ^ swizzle(row), so that
 // neighbouring lanes of an operand read (rows in the order of the operand, one
 // chunk) touch different banks: 8 of them different places of 128 bytes, 16 of them
-// of 256.  For rows of 128 and of 64 bytes:
+// of 256.  For rows of 8 chunks, and of 4 (results on their way out):
 template <int CHUNKS>
 __device__ __forceinline__ int swizzle_row(int row) {
   return CHUNKS == 8 ? ((row >> 1) & 3) << 1 | ((row ^ (row >> 3)) & 1)
                      : ((row >> 2) & 1) << 1 | (((row >> 1) ^ (row >> 3)) & 1);
 }
 __device__ __forceinline__ int swizzle_w(int row) {
-  const int h = (row >> 4) & 1;
-  return kRowChunks == 8 ? ((row >> 1) & 1) << 2 | h << 1 | ((row ^ (row >> 2)) & 1)
-                         : h << 1 | (((row >> 1) ^ (row >> 2)) & 1);
+  return ((row >> 1) & 1) << 2 | ((row >> 4) & 1) << 1 | ((row ^ (row >> 2)) & 1);
 }
 
 // Where a tile lies.
@@ -623,8 +637,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
     int full = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) full += tiles_of(kTileM, i);
-    // row tiles of the full height: with fewer of them than two for a workgroup,
-    // tiles of half the height keep more CUs at work
+    // tiles of the full height: with fewer of them than two for a workgroup, tiles of
+    // half the height keep more CUs at work (FFN of 16 experts, 64 rows each: 53.6 -> 42.2
+    // us; with more tiles half of them are slower: 1024 rows for each of 128, 840 ->
+    // 1039 us)
     if (__builtin_amdgcn_readlane(wave_scan(full), 63) * cols < 2 * (int)gridDim.x) height = kTileM / 2;
     int mine = 0, n[4];
 #pragma unroll
@@ -734,13 +750,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
 }
 
 // Up to this many rows for an expert on average (of the capacity: the host does not
-// know more) go without the tiles.
-constexpr int kSkinnyRows = 16;
-constexpr int kFusedRows = 8, kFusedCols = 1536;
-
-// Waves that share K: where it is short, two, and twice the columns, so that a wave
-// has enough loads in flight (768: 64 tokens of the whole layer 51 -> 39 us).
-int split_of(int K) { return K > 1024 ? 4 : 2; }
+// know more) go without the tiles.  The FFN, without and with them: 128 experts of
+// 2048 x 768, 8 rows on average 115 and 130 us, 12: 129 and 133, 16: 141 and 134; 64
+// experts of 2048 x 2048, 8 rows 164 and 173, 16: 198 and 179.
+constexpr int kSkinnyRows = 12;
 
 template <bool GU>
 hipError_t launch_product(const ProductI8& p, int R_cap, int kernel_id, hipStream_t s) {
@@ -780,13 +793,11 @@ hipError_t launch_ffn_fwd_i8(const int8_t* x, const float* xs, const int32_t* sr
   hipError_t e = launch_product<true>(up, R_cap, MOE_KERNEL_FFN_GATEUP_I8, s);
   if (e != hipSuccess) return e;
   const ProductI8 down = {hq, hs, nullptr, R_cap, offsets, E_l, I, H, wd, nullptr, wds, nullptr, y, h};
-  // Few rows for an expert on average, short enough for their codes in LDS.
   if ((long)R_cap <= (long)kFusedRows * E_l && I <= kFusedCols) {
     ProfScope ps(MOE_KERNEL_FFN_DOWN_I8, s);
-    const int split = split_of(I), cols = kFewWaves / split * few_cols<false>();
+    const int cols = kFewWaves / kFusedSplit * few_cols<false>();
     const dim3 grid((H + cols - 1) / cols, std::min(E_l, R_cap));
-    if (split == 4) skinny_quantize_i8_kernel<4><<<grid, 256, 16 * I, s>>>(down);
-    else skinny_quantize_i8_kernel<2><<<grid, 256, 16 * I, s>>>(down);
+    skinny_quantize_i8_kernel<<<grid, 256, 16 * I, s>>>(down);
     return hipGetLastError();
   }
   e = launch_quantize_i8(h, R_cap, I, I, true, offsets + E_l, hq, hs, s);

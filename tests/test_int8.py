@@ -341,7 +341,10 @@ def test_rows_near_the_end_of_the_address_range():
 
 
 FFN = [([2, 0, 1], 64, 48), ([1] * 8, 2048, 768), ([5, 3, 40, 0, 64], 144, 80), ([70, 300, 10], 256, 208),
-       ([256, 257, 1, 0], 512, 128), ([64, 65], 16, 16), ([4] * 128, 256, 64)]
+       ([256, 257, 1, 0], 512, 128), ([64, 65], 16, 16), ([4] * 128, 256, 64),
+       # few rows, whose h the down product quantizes itself, in groups of up to 16 and above
+       ([1, 2, 0, 1] + [0] * 8, 2048, 768), ([0] * 40 + [37] + [1] * 20, 272, 1024), ([0] * 9 + [5], 64, 16),
+       ([1] * 8 + [0] * 8, 64, 1040)]
 
 
 @gpu
