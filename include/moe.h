@@ -43,6 +43,8 @@
  *     ranges: R_cap * max(H, 2I) * elem, 2 * I * H * elem (one expert's gate
  *     and up weights) and, for the bf16 router weight gradient, T * H * 2
  *     must each stay below 2^31 bytes (else MOE_EUNSUPPORTED).
+ *   - The operators around the layer and the int8 products have limits of their
+ *     own, stated with each of them.
  */
 #ifndef MOE_H
 #define MOE_H
@@ -631,8 +633,8 @@ int moe_norm(const void* x, const void* delta, const float* weight, double eps, 
  *   ws  moe_norm_ws_bytes(H) bytes.  T = 0 writes (or keeps) dweight only. */
 int64_t moe_norm_ws_bytes(int H);
 int moe_norm_bwd(const void* dn, const void* dr, double dr_scale, const void* r,
-                 const float* weight, double eps, int T, int H, int dtype, void* dx, float* dweight, int accumulate, void* ws,
-                 size_t ws_bytes, void* stream);
+                 const float* weight, double eps, int T, int H, int dtype, void* dx,
+                 float* dweight, int accumulate, void* ws, size_t ws_bytes, void* stream);
 
 /* The weighted combine with the RMS norm after the layer, a gate and the scaled
  * residual, for every token:

@@ -15,9 +15,12 @@ moe_quantize_fp8_w; weight gradients:
 moe_quantize_fp8_group_t, moe_grouped_ffn_wgrad_fp8, and its two halves
 moe_grouped_ffn_wgrad_fp8_begin / _end; around the layer: the router's
 auxiliary losses moe_balance_loss / _bwd with moe_route_bwd_add, and the combine
-with dropout moe_combine_dropout / _bwd, and low-rank adapters moe_adapter_fwd /
-_bwd with moe_adapter_rows and moe_grouped_ffn_fwd_adapter) and return
-freshly allocated torch tensors; each also accepts preallocated outputs via
+with dropout moe_combine_dropout / _bwd, low-rank adapters moe_adapter_fwd /
+_bwd with moe_adapter_rows and moe_grouped_ffn_fwd_adapter, the norms before and
+after the layer moe_norm / _bwd and moe_combine_norm / _bwd; and on 8-bit
+integers: moe_quantize_i8, moe_dequantize_i8, activation checkpoints with
+moe_swiglu_restore_i8, the products moe_grouped_gemm_i8 and
+moe_grouped_ffn_fwd_i8) and return freshly allocated torch tensors; each also accepts preallocated outputs via
 ``out=`` dictionaries so that steady-state loops allocate nothing.
 """
 from __future__ import annotations

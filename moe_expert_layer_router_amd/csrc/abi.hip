@@ -1327,8 +1327,8 @@ int64_t moe_norm_ws_bytes(int H) {
 }
 
 int moe_norm_bwd(const void* dn, const void* dr, double dr_scale, const void* r,
-                 const float* weight, double eps, int T, int H, int dtype, void* dx, float* dweight, int accumulate, void* ws,
-                 size_t ws_bytes, void* stream) {
+                 const float* weight, double eps, int T, int H, int dtype, void* dx, float* dweight,
+                 int accumulate, void* ws, size_t ws_bytes, void* stream) {
   const char* fn = "moe_norm_bwd";
   if (int rc = check_norm(T, H, dtype, eps, weight, fn)) return rc;
   if (int rc = check_accumulate(accumulate, fn)) return rc;
@@ -1340,8 +1340,9 @@ int moe_norm_bwd(const void* dn, const void* dr, double dr_scale, const void* r,
   }
   if (int rc = check_ptr(dweight, "dweight", fn)) return rc;
   if (int rc = check_ws(ws, ws_bytes, norm_ws_bytes(H), fn)) return rc;
-  return hip_status(launch_norm_bwd(dn, dr, dr != nullptr ? (float)dr_scale : 0.f, r, weight, (float)eps, T, H, dtype == MOE_BF16,
-                                    dx, dweight, accumulate != 0, ws, begin_launch(stream)),
+  return hip_status(launch_norm_bwd(dn, dr, dr != nullptr ? (float)dr_scale : 0.f, r, weight, (float)eps,
+                                    T, H, dtype == MOE_BF16, dx, dweight, accumulate != 0, ws,
+                                    begin_launch(stream)),
                     fn);
 }
 

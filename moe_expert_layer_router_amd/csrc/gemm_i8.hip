@@ -10,18 +10,18 @@
 //     owns 32 columns of one expert (64 where K is short); its waves split K and
 //     take the weights straight from memory into MFMA operands, each byte once for
 //     up to 64 rows, and add their sums through LDS.  64 tokens of the whole layer
-//     (128 experts of 2048 x 768, top-8): gate and up 58 us, down 39, 598 MB together
-//     at 6.2 TB/s.
+//     (128 experts of 2048 x 768, top-8): gate and up 56 us, down 32, 598 MB together
+//     at 6.8 TB/s.
 //   many rows (tile_i8_kernel): bound by the matrix cores and what feeds them.
 //     Tiles of 256 rows x 256 weight rows in a workgroup of eight waves that stays
 //     on its CU and takes tile after tile; operands through two LDS stages of 128
 //     bytes of K (whole cache lines) filled by DMA, the next tile's first stages on
 //     their way while the results of the last are written.  16384 tokens of the whole
-//     layer: gate and up 473 us (1743 TOP/s), down 357 (1155).  Bound by what fills the
+//     layer: gate and up 417 us (1975 TOP/s), down 324 (1274).  Bound by what fills the
 //     LDS: some 20 bytes a clock and CU arrive (64 lines in flight at 412 clocks each),
-//     1.75 us for the 64 KB of a step, which is 2450 TOP/s in the steady state; the
-//     products alone would take 1.15 us (3740 TOP/s on random operands).  The rest are the
-//     ends of the tiles, for the down product with its 6 steps a tile a third.
+//     1.5 to 1.75 us for the 64 KB of a step, 2450 TOP/s and more in the steady state;
+//     the products alone would take 1.15 us (3740 TOP/s on random operands).  The rest
+//     are the ends of the tiles, for the down product with its 6 steps a tile a third.
 // Weights are the first operand of the MFMA, so that a lane's results are
 // neighbouring columns of one row; which weight row takes which place in the
 // operand is chosen so that they are 16 or 32 in a run.
