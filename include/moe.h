@@ -641,8 +641,9 @@ int moe_norm_bwd(const void* dn, const void* dr, double dr_scale, const void* r,
  *   c    = sum_{j: dest_row[t*k+j] >= 0} topk_w[t,j] * y_perm[dest_row[t*k+j]]
  *   y[t] = residual_scale * residual[t] + gate[t] * (c / sqrt(mean_h c^2 + eps)) * weight
  * in fp32, rounded once.  A token without a local slot gets residual_scale *
- * residual[t].  (The norm is of the whole combined row: with experts on several
- * ranks the parts have to be added up first.)
+ * residual[t].  A token's bits do not depend on T or on the other tokens.  (The norm
+ * is of the whole combined row: with experts on several ranks the parts have to be
+ * added up first.)
  *   gate: MOE_GATE_NONE NULL (1); MOE_GATE_TOKEN [T] fp32; MOE_GATE_FULL [T,H] dtype
  *   residual [T,H] dtype or NULL (0); y may be residual; weight [H] fp32
  *   other arguments as moe_combine.  Limits as moe_norm. */

@@ -52,6 +52,35 @@ __device__ __forceinline__ void team_sum(float (&v)[M], float* lds) {
   }
 }
 
+// The sum of a row from each lane's sums v of its chunks: over 64 neighbouring chunks
+// first, then four of those, then the rest, each in the row's order, so that its bits do
+// not depend on how many waves hold the row.  lds [waves][NC].
+template <int W, int NC>
+__device__ __forceinline__ float row_sum(float (&v)[NC], float* lds) {
+  constexpr int kAll = W * NC;
+  float all[kAll], sum = 0.f;
+#pragma unroll
+  for (int u = 0; u < NC; ++u) v[u] = wave_sum(v[u]);
+  if constexpr (W > 1) {
+    const int wave = threadIdx.x >> 6;
+    if (lane_id() == 0) {
+#pragma unroll
+      for (int u = 0; u < NC; ++u) lds[wave * NC + u] = v[u];
+    }
+    lds_barrier();
+  }
+#pragma unroll
+  for (int i = 0; i < kAll; ++i) all[i] = W > 1 ? lds[(threadIdx.x >> 6) / W * kAll + i] : v[i % NC];
+#pragma unroll
+  for (int i = 0; i < kAll; i += 4) {
+    float four = all[i];
+#pragma unroll
+    for (int q = i + 1; q < i + 4 && q < kAll; ++q) four += all[q];
+    sum += four;
+  }
+  return sum;
+}
+
 constexpr int threads_of(int W) { return W > 4 ? W * kWave : 256; }
 
 // Where a lane's chunks lie: chunk(u) = first + 64 u of the row's nch.
@@ -277,7 +306,7 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_kernel(
     const void* __restrict__ gate, int gate_kind, const float* __restrict__ weight, float eps, int T,
     int H, int k, void* y) {
   using R = Row<BF16>;
-  __shared__ float lds[threads_of(W) / kWave];
+  __shared__ float lds[threads_of(W) / kWave * NC];
   const Place<W, NC> at;
   const int t = blockIdx.x * at.kTeams + at.team;
   if (W == 1 && t >= T) return;
@@ -298,14 +327,16 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_kernel(
   constexpr int kAtOnce = NC == 1 ? 8 : NC == 2 ? 4 : 2;  // slots whose rows are in flight
   gather_rows<BF16, true, NC, kAtOnce>(y_perm, H, nch, at.first - lane_id(), slot.n, slot.dc, slot.wc,
                                        acc);
-  float ss[1] = {0.f};
+  float ss[NC];
 #pragma unroll
-  for (int u = 0; u < NC; ++u)
+  for (int u = 0; u < NC; ++u) {
+    ss[u] = 0.f;
 #pragma unroll
-    for (int i = 0; i < R::N; ++i) ss[0] = fmaf(acc[u][i], acc[u][i], ss[0]);
-  team_sum<W>(ss, lds);
+    for (int i = 0; i < R::N; ++i) ss[u] = fmaf(acc[u][i], acc[u][i], ss[u]);
+  }
+  const float sum = row_sum<W>(ss, lds);
   if (t >= T) return;
-  const float s = 1.f / sqrtf(ss[0] / (float)H + eps);
+  const float s = 1.f / sqrtf(sum / (float)H + eps);
   const float g1 = gate_kind == kGateToken ? ((const float*)gate)[t] : 1.f;
 #pragma unroll
   for (int u = 0; u < NC; ++u) {
@@ -471,7 +502,7 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
 // Up to this many tokens a token's slots are loaded at once by a team with one
 // chunk a lane: fewer round trips, which is what few tokens wait for (columns of 2048,
 // top-8, 512 tokens 8.8 -> 6.7 us, 1024: 10.9 -> 9.2, 2048: no difference; 4096 tokens
-// with one local slot lose by it, 11.9 -> 13.0).
+// with one local slot lose by it, 11.9 -> 13.0).  A token's bits are the same in both.
 constexpr int kFewTokens = 4 * kCUs;
 
 // Partial rows of the weight's gradient: workgroups of the backward (16384 tokens of

@@ -431,3 +431,20 @@ def test_binding_refusals():
             moe.moe_combine_norm_bwd(**{**ok, n: v})
     with pytest.raises(moe.MoEError, match="eps"):
         moe.moe_norm(x, w, eps=0.0)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [64, 520, 1024, 2048, 3000, 4096, 8192, 9000])
+def test_a_token_has_the_same_bits_among_few_and_many(H, dtype):
+    dt, T, k, few = TYPES[dtype], 1100, 3, 37
+    g = torch.Generator(device=DEV).manual_seed(H)
+    yp = torch.randn((T * k, H), generator=g, device=DEV).to(dt)
+    tw = torch.rand((T, k), generator=g, device=DEV)
+    dest = torch.randperm(T * k, generator=g, device=DEV).to(torch.int32)
+    dest[1::7] = -1
+    w = torch.rand(H, generator=g, device=DEV) + 0.5
+    y = moe.moe_combine_norm(yp, tw, dest, T, w)
+    for t0 in (0, T - few):
+        part = moe.moe_combine_norm(yp, tw[t0:t0 + few], dest[t0 * k:(t0 + few) * k].contiguous(), few, w)
+        assert torch.equal(y[t0:t0 + few], part)
