@@ -5,7 +5,7 @@
 // int32, so every variant and every split of K gives the same bits; the two
 // scales are applied in fp32 and the result is rounded once.
 //
-// Two kernels, chosen by the rows for an expert on average:
+// Two kernels, chosen by the rows for an expert on average and by the size of the whole:
 //   few rows (skinny_i8_kernel): bound by the read of the weights.  A workgroup
 //     owns 32 columns of one expert (64 where K is short); its waves split K and
 //     take the weights straight from memory into MFMA operands, each byte once for
@@ -237,8 +237,9 @@ __global__ __launch_bounds__(256, 2) void skinny_i8_kernel(ProductI8 p) {
   int e, lo, hi;
   if (!nth_expert(p.offsets, p.E_l, (int)blockIdx.y, e, lo, hi)) return;
   const int n0 = (int)blockIdx.x * (kFewWaves / SPLIT * few_cols<GU>());
-  for (int r0 = lo; r0 < hi; r0 += kFew) {
-    if (r0 > lo) __syncthreads();  // the last sums have been read
+  const int from = lo + (int)blockIdx.z * kFew, by = (int)gridDim.z * kFew;
+  for (int r0 = from; r0 < hi; r0 += by) {
+    if (r0 > from) __syncthreads();  // the last sums have been read
     const int left = hi - r0;
     if (left <= 16) skinny_rows<GU, 1, SPLIT>(p, e, n0, r0, hi, red);
     else if (left <= 32) skinny_rows<GU, 2, SPLIT>(p, e, n0, r0, hi, red);
@@ -755,12 +756,25 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_i8_kernel(ProductI8 p
 // experts of 2048 x 2048, 8 rows 164 and 173, 16: 198 and 179.
 constexpr int kSkinnyRows = 12;
 
+// Small products go without the tiles too, which would leave most CUs idle, with several
+// workgroups for the rows of an expert, 64 at a time.  What then counts are the rows of
+// K that the workgroups read: each weight row once for every block of rows, each row once
+// for every 32 weight rows (as many as there may be: the host knows the capacity).  Products with and without tiles: 777
+// rows of 5 experts, 1040 x 528 (23 thousand) 12.8 and 6.4 us; 2000 of 8, 1024 x 512 (53)
+// 11.9 and 9.1; 512 of one, 2048 x 2048 (52) 16.7 and 13.9; 700 of one (68) 16.8 and
+// 19.2; 777 of 5 (87) 17.3 and 23.1.
+constexpr long kSkinnyReads = 60000;
+constexpr int kFewBlocks = 1024;  // (expert, block) pairs of a launch, as far as experts allow
+
 template <bool GU>
 hipError_t launch_product(const ProductI8& p, int R_cap, int kernel_id, hipStream_t s) {
   ProfScope ps(kernel_id, s);
-  if ((long)R_cap <= (long)kSkinnyRows * p.E_l) {
+  const long experts = std::min(p.E_l, R_cap), wrows = (long)p.N * (GU ? 2 : 1);
+  const bool few = R_cap <= kSkinnyRows * experts;
+  if (few || wrows * (experts + R_cap / kFew + (R_cap + 8 * experts) / 32) <= kSkinnyReads) {
     const int split = split_of(p.K), cols = kFewWaves / split * few_cols<GU>();
-    const dim3 grid((p.N + cols - 1) / cols, std::min(p.E_l, R_cap));
+    const int blocks = few ? 1 : std::min((R_cap + kFew - 1) / kFew, kFewBlocks / (int)experts);
+    const dim3 grid((p.N + cols - 1) / cols, (int)experts, blocks);
     if (split == 4) skinny_i8_kernel<GU, 4><<<grid, 256, 0, s>>>(p);
     else skinny_i8_kernel<GU, 2><<<grid, 256, 0, s>>>(p);
   } else {

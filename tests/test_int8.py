@@ -250,7 +250,13 @@ def to_gpu(*a):
 PRODUCTS = [([1], 16, 16), ([1], 2048, 48), ([16], 64, 32), ([17], 48, 80), ([3, 0, 5, 1], 1040, 528), ([0, 0, 33], 80, 16),
             ([64], 128, 128), ([65], 128, 128), ([70, 1, 0, 300], 64, 144), ([256], 192, 128), ([257], 208, 112),
             ([300, 64, 65, 512, 0, 2], 272, 400), ([1] * 256, 32, 32), ([129, 128, 160, 190], 1024, 256),
-            ([1000], 768, 2048), ([33] * 16, 512, 272), ([40, 200], 65536, 16), ([600] + [3] * 100, 96, 64)]
+            ([1000], 768, 2048), ([33] * 16, 512, 272), ([40, 200], 65536, 16), ([600] + [3] * 100, 96, 64),
+            # blocks of an expert's rows in several workgroups, more of them than those too
+            ([5000], 64, 32), ([300] + [13] * 255, 32, 16), ([0, 64, 0, 65, 128, 1, 129], 2064, 48),
+            # large enough for the tiles
+            ([256], 192, 4624), ([257], 208, 4624), ([70, 1, 0, 300], 64, 2896), ([300, 64, 65, 512, 0, 2], 272, 2064),
+            ([129, 128, 160, 190], 1024, 2064), ([1] * 8 + [400], 1040, 2064), ([33] * 16, 512, 1552),
+            ([600] + [3] * 40, 96, 1040), ([1024], 65536, 1280), ([2000] + [0] * 90 + [1], 16, 1040)]
 
 
 @gpu
@@ -274,7 +280,7 @@ def test_products(sizes, K, N):
 
 
 @gpu
-@pytest.mark.parametrize("E,rows", [(3, 5), (1, 400), (256, 4200)])
+@pytest.mark.parametrize("E,rows", [(3, 5), (1, 400), (256, 4200), (64, 30000)])
 def test_no_rows_at_all(E, rows):
     """Every group empty, in both kernels and in the FFN: nothing is written."""
     K, N = 64, 48
@@ -306,11 +312,12 @@ def test_a_row_that_is_no_number_stays_alone():
 
 
 @gpu
-def test_the_split_into_groups_changes_no_bit():
-    """1030 rows as one group (tiles), as groups of 1 to 64 rows beside large ones (both kernels), and as
-    groups that go without tiles."""
+@pytest.mark.parametrize("N", [208, 1296])
+def test_the_split_into_groups_changes_no_bit(N):
+    """1030 rows as one group, as groups of 1 to 64 rows beside large ones (tiles for the wider product),
+    and as groups that go without tiles."""
     rng = np.random.default_rng(5)
-    K, N, R = 336, 208, 1030
+    K, R = 336, 1030
     x, xs, src, _, w, ws = product_case(rng, [R], K, N)
     got = []
     for sizes in ([R], [64, 1, 300, 17, 0, 600, 48], [10] * 103, [R] + [0] * 99):
@@ -323,9 +330,10 @@ def test_the_split_into_groups_changes_no_bit():
 
 
 @gpu
-def test_rows_near_the_end_of_the_address_range():
+@pytest.mark.parametrize("N", [128, 2944])
+def test_rows_near_the_end_of_the_address_range(N):
     """2^31 - 2048 bytes of token rows: the last rows through the map, in both kernels."""
-    K, N, x_rows = 2048, 128, (1 << 20) - 1
+    K, x_rows = 2048, (1 << 20) - 1
     g = torch.Generator(device=DEV).manual_seed(0)
     x = torch.randint(-127, 128, (x_rows, K), generator=g, device=DEV, dtype=torch.int8)
     xs = torch.rand(x_rows, generator=g, device=DEV) + 0.5
@@ -341,7 +349,7 @@ def test_rows_near_the_end_of_the_address_range():
 
 
 FFN = [([2, 0, 1], 64, 48), ([1] * 8, 2048, 768), ([5, 3, 40, 0, 64], 144, 80), ([70, 300, 10], 256, 208),
-       ([256, 257, 1, 0], 512, 128), ([64, 65], 16, 16), ([4] * 128, 256, 64),
+       ([256, 257, 1, 0], 512, 128), ([64, 65], 16, 16), ([4] * 128, 256, 64), ([256, 257, 1, 0], 2080, 1040),
        # few rows, whose h the down product quantizes itself, in groups of up to 16 and above
        ([1, 2, 0, 1] + [0] * 8, 2048, 768), ([0] * 40 + [37] + [1] * 20, 272, 1024), ([0] * 9 + [5], 64, 16),
        ([1] * 8 + [0] * 8, 64, 1040)]
