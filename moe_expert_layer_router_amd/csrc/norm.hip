@@ -26,30 +26,70 @@ namespace moe {
 
 namespace {
 
+// Sums of M values (a power of two) over a wave's lanes: lane l gets that of value
+// l M / 64.  Halves of the lanes take halves of the values first, so that M values cost
+// M - 1 + log2(64 / M) exchanges in place of 6 M.
+template <int M>
+__device__ __forceinline__ float wave_sums(float (&v)[M]) {
+  const int lane = lane_id();
+  int o = kWave / 2;
+#pragma unroll
+  for (int m = M / 2; m > 0; m /= 2, o /= 2) {
+    const bool high = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float keep = high ? v[i + m] : v[i], give = high ? v[i] : v[i + m];
+      v[i] = keep + __shfl_xor(give, o, kWave);
+    }
+  }
+  float sum = v[0];
+#pragma unroll
+  for (; o > 0; o /= 2) sum += __shfl_xor(sum, o, kWave);
+  return sum;
+}
+
 // Sums of M values over the W waves of a team, in a fixed order; every lane gets
 // them.  A workgroup with teams of several waves calls it from all its threads.
 // The waves' sums meet in lds [W waves of each team][M]; the caller keeps two
 // calls on the same lds apart by a barrier (a call on another lds has one).
 template <int W, int M>
 __device__ __forceinline__ void team_sum(float (&v)[M], float* lds) {
-#pragma unroll
-  for (int i = 0; i < M; ++i) v[i] = wave_sum(v[i]);
+  constexpr int kLanes = kWave / M;  // with the same sum
+  const float mine = wave_sums(v);
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
   if constexpr (W > 1) {
-    const int wave = threadIdx.x >> 6;
-    if (lane_id() == 0) {
-#pragma unroll
-      for (int i = 0; i < M; ++i) lds[wave * M + i] = v[i];
-    }
+    if (lane % kLanes == 0) lds[wave * M + lane / kLanes] = mine;
     lds_barrier();
-    const float* team = lds + (wave / W) * W * M;
+  }
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      float sum = 0.f;
+  for (int i = 0; i < M; ++i) {
+    v[i] = W > 1 ? 0.f : __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), i * kLanes));
+    if constexpr (W > 1) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) sum += team[w * M + i];
-      v[i] = sum;
+      for (int w = 0; w < W; ++w) v[i] += lds[(wave / W * W + w) * M + i];
     }
   }
+}
+
+// The same where one thread wants each sum: returns that of value `which` in the lanes
+// where `has` is set.
+template <int W, int M>
+__device__ __forceinline__ float team_sum_apart(float (&v)[M], float* lds, int& which, bool& has) {
+  constexpr int kLanes = kWave / M;
+  float sum = wave_sums(v);
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  which = lane / kLanes;
+  has = lane % kLanes == 0;
+  if constexpr (W > 1) {
+    if (has) lds[wave * M + which] = sum;
+    lds_barrier();
+    which = lane % M;
+    has = threadIdx.x % (W * kWave) < M;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += lds[(wave / W * W + w) * M + which];
+  }
+  return sum;
 }
 
 // The sum of a row from each lane's sums v of its chunks: over 64 neighbouring chunks
@@ -115,6 +155,16 @@ __global__ __launch_bounds__(threads_of(W)) void norm_kernel(
     raw[u] = live && c < nch ? R::ld_s(x, e) : u32x4_t{};
     add[u] = live && c < nch && delta != nullptr ? R::ld_s(delta, e) : u32x4_t{};
   }
+  // One wave a row fetches the weights beside the row (16384 x 2048 48.5 -> 47.1 us);
+  // with several the registers cost more than the wait (8192 fp32 x 2048 42.8 -> 44.0).
+  constexpr bool kAhead = W == 1;
+  float wt[kAhead ? NC : 1][R::N];
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int u = 0; u < NC; ++u)
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) wt[u][i] = weight[min(at.first + u * kWave, nch - 1) * R::N + i];
+  }
   float ss[1] = {0.f};
 #pragma unroll
   for (int u = 0; u < NC; ++u) {
@@ -140,7 +190,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_kernel(
     if (delta != nullptr) R::st_s(r, e, raw[u]);
     float o[R::N];
 #pragma unroll
-    for (int i = 0; i < R::N; ++i) o[i] = v[u][i] * s * weight[c * R::N + i];
+    for (int i = 0; i < R::N; ++i) o[i] = v[u][i] * s * (kAhead ? wt[kAhead ? u : 0][i] : weight[c * R::N + i]);
     R::st(n, e, R::from_f32(o));  // read next by the router and the products
   }
 }
@@ -297,6 +347,7 @@ struct Slots {
     }
     n = pack_slots(d, w, dc, wc, jc);
   }
+  __device__ Slots(int d, float w) { n = pack_slots(d, w, dc, wc, jc); }  // of this lane's slot
 };
 
 template <bool BF16, int W, int NC>
@@ -354,13 +405,11 @@ __global__ __launch_bounds__(threads_of(W)) void combine_norm_kernel(
   }
 }
 
-// Slots whose rows a lane holds at once; where they are all of a token's, they
-// stay in registers between c and its gradient.
-constexpr int held(int W, int NC) { return NC > 1 ? 2 : W > 8 ? 4 : 8; }
-
 // Four waves a SIMD: with registers as the compiler likes two, and 16384 tokens of
 // 2048, top-8, take 271 us for 239.
-template <bool BF16, int W, int NC>
+// HELD slots' rows are in a lane's registers at once; where they are all of a token's,
+// they stay there between c and its gradient.
+template <bool BF16, int W, int NC, int HELD>
 __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
     const void* __restrict__ dy, const void* __restrict__ y_perm, const float* __restrict__ topk_w,
     const int32_t* __restrict__ dest_row, const void* __restrict__ gate, int gate_kind,
@@ -368,8 +417,7 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
     float* __restrict__ d_topk_w, void* __restrict__ dgate, float* __restrict__ part,
     float* __restrict__ dweight, int accumulate) {
   using R = Row<BF16>;
-  constexpr int kHeld = held(W, NC);
-  __shared__ float lds[2 * threads_of(W) / kWave], dots[kHeld * threads_of(W) / kWave];
+  __shared__ float lds[2 * threads_of(W) / kWave], dots[HELD * threads_of(W) / kWave];
   __shared__ __align__(16) float sums[partial_lds<BF16, W, NC>()];
   const Place<W, NC> at;
   const int nch = H / R::N;
@@ -378,15 +426,28 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
   for (int u = 0; u < NC; ++u)
 #pragma unroll
     for (int i = 0; i < R::N; ++i) dw[u][i] = 0.f;
+  // A token's slots are fetched one token ahead where few rows are held and the wait
+  // shows (16384 tokens of 1024, one slot: 38 -> 33 us; with eight held the registers
+  // are missing elsewhere, 244 -> 250 for 2048 columns).
+  constexpr bool kAhead = HELD <= (BF16 ? 2 : 4);
+  int d0 = -1;
+  float w0 = 0.f;
+  const auto fetch = [&](int t) {
+    const size_t i = (size_t)min(t, T - 1) * k + min(lane_id(), k - 1);
+    w0 = topk_w[i];
+    d0 = t < T && lane_id() < k ? dest_row[i] : -1;
+  };
+  if (kAhead) fetch(blockIdx.x * at.kTeams + at.team);
   for (int t0 = blockIdx.x * at.kTeams; t0 < T; t0 += gridDim.x * at.kTeams) {
     const int t = t0 + at.team;
-    const Slots slot(dest_row, topk_w, t, T, k);
-    if (t < T && threadIdx.x % (W * kWave) < k && dest_row[(size_t)t * k + lane_id()] < 0)
-      d_topk_w[(size_t)t * k + lane_id()] = 0.f;
+    if (!kAhead) fetch(t);
+    const Slots slot(d0, w0);
+    if (t < T && threadIdx.x % (W * kWave) < k && d0 < 0) d_topk_w[(size_t)t * k + lane_id()] = 0.f;
+    if (kAhead) fetch(t + gridDim.x * at.kTeams);
     // the most slots of the workgroup's tokens: the teams take part in each other's barriers
     int most = slot.n;
     if constexpr (W > 1 && Place<W, NC>::kTeams > 1) most = k;
-    u32x4_t raw[kHeld][NC], dyr[NC], gt[NC];
+    u32x4_t raw[HELD][NC], dyr[NC], gt[NC];
     float c_[NC][R::N];
 #pragma unroll
     for (int u = 0; u < NC; ++u) {
@@ -401,7 +462,7 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
     const float g1 = t < T && gate_kind == kGateToken ? ((const float*)gate)[t] : 1.f;
     const auto load = [&](int j0) {
 #pragma unroll
-      for (int q = 0; q < kHeld; ++q) {
+      for (int q = 0; q < HELD; ++q) {
         const int d = __shfl(slot.dc, j0 + q, kWave);
 #pragma unroll
         for (int u = 0; u < NC; ++u) {
@@ -411,10 +472,10 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
         }
       }
     };
-    for (int j0 = 0; j0 < slot.n; j0 += kHeld) {
+    for (int j0 = 0; j0 < slot.n; j0 += HELD) {
       load(j0);
 #pragma unroll
-      for (int q = 0; q < kHeld; ++q) {
+      for (int q = 0; q < HELD; ++q) {
         const float w = j0 + q < slot.n ? __shfl(slot.wc, j0 + q, kWave) : 0.f;
 #pragma unroll
         for (int u = 0; u < NC; ++u) {
@@ -465,11 +526,11 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
       if (gate_kind == kGateFull && t < T && c < nch)
         R::st_s(dgate, (size_t)t * H + (size_t)c * R::N, R::from_f32(o));
     }
-    for (int j0 = 0; j0 < most; j0 += kHeld) {
-      if (slot.n > kHeld) load(j0);  // (up to kHeld rows are still in registers)
-      float dot[kHeld];
+    for (int j0 = 0; j0 < most; j0 += HELD) {
+      if (slot.n > HELD) load(j0);  // (up to HELD rows are still in registers)
+      float dot[HELD];
 #pragma unroll
-      for (int q = 0; q < kHeld; ++q) {
+      for (int q = 0; q < HELD; ++q) {
         const int d = __shfl(slot.dc, j0 + q, kWave);
         const float w = __shfl(slot.wc, j0 + q, kWave);
         dot[q] = 0.f;
@@ -487,12 +548,11 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
         }
       }
       if (W > 1 && j0 > 0) lds_barrier();  // the last group's sums have been read
-      team_sum<W>(dot, dots);
-#pragma unroll
-      for (int q = 0; q < kHeld; ++q) {
-        const int j = __shfl(slot.jc, j0 + q, kWave);
-        if (threadIdx.x % (W * kWave) == 0 && j0 + q < slot.n) d_topk_w[(size_t)t * k + j] = dot[q];
-      }
+      int q;
+      bool has;
+      const float sum = team_sum_apart<W>(dot, dots, q, has);
+      const int j = __shfl(slot.jc, j0 + q, kWave);
+      if (has && j0 + q < slot.n) d_topk_w[(size_t)t * k + j] = sum;
     }
     if (W > 1 && most == 0) lds_barrier();  // lds is read before the next token's sums (no slots: no other barrier)
   }
@@ -505,14 +565,16 @@ __global__ __launch_bounds__(threads_of(W), 4) void combine_norm_bwd_kernel(
 // with one local slot lose by it, 11.9 -> 13.0).  A token's bits are the same in both.
 constexpr int kFewTokens = 4 * kCUs;
 
-// Partial rows of the weight's gradient: workgroups of the backward (16384 tokens of
-// 4096: 97 us, as with 512 of them; 106 with 768, 120 with 256).
-constexpr int kNormParts = 1024;
+// Partial rows of the weight's gradient, workgroups of the backward at the most: fewer
+// for wide rows, which else move more bytes of them than of the rows themselves
+// (2048 rows of 8192: 56 us with 1024, 39 with 512, 38 with 256), and one a CU at the
+// least (16384 of 4096: 97 us with 1024 or 512, 120 with 256).
+int parts_of(int H) { return std::max(kCUs, std::min(1024, (1 << 21) / H)); }
 
 template <int W>
-int bwd_blocks(int T) {
+int bwd_blocks(int T, int H) {
   const int teams = threads_of(W) / (W * kWave);
-  return std::min((T + teams - 1) / teams, kNormParts);
+  return std::min((T + teams - 1) / teams, parts_of(H));
 }
 
 }  // namespace
@@ -520,14 +582,16 @@ int bwd_blocks(int T) {
 // Teams of one wave up to 256 chunks of 16 bytes: no barrier in a row.
 #define MOE_NORM_SHAPES(B, M) \
   if (nch <= 64) M(B, 1, 1) else if (nch <= 128) M(B, 1, 2) else if (nch <= 256) M(B, 1, 4) \
-  else if (nch <= 512) M(B, 4, 2) else if (nch <= 1024) M(B, 4, 4) else M(B, 16, 4)
+  else if (nch <= 512) M(B, 4, 2) else if (nch <= 1024) M(B, 4, 4) else if (nch <= 2048) M(B, 16, 2) \
+  else if constexpr (!B) M(B, 16, 4)
 // One chunk a lane, so that eight slots' rows and the sums fit the registers (the
 // backward then reads each grouped row once).
 #define MOE_NORM_SHAPES1(B, M) \
   if (nch <= 64) M(B, 1, 1) else if (nch <= 128) M(B, 2, 1) else if (nch <= 256) M(B, 4, 1) \
-  else if (nch <= 512) M(B, 8, 1) else if (nch <= 1024) M(B, 16, 1) else M(B, 16, 4)
+  else if (nch <= 512) M(B, 8, 1) else if (nch <= 1024) M(B, 16, 1) else if (nch <= 2048) M(B, 16, 2) \
+  else if constexpr (!B) M(B, 16, 4)
 
-size_t norm_ws_bytes(int H) { return ((size_t)kNormParts * H * sizeof(float) + 255) & ~(size_t)255; }
+size_t norm_ws_bytes(int H) { return ((size_t)parts_of(H) * H * sizeof(float) + 255) & ~(size_t)255; }
 
 hipError_t launch_norm(const void* x, const void* delta, const float* weight, float eps, int T, int H,
                        bool bf16, void* r, void* n, hipStream_t s) {
@@ -552,7 +616,7 @@ hipError_t launch_norm_bwd(const void* dn, const void* dr, float dr_scale, const
   int blocks = 0;
 #define MOE_LAUNCH(B, W, NC)                                                                        \
   {                                                                                                 \
-    blocks = bwd_blocks<W>(T);                                                                      \
+    blocks = bwd_blocks<W>(T, H);                                                                      \
     if (blocks > 0)                                                                                 \
       norm_bwd_kernel<B, W, NC><<<blocks, threads_of(W), 0, s>>>(dn, dr, dr_scale, r, weight, eps,   \
                                                                  T, H, dx, (float*)ws, dweight,     \
@@ -596,16 +660,26 @@ hipError_t launch_combine_norm_bwd(const void* dy, const void* y_perm, const flo
   ProfScope ps(MOE_KERNEL_COMBINE_NORM_BWD, s);
   const int nch = H / (bf16 ? 8 : 4);
   int blocks = 0;
-#define MOE_LAUNCH(B, W, NC)                                                                         \
-  {                                                                                                  \
-    blocks = bwd_blocks<W>(T);                                                                       \
-    if (blocks > 0)                                                                                  \
-      combine_norm_bwd_kernel<B, W, NC><<<blocks, threads_of(W), 0, s>>>(                            \
-          dy, y_perm, topk_w, dest_row, gate, gate_kind, weight, eps, T, H, k, dy_perm, d_topk_w,    \
-          dgate, (float*)ws, dweight, accumulate);                                                   \
+  // As many slots in registers as a token has, up to what fits beside the rest (8 held
+  // for 2: 16384 tokens of 2048 132 us, 81 with 2; of 4096 x 4096, top-2, 79 and 45).
+#define MOE_LAUNCH_HELD(B, W, NC, HELD)                                                              \
+  combine_norm_bwd_kernel<B, W, NC, HELD><<<blocks, threads_of(W), 0, s>>>(                          \
+      dy, y_perm, topk_w, dest_row, gate, gate_kind, weight, eps, T, H, k, dy_perm, d_topk_w, dgate, \
+      (float*)ws, dweight, accumulate)
+#define MOE_LAUNCH(B, W, NC)                                        \
+  {                                                                 \
+    blocks = bwd_blocks<W>(T, H);                                   \
+    if (blocks > 0) {                                               \
+      if constexpr (NC > 1) MOE_LAUNCH_HELD(B, W, NC, 2);           \
+      else if (k <= 2) MOE_LAUNCH_HELD(B, W, NC, 2);                \
+      else if constexpr (W > 8) MOE_LAUNCH_HELD(B, W, NC, 4);       \
+      else if (k <= 4) MOE_LAUNCH_HELD(B, W, NC, 4);                \
+      else MOE_LAUNCH_HELD(B, W, NC, 8);                            \
+    }                                                               \
   }
   if (bf16) { MOE_NORM_SHAPES1(true, MOE_LAUNCH) } else { MOE_NORM_SHAPES1(false, MOE_LAUNCH) }
 #undef MOE_LAUNCH
+#undef MOE_LAUNCH_HELD
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (blocks != 1)  // (none: zeros)
