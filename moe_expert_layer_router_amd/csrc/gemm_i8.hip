@@ -17,7 +17,7 @@
 //     on its CU and takes tile after tile; operands through two LDS stages of 128
 //     bytes of K (whole cache lines) filled by DMA, the next tile's first stages on
 //     their way while the results of the last are written.  16384 tokens of the whole
-//     layer: gate and up 417 us (1975 TOP/s), down 324 (1274).  Bound by what fills the
+//     layer: gate and up 400 to 417 us (2000 TOP/s), down 320 (1290).  Bound by what fills the
 //     LDS: some 20 bytes a clock and CU arrive (64 lines in flight at 412 clocks each),
 //     1.5 to 1.75 us for the 64 KB of a step, 2450 TOP/s and more in the steady state;
 //     the products alone would take 1.15 us (3740 TOP/s on random operands).  The rest

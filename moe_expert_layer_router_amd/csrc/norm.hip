@@ -15,8 +15,8 @@
 // bytes; everything of the row stays in registers between its sums and its
 // stores, so each matrix crosses the memory once, which is what bounds all four.
 // 16384 tokens of 2048 bf16 columns, top-8, moved bytes over time: before 47 us, 5.7
-// TB/s, its backward 56 us, 4.8 TB/s; after 113 us, 5.9 TB/s, its backward 239 us,
-// 4.8 TB/s, with 5 us behind each backward for the sum of the partial rows (a copy of
+// TB/s, its backward 56 us, 4.8 TB/s; after 114 us, 5.9 TB/s, its backward 233 us,
+// 4.9 TB/s, with 5 us behind each backward for the sum of the partial rows (a copy of
 // 1 GiB reaches 5.0, a fill 6.9).
 #include <algorithm>
 

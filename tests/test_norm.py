@@ -187,6 +187,10 @@ NORM = [("bf16", 1, 2048), ("bf16", 3, 8), ("bf16", 130, 512), ("bf16", 129, 102
         ("bf16", 2051, 2048), ("bf16", 37, 2056), ("bf16", 9, 8192), ("bf16", 5, 16384), ("f32", 1, 4),
         ("f32", 77, 64), ("f32", 1003, 516), ("f32", 33, 1024), ("f32", 33, 2052), ("f32", 7, 4096),
         ("f32", 4, 16384), ("bf16", 9000, 64)]
+# more rows than one a team of the backward, in every shape
+NORM += [(dt, T, H // (1 if dt == "bf16" else 2)) for dt in ("bf16", "f32")
+         for T, H in ((4200, 512), (4200, 1024), (4200, 2048), (600, 4096), (300, 8192), (270, 9008))]
+NORM += [("f32", 260, 9008), ("f32", 260, 16384)]
 
 
 @gpu
@@ -232,6 +236,11 @@ AFTER = [("bf16", 1, 2048, 8, "none", 1.0), ("bf16", 33, 2048, 8, "full", 1.0), 
          ("f32", 256, 64, 2, "token", 1.0), ("f32", 19, 516, 6, "full", 0.8), ("f32", 23, 1024, 8, "none", 1.0),
          ("f32", 9, 2052, 20, "full", 0.9), ("f32", 5, 16384, 3, "token", 1.0), ("f32", 13, 260, 5, "none", 0.0),
          ("bf16", 3000, 2048, 2, "token", 0.6)]
+# every shape of a row's waves with one to eight slots held, more tokens than one a team of the backward
+AFTER += [(dt, T, H // (1 if dt == "bf16" else 2), k, gate, 0.8) for dt in ("bf16", "f32")
+          for T, H in ((4200, 512), (2100, 1024), (1100, 2048), (560, 4096), (300, 8192), (270, 9008))
+          for k, gate in ((1, "full"), (4, "none"), (7, "token"))]
+AFTER += [("f32", 260, 9008, 2, "none", 0.8), ("f32", 260, 8192, 3, "token", 0.8), ("f32", 260, 16384, 4, "full", 0.9)]
 
 
 @gpu
