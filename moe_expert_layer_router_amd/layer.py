@@ -6,7 +6,8 @@ maps only and its FFN reads the token rows through src_row), and for the
 backward the router weight's transpose ->
 combine_bwd -> grouped FFN backward -> unweighted combine of dx_perm plus the
 router's dx (on that transpose) -> route_bwd.
-All buffers and workspaces are allocated once in the constructor, so
+All buffers and workspaces are allocated once in the constructor (the gate's
+gradient in the first backward with a gate of its form), so
 forward()/backward() only enqueue kernels (and can be captured into a HIP
 graph).  In the backward, the grouped FFN's weight gradients and then the
 router backward run on a second stream (default priority) beside the data
@@ -80,6 +81,9 @@ def _group(*widths: int) -> int:
 
 class MoELayer:
     ADAPTER_KEYS = frozenset(("token_adapter", "n", "gate", "up", "down", "scale"))
+    # The gate's gradient has a buffer for each form of the gate ([T] and [T,H]), made by its first
+    # backward and never replaced: a captured step goes on writing the one that it was captured with.
+    DGATE = {1: "dgate", 2: "dgate_full"}
 
     def __init__(self, T: int, H: int, I: int, E: int, k: int, e_lo: int, e_hi: int,
                  dtype: torch.dtype, device="cuda", train: bool = True, fp8: bool = False,
@@ -498,10 +502,10 @@ class MoELayer:
         if self.post_norm is not None:
             out = {"dy_perm": b["dy_perm"], "d_topk_w": b["d_topk_w"], "dweight": b["dpost_weight"]}
             if gate is not None:
-                g = b.get("dgate")
-                if g is None or g.shape != gate.shape or g.dtype != gate.dtype:
-                    b["dgate"] = torch.empty_like(gate)
-                out["dgate"] = b["dgate"]
+                name = self.DGATE[gate.dim()]
+                if name not in b:
+                    b[name] = torch.empty_like(gate)
+                out["dgate"] = b[name]
             moe_combine_norm_bwd(dy, b["y_perm"], b["topk_w"], b["dest_row"], post_weight, self.post_norm,
                                  gate=gate, ws=self.ws_norm, out=out)
         elif self._drop is not None:
@@ -546,7 +550,7 @@ class MoELayer:
         if self.post_norm is not None:
             got["dpost_weight"] = b["dpost_weight"]
             if gate is not None:
-                got["dgate"] = b["dgate"]
+                got["dgate"] = b[self.DGATE[gate.dim()]]
         if self.pre_norm is not None:
             moe_norm_bwd(b["dx"], residual, pre_weight, self.pre_norm, dr=dy, dr_scale=residual_scale,
                          ws=self.ws_norm, out={"dx": b["dx_in"], "dweight": b["dpre_weight"]})
