@@ -111,7 +111,7 @@ class MoELayer:
         self.aux = balance_coef != 0.0 or z_coef != 0.0
         self.adapters = adapters
         self._drop = None  # the forward's dropout numbers
-        self._norms = (None, None, None, None, 1.0)  # and its residual, norm weights, gate and scale
+        self._norms = (None, None, None, None, 1.0)  # what the norms' backward reads: r, weights, gate, scale
         if fp8 and (dtype != torch.bfloat16 or H % 128 or I % 128 or I > 2048):
             raise ValueError("the FP8 layer needs bf16 tensors, H % 128 == 0, I % 128 == 0 "
                              "and I <= 2048")
@@ -293,7 +293,9 @@ class MoELayer:
         if self.pre_norm is not None:
             moe_norm(x, pre_weight, self.pre_norm, delta=delta, out={"n": b["n"], "r": b["r"]})
             residual, x = x if delta is None else b["r"], b["n"]
-        self._norms = (residual, pre_weight, post_weight, gate, residual_scale)
+        if self.train:  # (tensors of a layer that reads none of them again are not held)
+            self._norms = (residual if self.pre_norm is not None else None, pre_weight, post_weight, gate,
+                           residual_scale)
         if self.fp8:
             self._quantize_weights_fp8(w_gate, w_up, w_down)
         _check(lib.moe_route(_p(x), _p(w_router), _p(bias), T, H, E, k, self.dt,

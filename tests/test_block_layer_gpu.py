@@ -1,5 +1,7 @@
 """The layer with norms around it: what it keeps between calls, and each of its options against the calls
 that it is made of."""
+import weakref
+
 import pytest
 import torch
 
@@ -52,3 +54,27 @@ def test_a_captured_gate_gradient_outlives_a_gate_of_the_other_form():
         assert any(t is captured for t in layer.buf.values())
         assert torch.equal(captured, step(other, token)) and torch.equal(got, keep)
         assert step(layer, token).data_ptr() == captured.data_ptr()
+
+
+@pytest.mark.parametrize("form", ["train", "serve", "serve norms", "train post", "train pre"])
+def test_a_layer_holds_no_tensor_that_it_does_not_read_again(form):
+    """The residual, and in a layer built for the forward alone every input, is its caller's alone once
+    forward() is back.  Training with a norm holds what the norm's backward reads."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    T, H, I, E, k, eps = 24, 64, 64, 4, 2, 1e-6
+    w = weights(g, H, I, E, bf)
+    train, pre, post = form.startswith("train"), form in ("serve norms", "train pre"), form in ("serve norms", "train post")
+    layer = moe.MoELayer(T, H, I, E, k, 0, E, bf, DEV, train=train, pre_norm=eps if pre else None,
+                         post_norm=eps if post else None)
+    given = {"x": rand(g, T, H, dt=bf)}
+    if pre:
+        given["pre_weight"] = torch.ones(H, device=DEV)
+    else:
+        given["residual"] = rand(g, T, H, dt=bf)
+    if post:
+        given.update(post_weight=torch.ones(H, device=DEV), gate=torch.rand(T, device=DEV))
+    refs = {n: weakref.ref(t) for n, t in given.items()}
+    layer.forward(given.pop("x"), *w, **given)
+    del given
+    held = {n for n, r in refs.items() if r() is not None}
+    assert held == ({"train post": {"post_weight", "gate"}, "train pre": {"x", "pre_weight"}}.get(form, set()))
