@@ -95,9 +95,9 @@ class MoELayer:
             raise ValueError(f"dropout={dropout} outside [0, 1)")
         if adapters and (fp8 or train):
             raise ValueError("adapters=True needs a layer built for the forward alone (not fp8)")
-        if int8 and (train or fp8 or adapters or dtype != torch.bfloat16 or H % 16 or I % 16):
+        if int8 and (train or fp8 or adapters or dtype != torch.bfloat16 or H % 64 or I % 16):
             raise ValueError("int8=True needs a bf16 layer built for the forward alone (not fp8, no "
-                             "adapters), H and I multiples of 16")
+                             "adapters), H a multiple of 64 (the bf16 router's) and I of 16")
         if checkpoint is not None and (not train or fp8 or not _group(I, H)):
             raise ValueError("checkpoint needs a layer built for training (not fp8), H and I multiples of 32")
         if (pre_norm is not None or post_norm is not None) and (e_lo, e_hi) != (0, E):
