@@ -103,6 +103,14 @@ class MoELayer:
         if (pre_norm is not None or post_norm is not None) and (e_lo, e_hi) != (0, E):
             raise ValueError("the norms need all experts of the layer: a rank's part of the combined row is "
                              "not the row")
+        for name, eps in (("pre_norm", pre_norm), ("post_norm", post_norm)):
+            # a positive normal fp32 number, as the kernels hold it
+            if eps is not None and not torch.finfo(torch.float32).tiny <= eps <= torch.finfo(torch.float32).max:
+                raise ValueError(f"{name}={eps} is the eps of its norm and has to be a positive normal fp32 number")
+        if pre_norm is not None or post_norm is not None:
+            norm_ws = lib.moe_norm_ws_bytes(H)  # refuses rows that the norms do not take
+            if norm_ws < 0:
+                _check(int(norm_ws), "moe_norm_ws_bytes")
         if post_norm is not None and dropout > 0.0:
             raise ValueError("dropout and post_norm do not go together")
         self.int8, self.pre_norm, self.post_norm = int8, pre_norm, post_norm
@@ -168,10 +176,7 @@ class MoELayer:
                 _check(int(nb), "moe_ffn_i8_ws_bytes")
             self.ws_i8 = torch.empty(max(int(nb), 256), dtype=torch.uint8, device=dev)
         if train and (pre_norm is not None or post_norm is not None):
-            nb = lib.moe_norm_ws_bytes(H)
-            if nb < 0:
-                _check(int(nb), "moe_norm_ws_bytes")
-            self.ws_norm = torch.empty(int(nb), dtype=torch.uint8, device=dev)
+            self.ws_norm = torch.empty(norm_ws, dtype=torch.uint8, device=dev)
             if pre_norm is not None:
                 b["dx_in"] = torch.empty((T, H), dtype=dtype, device=dev)
                 b["dpre_weight"] = torch.empty(H, dtype=f32, device=dev)
