@@ -112,8 +112,9 @@ def test_waits_at_a_tiles_end_leave_what_follows_the_steps(asm, gate_up):
         if ev != "B":
             continue
         for s, end in paths(code, i):
-            if s.count("D") != 2 * STEP:  # not the way through a tile's end
+            if end == "B" or "D" not in s:  # not the way through a tile's end
                 continue
+            assert s.count("D") == 2 * STEP, (s, end)
             ops = s.replace("0", "").replace("w", "")
             at = [j for j, c in enumerate(ops) if c == "D"]
             behind = len(ops) - 1 - at[STEP - 1], len(ops) - 1 - at[2 * STEP - 1]
