@@ -15,13 +15,18 @@
 //   many rows (tile_i8_kernel): bound by the matrix cores and what feeds them.
 //     Tiles of 256 rows x 256 weight rows in a workgroup of eight waves that stays
 //     on its CU and takes tile after tile; operands through two LDS stages of 128
-//     bytes of K (whole cache lines) filled by DMA, the next tile's first stages on
-//     their way while the results of the last are written.  16384 tokens of the whole
-//     layer: gate and up 400 to 417 us (2000 TOP/s), down 320 (1290).  Bound by what fills the
-//     LDS: some 20 bytes a clock and CU arrive (64 lines in flight at 412 clocks each),
+//     bytes of K (whole cache lines) filled by DMA, the next tile's first stages
+//     issued between the stores of the last one's results.  16384 tokens of the whole
+//     layer: gate and up 400 to 417 us (2000 TOP/s), down 320 (1290).  The steps are bound by
+//     what fills the LDS: by the clocks of a step some 20 bytes a clock and CU arrive,
 //     1.5 to 1.75 us for the 64 KB of a step, 2450 TOP/s and more in the steady state;
 //     the products alone would take 1.15 us (3740 TOP/s on random operands).  The rest
 //     are the ends of the tiles, for the down product with its 6 steps a tile a third.
+//     Two waits that the compiler adds there make them longer than the counted ones ask:
+//     before a tile's first products one for everything (the clamp of the next tile's row map uses
+//     the loaded rows at once), which waits for the second step and the last tile's
+//     stores as well; and in the down product seven reloads of spilled registers, each with one,
+//     between the last stores of a tile.
 // Weights are the first operand of the MFMA, so that a lane's results are
 // neighbouring columns of one row; which weight row takes which place in the
 // operand is chosen so that they are 16 or 32 in a run.

@@ -12,8 +12,14 @@
 // the grouped rows for the gate weights' gradient anyway and forms c again.
 //
 // A row belongs to a team of W waves, each lane of which holds NC chunks of 16
-// bytes; everything of the row stays in registers between its sums and its
-// stores, so each matrix crosses the memory once, which is what bounds all four.
+// bytes of it between its sums and its stores, so each matrix of token rows crosses
+// the memory once, which is what bounds all four.  So does y_perm in the backward of
+// "after" while a token's local slots are no more than a lane can hold: 8 slots for
+// rows of up to 512 chunks (4096 bf16 or 2048 fp32 columns), 4 up to twice and 2 up to
+// four (fp32: eight) times that; tokens with more read their grouped rows twice.  The registers of
+// four waves a SIMD do not hold all of it everywhere: the compiler spills 4 to 22 of them with
+// 8 slots of bf16 (11 for the 2048 columns below), 7 with 4 slots of 8192 columns, 47 and 85
+// (bf16, fp32) with 16384 columns, whose norm_bwd_kernel spills 21 and 59.
 // 16384 tokens of 2048 bf16 columns, top-8, moved bytes over time: before 47 us, 5.7
 // TB/s, its backward 56 us, 4.8 TB/s; after 114 us, 5.9 TB/s, its backward 233 us,
 // 4.9 TB/s, with 5 us behind each backward for the sum of the partial rows (a copy of
@@ -584,8 +590,9 @@ int bwd_blocks(int T, int H) {
   if (nch <= 64) M(B, 1, 1) else if (nch <= 128) M(B, 1, 2) else if (nch <= 256) M(B, 1, 4) \
   else if (nch <= 512) M(B, 4, 2) else if (nch <= 1024) M(B, 4, 4) else if (nch <= 2048) M(B, 16, 2) \
   else if constexpr (!B) M(B, 16, 4)
-// One chunk a lane, so that eight slots' rows and the sums fit the registers (the
-// backward then reads each grouped row once).
+// One chunk a lane as long as there are waves for it, so that a lane can hold the rows of
+// several slots: with eight (up to 512 chunks), four (1024) or two (above) of a token's, the
+// backward reads its grouped rows once, with more of them twice.
 #define MOE_NORM_SHAPES1(B, M) \
   if (nch <= 64) M(B, 1, 1) else if (nch <= 128) M(B, 2, 1) else if (nch <= 256) M(B, 4, 1) \
   else if (nch <= 512) M(B, 8, 1) else if (nch <= 1024) M(B, 16, 1) else if (nch <= 2048) M(B, 16, 2) \

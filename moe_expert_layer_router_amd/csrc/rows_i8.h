@@ -6,7 +6,9 @@
 // are defined bit for bit.  |v (127 / a)| rounds to 127 at most.  A group whose a
 // is below 2^-100 (where 127 / a would leave fp32) has scale 0 and codes 0; a
 // group with an infinity or a NaN has that as its scale, so that it comes back
-// as NaN rather than as a number.
+// as NaN rather than as a number (whatever its codes: those next to a NaN are the
+// low byte of its payload).  A group whose a is the largest fp32 number comes back with an
+// infinity in a's place: a / 127 is rounded up.
 #pragma once
 
 #include "rows.h"
@@ -43,8 +45,8 @@ struct Scale {
 };
 
 // Codes of four values: adding 1.5 * 2^23 rounds a product within +-127 to the
-// nearest whole number, ties to even, and leaves it in the low byte; NaN
-// (an infinity times 0) leaves 0 there.  The product is rounded by itself.
+// nearest whole number, ties to even, and leaves it in the low byte; an infinity
+// times 0 leaves 0 there.  The product is rounded by itself.
 __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
 #pragma clang fp contract(off)
   uint32_t b[4];

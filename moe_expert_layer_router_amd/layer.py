@@ -30,7 +30,8 @@ router backward stay as in the bf16 layer.
 
 With int8=True (forward only) the expert FFN runs on int8 codes: forward() takes
 each expert weight as the pair (codes, scales) that moe_quantize_i8 made of it
-once, and quantizes the token rows itself.
+once, and quantizes the token rows itself.  Routing stays bf16: H is a multiple of
+64, I of 16.
 
 Options around the layer, in any of its forms unless said otherwise:
  - balance_coef, z_coef: the router's auxiliary losses, in buf["aux_loss"] (and
@@ -44,7 +45,8 @@ Options around the layer, in any of its forms unless said otherwise:
  - checkpoint=pool (training, not fp8): what the backward needs of the grouped
    rows is kept as 8-bit codes (gate and up, and the expert outputs), and the
    large buffers (x_perm, gu, h_perm, y_perm) are those of the dict `pool`, which
-   layers of the same sizes share: the first one fills it.  forward() leaves the
+   layers of the same sizes share: the first one fills it (the backward's own dy_perm
+   and dx_perm stay with each layer).  forward() leaves the
    codes, backward() restores the buffers from them and permutes x again, so
    layers may run forward one after another and backward in the other order.
  - pre_norm, post_norm (whole layers, [e_lo, e_hi) = [0, E)): with pre_norm the
